@@ -334,10 +334,7 @@ def _own(s):
             out["dgate"] = g.dgate
         return out
     if op == "logprobs":
-        ws = _kept(s, "workspace", lambda: torch.empty(
-            mk.muon_token_logprobs_workspace_bytes(c["rows"], c["vocab"], c["top"]), dtype=torch.uint8,
-            device="cuda"))
-        got = mk.muon_token_logprobs(s["logits"], s["tokens"], top=c["top"], workspace=ws)
+        got = mk.muon_token_logprobs(s["logits"], s["tokens"], top=c["top"])
         out = {"logp": got.logp, "entropy": got.entropy, "lse": got.lse}
         if c["top"]:
             out |= {"top_ids": got.top_ids, "top_logp": got.top_logp}
