@@ -303,6 +303,179 @@ int muon_adamw_update_f32(float *param, const float *grad, float *exp_avg, float
                           float lr, float beta1, float beta2, float eps, float weight_decay, int64_t step,
                           muon_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Gated feed-forward block over whole expert matrices: the operator whose
+ * weights the Muon step updates (an expert holds w1 and w3, hidden x ffn, and
+ * w2, ffn x hidden), and its gradients, in the layout the step reads.
+ * Rows (tokens) are sorted by expert: rows offsets[e] .. offsets[e+1]-1 are
+ * expert e's.  For a row x of expert e:
+ *   g = x w1[e];  u = x w3[e];  h = act(g) * u;  y = h w2[e]
+ *   x         device, bf16, rows x hidden, rows x_stride elements apart
+ *   w1, w3    device, bf16, [experts][hidden][ffn];  w2 [experts][ffn][hidden]
+ *   offsets   device, experts + 1 int64 values, non-decreasing from 0 to rows
+ *             (an expert may have no rows); NULL with experts == 1: all rows.
+ *             Read on the device when the work runs: values that break this
+ *             rule are clamped, so that no access leaves the arrays, and
+ *             reported as MUON_ERR_DEVICE; rows of no group are not written.
+ *   act       MUON_ACT_SILU, or MUON_ACT_GELU (tanh form)
+ *   y         device, bf16, rows x hidden, y_stride elements apart (written)
+ *   gate, up  device, bf16, [rows][ffn] dense: g and u for the backward pass;
+ *             NULL (both) when it will not run (serving)
+ * Arithmetic: bf16 operands, fp32 accumulation; h is rounded to bf16 between
+ * the products, y, gate and up once at the end.  x, y and the rest must not
+ * overlap.  A row's result depends on that row alone; the kernel that
+ * computes it, and with it the order of its sums, is chosen by the sizes.
+ * Requirements: hidden, ffn and the strides multiples of 8, pointers 16-byte
+ * aligned (offsets: 8), else MUON_ERR_UNSUPPORTED.  rows == 0 is a no-op.
+ * workspace: device, 256-byte aligned, muon_gated_ffn_workspace_bytes() bytes,
+ * used until the enqueued work has finished; NULL allocates and frees it
+ * stream-ordered.  Errors: MUON_ERR_INVALID_ARG for null pointers, bad sizes
+ * or strides below hidden, MUON_ERR_NO_MEMORY as muon_step_batched.
+ */
+typedef enum { MUON_ACT_SILU = 0, MUON_ACT_GELU = 1 } muon_activation;
+
+size_t muon_gated_ffn_workspace_bytes(int64_t rows, int64_t experts, int64_t hidden, int64_t ffn);
+int muon_gated_ffn(const void *x, int64_t x_stride, const void *w1, const void *w3, const void *w2,
+                   const int64_t *offsets, int64_t rows, int64_t experts, int64_t hidden, int64_t ffn, int act,
+                   void *y, int64_t y_stride, void *gate, void *up, void *workspace, size_t workspace_bytes,
+                   muon_stream_t stream);
+
+/* Its gradients.  With dh = dy w2^T, dg = dh u act'(g), du = dh act(g):
+ *   dx = dg w1^T + du w3^T;  dw1 = x^T dg;  dw3 = x^T du;  dw2 = h^T dy
+ * dy and the outputs are bf16 in the layouts above; gate and up are what the
+ * forward pass kept.  The weight gradients are overwritten (zeros for an
+ * expert without rows) and are what muon_step_batched reads as `grad`.  dx may
+ * be NULL (not wanted: w1 and w3 are then not read), or dw1, dw3, dw2 (all
+ * three: x is then not read).  dg, du and h are rounded to bf16 before the
+ * products that read them; sums are fp32.  A NaN or infinity in one expert's
+ * rows does not reach another's gradients.  rows == 0 writes zero weight
+ * gradients.  Requirements, workspace and errors as muon_gated_ffn. */
+size_t muon_gated_ffn_backward_workspace_bytes(int64_t rows, int64_t experts, int64_t hidden, int64_t ffn);
+int muon_gated_ffn_backward(const void *dy, int64_t dy_stride, const void *x, int64_t x_stride, const void *gate,
+                            const void *up, const void *w1, const void *w3, const void *w2, const int64_t *offsets,
+                            int64_t rows, int64_t experts, int64_t hidden, int64_t ffn, int act, void *dx,
+                            int64_t dx_stride, void *dw1, void *dw3, void *dw2, void *workspace,
+                            size_t workspace_bytes, muon_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * RMS norms after a block and before the next, with the block's gate and the
+ * residual scale, in one pass:
+ *   n  = block * rstd_post * w_post;   rstd_post = 1/sqrt(mean(block^2) + eps)
+ *   r' = residual + scale * gate * n                       (residual_out)
+ *   y  = r' * rstd_pre * w_pre;        rstd_pre = 1/sqrt(mean(r'^2) + eps)  (normed)
+ * block == NULL: only the norm before a block (r' = residual, residual_out is
+ * not written).  normed == NULL: only the norm after one.  A null w_post, gate
+ * or w_pre stands for ones.  All arrays are on the device, rows x hidden with
+ * rows *_stride elements apart; the residual arrays have residual_type, block,
+ * gate, normed and the weights branch_type: bf16 with bf16, fp32 with bf16 or
+ * fp32 with fp32 (bf16 with fp32 is MUON_ERR_UNSUPPORTED).  gate_stride 0
+ * gives one gate row for all rows.  rstd_post and rstd_pre (fp32, rows; may be
+ * NULL) are what the backward pass takes.  All arithmetic is fp32; normed is
+ * formed from r' before r' is rounded to its type.  residual_out may be
+ * residual.  hidden <= 16384, else MUON_ERR_UNSUPPORTED; any alignment of the
+ * element type (hidden and strides multiples of 8 and 16-byte aligned
+ * pointers take the vector path).  rows == 0 is a no-op.
+ */
+typedef enum { MUON_BF16 = 0, MUON_F32 = 1 } muon_dtype;
+
+typedef struct {
+  int64_t rows, hidden;
+  int residual_type, branch_type;   /* muon_dtype */
+  const void *residual;
+  int64_t residual_stride;
+  const void *block;
+  int64_t block_stride;
+  const void *w_post, *gate;
+  int64_t gate_stride;
+  const void *w_pre;
+  float scale, eps;
+  void *residual_out;
+  int64_t residual_out_stride;
+  void *normed;
+  int64_t normed_stride;
+  float *rstd_post, *rstd_pre;
+} muon_block_norm_args;
+
+int muon_block_norm(const muon_block_norm_args *args, muon_stream_t stream);
+
+/* Its gradients, from dresidual_out (the gradient of r' through everything
+ * after; NULL: zero) and dnormed (NULL: no norm before a block), with residual
+ * = r' as the forward pass stored it:
+ *   dr = dresidual_out + rstd_pre (w_pre dnormed - xh mean(w_pre dnormed xh)),  xh = r' rstd_pre
+ *   dn = scale gate dr;   bh = block rstd_post
+ *   dblock = rstd_post (w_post dn - bh mean(w_post dn bh));   dresidual = dr
+ *   dw_pre = sum dnormed xh;  dw_post = sum dn bh;  dgate = scale dr bh w_post
+ * Sums run over the rows, in fp32 and a fixed order, and are rounded once to
+ * branch_type; dgate is summed for a shared gate (gate_stride 0, hidden
+ * values) and per row otherwise (rows dgate_stride apart).  Outputs may be
+ * NULL when not wanted; dresidual may be dresidual_out.  workspace (for the
+ * sums): device, 256-byte aligned,
+ * muon_block_norm_backward_workspace_bytes(); NULL allocates it
+ * stream-ordered.  rows == 0 writes zero sums.  Errors as muon_block_norm and
+ * MUON_ERR_NO_MEMORY. */
+typedef struct {
+  int64_t rows, hidden;
+  int residual_type, branch_type;
+  const void *dresidual_out;
+  int64_t dresidual_out_stride;
+  const void *dnormed;
+  int64_t dnormed_stride;
+  const void *residual;
+  int64_t residual_stride;
+  const void *block;
+  int64_t block_stride;
+  const void *w_post, *gate;
+  int64_t gate_stride;
+  const void *w_pre;
+  const float *rstd_post, *rstd_pre;
+  float scale;
+  void *dresidual;
+  int64_t dresidual_stride;
+  void *dblock;
+  int64_t dblock_stride;
+  void *dw_post, *dgate;
+  int64_t dgate_stride;
+  void *dw_pre;
+} muon_block_norm_backward_args;
+
+size_t muon_block_norm_backward_workspace_bytes(int64_t rows, int64_t hidden);
+int muon_block_norm_backward(const muon_block_norm_backward_args *args, void *workspace, size_t workspace_bytes,
+                             muon_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Log probabilities of given tokens, with entropy and top alternatives:
+ *   lse = log sum_v exp x_v;  logp = x[token] - lse;  entropy = lse - sum_v p_v x_v
+ *   logits    device, rows x vocab of `type` (bf16 or fp32), rows `stride`
+ *             elements apart, any alignment of the element type
+ *   tokens    device, int64, rows.  A negative token is not scored (logp 0);
+ *             one >= vocab gives NaN and MUON_ERR_DEVICE.  May be NULL with
+ *             logp NULL.
+ *   logp, entropy, lse   device, fp32, rows (each may be NULL)
+ *   top       0..32: the `top` largest logits of each row, in descending
+ *             order, equal ones by ascending index, NaN first: top_ids (int64,
+ *             rows x top) and top_logp (fp32, rows x top; may be NULL)
+ * -inf is a masked entry (probability 0).  A row with nothing but -inf gets
+ * lse = logp = top_logp = -inf and entropy 0.  A NaN or +inf makes the row's
+ * lse, logp and entropy NaN.  Sums are fp32.  No workspace.
+ * MUON_ERR_UNSUPPORTED: top > 32, vocab > 2^30, rows > 2^27, or a pointer not
+ * aligned to its element.
+ */
+int muon_token_logprobs(const void *logits, int64_t stride, const int64_t *tokens, int64_t rows, int64_t vocab,
+                        int type, float *logp, float *entropy, float *lse, int top, int64_t *top_ids, float *top_logp,
+                        muon_stream_t stream);
+
+/* The gradient of sum_rows dlogp logp + dentropy entropy in the logits:
+ *   dlogits_v = dlogp (1[v = token] - p_v) - dentropy p_v (x_v - lse + entropy)
+ * lse and entropy are the forward call's (entropy may be NULL when dentropy
+ * is); dlogp or dentropy may be NULL (zero).  A row that is not scored
+ * (negative token) takes no part in dlogp.  A row with lse = -inf, or with both
+ * factors zero, gets zeros.  dlogits has `type`, rows dlogits_stride apart, and
+ * may be the logits themselves (same stride). */
+int muon_token_logprobs_backward(const void *logits, int64_t stride, const int64_t *tokens, const float *lse,
+                                 const float *entropy, const float *dlogp, const float *dentropy, int64_t rows,
+                                 int64_t vocab, int type, void *dlogits, int64_t dlogits_stride,
+                                 muon_stream_t stream);
+
 /* The default shape scale sqrt(max(1, rows/cols)). */
 float muon_default_scale(int64_t rows, int64_t cols);
 
@@ -313,7 +486,8 @@ float muon_default_scale(int64_t rows, int64_t cols);
  * word: MUON_ERR_TIMEOUT if a bounded wait ran out, MUON_ERR_DEVICE if a
  * Newton-Schulz input (or fused step's u) had a Frobenius norm that is not
  * finite in fp32 (an Inf or NaN entry, or entries beyond ~1.8e19; its output
- * is then zero or NaN), MUON_ERR_CUDA for a CUDA error, else MUON_OK. */
+ * is then zero or NaN) or a feed-forward or log-probability call met offsets or
+ * a token out of range, MUON_ERR_CUDA for a CUDA error, else MUON_OK. */
 int muon_get_device_status(muon_stream_t stream);
 
 /* Human-readable name of a muon_status value (static string). */

@@ -13,6 +13,7 @@ whole-expert ownership so that the step needs no communication.
 
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -55,6 +56,31 @@ class HostGroup(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class BlockNormArgs(ctypes.Structure):
+    """muon_block_norm_args"""
+    _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int64), ("residual_type", ctypes.c_int),
+                ("branch_type", ctypes.c_int), ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64),
+                ("block", ctypes.c_void_p), ("block_stride", ctypes.c_int64), ("w_post", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_int64), ("w_pre", ctypes.c_void_p),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("residual_out", ctypes.c_void_p),
+                ("residual_out_stride", ctypes.c_int64), ("normed", ctypes.c_void_p),
+                ("normed_stride", ctypes.c_int64), ("rstd_post", ctypes.c_void_p), ("rstd_pre", ctypes.c_void_p)]
+
+
+class BlockNormBackwardArgs(ctypes.Structure):
+    """muon_block_norm_backward_args"""
+    _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int64), ("residual_type", ctypes.c_int),
+                ("branch_type", ctypes.c_int), ("dresidual_out", ctypes.c_void_p),
+                ("dresidual_out_stride", ctypes.c_int64), ("dnormed", ctypes.c_void_p),
+                ("dnormed_stride", ctypes.c_int64), ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64),
+                ("block", ctypes.c_void_p), ("block_stride", ctypes.c_int64), ("w_post", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_int64), ("w_pre", ctypes.c_void_p),
+                ("rstd_post", ctypes.c_void_p), ("rstd_pre", ctypes.c_void_p), ("scale", ctypes.c_float),
+                ("dresidual", ctypes.c_void_p), ("dresidual_stride", ctypes.c_int64), ("dblock", ctypes.c_void_p),
+                ("dblock_stride", ctypes.c_int64), ("dw_post", ctypes.c_void_p), ("dgate", ctypes.c_void_p),
+                ("dgate_stride", ctypes.c_int64), ("dw_pre", ctypes.c_void_p)]
+
+
 SIGNATURES = {
     "muon_momentum_update": (_INT, [_P, _P, _P, _I64, _F, _INT, _P]),
     "muon_momentum_update_f32": (_INT, [_P, _P, _P, _I64, _F, _INT, _P]),
@@ -79,6 +105,17 @@ SIGNATURES = {
     "muon_step_host_grouped": (_INT, [_P, _INT, _F, _INT, _INT, _P, _F, _F, _F, _I64, _P]),
     "muon_adamw_update": (_INT, [_P, _P, _P, _P, _I64, _F, _F, _F, _F, _F, _I64, _P]),
     "muon_adamw_update_f32": (_INT, [_P, _P, _P, _P, _I64, _F, _F, _F, _F, _F, _I64, _P]),
+    "muon_gated_ffn_workspace_bytes": (_SIZE, [_I64, _I64, _I64, _I64]),
+    "muon_gated_ffn": (_INT, [_P, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _INT, _P, _I64, _P, _P, _P, _SIZE,
+                              _P]),
+    "muon_gated_ffn_backward_workspace_bytes": (_SIZE, [_I64, _I64, _I64, _I64]),
+    "muon_gated_ffn_backward": (_INT, [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _INT, _P,
+                                       _I64, _P, _P, _P, _P, _SIZE, _P]),
+    "muon_block_norm": (_INT, [_P, _P]),
+    "muon_block_norm_backward_workspace_bytes": (_SIZE, [_I64, _I64]),
+    "muon_block_norm_backward": (_INT, [_P, _P, _SIZE, _P]),
+    "muon_token_logprobs": (_INT, [_P, _I64, _P, _I64, _I64, _INT, _P, _P, _P, _INT, _P, _P, _P]),
+    "muon_token_logprobs_backward": (_INT, [_P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _INT, _P, _I64, _P]),
     "muon_get_device_status": (_INT, [_P]),
     "muon_status_string": (ctypes.c_char_p, [_INT]),
     "muon_set_wait_timeout_ns": (_U64, [_U64]),
@@ -408,6 +445,334 @@ def muon_step_host_grouped(groups, *, mu=0.95, nesterov=True, steps=5, coeffs=QU
     _check("muon_step_host_grouped", lib().muon_step_host_grouped(
         ctypes.cast(arr, ctypes.c_void_p), len(groups), float(mu), int(bool(nesterov)), int(steps), _coeffs(coeffs),
         float(eps), float(lr), float(weight_decay), int(chunk), _stream_handle(stream)))
+
+
+# ---------------------------------------------------------------------------- operators around the step
+ACTIVATIONS = {"silu": 0, "gelu": 1}
+BlockNormGrads = collections.namedtuple("BlockNormGrads", "dresidual dblock dw_post dgate dw_pre")
+TokenLogprobs = collections.namedtuple("TokenLogprobs", "logp entropy lse top_ids top_logp")
+
+
+def _rows(t, dtype, shape, name, contiguous=False):
+    """Checks a CUDA tensor of `shape` whose last axis is dense; returns its row stride."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return shape[-1]
+    if contiguous:
+        raise ValueError(f"{name} must be contiguous")
+    stride = t.stride()
+    if len(stride) != 2 or (stride[1] != 1 and shape[1] > 1) or (stride[0] < shape[1] and shape[0] > 1):
+        raise ValueError(f"{name} must be dense along its last axis, with rows that do not overlap")
+    return max(stride[0], shape[1])   # the stride of a single row says nothing
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("all tensors must be on one device")
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def _workspace(workspace):
+    import torch
+    if workspace is None:
+        return None, 0
+    _need(workspace, torch.uint8, "workspace")
+    return workspace.data_ptr(), workspace.numel()
+
+
+def _ffn_shapes(x, w1, w3, w2, offsets, act):
+    import torch
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
+    if w1.dim() not in (2, 3):
+        raise ValueError("w1 must be (experts, hidden, ffn) or (hidden, ffn)")
+    lead, (H, F) = w1.shape[:-2], w1.shape[-2:]
+    E = lead[0] if lead else 1
+    bf = torch.bfloat16
+    _rows(w1, bf, w1.shape, "w1", True)
+    _rows(w3, bf, w1.shape, "w3", True)
+    _rows(w2, bf, torch.Size((*lead, F, H)), "w2", True)
+    if offsets is None:
+        if E != 1:
+            raise ValueError("offsets are needed with more than one expert")
+    else:
+        _rows(offsets, torch.int64, torch.Size((E + 1,)), "offsets", True)
+    ldx = _rows(x, bf, torch.Size((len(x), H)), "x")
+    _same_device(x, w1, w3, w2, offsets)
+    return ldx, len(x), E, H, F
+
+
+def muon_gated_ffn_workspace_bytes(rows, experts, hidden, ffn):
+    return int(lib().muon_gated_ffn_workspace_bytes(rows, experts, hidden, ffn))
+
+
+def muon_gated_ffn(x, w1, w3, w2, offsets=None, *, act="silu", keep=False, out=None, workspace=None, stream=None):
+    """Gated feed-forward block over expert matrices: (act(x w1) * (x w3)) w2, bf16; see muon.h.
+
+    x (rows, hidden), rows sorted by expert; w1, w3 (experts, hidden, ffn) and
+    w2 (experts, ffn, hidden) as the Muon step holds them (or one expert's 2-D
+    matrices); offsets int64 (experts + 1) on the GPU, the first row of each
+    expert and the end (None: one expert with all rows).  Returns y, or with
+    ``keep`` (y, gate, up) for the backward pass.
+    """
+    import torch
+    ldx, T, E, H, F = _ffn_shapes(x, w1, w3, w2, offsets, act)
+    gate = up = None
+    if keep:
+        gate, up = x.new_empty(T, F), x.new_empty(T, F)
+    if out is None:
+        out = x.new_empty(T, H)
+    ldy = _rows(out, torch.bfloat16, torch.Size((T, H)), "out")
+    ws, ws_bytes = _workspace(workspace)
+    _same_device(x, out, workspace)
+    _check("muon_gated_ffn", lib().muon_gated_ffn(
+        x.data_ptr(), ldx, w1.data_ptr(), w3.data_ptr(), w2.data_ptr(), _opt(offsets), T, E, H, F, ACTIVATIONS[act],
+        out.data_ptr(), ldy, _opt(gate), _opt(up), ws, ws_bytes, _stream_handle(stream)))
+    return (out, gate, up) if keep else out
+
+
+def muon_gated_ffn_backward_workspace_bytes(rows, experts, hidden, ffn):
+    return int(lib().muon_gated_ffn_backward_workspace_bytes(rows, experts, hidden, ffn))
+
+
+def muon_gated_ffn_backward(dy, x, gate, up, w1, w3, w2, offsets=None, *, act="silu", dx=None, dw=None, need_dx=True,
+                            need_dw=True, workspace=None, stream=None):
+    """Gradients of muon_gated_ffn: (dx, dw1, dw3, dw2), bf16, the last three what the Muon step takes.
+
+    gate and up are what the forward call kept.  dx and dw = (dw1, dw3, dw2)
+    are written (and overwritten) when given; what is not needed is None.
+    """
+    import torch
+    ldx, T, E, H, F = _ffn_shapes(x, w1, w3, w2, offsets, act)
+    bf = torch.bfloat16
+    rows_h, rows_f = torch.Size((T, H)), torch.Size((T, F))
+    lddy = _rows(dy, bf, rows_h, "dy")
+    _rows(gate, bf, rows_f, "gate", True)
+    _rows(up, bf, rows_f, "up", True)
+    lddx, dw1, dw3, dw2 = H, None, None, None
+    if need_dx:
+        if dx is None:
+            dx = x.new_empty(T, H)
+        lddx = _rows(dx, bf, rows_h, "dx")
+    else:
+        dx = None
+    if need_dw:
+        dw1, dw3, dw2 = dw if dw is not None else (torch.empty_like(w) for w in (w1, w3, w2))
+        for d, w, n in ((dw1, w1, "dw1"), (dw3, w3, "dw3"), (dw2, w2, "dw2")):
+            _rows(d, bf, w.shape, n, True)
+    ws, ws_bytes = _workspace(workspace)
+    _same_device(x, dy, gate, up, dx, dw1, dw3, dw2, workspace)
+    _check("muon_gated_ffn_backward", lib().muon_gated_ffn_backward(
+        dy.data_ptr(), lddy, x.data_ptr(), ldx, gate.data_ptr(), up.data_ptr(), w1.data_ptr(), w3.data_ptr(),
+        w2.data_ptr(), _opt(offsets), T, E, H, F, ACTIVATIONS[act], _opt(dx), lddx, _opt(dw1), _opt(dw3), _opt(dw2),
+        ws, ws_bytes, _stream_handle(stream)))
+    return dx, dw1, dw3, dw2
+
+
+def _dtype_code(t, name):
+    import torch
+    if t.dtype is torch.bfloat16:
+        return 0
+    if t.dtype is torch.float32:
+        return 1
+    raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+
+
+def _gate(gate, dtype, T, H):
+    """A gate's row stride: 0 for one gate for all rows."""
+    import torch
+    if gate.dim() == 1:
+        _rows(gate, dtype, torch.Size((H,)), "gate", True)
+        return 0
+    return _rows(gate, dtype, torch.Size((T, H)), "gate")
+
+
+def muon_block_norm(residual, block=None, *, w_post=None, gate=None, w_pre=None, scale=1.0, eps=1e-6, norm_next=True,
+                    out=None, normed=None, stream=None):
+    """RMS norms after a block and before the next, with gate and residual scale; see muon.h.
+
+    r' = residual + scale * gate * rmsnorm(block) * w_post, y = rmsnorm(r') *
+    w_pre.  residual (rows, hidden) bf16 or fp32; block, gate ((hidden,) for
+    all rows or (rows, hidden)), weights and y share one type.  Without block
+    r' is residual itself; without norm_next there is no y.  Returns
+    (r', y, rstd_post, rstd_pre), None in the place of what there is not.
+    """
+    import torch
+    if residual.dim() != 2:
+        raise ValueError("residual must be (rows, hidden)")
+    T, H = shape = residual.shape
+    rt, dev, f32 = residual.dtype, residual.device, torch.float32
+    branch = next((t for t in (block, w_pre, w_post, gate, normed) if t is not None), residual)
+    bt = branch.dtype
+    a = BlockNormArgs(rows=T, hidden=H, residual_type=_dtype_code(residual, "residual"),
+                      branch_type=_dtype_code(branch, "block"), scale=scale, eps=eps)
+    a.residual, a.residual_stride = residual.data_ptr(), _rows(residual, rt, shape, "residual")
+    rstd_post = rstd_pre = None
+    if block is None:
+        if w_post is not None or gate is not None or out is not None:
+            raise ValueError("w_post, gate and out belong to a block")
+        if not norm_next:
+            raise ValueError("there is nothing to compute without a block and without norm_next")
+        out = residual
+    else:
+        a.block, a.block_stride = block.data_ptr(), _rows(block, bt, shape, "block")
+        if w_post is not None:
+            _rows(w_post, bt, shape[1:], "w_post", True)
+            a.w_post = w_post.data_ptr()
+        if gate is not None:
+            a.gate_stride = _gate(gate, bt, T, H)
+            a.gate = gate.data_ptr()
+        if out is None:
+            out = torch.empty(shape, dtype=rt, device=dev)
+        a.residual_out, a.residual_out_stride = out.data_ptr(), _rows(out, rt, shape, "out")
+        rstd_post = torch.empty(T, dtype=f32, device=dev)
+        a.rstd_post = rstd_post.data_ptr()
+    if norm_next:
+        if w_pre is not None:
+            _rows(w_pre, bt, shape[1:], "w_pre", True)
+            a.w_pre = w_pre.data_ptr()
+        if normed is None:
+            normed = torch.empty(shape, dtype=bt, device=dev)
+        a.normed, a.normed_stride = normed.data_ptr(), _rows(normed, bt, shape, "normed")
+        rstd_pre = torch.empty(T, dtype=f32, device=dev)
+        a.rstd_pre = rstd_pre.data_ptr()
+    elif w_pre is not None or normed is not None:
+        raise ValueError("w_pre and normed belong to the norm before the next block")
+    _same_device(residual, block, w_post, gate, w_pre, out, normed)
+    _check("muon_block_norm", lib().muon_block_norm(ctypes.byref(a), _stream_handle(stream)))
+    return out, normed, rstd_post, rstd_pre
+
+
+def muon_block_norm_backward_workspace_bytes(rows, hidden):
+    return int(lib().muon_block_norm_backward_workspace_bytes(rows, hidden))
+
+
+def muon_block_norm_backward(dresidual, dnormed, residual, block=None, rstd_post=None, rstd_pre=None, *, w_post=None,
+                             gate=None, w_pre=None, scale=1.0, workspace=None, stream=None):
+    """Gradients of muon_block_norm: BlockNormGrads(dresidual, dblock, dw_post, dgate, dw_pre).
+
+    dresidual (None: zero) and dnormed (None: there was no y) are the
+    gradients of what the forward call returned, residual is the r' it
+    returned, the rest what it took and returned.  A gradient is None where
+    the forward call had no such input.
+    """
+    import torch
+    if residual.dim() != 2:
+        raise ValueError("residual must be (rows, hidden)")
+    T, H = shape = residual.shape
+    rt, dev, f32 = residual.dtype, residual.device, torch.float32
+    branch = next((t for t in (dnormed, block, w_pre, w_post, gate) if t is not None), residual)
+    bt = branch.dtype
+    a = BlockNormBackwardArgs(rows=T, hidden=H, residual_type=_dtype_code(residual, "residual"),
+                              branch_type=_dtype_code(branch, "block"), scale=scale)
+    if dresidual is None and dnormed is None:
+        raise ValueError("dresidual or dnormed must be given")
+    if dresidual is not None:
+        a.dresidual_out, a.dresidual_out_stride = dresidual.data_ptr(), _rows(dresidual, rt, shape, "dresidual")
+    dblock = dw_post = dgate = dw_pre = None
+    a.residual, a.residual_stride = residual.data_ptr(), _rows(residual, rt, shape, "residual")
+    if dnormed is not None:
+        a.dnormed, a.dnormed_stride = dnormed.data_ptr(), _rows(dnormed, bt, shape, "dnormed")
+        _rows(rstd_pre, f32, shape[:1], "rstd_pre", True)
+        a.rstd_pre = rstd_pre.data_ptr()
+        if w_pre is not None:
+            _rows(w_pre, bt, shape[1:], "w_pre", True)
+            dw_pre = torch.empty_like(w_pre)
+            a.w_pre, a.dw_pre = w_pre.data_ptr(), dw_pre.data_ptr()
+    elif w_pre is not None:
+        raise ValueError("w_pre belongs to the norm before the next block")
+    if block is not None:
+        a.block, a.block_stride = block.data_ptr(), _rows(block, bt, shape, "block")
+        _rows(rstd_post, f32, shape[:1], "rstd_post", True)
+        a.rstd_post = rstd_post.data_ptr()
+        dblock = torch.empty(shape, dtype=bt, device=dev)
+        a.dblock, a.dblock_stride = dblock.data_ptr(), H
+        if w_post is not None:
+            _rows(w_post, bt, shape[1:], "w_post", True)
+            dw_post = torch.empty_like(w_post)
+            a.w_post, a.dw_post = w_post.data_ptr(), dw_post.data_ptr()
+        if gate is not None:
+            a.gate_stride = _gate(gate, bt, T, H)
+            dgate = torch.empty(gate.shape, dtype=bt, device=dev)
+            a.gate, a.dgate, a.dgate_stride = gate.data_ptr(), dgate.data_ptr(), H
+    elif w_post is not None or gate is not None:
+        raise ValueError("w_post and gate belong to a block")
+    dr = torch.empty(shape, dtype=rt, device=dev)
+    a.dresidual, a.dresidual_stride = dr.data_ptr(), H
+    ws, ws_bytes = _workspace(workspace)
+    _same_device(residual, dresidual, dnormed, block, rstd_post, rstd_pre, w_post, gate, w_pre, workspace)
+    _check("muon_block_norm_backward", lib().muon_block_norm_backward(ctypes.byref(a), ws, ws_bytes,
+                                                                      _stream_handle(stream)))
+    return BlockNormGrads(dr, dblock, dw_post, dgate, dw_pre)
+
+
+def muon_token_logprobs(logits, tokens=None, *, top=0, stream=None):
+    """Log probabilities of tokens (int64, rows) under logits (rows, vocab), bf16 or fp32; see muon.h.
+
+    Returns TokenLogprobs(logp, entropy, lse, top_ids, top_logp), fp32 but the
+    int64 ids; logp is None without tokens, the last two without ``top``.
+    """
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits must be (rows, vocab)")
+    code = _dtype_code(logits, "logits")
+    T, V = logits.shape
+    stride = _rows(logits, logits.dtype, logits.shape, "logits")
+    dev, f32 = logits.device, torch.float32
+    logp = top_ids = top_logp = None
+    if tokens is not None:
+        _rows(tokens, torch.int64, logits.shape[:1], "tokens", True)
+        logp = torch.empty(T, dtype=f32, device=dev)
+    entropy, lse = torch.empty(T, dtype=f32, device=dev), torch.empty(T, dtype=f32, device=dev)
+    if top:
+        top_ids = torch.empty(T, max(0, top), dtype=torch.int64, device=dev)
+        top_logp = torch.empty(T, max(0, top), dtype=f32, device=dev)
+    _same_device(logits, tokens)
+    _check("muon_token_logprobs", lib().muon_token_logprobs(
+        logits.data_ptr(), stride, _opt(tokens), T, V, code, _opt(logp), entropy.data_ptr(), lse.data_ptr(), top,
+        _opt(top_ids), _opt(top_logp), _stream_handle(stream)))
+    return TokenLogprobs(logp, entropy, lse, top_ids, top_logp)
+
+
+def muon_token_logprobs_backward(logits, tokens, lse, entropy=None, dlogp=None, dentropy=None, *, out=None,
+                                 stream=None):
+    """The gradient of sum(dlogp * logp + dentropy * entropy) in the logits, in their type.
+
+    lse and entropy are the forward call's; ``out`` may be the logits themselves.
+    """
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits must be (rows, vocab)")
+    code = _dtype_code(logits, "logits")
+    T, V = logits.shape
+    stride = _rows(logits, logits.dtype, logits.shape, "logits")
+    if tokens is not None:
+        _rows(tokens, torch.int64, logits.shape[:1], "tokens", True)
+    elif dlogp is not None:
+        raise ValueError("dlogp needs tokens")
+    if dentropy is not None and entropy is None:
+        raise ValueError("dentropy needs entropy")
+    for t, n in ((lse, "lse"), (entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy")):
+        if t is not None or n == "lse":
+            _rows(t, torch.float32, logits.shape[:1], n, True)
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    out_stride = _rows(out, logits.dtype, logits.shape, "out")
+    _same_device(logits, tokens, lse, entropy, dlogp, dentropy, out)
+    _check("muon_token_logprobs_backward", lib().muon_token_logprobs_backward(
+        logits.data_ptr(), stride, _opt(tokens), lse.data_ptr(), _opt(entropy), _opt(dlogp), _opt(dentropy), T, V,
+        code, out.data_ptr(), out_stride, _stream_handle(stream)))
+    return out
 
 
 def muon_default_scale(rows, cols):

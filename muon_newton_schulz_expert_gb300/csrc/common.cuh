@@ -32,6 +32,18 @@ enum TraceKind : int {
   kTraceAdamW,
   kTraceMomentumNorm,  // momentum fused with the per-matrix sum of squares
   kTraceAxpyApply,     // last iteration's X' = s (a X + B X) fused with W' = kw W + ko X'
+  kTraceFfnUp,         // Hid = act(X W1) * (X W3) (tensor cores)
+  kTraceFfnDown,       // Y = Hid W2
+  kTraceFfnDh,         // dG, dU, Hid from dY W2^T
+  kTraceFfnDx,         // dX = dG W1^T + dU W3^T
+  kTraceFfnTail,       // zero-padded copies of each group's last rows
+  kTraceFfnDw13,       // dW1 = X^T dG, dW3 = X^T dU
+  kTraceFfnDw2,        // dW2 = Hid^T dY
+  kTraceBlockNorm,
+  kTraceBlockNormBwd,
+  kTraceNormWeightSum,
+  kTraceLogprobs,
+  kTraceLogprobsBwd,
   kTraceKinds
 };
 
@@ -120,6 +132,29 @@ int ns_axpy(const void *B, const void *X, int tin, const uint8_t *X_lo, float lo
 int ns_axpy_apply(const void *B, const void *X, int tin, __nv_bfloat16 *W, int64_t batch, int64_t m, int64_t n,
                   float a, const float *s1, float mul, float kw, float ko, bool transposed, cudaStream_t s);
 int selftest_wait(unsigned long long timeout_ns, cudaStream_t s);
+
+// ---- products of the gated feed-forward block (ffn_tc.cu) ----
+// rows sorted by expert: rows offsets[e] .. offsets[e+1] (device) are expert
+// e's; null offsets: one expert with all rows.  Sizes are at least 1, hidden
+// and ffn multiples of 8, every array 16-byte aligned, row strides (ld, in
+// elements) multiples of 8; hid, gate, up, dg, du are dense [rows][ffn].
+struct FfnShape {
+  const int64_t *offsets;
+  int64_t rows, experts, hidden, ffn;
+  int act;
+};
+// hid = act(x w1) * (x w3); gate and up (both or neither null) get the two products
+int ffn_up(const FfnShape &f, const void *x, int64_t ldx, const void *w1, const void *w3, void *hid, void *gate,
+           void *up, cudaStream_t s);
+int ffn_down(const FfnShape &f, const void *hid, const void *w2, void *y, int64_t ldy, cudaStream_t s);
+int ffn_dh(const FfnShape &f, const void *dy, int64_t lddy, const void *w2, const void *gate, const void *up, void *dg,
+           void *du, void *hid, cudaStream_t s);
+int ffn_dx(const FfnShape &f, const void *dg, const void *du, const void *w1, const void *w3, void *dx, int64_t lddx,
+           cudaStream_t s);
+// scratch of ffn_dw, in bf16 elements
+size_t ffn_tail_elems(const FfnShape &f);
+int ffn_dw(const FfnShape &f, const void *x, int64_t ldx, const void *dy, int64_t lddy, const void *dg, const void *du,
+           const void *hid, void *tails, void *dw1, void *dw3, void *dw2, cudaStream_t s);
 
 // ---- fp32 SIMT GEMMs for the verification mode (gemm_f32.cu) ----
 // mode 0: C = s2 * P P^T (P m x k);  mode 1: C = b*P + c*P P (P m x m);

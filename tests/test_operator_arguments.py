@@ -1,0 +1,117 @@
+"""Argument errors of the operators around the step, returned on the host before any CUDA call."""
+
+import ctypes
+
+import pytest
+
+import muon_newton_schulz_expert_gb300 as mk
+from muon_newton_schulz_expert_gb300 import build as mkbuild
+
+P = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def lib():
+    mkbuild.build()
+    return mk.lib()
+
+
+def ffn(lib, x=P(256), xs=64, w=P(256), off=P(256), rows=4, experts=2, hidden=64, ffn_=72, act=0, y=P(256), ys=64,
+        gate=None, up=None, ws=P(256), wsb=0):
+    return lib.muon_gated_ffn(x, xs, w, w, w, off, rows, experts, hidden, ffn_, act, y, ys, gate, up, ws, wsb, None)
+
+
+def test_gated_ffn(lib):
+    for bad in (dict(rows=-1), dict(experts=0), dict(hidden=0), dict(ffn_=0), dict(act=2), dict(off=None),
+                dict(x=None), dict(w=None), dict(y=None), dict(gate=P(256)), dict(up=P(256)), dict(xs=56),
+                dict(ys=56), dict(ws=P(256 + 16))):
+        assert ffn(lib, **bad) == -1, bad
+    for bad in (dict(hidden=60, xs=64), dict(ffn_=4), dict(xs=68), dict(ys=65), dict(x=P(264)), dict(y=P(258)),
+                dict(w=P(8)), dict(rows=1 << 31), dict(experts=1 << 17), dict(gate=P(264), up=P(256))):
+        assert ffn(lib, **bad) == -2, bad
+    assert ffn(lib, wsb=10) == -4
+    assert ffn(lib, rows=0, x=None, y=None) == 0
+
+
+def test_gated_ffn_backward(lib):
+    def call(dy=P(256), dys=64, x=P(256), xs=64, gate=P(256), up=P(256), w=P(256), off=P(256), rows=4, experts=2,
+             hidden=64, ffn_=72, act=0, dx=P(256), dxs=64, dw1=P(256), dw3=P(256), dw2=P(256), ws=P(256), wsb=0):
+        return lib.muon_gated_ffn_backward(dy, dys, x, xs, gate, up, w, w, w, off, rows, experts, hidden, ffn_, act,
+                                           dx, dxs, dw1, dw3, dw2, ws, wsb, None)
+
+    for bad in (dict(rows=-1), dict(act=-1), dict(dy=None), dict(x=None), dict(gate=None), dict(up=None),
+                dict(w=None), dict(dw1=None), dict(dw2=None), dict(dx=None, dw1=None, dw3=None, dw2=None),
+                dict(dys=8), dict(dxs=8), dict(ws=P(8))):
+        assert call(**bad) == -1, bad
+    for bad in (dict(hidden=68, dys=72, xs=72, dxs=72), dict(dys=68), dict(dw3=P(264))):
+        assert call(**bad) == -2, bad
+    assert call(wsb=1000) == -4
+    assert call(rows=0, dw1=None, dw3=None, dw2=None) == 0
+
+
+def test_workspace_sizes(lib):
+    assert lib.muon_gated_ffn_workspace_bytes(100, 3, 64, 72) >= 100 * 72 * 2
+    assert lib.muon_gated_ffn_backward_workspace_bytes(100, 3, 64, 72) >= 3 * 100 * 72 * 2
+    for bad in ((0, 1, 64, 72), (1, 0, 64, 72), (1, 1, 60, 72), (1, 1, 64, -8)):
+        assert lib.muon_gated_ffn_workspace_bytes(*bad) == 0
+        assert lib.muon_gated_ffn_backward_workspace_bytes(*bad) == 0
+    assert lib.muon_block_norm_backward_workspace_bytes(0, 64) == 0
+    assert lib.muon_block_norm_backward_workspace_bytes(1, 1 << 20) == 0
+
+
+def test_block_norm(lib):
+    def call(**kw):
+        base = dict(rows=2, hidden=64, residual=256, residual_stride=64, block=256, block_stride=64, scale=1.0,
+                    eps=1e-6, residual_out=256, residual_out_stride=64, normed=256, normed_stride=64)
+        return lib.muon_block_norm(ctypes.byref(mk.BlockNormArgs(**{**base, **kw})), None)
+
+    assert lib.muon_block_norm(None, None) == -1
+    for bad in (dict(rows=-1), dict(hidden=0), dict(residual_type=2), dict(branch_type=-1), dict(eps=-1.0),
+                dict(eps=float("nan")), dict(scale=float("inf")), dict(residual=None), dict(residual_out=None),
+                dict(block=None, normed=None), dict(residual_stride=63), dict(block_stride=0),
+                dict(normed_stride=10), dict(gate=256, gate_stride=5)):
+        assert call(**bad) == -1, bad
+    assert call(branch_type=1) == -2
+    assert call(hidden=16385, residual_stride=20000) == -2
+    assert call(rows=0, residual=None) == 0
+
+
+def test_block_norm_backward(lib):
+    def call(ws=P(256), wsb=0, **kw):
+        base = dict(rows=2, hidden=64, dresidual_out=256, dresidual_out_stride=64, dnormed=256, dnormed_stride=64,
+                    residual=256, residual_stride=64, block=256, block_stride=64, rstd_post=256, rstd_pre=256,
+                    scale=1.0, dresidual=256, dresidual_stride=64, dblock=256, dblock_stride=64, dw_pre=256)
+        return lib.muon_block_norm_backward(ctypes.byref(mk.BlockNormBackwardArgs(**{**base, **kw})), ws, wsb, None)
+
+    assert lib.muon_block_norm_backward(None, None, 0, None) == -1
+    for bad in (dict(rows=-1), dict(residual_type=7), dict(scale=float("nan")), dict(residual=None),
+                dict(rstd_pre=None), dict(rstd_post=None), dict(dnormed=None), dict(block=None),
+                dict(dnormed=None, dresidual_out=None, dw_pre=None), dict(dgate=256), dict(gate_stride=-1),
+                dict(dresidual=None, dblock=None, dw_pre=None), dict(dblock_stride=3), dict(ws=P(16), wsb=1 << 30)):
+        assert call(**bad) == -1, bad
+    assert call(hidden=20000) == -2
+    assert call(rows=0, dw_pre=None) == 0
+
+
+def test_token_logprobs(lib):
+    def call(x=P(256), stride=100, tokens=P(256), rows=2, vocab=100, type_=0, logp=P(256), entropy=None, lse=None,
+             top=0, ids=None, tlp=None):
+        return lib.muon_token_logprobs(x, stride, tokens, rows, vocab, type_, logp, entropy, lse, top, ids, tlp, None)
+
+    for bad in (dict(rows=-1), dict(vocab=0), dict(type_=3), dict(stride=99), dict(top=-1), dict(top=5),
+                dict(ids=P(256)), dict(x=None), dict(tokens=None), dict(logp=None),
+                dict(top=20, ids=P(256), vocab=10)):
+        assert call(**bad) == -1, bad
+    assert call(top=33, ids=P(256)) == -2
+    assert call(rows=0, x=None) == 0
+
+    def back(x=P(256), stride=100, tokens=P(256), lse=P(256), ent=P(256), dlogp=P(256), dent=P(256), rows=2,
+             vocab=100, type_=0, out=P(256), out_stride=100):
+        return lib.muon_token_logprobs_backward(x, stride, tokens, lse, ent, dlogp, dent, rows, vocab, type_, out,
+                                                out_stride, None)
+
+    for bad in (dict(rows=-1), dict(vocab=0), dict(type_=2), dict(stride=1), dict(out_stride=99), dict(x=None),
+                dict(lse=None), dict(ent=None), dict(tokens=None), dict(dlogp=None, dent=None), dict(out=None)):
+        assert back(**bad) == -1, bad
+    assert back(x=P(257)) == -2
+    assert back(rows=0) == 0
