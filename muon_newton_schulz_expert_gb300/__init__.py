@@ -16,6 +16,7 @@ from __future__ import annotations
 import collections
 import ctypes
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # MUON_CHECKED=1 loads the checked build (device-side checks of the kernels'
@@ -54,31 +55,6 @@ class HostGroup(ctypes.Structure):
     _fields_ = [("param_host", ctypes.c_void_p), ("grad_host", ctypes.c_void_p), ("momentum_host", ctypes.c_void_p),
                 ("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
                 ("scale", ctypes.c_float)]
-
-
-class BlockNormArgs(ctypes.Structure):
-    """muon_block_norm_args"""
-    _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int64), ("residual_type", ctypes.c_int),
-                ("branch_type", ctypes.c_int), ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64),
-                ("block", ctypes.c_void_p), ("block_stride", ctypes.c_int64), ("w_post", ctypes.c_void_p),
-                ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_int64), ("w_pre", ctypes.c_void_p),
-                ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("residual_out", ctypes.c_void_p),
-                ("residual_out_stride", ctypes.c_int64), ("normed", ctypes.c_void_p),
-                ("normed_stride", ctypes.c_int64), ("rstd_post", ctypes.c_void_p), ("rstd_pre", ctypes.c_void_p)]
-
-
-class BlockNormBackwardArgs(ctypes.Structure):
-    """muon_block_norm_backward_args"""
-    _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int64), ("residual_type", ctypes.c_int),
-                ("branch_type", ctypes.c_int), ("dresidual_out", ctypes.c_void_p),
-                ("dresidual_out_stride", ctypes.c_int64), ("dnormed", ctypes.c_void_p),
-                ("dnormed_stride", ctypes.c_int64), ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64),
-                ("block", ctypes.c_void_p), ("block_stride", ctypes.c_int64), ("w_post", ctypes.c_void_p),
-                ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_int64), ("w_pre", ctypes.c_void_p),
-                ("rstd_post", ctypes.c_void_p), ("rstd_pre", ctypes.c_void_p), ("scale", ctypes.c_float),
-                ("dresidual", ctypes.c_void_p), ("dresidual_stride", ctypes.c_int64), ("dblock", ctypes.c_void_p),
-                ("dblock_stride", ctypes.c_int64), ("dw_post", ctypes.c_void_p), ("dgate", ctypes.c_void_p),
-                ("dgate_stride", ctypes.c_int64), ("dw_pre", ctypes.c_void_p)]
 
 
 SIGNATURES = {
@@ -453,28 +429,43 @@ BlockNormGrads = collections.namedtuple("BlockNormGrads", "dresidual dblock dw_p
 TokenLogprobs = collections.namedtuple("TokenLogprobs", "logp entropy lse top_ids top_logp")
 
 
-def _rows(t, dtype, shape, name, contiguous=False):
+# The binding's own time counts in calls of a few microseconds: argument structs are packed in one go, and the
+# checks look at each tensor once.
+_NORM_ARGS = struct.Struct("@qqii" "Pq" "Pq" "PPqP" "ff" "Pq" "Pq" "PP")        # muon_block_norm_args
+_NORM_BACKWARD_ARGS = struct.Struct("@qqii" "PqPqPqPq" "PPqP" "PP" "f" "PqPq" "PPqP")   # muon_block_norm_backward_args
+
+
+def _rows(t, dtype, shape, name):
     """Checks a CUDA tensor of `shape` whose last axis is dense; returns its row stride."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    _dense(t, dtype, shape, name, True)
     if t.is_contiguous():
         return shape[-1]
-    if contiguous:
-        raise ValueError(f"{name} must be contiguous")
     stride = t.stride()
     if len(stride) != 2 or (stride[1] != 1 and shape[1] > 1) or (stride[0] < shape[1] and shape[0] > 1):
         raise ValueError(f"{name} must be dense along its last axis, with rows that do not overlap")
     return max(stride[0], shape[1])   # the stride of a single row says nothing
 
 
-def _same_device(first, *others):
+def _dense(t, dtype, shape, name, any_stride=False):
+    try:
+        if t.is_cuda and t.dtype is dtype and t.shape == shape and (any_stride or t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _one_device(first, *others):
+    index = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
             raise ValueError("all tensors must be on one device")
 
 
@@ -482,34 +473,48 @@ def _opt(t):
     return None if t is None else t.data_ptr()
 
 
+def _raw_stream(stream):
+    """The stream's handle; None is the current stream of the current device."""
+    if stream is None:
+        from torch import _C
+        return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _workspace(workspace):
-    import torch
     if workspace is None:
         return None, 0
+    import torch
     _need(workspace, torch.uint8, "workspace")
     return workspace.data_ptr(), workspace.numel()
 
 
 def _ffn_shapes(x, w1, w3, w2, offsets, act):
+    """(row stride of x, rows, experts, hidden, ffn, activation), after the checks that both directions share."""
     import torch
-    if act not in ACTIVATIONS:
+    code = ACTIVATIONS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
-    if w1.dim() not in (2, 3):
-        raise ValueError("w1 must be (experts, hidden, ffn) or (hidden, ffn)")
-    lead, (H, F) = w1.shape[:-2], w1.shape[-2:]
-    E = lead[0] if lead else 1
-    bf = torch.bfloat16
-    _rows(w1, bf, w1.shape, "w1", True)
-    _rows(w3, bf, w1.shape, "w3", True)
-    _rows(w2, bf, torch.Size((*lead, F, H)), "w2", True)
-    if offsets is None:
-        if E != 1:
-            raise ValueError("offsets are needed with more than one expert")
+    shape = w1.shape
+    if len(shape) == 3:
+        E, H, F = shape
+        w2_shape = (E, F, H)
+    elif len(shape) == 2:
+        E, (H, F) = 1, shape
+        w2_shape = (F, H)
     else:
-        _rows(offsets, torch.int64, torch.Size((E + 1,)), "offsets", True)
-    ldx = _rows(x, bf, torch.Size((len(x), H)), "x")
-    _same_device(x, w1, w3, w2, offsets)
-    return ldx, len(x), E, H, F
+        raise ValueError("w1 must be (experts, hidden, ffn) or (hidden, ffn)")
+    bf = torch.bfloat16
+    T = x.shape[0]
+    ldx = _rows(x, bf, (T, H), "x")
+    _dense(w1, bf, shape, "w1")
+    _dense(w3, bf, shape, "w3")
+    _dense(w2, bf, w2_shape, "w2")
+    if offsets is not None:
+        _dense(offsets, torch.int64, (E + 1,), "offsets")
+    elif E != 1:
+        raise ValueError("offsets are needed with more than one expert")
+    return ldx, T, E, H, F, code
 
 
 def muon_gated_ffn_workspace_bytes(rows, experts, hidden, ffn):
@@ -525,19 +530,21 @@ def muon_gated_ffn(x, w1, w3, w2, offsets=None, *, act="silu", keep=False, out=N
     expert and the end (None: one expert with all rows).  Returns y, or with
     ``keep`` (y, gate, up) for the backward pass.
     """
-    import torch
-    ldx, T, E, H, F = _ffn_shapes(x, w1, w3, w2, offsets, act)
-    gate = up = None
+    ldx, T, E, H, F, code = _ffn_shapes(x, w1, w3, w2, offsets, act)
+    gate = up = gate_ptr = up_ptr = None
     if keep:
-        gate, up = x.new_empty(T, F), x.new_empty(T, F)
+        gate, up = x.new_empty((T, F)), x.new_empty((T, F))
+        gate_ptr, up_ptr = gate.data_ptr(), up.data_ptr()
+    ldy = H
     if out is None:
-        out = x.new_empty(T, H)
-    ldy = _rows(out, torch.bfloat16, torch.Size((T, H)), "out")
+        out = x.new_empty((T, H))
+    else:
+        ldy = _rows(out, x.dtype, (T, H), "out")
     ws, ws_bytes = _workspace(workspace)
-    _same_device(x, out, workspace)
+    _one_device(x, w1, w3, w2, offsets, out, workspace)
     _check("muon_gated_ffn", lib().muon_gated_ffn(
-        x.data_ptr(), ldx, w1.data_ptr(), w3.data_ptr(), w2.data_ptr(), _opt(offsets), T, E, H, F, ACTIVATIONS[act],
-        out.data_ptr(), ldy, _opt(gate), _opt(up), ws, ws_bytes, _stream_handle(stream)))
+        x.data_ptr(), ldx, w1.data_ptr(), w3.data_ptr(), w2.data_ptr(), _opt(offsets), T, E, H, F, code,
+        out.data_ptr(), ldy, gate_ptr, up_ptr, ws, ws_bytes, _raw_stream(stream)))
     return (out, gate, up) if keep else out
 
 
@@ -552,30 +559,32 @@ def muon_gated_ffn_backward(dy, x, gate, up, w1, w3, w2, offsets=None, *, act="s
     gate and up are what the forward call kept.  dx and dw = (dw1, dw3, dw2)
     are written (and overwritten) when given; what is not needed is None.
     """
-    import torch
-    ldx, T, E, H, F = _ffn_shapes(x, w1, w3, w2, offsets, act)
-    bf = torch.bfloat16
-    rows_h, rows_f = torch.Size((T, H)), torch.Size((T, F))
-    lddy = _rows(dy, bf, rows_h, "dy")
-    _rows(gate, bf, rows_f, "gate", True)
-    _rows(up, bf, rows_f, "up", True)
+    ldx, T, E, H, F, code = _ffn_shapes(x, w1, w3, w2, offsets, act)
+    bf = x.dtype
+    lddy = _rows(dy, bf, (T, H), "dy")
+    _dense(gate, bf, (T, F), "gate")
+    _dense(up, bf, (T, F), "up")
     lddx, dw1, dw3, dw2 = H, None, None, None
-    if need_dx:
-        if dx is None:
-            dx = x.new_empty(T, H)
-        lddx = _rows(dx, bf, rows_h, "dx")
-    else:
+    if not need_dx:
         dx = None
+    elif dx is None:
+        dx = x.new_empty((T, H))
+    else:
+        lddx = _rows(dx, bf, (T, H), "dx")
     if need_dw:
-        dw1, dw3, dw2 = dw if dw is not None else (torch.empty_like(w) for w in (w1, w3, w2))
-        for d, w, n in ((dw1, w1, "dw1"), (dw3, w3, "dw3"), (dw2, w2, "dw2")):
-            _rows(d, bf, w.shape, n, True)
+        if dw is None:
+            dw1, dw3, dw2 = (w.new_empty(w.shape) for w in (w1, w3, w2))
+        else:
+            dw1, dw3, dw2 = dw
+            _dense(dw1, bf, w1.shape, "dw1")
+            _dense(dw3, bf, w3.shape, "dw3")
+            _dense(dw2, bf, w2.shape, "dw2")
     ws, ws_bytes = _workspace(workspace)
-    _same_device(x, dy, gate, up, dx, dw1, dw3, dw2, workspace)
+    _one_device(x, w1, w3, w2, offsets, dy, gate, up, dx, dw1, dw3, dw2, workspace)
     _check("muon_gated_ffn_backward", lib().muon_gated_ffn_backward(
         dy.data_ptr(), lddy, x.data_ptr(), ldx, gate.data_ptr(), up.data_ptr(), w1.data_ptr(), w3.data_ptr(),
-        w2.data_ptr(), _opt(offsets), T, E, H, F, ACTIVATIONS[act], _opt(dx), lddx, _opt(dw1), _opt(dw3), _opt(dw2),
-        ws, ws_bytes, _stream_handle(stream)))
+        w2.data_ptr(), _opt(offsets), T, E, H, F, code, _opt(dx), lddx, _opt(dw1), _opt(dw3), _opt(dw2), ws, ws_bytes,
+        _raw_stream(stream)))
     return dx, dw1, dw3, dw2
 
 
@@ -590,11 +599,10 @@ def _dtype_code(t, name):
 
 def _gate(gate, dtype, T, H):
     """A gate's row stride: 0 for one gate for all rows."""
-    import torch
     if gate.dim() == 1:
-        _rows(gate, dtype, torch.Size((H,)), "gate", True)
+        _dense(gate, dtype, (H,), "gate")
         return 0
-    return _rows(gate, dtype, torch.Size((T, H)), "gate")
+    return _rows(gate, dtype, (T, H), "gate")
 
 
 def muon_block_norm(residual, block=None, *, w_post=None, gate=None, w_pre=None, scale=1.0, eps=1e-6, norm_next=True,
@@ -611,46 +619,51 @@ def muon_block_norm(residual, block=None, *, w_post=None, gate=None, w_pre=None,
     if residual.dim() != 2:
         raise ValueError("residual must be (rows, hidden)")
     T, H = shape = residual.shape
-    rt, dev, f32 = residual.dtype, residual.device, torch.float32
+    rt = residual.dtype
     branch = next((t for t in (block, w_pre, w_post, gate, normed) if t is not None), residual)
     bt = branch.dtype
-    a = BlockNormArgs(rows=T, hidden=H, residual_type=_dtype_code(residual, "residual"),
-                      branch_type=_dtype_code(branch, "block"), scale=scale, eps=eps)
-    a.residual, a.residual_stride = residual.data_ptr(), _rows(residual, rt, shape, "residual")
+    rcode, bcode = _dtype_code(residual, "residual"), _dtype_code(branch, "block")
+    ldr = _rows(residual, rt, shape, "residual")
+    ldb = ldg = ldo = 0
     rstd_post = rstd_pre = None
     if block is None:
         if w_post is not None or gate is not None or out is not None:
             raise ValueError("w_post, gate and out belong to a block")
         if not norm_next:
             raise ValueError("there is nothing to compute without a block and without norm_next")
-        out = residual
     else:
-        a.block, a.block_stride = block.data_ptr(), _rows(block, bt, shape, "block")
+        ldb = _rows(block, bt, shape, "block")
         if w_post is not None:
-            _rows(w_post, bt, shape[1:], "w_post", True)
-            a.w_post = w_post.data_ptr()
+            _dense(w_post, bt, (H,), "w_post")
         if gate is not None:
-            a.gate_stride = _gate(gate, bt, T, H)
-            a.gate = gate.data_ptr()
+            ldg = _gate(gate, bt, T, H)
         if out is None:
-            out = torch.empty(shape, dtype=rt, device=dev)
-        a.residual_out, a.residual_out_stride = out.data_ptr(), _rows(out, rt, shape, "out")
-        rstd_post = torch.empty(T, dtype=f32, device=dev)
-        a.rstd_post = rstd_post.data_ptr()
+            out, ldo = residual.new_empty(shape), H
+        else:
+            ldo = _rows(out, rt, shape, "out")
     if norm_next:
         if w_pre is not None:
-            _rows(w_pre, bt, shape[1:], "w_pre", True)
-            a.w_pre = w_pre.data_ptr()
+            _dense(w_pre, bt, (H,), "w_pre")
         if normed is None:
-            normed = torch.empty(shape, dtype=bt, device=dev)
-        a.normed, a.normed_stride = normed.data_ptr(), _rows(normed, bt, shape, "normed")
-        rstd_pre = torch.empty(T, dtype=f32, device=dev)
-        a.rstd_pre = rstd_pre.data_ptr()
-    elif w_pre is not None or normed is not None:
-        raise ValueError("w_pre and normed belong to the norm before the next block")
-    _same_device(residual, block, w_post, gate, w_pre, out, normed)
-    _check("muon_block_norm", lib().muon_block_norm(ctypes.byref(a), _stream_handle(stream)))
-    return out, normed, rstd_post, rstd_pre
+            normed, ldn = branch.new_empty(shape), H
+        else:
+            ldn = _rows(normed, bt, shape, "normed")
+    else:
+        if w_pre is not None or normed is not None:
+            raise ValueError("w_pre and normed belong to the norm before the next block")
+        ldn = 0
+    stats = torch.empty((2, T), dtype=torch.float32, device=residual.device)   # both rows' factors
+    at = stats.data_ptr()
+    if block is not None:
+        rstd_post = stats[0]
+    if norm_next:
+        rstd_pre = stats[1]
+    _one_device(residual, block, w_post, gate, w_pre, out, normed)
+    _check("muon_block_norm", lib().muon_block_norm(_NORM_ARGS.pack(
+        T, H, rcode, bcode, residual.data_ptr(), ldr, *((0, 0) if block is None else (block.data_ptr(), ldb)),
+        _opt(w_post) or 0, _opt(gate) or 0, ldg, _opt(w_pre) or 0, scale, eps, _opt(out) or 0, ldo, _opt(normed) or 0,
+        ldn, at if block is not None else 0, at + 4 * T if norm_next else 0), _raw_stream(stream)))
+    return residual if block is None else out, normed, rstd_post, rstd_pre
 
 
 def muon_block_norm_backward_workspace_bytes(rows, hidden):
@@ -666,53 +679,54 @@ def muon_block_norm_backward(dresidual, dnormed, residual, block=None, rstd_post
     returned, the rest what it took and returned.  A gradient is None where
     the forward call had no such input.
     """
-    import torch
     if residual.dim() != 2:
         raise ValueError("residual must be (rows, hidden)")
     T, H = shape = residual.shape
-    rt, dev, f32 = residual.dtype, residual.device, torch.float32
+    rt = residual.dtype
     branch = next((t for t in (dnormed, block, w_pre, w_post, gate) if t is not None), residual)
     bt = branch.dtype
-    a = BlockNormBackwardArgs(rows=T, hidden=H, residual_type=_dtype_code(residual, "residual"),
-                              branch_type=_dtype_code(branch, "block"), scale=scale)
+    rcode, bcode = _dtype_code(residual, "residual"), _dtype_code(branch, "block")
     if dresidual is None and dnormed is None:
         raise ValueError("dresidual or dnormed must be given")
-    if dresidual is not None:
-        a.dresidual_out, a.dresidual_out_stride = dresidual.data_ptr(), _rows(dresidual, rt, shape, "dresidual")
+    import torch
+    f32 = torch.float32
+    ldr = _rows(residual, rt, shape, "residual")
+    ldd = ldn = ldb = ldg = 0
     dblock = dw_post = dgate = dw_pre = None
-    a.residual, a.residual_stride = residual.data_ptr(), _rows(residual, rt, shape, "residual")
+    if dresidual is not None:
+        ldd = _rows(dresidual, rt, shape, "dresidual")
     if dnormed is not None:
-        a.dnormed, a.dnormed_stride = dnormed.data_ptr(), _rows(dnormed, bt, shape, "dnormed")
-        _rows(rstd_pre, f32, shape[:1], "rstd_pre", True)
-        a.rstd_pre = rstd_pre.data_ptr()
+        ldn = _rows(dnormed, bt, shape, "dnormed")
+        _dense(rstd_pre, f32, (T,), "rstd_pre")
         if w_pre is not None:
-            _rows(w_pre, bt, shape[1:], "w_pre", True)
-            dw_pre = torch.empty_like(w_pre)
-            a.w_pre, a.dw_pre = w_pre.data_ptr(), dw_pre.data_ptr()
-    elif w_pre is not None:
-        raise ValueError("w_pre belongs to the norm before the next block")
+            _dense(w_pre, bt, (H,), "w_pre")
+            dw_pre = w_pre.new_empty((H,))
+    else:
+        if w_pre is not None:
+            raise ValueError("w_pre belongs to the norm before the next block")
+        rstd_pre = None
     if block is not None:
-        a.block, a.block_stride = block.data_ptr(), _rows(block, bt, shape, "block")
-        _rows(rstd_post, f32, shape[:1], "rstd_post", True)
-        a.rstd_post = rstd_post.data_ptr()
-        dblock = torch.empty(shape, dtype=bt, device=dev)
-        a.dblock, a.dblock_stride = dblock.data_ptr(), H
+        ldb = _rows(block, bt, shape, "block")
+        _dense(rstd_post, f32, (T,), "rstd_post")
+        dblock = block.new_empty(shape)
         if w_post is not None:
-            _rows(w_post, bt, shape[1:], "w_post", True)
-            dw_post = torch.empty_like(w_post)
-            a.w_post, a.dw_post = w_post.data_ptr(), dw_post.data_ptr()
+            _dense(w_post, bt, (H,), "w_post")
+            dw_post = w_post.new_empty((H,))
         if gate is not None:
-            a.gate_stride = _gate(gate, bt, T, H)
-            dgate = torch.empty(gate.shape, dtype=bt, device=dev)
-            a.gate, a.dgate, a.dgate_stride = gate.data_ptr(), dgate.data_ptr(), H
-    elif w_post is not None or gate is not None:
-        raise ValueError("w_post and gate belong to a block")
-    dr = torch.empty(shape, dtype=rt, device=dev)
-    a.dresidual, a.dresidual_stride = dr.data_ptr(), H
+            ldg = _gate(gate, bt, T, H)
+            dgate = gate.new_empty(gate.shape)
+    else:
+        if w_post is not None or gate is not None:
+            raise ValueError("w_post and gate belong to a block")
+        rstd_post = None
+    dr = residual.new_empty(shape)
     ws, ws_bytes = _workspace(workspace)
-    _same_device(residual, dresidual, dnormed, block, rstd_post, rstd_pre, w_post, gate, w_pre, workspace)
-    _check("muon_block_norm_backward", lib().muon_block_norm_backward(ctypes.byref(a), ws, ws_bytes,
-                                                                      _stream_handle(stream)))
+    _one_device(residual, dresidual, dnormed, block, rstd_post, rstd_pre, w_post, gate, w_pre, workspace)
+    _check("muon_block_norm_backward", lib().muon_block_norm_backward(_NORM_BACKWARD_ARGS.pack(
+        T, H, rcode, bcode, _opt(dresidual) or 0, ldd, _opt(dnormed) or 0, ldn, residual.data_ptr(), ldr,
+        _opt(block) or 0, ldb, _opt(w_post) or 0, _opt(gate) or 0, ldg, _opt(w_pre) or 0, _opt(rstd_post) or 0,
+        _opt(rstd_pre) or 0, scale, dr.data_ptr(), H, _opt(dblock) or 0, H, _opt(dw_post) or 0, _opt(dgate) or 0, H,
+        _opt(dw_pre) or 0), ws, ws_bytes, _raw_stream(stream)))
     return BlockNormGrads(dr, dblock, dw_post, dgate, dw_pre)
 
 
@@ -728,20 +742,20 @@ def muon_token_logprobs(logits, tokens=None, *, top=0, stream=None):
     code = _dtype_code(logits, "logits")
     T, V = logits.shape
     stride = _rows(logits, logits.dtype, logits.shape, "logits")
-    dev, f32 = logits.device, torch.float32
     logp = top_ids = top_logp = None
     if tokens is not None:
-        _rows(tokens, torch.int64, logits.shape[:1], "tokens", True)
-        logp = torch.empty(T, dtype=f32, device=dev)
-    entropy, lse = torch.empty(T, dtype=f32, device=dev), torch.empty(T, dtype=f32, device=dev)
+        _dense(tokens, torch.int64, (T,), "tokens")
+    out = torch.empty((3, T), dtype=torch.float32, device=logits.device)
+    lse, entropy, logp = out.unbind()
+    at = out.data_ptr()
     if top:
-        top_ids = torch.empty(T, max(0, top), dtype=torch.int64, device=dev)
-        top_logp = torch.empty(T, max(0, top), dtype=f32, device=dev)
-    _same_device(logits, tokens)
+        top_ids = torch.empty((T, max(0, top)), dtype=torch.int64, device=logits.device)
+        top_logp = torch.empty((T, max(0, top)), dtype=torch.float32, device=logits.device)
+    _one_device(logits, tokens)
     _check("muon_token_logprobs", lib().muon_token_logprobs(
-        logits.data_ptr(), stride, _opt(tokens), T, V, code, _opt(logp), entropy.data_ptr(), lse.data_ptr(), top,
-        _opt(top_ids), _opt(top_logp), _stream_handle(stream)))
-    return TokenLogprobs(logp, entropy, lse, top_ids, top_logp)
+        logits.data_ptr(), stride, _opt(tokens), T, V, code, None if tokens is None else at + 8 * T, at + 4 * T, at,
+        top, _opt(top_ids), _opt(top_logp), _raw_stream(stream)))
+    return TokenLogprobs(None if tokens is None else logp, entropy, lse, top_ids, top_logp)
 
 
 def muon_token_logprobs_backward(logits, tokens, lse, entropy=None, dlogp=None, dentropy=None, *, out=None,
@@ -757,21 +771,22 @@ def muon_token_logprobs_backward(logits, tokens, lse, entropy=None, dlogp=None, 
     T, V = logits.shape
     stride = _rows(logits, logits.dtype, logits.shape, "logits")
     if tokens is not None:
-        _rows(tokens, torch.int64, logits.shape[:1], "tokens", True)
+        _dense(tokens, torch.int64, (T,), "tokens")
     elif dlogp is not None:
         raise ValueError("dlogp needs tokens")
     if dentropy is not None and entropy is None:
         raise ValueError("dentropy needs entropy")
     for t, n in ((lse, "lse"), (entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy")):
         if t is not None or n == "lse":
-            _rows(t, torch.float32, logits.shape[:1], n, True)
+            _dense(t, torch.float32, (T,), n)
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    out_stride = _rows(out, logits.dtype, logits.shape, "out")
-    _same_device(logits, tokens, lse, entropy, dlogp, dentropy, out)
+        out, out_stride = logits.new_empty((T, V)), V
+    else:
+        out_stride = _rows(out, logits.dtype, (T, V), "out")
+    _one_device(logits, tokens, lse, entropy, dlogp, dentropy, out)
     _check("muon_token_logprobs_backward", lib().muon_token_logprobs_backward(
         logits.data_ptr(), stride, _opt(tokens), lse.data_ptr(), _opt(entropy), _opt(dlogp), _opt(dentropy), T, V,
-        code, out.data_ptr(), out_stride, _stream_handle(stream)))
+        code, out.data_ptr(), out_stride, _raw_stream(stream)))
     return out
 
 

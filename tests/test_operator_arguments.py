@@ -1,6 +1,7 @@
 """Argument errors of the operators around the step, returned on the host before any CUDA call."""
 
 import ctypes
+import re
 
 import pytest
 
@@ -8,6 +9,29 @@ import muon_newton_schulz_expert_gb300 as mk
 from muon_newton_schulz_expert_gb300 import build as mkbuild
 
 P = ctypes.c_void_p
+NORM = ("rows hidden residual_type branch_type residual residual_stride block block_stride w_post gate gate_stride w_pre "
+        "scale eps residual_out residual_out_stride normed normed_stride rstd_post rstd_pre").split()
+NORM_BACKWARD = ("rows hidden residual_type branch_type dresidual_out dresidual_out_stride dnormed dnormed_stride residual "
+                 "residual_stride block block_stride w_post gate gate_stride w_pre rstd_post rstd_pre scale dresidual "
+                 "dresidual_stride dblock dblock_stride dw_post dgate dgate_stride dw_pre").split()
+
+
+def header_fields(name):
+    """The fields of a struct of the header, in order."""
+    src = re.sub(r"/\*.*?\*/", "", open(mkbuild.INCLUDE + "/muon.h").read(), flags=re.S)
+    body = re.search(r"typedef struct \{([^}]*)\} %s;" % name, src).group(1)
+    return [re.sub(r".*[ *]", "", f.strip()) for d in body.split(";") for f in d.split(",") if f.strip()]
+
+
+def packed(layout, names, values):
+    return layout.pack(*[values.get(n) or 0 for n in names])
+
+
+def test_packed_structs_follow_the_header():
+    assert header_fields("muon_block_norm_args") == NORM
+    assert header_fields("muon_block_norm_backward_args") == NORM_BACKWARD
+    # native alignment, every pointer and int64 8 bytes
+    assert mk._NORM_ARGS.size == 2 * 8 + 8 + 14 * 8 + 8 and mk._NORM_BACKWARD_ARGS.size == 2 * 8 + 8 + 22 * 8 + 8
 
 
 @pytest.fixture(scope="module")
@@ -63,7 +87,7 @@ def test_block_norm(lib):
     def call(**kw):
         base = dict(rows=2, hidden=64, residual=256, residual_stride=64, block=256, block_stride=64, scale=1.0,
                     eps=1e-6, residual_out=256, residual_out_stride=64, normed=256, normed_stride=64)
-        return lib.muon_block_norm(ctypes.byref(mk.BlockNormArgs(**{**base, **kw})), None)
+        return lib.muon_block_norm(packed(mk._NORM_ARGS, NORM, {**base, **kw}), None)
 
     assert lib.muon_block_norm(None, None) == -1
     for bad in (dict(rows=-1), dict(hidden=0), dict(residual_type=2), dict(branch_type=-1), dict(eps=-1.0),
@@ -81,7 +105,8 @@ def test_block_norm_backward(lib):
         base = dict(rows=2, hidden=64, dresidual_out=256, dresidual_out_stride=64, dnormed=256, dnormed_stride=64,
                     residual=256, residual_stride=64, block=256, block_stride=64, rstd_post=256, rstd_pre=256,
                     scale=1.0, dresidual=256, dresidual_stride=64, dblock=256, dblock_stride=64, dw_pre=256)
-        return lib.muon_block_norm_backward(ctypes.byref(mk.BlockNormBackwardArgs(**{**base, **kw})), ws, wsb, None)
+        return lib.muon_block_norm_backward(packed(mk._NORM_BACKWARD_ARGS, NORM_BACKWARD, {**base, **kw}), ws, wsb,
+                                            None)
 
     assert lib.muon_block_norm_backward(None, None, 0, None) == -1
     for bad in (dict(rows=-1), dict(residual_type=7), dict(scale=float("nan")), dict(residual=None),
