@@ -4,15 +4,23 @@
 //   lse = log sum_v exp x_v,  logp = x_token - lse,  entropy = lse - sum_v p_v x_v
 //   dx_v = dlogp (1[v = token] - p_v) - dentropy p_v (x_v - lse + entropy)
 //
-// Forward: one pass over a row with the running maximum m, sum of e = exp(x - m)
-// and sum of e (x - m); the entropy is log(sum e) - sum e (x - m) / sum e, which
-// has no cancellation against large logits.  A row is taken by one block or,
-// when there are few rows, by a cluster of up to 8 blocks whose sums and top
-// lists the first block reads through distributed shared memory: one launch
-// and no workspace.  The top list of a warp is a sorted list of 32 keys, one
-// per lane; an element costs a compare against the list's last place unless it
-// enters.  A key holds the value's order and the complemented index, so equal
-// values keep the lowest index first, and NaN counts as the largest.
+// Forward: one pass over a row with a running reference m, the sum of e =
+// exp(x - m) and the sum of e (x - m); entropy = log(sum e) - sum e (x - m) /
+// sum e, which has no cancellation against large logits.  An element costs a
+// difference, a product with log2(e), an exponential and two accumulations,
+// all but the exponential in pairs (f32x2).  m moves only when an element
+// passes it by 11 (a factor 2^16, far from fp32's range), so that threads
+// hardly ever rescale.  A row is taken by one block or, when there are few
+// rows, by a cluster of up to 8 blocks whose sums and top lists the first block
+// reads through distributed shared memory: one launch and no workspace.
+//
+// Top alternatives: the pass also keeps each thread's maximum.  The top-th
+// largest of a block's thread maxima bounds its top-th largest element from
+// below, so a second pass over the slice (from L2) collects the few elements
+// at or above that bound, which are sorted.  Where more than kCandidates reach
+// it (ties), warps keep sorted lists of 32 keys instead, one per lane.  A key
+// holds the value's order and the complemented index, so equal values keep the
+// lowest index first, and NaN counts as the largest.
 #include <math.h>
 
 #include <algorithm>
@@ -52,43 +60,157 @@ __device__ __forceinline__ void unpack(const uint4 &x, float (&v)[kVec<T>]) {
   }
 }
 
-// Running softmax sums: m the maximum (never below the lowest finite value, so
-// that x - m is -inf and not NaN for x = -inf), s = sum e, w = sum e (x - m).
+// Running softmax sums: s = sum e and w = sum e (x - m) with e = exp(x - m).  m
+// starts at the lowest finite value, so that x - m is -inf and not NaN for x =
+// -inf.
 struct Sums {
   float m, s, w;
 };
 
-__device__ __forceinline__ Sums join(const Sums &a, const Sums &b) {
-  Sums r;
-  r.m = fmaxf(a.m, b.m);
-  const float da = a.m - r.m, db = b.m - r.m, ea = exp2f(da * kLog2e), eb = exp2f(db * kLog2e);
-  r.s = a.s * ea + b.s * eb;
-  // (x - r.m) = (x - a.m) + da; an empty or vanished part adds nothing
-  r.w = (ea > 0.f ? ea * fmaf(a.s, da, a.w) : 0.f * a.w) + (eb > 0.f ? eb * fmaf(b.s, db, b.w) : 0.f * b.w);
-  return r;
+constexpr float kFar = 1e30f;   // a difference beyond which exp(-kFar) is 0 whatever it is
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// Adds N values.  A NaN, or +inf, makes s and w NaN (x - m is NaN); a masked
+// moves the reference up to m
+__device__ __forceinline__ void rebase(Sums &a, float m) {
+  const float d = fmaxf(a.m - m, -kFar), e = ex2(d * kLog2e);   // finite: an empty side adds 0 and not 0 * inf
+  a.w = e * fmaf(a.s, d, a.w);
+  a.s *= e;
+  a.m = m;
+}
+
+__device__ __forceinline__ Sums join(Sums a, Sums b) {
+  const float m = fmaxf(a.m, b.m);
+  rebase(a, m);
+  rebase(b, m);
+  return {m, a.s + b.s, a.w + b.w};
+}
+
+// Any values.  A NaN, or +inf, makes s and w NaN (x - m is NaN); a masked
 // -inf adds zero to both.
 template <int N>
-__device__ __forceinline__ float add_values(Sums &a, const float (&x)[N]) {
+__device__ void add_any(Sums &a, const float (&x)[N]) {
   float top = x[0];
 #pragma unroll
   for (int i = 1; i < N; ++i) top = fmaxf(top, x[i]);
-  if (top > a.m) {
-    const float d = a.m - top, e = exp2f(d * kLog2e);
-    a.w = a.s > 0.f ? e * fmaf(a.s, fmaxf(d, -1e30f), a.w) : a.w;
-    a.s *= e;
-    a.m = top;
-  }
+  if (top > a.m) rebase(a, top);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float t = x[i] - a.m, e = exp2f(t * kLog2e);
+    const float t = x[i] - a.m, e = ex2(t * kLog2e);
     a.s += e;
-    a.w = fmaf(e, fmaxf(t, -1e30f), a.w);
+    a.w = fmaf(e, fmaxf(t, -kFar), a.w);
   }
-  return top;
 }
+
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float x, float y) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void split(f32x2 v, float &x, float &y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The largest of a vector's elements (NaN if one is), and the elements raised
+// to -kFar (about) at least, so that a masked one's x - m is finite.
+template <typename T>
+__device__ __forceinline__ float clamp_vector(uint4 &x) {
+  if constexpr (sizeof(T) == 2) {
+    constexpr uint32_t low = 0xf149f149u;   // -1e30 in bf16, twice
+    x.x = max_nan_bf16x2(x.x, low), x.y = max_nan_bf16x2(x.y, low);
+    x.z = max_nan_bf16x2(x.z, low), x.w = max_nan_bf16x2(x.w, low);
+    const uint32_t m = max_nan_bf16x2(max_nan_bf16x2(x.x, x.y), max_nan_bf16x2(x.z, x.w));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  } else {
+    x.x = __float_as_uint(max_nan(__uint_as_float(x.x), -kFar));
+    x.y = __float_as_uint(max_nan(__uint_as_float(x.y), -kFar));
+    x.z = __float_as_uint(max_nan(__uint_as_float(x.z), -kFar));
+    x.w = __float_as_uint(max_nan(__uint_as_float(x.w), -kFar));
+    return max_nan(max_nan(__uint_as_float(x.x), __uint_as_float(x.y)),
+                   max_nan(__uint_as_float(x.z), __uint_as_float(x.w)));
+  }
+}
+
+// A thread's sums over vectors: two halves of s and w, and the reference.
+template <typename T>
+struct VectorSums {
+  float m = kLowest, top = -INFINITY;   // top: the largest element, or less (masked ones and NaN left out)
+  f32x2 s = 0, w = 0;
+
+  __device__ Sums total() const {
+    float s0, s1, w0, w1;
+    split(s, s0, s1);
+    split(w, w0, w1);
+    return {m, s0 + s1, w0 + w1};
+  }
+  __device__ void set(const Sums &a) {
+    m = a.m;
+    s = pair(a.s, 0.f);
+    w = pair(a.w, 0.f);
+  }
+
+  __device__ __forceinline__ void add(uint4 raw) {
+    uint4 x = raw;
+    const float most = clamp_vector<T>(x);
+    if (most > -0.9f * kFar) top = fmaxf(top, most);   // else all it says is that they lie below
+    if (!(most <= m + 11.f) || m < -0.5f * kFar) {
+      // a new reference, a NaN or infinity, or nothing but masked elements so far
+      Sums a = total();
+      if (most > -0.9f * kFar && most < INFINITY) {
+        if (most > m) rebase(a, most);
+        set(a);
+      } else {
+        float v[kVec<T>];
+        unpack<T>(raw, v);
+        add_any(a, v);
+        set(a);
+        return;
+      }
+    }
+    const f32x2 l = pair(kLog2e, kLog2e), ref = pair(-m, -m);
+    float v[kVec<T>];
+    unpack<T>(x, v);
+#pragma unroll
+    for (int i = 0; i < kVec<T>; i += 2) {
+      const f32x2 d = add2(pair(v[i], v[i + 1]), ref);
+      float t0, t1;
+      split(mul2(d, l), t0, t1);
+      const f32x2 e = pair(ex2(t0), ex2(t1));
+      s = add2(s, e);
+      w = fma2(e, d, w);
+    }
+  }
+};
 
 __device__ __forceinline__ uint64_t top_key(float x, uint32_t index) {
   x += 0.f;   // -0 and 0 are equal
@@ -103,41 +225,61 @@ __device__ __forceinline__ float key_value(uint64_t key) {
   return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-// A warp's list: lane i holds the i-th largest key, `last` the key in place
-// top - 1 and `bound` its value.
+__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
+
+// a warp's keys, sorted in descending order over the lanes
+__device__ __forceinline__ uint64_t sort_keys(uint64_t key, int lane) {
+#pragma unroll
+  for (int n = 2; n <= 32; n <<= 1)
+#pragma unroll
+    for (int o = n >> 1; o; o >>= 1) {
+      const uint64_t q = shfl_xor64(key, o);
+      const bool larger = ((lane & o) == 0) == ((lane & n) == 0);   // the last level sorts one way: lane & 32 is 0
+      key = larger == (key > q) ? key : q;
+    }
+  return key;
+}
+
+// The 32 largest of two sorted lists (lane i holds the i-th key of each):
+// element-wise maxima of one against the other reversed are those 32 in
+// bitonic order, which five exchanges sort.
+__device__ __forceinline__ uint64_t merge_keys(uint64_t key, uint64_t other, int lane) {
+  const uint64_t rev = __shfl_sync(0xffffffffu, other, 31 - lane);
+  key = key > rev ? key : rev;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const uint64_t q = shfl_xor64(key, o);
+    key = ((lane & o) == 0) == (key > q) ? key : q;
+  }
+  return key;
+}
+
+// A warp's list: lane i holds the i-th largest key, `last` is the key in place
+// top - 1.
 struct TopList {
   uint64_t key = 0, last = 0;
-  float bound = -INFINITY;
   int top;
 
   __device__ void offer(uint64_t k, bool wanted, int lane) {
-    uint32_t who = __ballot_sync(0xffffffffu, wanted && k > last);
-    while (who) {
-      const int src = __ffs(who) - 1;
-      const uint64_t k2 = __shfl_sync(0xffffffffu, k, src);
-      const int at = __popc(__ballot_sync(0xffffffffu, key > k2));
-      const uint64_t up = __shfl_up_sync(0xffffffffu, key, 1);
-      if (lane == at) key = k2;
-      if (lane > at) key = up;
-      last = __shfl_sync(0xffffffffu, key, top - 1);
-      who = __ballot_sync(0xffffffffu, wanted && k > last) & (0xfffffffeu << src);
-    }
-    bound = last ? key_value(last) : -INFINITY;
-  }
-
-  // The 32 largest of this list and another sorted one (lane i holds its i-th
-  // key): element-wise maxima of one against the other reversed are those 32
-  // in bitonic order, which five exchanges sort.
-  __device__ void merge(uint64_t other, int lane) {
-    const uint64_t rev = __shfl_sync(0xffffffffu, other, 31 - lane);
-    key = key > rev ? key : rev;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const uint64_t q = __shfl_xor_sync(0xffffffffu, key, o);
-      key = ((lane & o) == 0) == (key > q) ? key : q;
-    }
+    wanted = wanted && k > last;
+    if (!__any_sync(0xffffffffu, wanted)) return;
+    key = merge_keys(key, sort_keys(wanted ? k : 0, lane), lane);
+    last = __shfl_sync(0xffffffffu, key, top - 1);
   }
 };
+
+// The block's sorted list from its warps' lists, in `lists[0]`.
+__device__ __forceinline__ void merge_lists(uint64_t key, uint64_t (*lists)[32], int warp, int lane) {
+  lists[warp][lane] = key;
+  __syncthreads();
+  for (int n = kWarps / 2; n; n >>= 1) {
+    if (warp < n) {
+      key = merge_keys(key, lists[warp + n][lane], lane);
+      lists[warp][lane] = key;
+    }
+    __syncthreads();
+  }
+}
 
 struct FwdArgs {
   const void *logits;
@@ -149,91 +291,135 @@ struct FwdArgs {
   unsigned *err;
 };
 
+constexpr int kCandidates = 64 * kWarps;   // two sorts of 32 keys per warp
+
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_constant__ FwdArgs a, int split) {
   __shared__ Sums sums[kWarps];
-  __shared__ uint64_t lists[kWarps][32];
+  __shared__ uint64_t lists[TOP ? kWarps : 1][32];
+  __shared__ uint64_t found[TOP ? kCandidates : 1];
+  __shared__ int count;
   constexpr int N = kVec<T>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = blockIdx.x / split;
   const int part = blockIdx.x % split;   // the block's rank in its cluster
   const T *x = static_cast<const T *>(a.logits) + row * a.stride;
-  // Elements before the first 16-byte boundary, whole vectors, the rest.
+  // Elements before the first 16-byte boundary, whole vectors, the rest: the
+  // first block of a row takes the ragged ends, one element a thread.
   int head = (int)(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T));
   if (head > a.vocab) head = a.vocab;
   const int vecs = (a.vocab - head) / N, tail0 = head + vecs * N;
+  const int ends = part == 0 ? head + (a.vocab - tail0) : 0;   // fewer than 2 N, one warp's
+  const int end_at = (int)threadIdx.x < head ? (int)threadIdx.x : tail0 + (int)threadIdx.x - head;
   const uint4 *xv = reinterpret_cast<const uint4 *>(x + head);
   const int v0 = (int)((int64_t)vecs * part / split), v1 = (int)((int64_t)vecs * (part + 1) / split);
-  Sums acc{kLowest, 0.f, 0.f};
-  TopList list;
-  if (TOP) list.top = a.top;
+  if (TOP && threadIdx.x == 0) count = 0;
+  VectorSums<T> mine;
   constexpr int U = 4;   // vectors in flight per thread
-  for (int v = v0 + warp * 32 * U; v < v1; v += kThreads * U) {
+  // The next vectors are on their way while these are added.
+  auto fetch = [&](int v) { return TOP ? __ldg(xv + v) : __ldcs(xv + v); };
+  int v = v0 + threadIdx.x;
+  uint4 next[U];
+  const bool full = v + (U - 1) * kThreads < v1;
+  if (full)
+#pragma unroll
+    for (int i = 0; i < U; ++i) next[i] = fetch(v + i * kThreads);
+  for (; v + (U - 1) * kThreads < v1; v += kThreads * U) {
     uint4 raw[U];
+    const bool more = v + (2 * U - 1) * kThreads < v1;
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int k = v + i * 32 + lane;
-      if (k < v1) raw[i] = __ldcs(xv + k);
-    }
+    for (int i = 0; i < U; ++i) raw[i] = next[i];
+    if (more)
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int k = v + i * 32 + lane;
-      const bool in = k < v1;
-      float f[N];
-      unpack<T>(raw[i], f);
-      if (!TOP) {
-        if (in) add_values<N>(acc, f);
-        continue;
-      }
-      bool some = false;
-      if (in) {
-        add_values<N>(acc, f);
+      for (int i = 0; i < U; ++i) next[i] = fetch(v + (U + i) * kThreads);
 #pragma unroll
-        for (int j = 0; j < N; ++j) some |= !(f[j] < list.bound);
-      }
-      if (__any_sync(0xffffffffu, some))
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-          list.offer(top_key(f[j], (uint32_t)(head + k * N + j)), in && !(f[j] < list.bound), lane);
-    }
+    for (int i = 0; i < U; ++i) mine.add(raw[i]);
   }
-  if (warp == 0 && part == 0) {   // fewer than 2 * N elements outside the vectors
-    for (int pass = 0; pass < 2; ++pass) {
-      const int k = pass ? tail0 + lane : lane, end = pass ? a.vocab : head;
-      const bool in = k < end;
-      const float f[1] = {in ? to_f(x[k]) : 0.f};
-      if (in) add_values<1>(acc, f);
-      if (TOP) list.offer(top_key(f[0], (uint32_t)k), in, lane);
-    }
+  for (; v < v1; v += kThreads) mine.add(fetch(v));
+  Sums acc = mine.total();
+  if ((int)threadIdx.x < ends) {
+    const float f[1] = {to_f(x[end_at])};
+    add_any(acc, f);
+    mine.top = fmaxf(mine.top, f[0]);
   }
-  // the block's sums and list
+  // the block's sums
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const Sums other{__shfl_xor_sync(0xffffffffu, acc.m, o), __shfl_xor_sync(0xffffffffu, acc.s, o),
-                     __shfl_xor_sync(0xffffffffu, acc.w, o)};
-    acc = join(acc, other);
-  }
+  for (int o = 16; o; o >>= 1)
+    acc = join(acc, Sums{__shfl_xor_sync(0xffffffffu, acc.m, o), __shfl_xor_sync(0xffffffffu, acc.s, o),
+                         __shfl_xor_sync(0xffffffffu, acc.w, o)});
   if (lane == 0) sums[warp] = acc;
-  if (TOP) lists[warp][lane] = list.key;
   __syncthreads();
-  if (TOP) {
-    for (int n = kWarps / 2; n; n >>= 1) {
-      if (warp < n) {
-        list.merge(lists[warp + n][lane], lane);
-        lists[warp][lane] = list.key;
-      }
-      __syncthreads();
-    }
-  }
   if (warp == 0) {
     acc = lane < kWarps ? sums[lane] : Sums{kLowest, 0.f, 0.f};
 #pragma unroll
-    for (int o = kWarps / 2; o; o >>= 1) {
-      const Sums other{__shfl_xor_sync(0xffffffffu, acc.m, o), __shfl_xor_sync(0xffffffffu, acc.s, o),
-                       __shfl_xor_sync(0xffffffffu, acc.w, o)};
-      acc = join(acc, other);
-    }
+    for (int o = kWarps / 2; o; o >>= 1)
+      acc = join(acc, Sums{__shfl_xor_sync(0xffffffffu, acc.m, o), __shfl_xor_sync(0xffffffffu, acc.s, o),
+                           __shfl_xor_sync(0xffffffffu, acc.w, o)});
     if (lane == 0) sums[0] = acc;
+  }
+  uint64_t key = 0;
+  if (TOP) {
+    // a lower bound of the block's top-th element: the top-th of its threads'
+    // maxima, taken before any element of that value (index bits 0)
+    const bool any = v0 + (int)threadIdx.x < v1 || (int)threadIdx.x < ends;
+    merge_lists(sort_keys(any ? top_key(mine.top, 0xffffffffu) : 0, lane), lists, warp, lane);
+    const uint64_t bound = lists[0][a.top - 1];
+    const float least = key_value(bound);
+    if (bound) {
+      for (int v = v0 + threadIdx.x; v < v1; v += kThreads * U) {
+        uint4 raw[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (v + i * kThreads < v1) raw[i] = __ldg(xv + v + i * kThreads);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          if (v + i * kThreads >= v1) break;
+          float f[N];
+          unpack<T>(raw[i], f);
+          bool some = false;
+#pragma unroll
+          for (int j = 0; j < N; ++j) some |= !(f[j] < least);
+          if (some)
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+              if (!(f[j] < least)) {
+                const int at = atomicAdd(&count, 1);
+                if (at < kCandidates) found[at] = top_key(f[j], (uint32_t)(head + (v + i * kThreads) * N + j));
+              }
+        }
+      }
+      if ((int)threadIdx.x < ends) {
+        const float f = to_f(x[end_at]);
+        if (!(f < least)) {
+          const int at = atomicAdd(&count, 1);
+          if (at < kCandidates) found[at] = top_key(f, (uint32_t)end_at);
+        }
+      }
+    }
+    __syncthreads();
+    const int n = count;
+    if (bound && n <= kCandidates) {
+      const int at = warp * 64 + lane;
+      if (warp * 64 < n) key = sort_keys(at < n ? found[at] : 0, lane);
+      if (warp * 64 + 32 < n) key = merge_keys(key, sort_keys(at + 32 < n ? found[at + 32] : 0, lane), lane);
+    } else {
+      TopList list;
+      list.top = a.top;
+      for (int v = v0 + warp * 32; v < v1; v += kThreads) {
+        const bool in = v + lane < v1;
+        float f[N];
+        unpack<T>(in ? __ldg(xv + v + lane) : make_uint4(0u, 0u, 0u, 0u), f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) list.offer(top_key(f[j], (uint32_t)(head + (v + lane) * N + j)), in, lane);
+      }
+      if (warp == 0) {
+        const bool in = lane < ends;
+        list.offer(top_key(in ? to_f(x[end_at]) : 0.f, (uint32_t)end_at), in, lane);
+      }
+      key = list.key;
+    }
+    merge_lists(key, lists, warp, lane);
+    if (warp == 0) key = lists[0][lane];
   }
   if (split > 1) {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
@@ -254,35 +440,36 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
                        : "r"((uint32_t)__cvta_generic_to_shared(&lists[0][lane])), "r"(r));
           uint64_t k;
           asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(k) : "r"(at) : "memory");
-          list.merge(k, lane);
+          key = merge_keys(key, k, lane);
         }
       }
     }
+    // no block leaves while the first may still read its shared memory
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
   }
   if (part != 0 || warp != 0) return;
   acc = {__shfl_sync(0xffffffffu, acc.m, 0), __shfl_sync(0xffffffffu, acc.s, 0), __shfl_sync(0xffffffffu, acc.w, 0)};
   // a row whose mask leaves nothing (s = 0): lse = -inf, logp = -inf, entropy = 0
-  const float ls = logf(acc.s), lse = acc.s == 0.f ? -INFINITY : acc.m + ls;
+  const bool none = acc.s == 0.f;
+  const float ls = logf(acc.s), lse = none ? -INFINITY : acc.m + ls;
   if (lane == 0) {
     const int64_t token = a.tokens ? a.tokens[row] : -1;
     if (a.lse) a.lse[row] = lse;
-    if (a.entropy) a.entropy[row] = acc.s == 0.f ? 0.f : ls - acc.w / acc.s;
+    if (a.entropy) a.entropy[row] = none ? 0.f : ls - acc.w / acc.s;
     if (a.logp) {
       float lp = 0.f;
       if (token >= a.vocab) {
         atomicOr(a.err, kErrDevice);
         lp = __uint_as_float(0x7fffffffu);
       } else if (token >= 0) {
-        lp = acc.s == 0.f ? -INFINITY : (to_f(x[token]) - acc.m) - ls;
+        lp = none ? -INFINITY : (to_f(x[token]) - acc.m) - ls;
       }
       a.logp[row] = lp;
     }
   }
   if (TOP && lane < a.top) {
-    const float v = key_value(list.key);
-    a.top_ids[row * a.top + lane] = (int64_t)(uint32_t)~(uint32_t)list.key;
-    if (a.top_logp) a.top_logp[row * a.top + lane] = acc.s == 0.f ? -INFINITY : (v - acc.m) - ls;
+    a.top_ids[row * a.top + lane] = (int64_t)(uint32_t)~(uint32_t)key;
+    if (a.top_logp) a.top_logp[row * a.top + lane] = none ? -INFINITY : (key_value(key) - acc.m) - ls;
   }
 }
 
@@ -299,9 +486,9 @@ struct BwdArgs {
 struct Slope {
   float lse, dlogp, dent, ent;
   __device__ float operator()(float x) const {
-    const float t = x - lse, p = exp2f(t * kLog2e);
+    const float t = x - lse, p = ex2(t * kLog2e);
     // p (x - lse + entropy) is zero where p is (x = -inf)
-    return -p * fmaf(dent, fmaxf(t, -1e30f) + ent, dlogp);
+    return -p * fmaf(dent, fmaxf(t, -kFar) + ent, dlogp);
   }
 };
 

@@ -11,12 +11,15 @@
 //   db   = q (w_post dn - bh mean(w_post dn bh))
 //   dw_pre = sum_rows dy xh,  dw_post = sum_rows dn bh,  dgate = scale dr' bh w_post
 //
-// One pass over memory: a row lives in the registers of one thread group
-// between its two reductions (the second depends on the first through r' or
-// dr').  All sums are fp32 and in a fixed order (no atomics): the weight
-// gradients accumulate in registers over the rows a group takes, each group
-// writes its sums, and a second kernel adds them.
+// One pass over memory.  A group of threads takes one row at a time and walks
+// the rows of the array; several groups on an SM overlap one's reductions with
+// another's loads.  The weights and a shared gate stay in L1, and so does the part of a row that is read a second time
+// after its reduction rather than held in registers.  The weights' gradients
+// stay in registers over a group's rows; each group writes its sums and a
+// second kernel adds them, in a fixed order (no atomics).  All arithmetic is
+// fp32, in pairs (f32x2) where vectors are moved.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -26,12 +29,25 @@ namespace {
 constexpr int kMaxHidden = 16384;
 constexpr int kRowsPerCta = 4;   // rows of one CTA where a warp holds a whole row
 
-// Largest block of an instance.  The backward kernel keeps three sums per
-// column in registers, so its blocks are smaller (768 threads leave it 85
-// registers, 512 leave 128).
+// Rows of more than 128 vectors give each thread kPlaces of them.  The largest
+// block of an instance and how many of them an SM has to hold fix its
+// registers: 56 a thread forward, 80 backward, where two sums per column are
+// kept besides.  Measured at 16384 x 6144: forward 240 us (86% of the measured
+// copy bandwidth; 245 us with 4 places and 4 blocks of 192 threads), backward
+// 300 us (59%; 315 us with 3 places and 2 blocks of 256, 332 us with one block
+// of 384 that keeps more in registers, 324 us with the next rows copied to
+// shared memory by cp.async): it is bound by the instructions it issues, about
+// 40 an element for 12 bytes.  Rows that need more threads than that take an
+// instance with wide blocks.
+constexpr int kPlaces = 2;
 constexpr int max_threads(int w, int vpt, bool backward) {
   if (w == 1) return vpt == 32 ? 512 : backward && vpt == 4 ? 512 : 1024;
-  return vpt == 1 ? (backward ? 768 : 256) : 512;
+  return vpt == 1 ? 128 : 384;
+}
+constexpr int kWideThreads = 1024;
+constexpr int blocks_per_sm(int w, int threads, bool backward) {
+  const int all = w == 1 ? (backward ? 512 : 1024) : backward ? 768 : 1152;
+  return threads > all / 2 ? 1 : all / (threads < 64 ? 64 : threads);
 }
 
 struct Row {
@@ -48,288 +64,440 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float
 __device__ __forceinline__ void from_f(float *d, float v) { *d = v; }
 __device__ __forceinline__ void from_f(__nv_bfloat16 *d, float v) { *d = __float2bfloat16_rn(v); }
 
-// W consecutive elements: W = 8 moves 16-byte vectors, W = 1 single elements
-// (widths or strides that are not multiples of 8, unaligned pointers).
-template <typename T, int W>
-__device__ __forceinline__ void load(const T *src, float (&v)[W]) {
-  if constexpr (W == 1) {
-    v[0] = to_f(*src);
-  } else if constexpr (sizeof(T) == 2) {
-    const uint4 x = *reinterpret_cast<const uint4 *>(src);
+// ------------------------------------------------------------ one or two floats
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 pair(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 halves(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float total(F2 a) {
+  const float2 h = halves(a);
+  return h.x + h.y;
+}
+__device__ __forceinline__ float total(float a) { return a; }
+template <typename P>
+__device__ __forceinline__ P both(float x) {
+  if constexpr (std::is_same_v<P, F2>) return pair(x, x);
+  else return x;
+}
+
+// W consecutive elements of a thread: four pairs (16-byte vectors), or one
+// element (widths or strides that are not multiples of 8, unaligned pointers).
+template <int W>
+using Item = std::conditional_t<W == 8, F2, float>;
+template <int W>
+constexpr int kItems = W == 8 ? 4 : 1;
+
+// Eight elements of type T from 16-byte vectors `step` vectors apart.
+template <typename T>
+__device__ __forceinline__ void widen(const uint4 *src, int step, F2 (&v)[4]) {
+  const uint4 x = src[0];
+  if constexpr (sizeof(T) == 2) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) v[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 x = reinterpret_cast<const float4 *>(src)[i];
-      v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
-    }
+    const uint4 y = src[step];
+    v[0] = pair(__uint_as_float(x.x), __uint_as_float(x.y)), v[1] = pair(__uint_as_float(x.z), __uint_as_float(x.w));
+    v[2] = pair(__uint_as_float(y.x), __uint_as_float(y.y)), v[3] = pair(__uint_as_float(y.z), __uint_as_float(y.w));
   }
 }
 
-template <typename T, int W>
-__device__ __forceinline__ void store(T *dst, const float (&v)[W]) {
-  if constexpr (W == 1) {
-    from_f(dst, v[0]);
-  } else if constexpr (sizeof(T) == 2) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = *reinterpret_cast<uint32_t *>(&h);
-    }
-    *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      reinterpret_cast<float4 *>(dst)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-  }
+template <typename T>
+__device__ __forceinline__ void load(const T *src, F2 (&v)[4]) {
+  widen<T>(reinterpret_cast<const uint4 *>(src), 1, v);
+}
+template <typename T>
+__device__ __forceinline__ void load(const T *src, float (&v)[1]) {
+  v[0] = to_f(*src);
 }
 
-// Sum over the threads of a row (blockDim.x, a multiple of 32); with one warp
-// per row no shared memory and no barrier is used.  Successive sums alternate
-// between two buffers, so one barrier each is enough: a buffer is written
-// again only after a barrier that every reader of its last sum has passed.
-__device__ __forceinline__ float row_sum(float v, float *buf) {
+// Rows are written once: evict-first, which leaves L2 to the rows being read.
+template <typename T>
+__device__ __forceinline__ void store(T *dst, const F2 (&v)[4]) {
+  const float2 a = halves(v[0]), b = halves(v[1]), c = halves(v[2]), d = halves(v[3]);
+  uint4 *out = reinterpret_cast<uint4 *>(dst);
+  if constexpr (sizeof(T) == 2) {
+    __nv_bfloat162 h[4] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(b.x, b.y),
+                           __floats2bfloat162_rn(c.x, c.y), __floats2bfloat162_rn(d.x, d.y)};
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(h);
+    __stcs(out, make_uint4(w[0], w[1], w[2], w[3]));
+  } else {
+    __stcs(reinterpret_cast<float4 *>(out), make_float4(a.x, a.y, b.x, b.y));
+    __stcs(reinterpret_cast<float4 *>(out) + 1, make_float4(c.x, c.y, d.x, d.y));
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store(T *dst, const float (&v)[1]) {
+  from_f(dst, v[0]);
+}
+
+// Sums of N values over the threads of a row (blockDim.x, a multiple of 32);
+// with one warp per row no shared memory and no barrier is used.  Successive
+// sums alternate between two buffers, so one barrier each is enough: a buffer
+// is written again only after a barrier that every reader of its last sums has
+// passed.  Every thread adds the warps' sums itself (broadcast reads).
+template <int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float4 (*buf)[8]) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (blockDim.x == 32) return v;
-  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  if (lane == 0) buf[threadIdx.x >> 5] = v;
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if (blockDim.x == 32) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  if (lane == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) reinterpret_cast<float *>(buf[i])[warp] = v[i];
   __syncthreads();
-  v = lane < warps ? buf[lane] : 0.f;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int i = 0; i < N; ++i) {
+    v[i] = 0.f;
+    for (int w = 0; w < warps; w += 4) {   // places past the last warp hold zeros
+      const float4 x = buf[i][w >> 2];
+      v[i] += (x.x + x.y) + (x.z + x.w);
+    }
+  }
+}
+// before the first row_sums
+template <int N>
+__device__ __forceinline__ void clear_sums(float4 (*buf)[N][8]) {
+  for (int i = threadIdx.x + threadIdx.y * blockDim.x; i < 2 * N * 8; i += blockDim.x * blockDim.y)
+    (&buf[0][0][0])[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncthreads();
+}
+
+// A thread's place in one input or output: its columns of the row at hand, and
+// the step to its group's next row.
+template <typename T>
+struct Walk {
+  T *p;
+  int64_t step;
+
+  __device__ Walk(const void *base, int64_t stride, int64_t row, int64_t rows, int c)
+      : p(base ? const_cast<T *>(static_cast<const T *>(base)) + row * stride + c : nullptr), step(rows * stride) {}
+  __device__ void next() { p += step; }
+};
+
+// Which parts a call has.  The forms with everything (both norms and their
+// weights, the incoming gradient, every output) are compiled with that
+// knowledge, which nearly halves their instructions; ANY asks at run time.
+enum Form { ANY = 0, FULL, FULL_SHARED_GATE, FULL_ROW_GATE };
+
+// Multiplies by a vector of the weights.
+template <typename T, int W>
+__device__ __forceinline__ void times(const T *w, Item<W> (&v)[kItems<W>]) {
+  Item<W> x[kItems<W>];
+  load(w, x);
+#pragma unroll
+  for (int j = 0; j < kItems<W>; ++j) v[j] = mul(v[j], x[j]);
 }
 
 struct FwdArgs {
-  Row residual, block, gate;   // gate stride 0: one gate for all rows
+  Row residual, block, gate;   // gate: a row for each token (a shared gate is a column factor)
   RowOut residual_out, normed;
-  const void *w_post, *w_pre;
+  const void *w_post, *shared_gate, *w_pre;
   float *rstd_post, *rstd_pre;
   int64_t rows;
   int hidden;
   float scale, eps;
 };
 
-template <typename R, typename B, int W, int VPT>
-__global__ void __launch_bounds__(max_threads(W, VPT, false)) block_norm_kernel(const __grid_constant__ FwdArgs a) {
-  __shared__ float red[2][32];
-  const int64_t row = blockIdx.x * (int64_t)blockDim.y + threadIdx.y;
-  if (row >= a.rows) return;   // only where a warp holds a row (no barriers)
-  const R *res = static_cast<const R *>(a.residual.p) + row * a.residual.stride;
-  float r[VPT][W];
+template <typename R, typename B, int W, int VPT, int THREADS, int FORM>
+__global__ void __launch_bounds__(THREADS, W == 1 ? 1 : blocks_per_sm(W, THREADS, false))
+    block_norm_kernel(const __grid_constant__ FwdArgs a) {
+  __shared__ float4 red[2][1][8];
+  using P = Item<W>;
+  constexpr int N = kItems<W>;
+  const int64_t group = blockIdx.x * (int64_t)blockDim.y + threadIdx.y, groups = gridDim.x * (int64_t)blockDim.y;
+  const int c0 = threadIdx.x * W, across = blockDim.x * W;   // this thread's columns: c0, c0 + across, ...
+  const float inv_h = 1.f / (float)a.hidden;
+  constexpr bool full = FORM != ANY;
+  const bool post = full || a.block.p, pre = full || a.normed.p;
+  const bool gate_rows = full ? FORM == FULL_ROW_GATE : a.gate.p != nullptr;
+  const bool gate_shared = full ? FORM == FULL_SHARED_GATE : a.shared_gate != nullptr;
+  clear_sums<1>(red);
+  Walk<R> res(a.residual.p, a.residual.stride, group, groups, c0);
+  Walk<B> blk(a.block.p, a.block.stride, group, groups, c0), gate(a.gate.p, a.gate.stride, group, groups, c0);
+  Walk<R> out(a.residual_out.p, a.residual_out.stride, group, groups, c0);
+  Walk<B> y(a.normed.p, a.normed.stride, group, groups, c0);
+  const B *w_post = static_cast<const B *>(a.w_post), *w_pre = static_cast<const B *>(a.w_pre);
+  const B *shared_gate = static_cast<const B *>(a.shared_gate);
+  int turn = 0;
+  for (int64_t row = group; row < a.rows; row += groups) {
+    P r[VPT][N], ss = both<P>(0.f);
+    float q = 0.f;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = (threadIdx.x + i * blockDim.x) * W;
-    if (c < a.hidden) load<R, W>(res + c, r[i]);
-  }
-  if (a.block.p) {
-    const B *blk = static_cast<const B *>(a.block.p) + row * a.block.stride;
-    const B *gate = static_cast<const B *>(a.gate.p) + (a.gate.p ? row * a.gate.stride : 0);
-    float b[VPT][W], ss = 0.f;
+    for (int i = 0; i < VPT; ++i)
+      if (c0 + i * across < a.hidden) load(res.p + i * across, r[i]);
+    if (post) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * W;
-      if (c < a.hidden) {
-        load<B, W>(blk + c, b[i]);
+      for (int i = 0; i < VPT; ++i)
+        if (c0 + i * across < a.hidden) {
+          P b[N];
+          load(blk.p + i * across, b);
 #pragma unroll
-        for (int j = 0; j < W; ++j) ss = fmaf(b[i][j], b[i][j], ss);
-      }
-    }
-    const float q = 1.f / sqrtf(row_sum(ss, red[0]) / (float)a.hidden + a.eps);
-    if (threadIdx.x == 0 && a.rstd_post) a.rstd_post[row] = q;
-    R *out = static_cast<R *>(a.residual_out.p) + row * a.residual_out.stride;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * W;
-      if (c < a.hidden) {
-        float w[W], g[W];
-        if (a.w_post) load<B, W>(static_cast<const B *>(a.w_post) + c, w);
-        if (a.gate.p) load<B, W>(gate + c, g);
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          float n = b[i][j] * q;
-          if (a.w_post) n *= w[j];
-          if (a.gate.p) n *= g[j];
-          r[i][j] = fmaf(a.scale, n, r[i][j]);
+          for (int j = 0; j < N; ++j) ss = fma(b[j], b[j], ss);
         }
-        store<R, W>(out + c, r[i]);
+      float sum[1] = {total(ss)};
+      row_sums(sum, red[turn]);
+      turn ^= 1;
+      q = rsqrtf(fmaf(sum[0], inv_h, a.eps));
+      if (threadIdx.x == 0 && a.rstd_post) a.rstd_post[row] = q;
+    }
+    ss = both<P>(0.f);
+    const P qs = both<P>(a.scale * q);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (c0 + i * across < a.hidden) {
+        const int c = c0 + i * across;
+        if (post) {
+          P b[N];
+          load(blk.p + i * across, b);   // again, from L1
+          if (full || w_post) times<B, W>(w_post + c, b);
+          if (gate_rows) times<B, W>(gate.p + i * across, b);
+          else if (gate_shared) times<B, W>(shared_gate + c, b);
+#pragma unroll
+          for (int j = 0; j < N; ++j) r[i][j] = fma(b[j], qs, r[i][j]);
+          store(out.p + i * across, r[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) ss = fma(r[i][j], r[i][j], ss);
       }
+    if (pre) {
+      // y is formed from r' before its rounding to the stream's type
+      float sum[1] = {total(ss)};
+      row_sums(sum, red[turn]);
+      turn ^= 1;
+      const float p = rsqrtf(fmaf(sum[0], inv_h, a.eps));
+      if (threadIdx.x == 0 && a.rstd_pre) a.rstd_pre[row] = p;
+      const P p2 = both<P>(p);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (c0 + i * across < a.hidden) {
+#pragma unroll
+          for (int j = 0; j < N; ++j) r[i][j] = mul(r[i][j], p2);
+          if (full || w_pre) times<B, W>(w_pre + c0 + i * across, r[i]);
+          store(y.p + i * across, r[i]);
+        }
     }
-  }
-  if (!a.normed.p) return;
-  // y is formed from r' before its rounding to the stream's type
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-    if ((threadIdx.x + i * blockDim.x) * W < a.hidden)
-#pragma unroll
-      for (int j = 0; j < W; ++j) ss = fmaf(r[i][j], r[i][j], ss);
-  const float p = 1.f / sqrtf(row_sum(ss, red[1]) / (float)a.hidden + a.eps);
-  if (threadIdx.x == 0 && a.rstd_pre) a.rstd_pre[row] = p;
-  B *y = static_cast<B *>(a.normed.p) + row * a.normed.stride;
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = (threadIdx.x + i * blockDim.x) * W;
-    if (c < a.hidden) {
-      float w[W], v[W];
-      if (a.w_pre) load<B, W>(static_cast<const B *>(a.w_pre) + c, w);
-#pragma unroll
-      for (int j = 0; j < W; ++j) v[j] = a.w_pre ? r[i][j] * p * w[j] : r[i][j] * p;
-      store<B, W>(y + c, v);
-    }
+    res.next(), blk.next(), gate.next(), out.next(), y.next();
   }
 }
 
 struct BwdArgs {
-  Row dresidual_out, dnormed, residual, block, gate;
-  RowOut dresidual, dblock, dgate;   // dgate here: one row per token
-  const void *w_post, *w_pre;
+  Row dresidual_out, dnormed, residual, block, gate;   // gate: a row for each token
+  RowOut dresidual, dblock, dgate;                     // dgate: a row for each token
+  const void *w_post, *shared_gate, *w_pre;
   const float *rstd_post, *rstd_pre;
-  float *partial;                    // [groups][3][hidden]: dw_pre, dw_post, shared dgate
+  float *partial;                    // [groups][2][hidden]: sums of dy xh, and of (per-row gate) dr bh
   int64_t rows;
   int hidden;
   float scale;
-  int want_pre, want_post, want_gate;   // which sums over rows are wanted
 };
 
-template <typename R, typename B, int W, int VPT>
-__global__ void __launch_bounds__(max_threads(W, VPT, true)) block_norm_backward_kernel(const __grid_constant__ BwdArgs a) {
-  __shared__ float red[2][32];
+// The two means of a row come from one reduction of three sums over the raw
+// rows.  With tp = p w_pre dy, z = dr_out + tp and k = scale gate w_post,
+//   dr = z - c1 r',           c1 = p^2 S1 / H,            S1 = sum tp r'
+//   db = q k dr - c2 b,       c2 = q^3 (S2 - c1 S3) / H,  S2 = sum k b z,  S3 = sum k b r'
+// For a shared gate, sum over rows of dr b q serves dw_post (times scale gate)
+// and dgate (times scale w_post) alike.
+template <typename R, typename B, int W, int VPT, int THREADS, int FORM>
+__global__ void __launch_bounds__(THREADS, W == 1 ? 1 : blocks_per_sm(W, THREADS, true))
+    block_norm_backward_kernel(const __grid_constant__ BwdArgs a) {
+  __shared__ float4 red[2][3][8];
+  using P = Item<W>;
+  constexpr int N = kItems<W>;
   const int64_t group = blockIdx.x * (int64_t)blockDim.y + threadIdx.y, groups = gridDim.x * (int64_t)blockDim.y;
+  const int c0 = threadIdx.x * W, across = blockDim.x * W;
   const float inv_h = 1.f / (float)a.hidden;
-  int turn = 0;   // which buffer the next sum uses
-  float dwp[VPT][W] = {}, dwq[VPT][W] = {}, dgs[VPT][W] = {};
-  for (int64_t row = group; row < a.rows; row += groups) {
-    float dr[VPT][W];
+  constexpr bool full = FORM != ANY;
+  const bool post = full || a.block.p, pre = full || a.dnormed.p;
+  const bool from_above = full || a.dresidual_out.p;
+  const bool gate_rows = full ? FORM == FULL_ROW_GATE : a.gate.p != nullptr;
+  const bool gate_shared = full ? FORM == FULL_SHARED_GATE : a.shared_gate != nullptr;
+  clear_sums<3>(red);
+  P dwp[VPT][N], dwq[VPT][N];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * W;
+  for (int i = 0; i < VPT; ++i)
 #pragma unroll
-      for (int j = 0; j < W; ++j) dr[i][j] = 0.f;
-      if (c < a.hidden && a.dresidual_out.p)
-        load<R, W>(static_cast<const R *>(a.dresidual_out.p) + row * a.dresidual_out.stride + c, dr[i]);
+    for (int j = 0; j < N; ++j) dwp[i][j] = dwq[i][j] = both<P>(0.f);
+  Walk<R> dres(a.dresidual_out.p, a.dresidual_out.stride, group, groups, c0);
+  Walk<R> res(a.residual.p, a.residual.stride, group, groups, c0);
+  Walk<B> dnorm(a.dnormed.p, a.dnormed.stride, group, groups, c0);
+  Walk<B> blk(a.block.p, a.block.stride, group, groups, c0), gate(a.gate.p, a.gate.stride, group, groups, c0);
+  Walk<R> dr(a.dresidual.p, a.dresidual.stride, group, groups, c0);
+  Walk<B> db(a.dblock.p, a.dblock.stride, group, groups, c0);
+  const B *w_post = static_cast<const B *>(a.w_post), *w_pre = static_cast<const B *>(a.w_pre);
+  const B *shared_gate = static_cast<const B *>(a.shared_gate);
+  // k / scale = gate w_post, in g
+  auto factors = [&](int i, P (&g)[N]) {
+    const int c = c0 + i * across;
+    if (gate_rows) {
+      load(gate.p + i * across, g);
+    } else if (gate_shared) {
+      load(shared_gate + c, g);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) g[j] = both<P>(1.f);
     }
-    if (a.dnormed.p) {
-      const float p = a.rstd_pre[row];
-      float t[VPT][W], xh[VPT][W], sum = 0.f;
+    if (full || w_post) times<B, W>(w_post + c, g);
+  };
+  int turn = 0;
+  for (int64_t row = group; row < a.rows; row += groups) {
+    const float p = pre ? a.rstd_pre[row] : 0.f, q = post ? a.rstd_post[row] : 0.f;
+    P z[VPT][N];
+    P s1 = both<P>(0.f), s2 = s1, s3 = s1;
+    const P p2 = both<P>(p);
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = (threadIdx.x + i * blockDim.x) * W;
-        if (c < a.hidden) {
-          float dy[W], w[W];
-          load<B, W>(static_cast<const B *>(a.dnormed.p) + row * a.dnormed.stride + c, dy);
-          load<R, W>(static_cast<const R *>(a.residual.p) + row * a.residual.stride + c, xh[i]);
-          if (a.w_pre) load<B, W>(static_cast<const B *>(a.w_pre) + c, w);
+    for (int i = 0; i < VPT; ++i)
+      if (c0 + i * across < a.hidden) {
+        P r[N];
+        if (from_above) {
+          load(dres.p + i * across, z[i]);
+        } else {
 #pragma unroll
-          for (int j = 0; j < W; ++j) {
-            xh[i][j] *= p;
-            dwp[i][j] = fmaf(dy[j], xh[i][j], dwp[i][j]);
-            t[i][j] = a.w_pre ? dy[j] * w[j] : dy[j];
-            sum = fmaf(t[i][j], xh[i][j], sum);
+          for (int j = 0; j < N; ++j) z[i][j] = both<P>(0.f);
+        }
+        if (pre) {
+          P t[N];
+          load(res.p + i * across, r);
+          load(dnorm.p + i * across, t);
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            t[j] = mul(t[j], p2);
+            dwp[i][j] = fma(t[j], r[j], dwp[i][j]);
+          }
+          if (full || w_pre) times<B, W>(w_pre + c0 + i * across, t);
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            s1 = fma(t[j], r[j], s1);
+            z[i][j] = add(z[i][j], t[j]);
+          }
+        }
+        if (post) {
+          P b[N], g[N];
+          load(blk.p + i * across, b);
+          factors(i, g);
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const P kb = mul(g[j], b[j]);
+            s2 = fma(kb, z[i][j], s2);
+            if (pre) s3 = fma(kb, r[j], s3);
           }
         }
       }
-      const float mean = row_sum(sum, red[turn]) * inv_h;
-      turn ^= 1;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-        if ((threadIdx.x + i * blockDim.x) * W < a.hidden)
-#pragma unroll
-          for (int j = 0; j < W; ++j) dr[i][j] = fmaf(p, fmaf(-xh[i][j], mean, t[i][j]), dr[i][j]);
-    }
-    if (a.dresidual.p)
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = (threadIdx.x + i * blockDim.x) * W;
-        if (c < a.hidden) store<R, W>(static_cast<R *>(a.dresidual.p) + row * a.dresidual.stride + c, dr[i]);
-      }
-    if (!a.block.p) continue;
-    const float q = a.rstd_post[row];
-    float bh[VPT][W], sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * W;
-      if (c < a.hidden) {
-        float w[W], g[W];
-        load<B, W>(static_cast<const B *>(a.block.p) + row * a.block.stride + c, bh[i]);
-        if (a.w_post) load<B, W>(static_cast<const B *>(a.w_post) + c, w);
-        if (a.gate.p) load<B, W>(static_cast<const B *>(a.gate.p) + row * a.gate.stride + c, g);
-        float dg[W];
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          bh[i][j] *= q;
-          const float sdr = a.scale * dr[i][j];
-          const float wj = a.w_post ? w[j] : 1.f;
-          dg[j] = sdr * bh[i][j] * wj;
-          dgs[i][j] += dg[j];
-          const float dn = a.gate.p ? sdr * g[j] : sdr;
-          dwq[i][j] = fmaf(dn, bh[i][j], dwq[i][j]);
-          dr[i][j] = dn * wj;
-          sum = fmaf(dr[i][j], bh[i][j], sum);
-        }
-        if (a.dgate.p) store<B, W>(static_cast<B *>(a.dgate.p) + row * a.dgate.stride + c, dg);
-      }
-    }
-    const float mean = row_sum(sum, red[turn]) * inv_h;
+    float sum[3] = {total(s1), total(s2), total(s3)};
+    row_sums(sum, red[turn]);
     turn ^= 1;
-    if (a.dblock.p)
+    // s2 and s3 lack the factor scale
+    const float c1 = p * p * sum[0] * inv_h, c2 = q * q * q * a.scale * (sum[1] - c1 * sum[2]) * inv_h;
+    const P c1n = both<P>(-c1), c2n = both<P>(-c2), q2 = both<P>(q), scale = both<P>(a.scale);
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = (threadIdx.x + i * blockDim.x) * W;
-        if (c < a.hidden) {
-          float v[W];
+    for (int i = 0; i < VPT; ++i)
+      if (c0 + i * across < a.hidden) {
+        if (pre) {
+          P r[N];
+          load(res.p + i * across, r);
 #pragma unroll
-          for (int j = 0; j < W; ++j) v[j] = q * fmaf(-bh[i][j], mean, dr[i][j]);
-          store<B, W>(static_cast<B *>(a.dblock.p) + row * a.dblock.stride + c, v);
+          for (int j = 0; j < N; ++j) z[i][j] = fma(c1n, r[j], z[i][j]);
+        }
+        if (full || dr.p) store(dr.p + i * across, z[i]);
+        if (post) {
+          P b[N], g[N];
+          load(blk.p + i * across, b);
+#pragma unroll
+          for (int j = 0; j < N; ++j) z[i][j] = mul(z[i][j], q2);   // dr q
+          if (full ? gate_rows : a.dgate.p != nullptr) {
+            P v[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = mul(mul(z[i][j], b[j]), scale);
+            if (full || w_post) times<B, W>(w_post + c0 + i * across, v);
+            store(static_cast<B *>(a.dgate.p) + row * a.dgate.stride + c0 + i * across, v);
+          }
+          if (gate_rows) {
+            load(gate.p + i * across, g);
+#pragma unroll
+            for (int j = 0; j < N; ++j) dwq[i][j] = fma(mul(z[i][j], g[j]), b[j], dwq[i][j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) dwq[i][j] = fma(z[i][j], b[j], dwq[i][j]);
+          }
+          factors(i, g);
+#pragma unroll
+          for (int j = 0; j < N; ++j) z[i][j] = fma(mul(g[j], scale), z[i][j], mul(c2n, b[j]));
+          if (full || db.p) store(db.p + i * across, z[i]);
         }
       }
+    dres.next(), res.next(), dnorm.next(), blk.next(), gate.next();
+    dr.next(), db.next();
   }
   if (!a.partial) return;
-  float *out = a.partial + group * 3 * a.hidden;
+  float *out = a.partial + group * 2 * a.hidden + c0;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = (threadIdx.x + i * blockDim.x) * W;
-    if (c < a.hidden)
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        if (a.want_pre) out[c + j] = dwp[i][j];
-        if (a.want_post) out[a.hidden + c + j] = dwq[i][j];
-        if (a.want_gate) out[2 * a.hidden + c + j] = dgs[i][j];
-      }
-  }
+  for (int i = 0; i < VPT; ++i)
+    if (c0 + i * across < a.hidden) {
+      if (pre) store(out + i * across, dwp[i]);
+      if (post) store(out + a.hidden + i * across, dwq[i]);
+    }
 }
 
-// out[s][c] = sum over groups of partial[group][s][c], in 16 interleaved
-// partial sums that are then added in a fixed order.
+// The weights' gradients from the groups' sums: dw_pre = sum of the first,
+// dw_post = scale (shared gate) times the sum of the second, and for a shared
+// gate dgate = scale w_post times it.  16 interleaved partial sums per column,
+// added in a fixed order.
 template <typename B>
-__global__ void __launch_bounds__(512) norm_weight_sum_kernel(const float *partial, int64_t groups, int hidden, B *d0,
-                                                              B *d1, B *d2) {
+__global__ void __launch_bounds__(512) norm_weight_sum_kernel(const float *partial, int64_t groups, int hidden,
+                                                              float scale, const B *w_post, const B *shared_gate,
+                                                              B *dw_pre, B *dw_post, B *dgate) {
   __shared__ float part[16][33];
   const int which = blockIdx.y;
-  B *dst = which == 0 ? d0 : which == 1 ? d1 : d2;
-  if (!dst) return;
+  if (which == 0 ? !dw_pre : !dw_post && !dgate) return;
   const int c = blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
   if (c < hidden)
-    for (int64_t g = threadIdx.y; g < groups; g += 16) v += partial[(g * 3 + which) * hidden + c];
+    for (int64_t g = threadIdx.y; g < groups; g += 16) v += partial[(g * 2 + which) * hidden + c];
   part[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
-  if (threadIdx.y == 0 && c < hidden) {
-    v = 0.f;
+  if (threadIdx.y != 0 || c >= hidden) return;
+  v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += part[i][threadIdx.x];
-    from_f(dst + c, v);
+  for (int i = 0; i < 16; ++i) v += part[i][threadIdx.x];
+  if (which == 0) {
+    from_f(dw_pre + c, v);
+    return;
   }
+  v *= scale;
+  if (dw_post) from_f(dw_post + c, shared_gate ? v * to_f(shared_gate[c]) : v);
+  if (dgate) from_f(dgate + c, w_post ? v * to_f(w_post[c]) : v);
 }
 
-// Threads, and elements per thread, of a row.
+// Threads, and places per thread, of a row.
 struct Plan {
   int w, vpt, threads, rows_per_cta;
 };
@@ -338,16 +506,17 @@ Plan plan_rows(int hidden, bool vec, bool backward) {
   Plan p{};
   p.w = vec ? 8 : 1;
   const int n = (hidden + p.w - 1) / p.w;
-  const int small = vec ? 1 : 4, mid = vec ? 2 : 8, large = vec ? 4 : 32;
-  p.vpt = n <= small * max_threads(p.w, small, backward) ? small
-          : n <= mid * max_threads(p.w, mid, backward)   ? mid
-                                                         : large;
+  if (vec) {
+    p.vpt = n <= 128 ? 1 : kPlaces;   // up to 128 places: one each
+  } else {
+    p.vpt = n <= 4 * max_threads(1, 4, backward) ? 4 : n <= 8 * max_threads(1, 8, backward) ? 8 : 32;
+  }
   p.threads = (n + p.vpt - 1) / p.vpt;
   p.threads = (p.threads + 31) / 32 * 32;
   p.rows_per_cta = p.threads == 32 ? kRowsPerCta : 1;
   return p;
 }
-static_assert(8 * 4 * max_threads(8, 4, true) >= kMaxHidden && 32 * max_threads(1, 32, true) >= kMaxHidden,
+static_assert(8 * kPlaces * kWideThreads >= kMaxHidden && 32 * max_threads(1, 32, true) >= kMaxHidden,
               "every width has a plan");
 
 inline bool vec_row(const void *p, int64_t stride, int type) {
@@ -355,45 +524,73 @@ inline bool vec_row(const void *p, int64_t stride, int type) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride % (type == MUON_BF16 ? 8 : 4) == 0;
 }
 
-int64_t backward_groups(const Plan &p, int64_t rows) {
-  const int per_sm = std::max(1, std::min(2048 / (p.threads * p.rows_per_cta), p.threads >= 512 ? 1 : 8));
-  const int64_t ctas = std::min<int64_t>((rows + p.rows_per_cta - 1) / p.rows_per_cta, (int64_t)num_sms() * per_sm);
-  return ctas * p.rows_per_cta;
+// Groups of threads, each walking its share of the rows: as many as the
+// registers of all SMs hold.
+int64_t groups_of(const Plan &p, int64_t rows, bool backward) {
+  const int per_sm = blocks_per_sm(p.w, p.threads * p.rows_per_cta, backward);
+  return std::min<int64_t>((rows + p.rows_per_cta - 1) / p.rows_per_cta, (int64_t)num_sms() * per_sm) * p.rows_per_cta;
+}
+
+template <typename Kernel, typename Args>
+int launch_rows(Kernel *kernel, const Args &a, const Plan &p, bool backward, int trace, cudaStream_t s) {
+  trace_before(trace, s);
+  kernel<<<dim3((unsigned)(groups_of(p, a.rows, backward) / p.rows_per_cta)), dim3(p.threads, p.rows_per_cta), 0, s>>>(
+      a);
+  return trace_after(trace, s);
+}
+
+template <typename R, typename B, int W, int VPT, int THREADS = max_threads(W, VPT, false)>
+int launch_fwd_as(const FwdArgs &a, const Plan &p, cudaStream_t s) {
+  auto go = [&](auto *kernel) { return launch_rows(kernel, a, p, false, kTraceBlockNorm, s); };
+  if constexpr (W == 8)
+    if (a.block.p && a.normed.p && a.w_post && a.w_pre) {
+      if (a.gate.p) return go(block_norm_kernel<R, B, W, VPT, THREADS, FULL_ROW_GATE>);
+      if (a.shared_gate) return go(block_norm_kernel<R, B, W, VPT, THREADS, FULL_SHARED_GATE>);
+      return go(block_norm_kernel<R, B, W, VPT, THREADS, FULL>);
+    }
+  return go(block_norm_kernel<R, B, W, VPT, THREADS, ANY>);
 }
 
 template <typename R, typename B>
 int launch_fwd(const FwdArgs &a, bool vec, cudaStream_t s) {
   const Plan p = plan_rows(a.hidden, vec, false);
-  const dim3 block(p.threads, p.rows_per_cta);
-  const dim3 grid((unsigned)((a.rows + p.rows_per_cta - 1) / p.rows_per_cta));
-  trace_before(kTraceBlockNorm, s);
-  if (p.w == 8 && p.vpt == 1) block_norm_kernel<R, B, 8, 1><<<grid, block, 0, s>>>(a);
-  else if (p.w == 8 && p.vpt == 2) block_norm_kernel<R, B, 8, 2><<<grid, block, 0, s>>>(a);
-  else if (p.w == 8) block_norm_kernel<R, B, 8, 4><<<grid, block, 0, s>>>(a);
-  else if (p.vpt == 4) block_norm_kernel<R, B, 1, 4><<<grid, block, 0, s>>>(a);
-  else if (p.vpt == 8) block_norm_kernel<R, B, 1, 8><<<grid, block, 0, s>>>(a);
-  else block_norm_kernel<R, B, 1, 32><<<grid, block, 0, s>>>(a);
-  return trace_after(kTraceBlockNorm, s);
+  if (p.w == 8 && p.vpt == 1) return launch_fwd_as<R, B, 8, 1>(a, p, s);
+  if (p.w == 8)
+    return p.threads <= max_threads(8, kPlaces, false) ? launch_fwd_as<R, B, 8, kPlaces>(a, p, s)
+                                                          : launch_fwd_as<R, B, 8, kPlaces, kWideThreads>(a, p, s);
+  if (p.vpt == 4) return launch_fwd_as<R, B, 1, 4>(a, p, s);
+  return p.vpt == 8 ? launch_fwd_as<R, B, 1, 8>(a, p, s) : launch_fwd_as<R, B, 1, 32>(a, p, s);
+}
+
+template <typename R, typename B, int W, int VPT, int THREADS = max_threads(W, VPT, true)>
+int launch_bwd_as(const BwdArgs &a, const Plan &p, cudaStream_t s) {
+  auto go = [&](auto *kernel) { return launch_rows(kernel, a, p, true, kTraceBlockNormBwd, s); };
+  if constexpr (W == 8)
+    if (a.dresidual_out.p && a.dnormed.p && a.block.p && a.w_post && a.w_pre && a.dresidual.p && a.dblock.p &&
+        !a.gate.p == !a.dgate.p) {
+      if (a.gate.p) return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, FULL_ROW_GATE>);
+      if (a.shared_gate) return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, FULL_SHARED_GATE>);
+      return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, FULL>);
+    }
+  return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, ANY>);
 }
 
 template <typename R, typename B>
 int launch_bwd(const BwdArgs &a, bool vec, void *dw_pre, void *dw_post, void *dgate, cudaStream_t s) {
   const Plan p = plan_rows(a.hidden, vec, true);
-  const int64_t groups = backward_groups(p, a.rows);
-  const dim3 block(p.threads, p.rows_per_cta);
-  const dim3 grid((unsigned)(groups / p.rows_per_cta));
-  trace_before(kTraceBlockNormBwd, s);
-  if (p.w == 8 && p.vpt == 1) block_norm_backward_kernel<R, B, 8, 1><<<grid, block, 0, s>>>(a);
-  else if (p.w == 8 && p.vpt == 2) block_norm_backward_kernel<R, B, 8, 2><<<grid, block, 0, s>>>(a);
-  else if (p.w == 8) block_norm_backward_kernel<R, B, 8, 4><<<grid, block, 0, s>>>(a);
-  else if (p.vpt == 4) block_norm_backward_kernel<R, B, 1, 4><<<grid, block, 0, s>>>(a);
-  else if (p.vpt == 8) block_norm_backward_kernel<R, B, 1, 8><<<grid, block, 0, s>>>(a);
-  else block_norm_backward_kernel<R, B, 1, 32><<<grid, block, 0, s>>>(a);
-  int st = trace_after(kTraceBlockNormBwd, s);
+  int st;
+  if (p.w == 8 && p.vpt == 1) st = launch_bwd_as<R, B, 8, 1>(a, p, s);
+  else if (p.w == 8 && p.threads <= max_threads(8, kPlaces, true)) st = launch_bwd_as<R, B, 8, kPlaces>(a, p, s);
+  else if (p.w == 8) st = launch_bwd_as<R, B, 8, kPlaces, kWideThreads>(a, p, s);
+  else if (p.vpt == 4) st = launch_bwd_as<R, B, 1, 4>(a, p, s);
+  else if (p.vpt == 8) st = launch_bwd_as<R, B, 1, 8>(a, p, s);
+  else st = launch_bwd_as<R, B, 1, 32>(a, p, s);
   if (st != MUON_OK || !a.partial) return st;
   trace_before(kTraceNormWeightSum, s);
-  norm_weight_sum_kernel<B><<<dim3((unsigned)((a.hidden + 31) / 32), 3), dim3(32, 16), 0, s>>>(
-      a.partial, groups, a.hidden, static_cast<B *>(dw_pre), static_cast<B *>(dw_post), static_cast<B *>(dgate));
+  norm_weight_sum_kernel<B><<<dim3((unsigned)((a.hidden + 31) / 32), 2), dim3(32, 16), 0, s>>>(
+      a.partial, groups_of(p, a.rows, true), a.hidden, a.scale, static_cast<const B *>(a.w_post),
+      static_cast<const B *>(a.shared_gate), static_cast<B *>(dw_pre), static_cast<B *>(dw_post),
+      static_cast<B *>(dgate));
   return trace_after(kTraceNormWeightSum, s);
 }
 
@@ -403,9 +600,9 @@ bool bad_type(int t) { return t != MUON_BF16 && t != MUON_F32; }
 
 size_t block_norm_backward_workspace(int64_t rows, int64_t hidden) {
   // the larger of the two plans' groups (vector and element-wise access)
-  const int64_t g = std::max(backward_groups(plan_rows((int)hidden, true, true), rows),
-                             backward_groups(plan_rows((int)hidden, false, true), rows));
-  return ((size_t)g * 3 * (size_t)hidden * sizeof(float) + 255) & ~size_t(255);
+  const int64_t g = std::max(groups_of(plan_rows((int)hidden, true, true), rows, true),
+                             groups_of(plan_rows((int)hidden, false, true), rows, true));
+  return ((size_t)g * 2 * (size_t)hidden * sizeof(float) + 255) & ~size_t(255);
 }
 
 }  // namespace muon
@@ -430,7 +627,9 @@ int muon_block_norm(const muon_block_norm_args *a, muon_stream_t stream) {
   FwdArgs k{};
   k.residual = {a->residual, a->residual_stride};
   k.block = {a->block, a->block_stride};
-  k.gate = {a->block ? a->gate : nullptr, a->gate_stride};
+  const void *gate = a->block ? a->gate : nullptr;
+  if (a->gate_stride) k.gate = {gate, a->gate_stride};
+  else k.shared_gate = gate;
   k.residual_out = {a->residual_out, a->residual_out_stride};
   k.normed = {a->normed, a->normed_stride};
   k.w_post = a->block ? a->w_post : nullptr;
@@ -443,7 +642,7 @@ int muon_block_norm(const muon_block_norm_args *a, muon_stream_t stream) {
   k.eps = a->eps;
   const int rt = a->residual_type, bt = a->branch_type;
   const bool vec = h % 8 == 0 && vec_row(a->residual, a->residual_stride, rt) &&
-                   vec_row(k.block.p, a->block_stride, bt) && vec_row(k.gate.p, a->gate_stride, bt) &&
+                   vec_row(k.block.p, a->block_stride, bt) && vec_row(gate, a->gate_stride, bt) &&
                    vec_row(k.block.p ? a->residual_out : nullptr, a->residual_out_stride, rt) &&
                    vec_row(a->normed, a->normed_stride, bt) && vec_row(k.w_post, 0, bt) && vec_row(a->w_pre, 0, bt);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -489,9 +688,10 @@ int muon_block_norm_backward(const muon_block_norm_backward_args *a, void *works
   BwdArgs k{};
   k.dresidual_out = {a->dresidual_out, a->dresidual_out_stride};
   k.dnormed = {a->dnormed, a->dnormed_stride};
-  k.residual = {a->residual, a->residual_stride};
+  if (pre) k.residual = {a->residual, a->residual_stride};
   k.block = {a->block, a->block_stride};
-  k.gate = {gate ? a->gate : nullptr, a->gate_stride};
+  if (gate_rows) k.gate = {a->gate, a->gate_stride};
+  else if (gate) k.shared_gate = a->gate;
   k.dresidual = {a->dresidual, a->dresidual_stride};
   k.dblock = {a->dblock, a->dblock_stride};
   k.dgate = {gate_rows ? a->dgate : nullptr, a->dgate_stride};
@@ -502,14 +702,12 @@ int muon_block_norm_backward(const muon_block_norm_backward_args *a, void *works
   k.rows = a->rows;
   k.hidden = (int)h;
   k.scale = a->scale;
-  k.want_pre = a->dw_pre != nullptr;
-  k.want_post = a->dw_post != nullptr;
-  k.want_gate = a->dgate && !gate_rows;
-  const bool sums = k.want_pre || k.want_post || k.want_gate;
+  void *dg = gate_rows ? nullptr : a->dgate;
+  const bool sums = a->dw_pre || a->dw_post || dg;
   const bool vec = h % 8 == 0 && vec_row(a->dresidual_out, a->dresidual_out_stride, rt) &&
                    vec_row(a->dnormed, a->dnormed_stride, bt) &&
                    vec_row(pre ? a->residual : nullptr, a->residual_stride, rt) &&
-                   vec_row(a->block, a->block_stride, bt) && vec_row(k.gate.p, a->gate_stride, bt) &&
+                   vec_row(a->block, a->block_stride, bt) && vec_row(gate ? a->gate : nullptr, a->gate_stride, bt) &&
                    vec_row(a->dresidual, a->dresidual_stride, rt) && vec_row(a->dblock, a->dblock_stride, bt) &&
                    vec_row(k.dgate.p, a->dgate_stride, bt) && vec_row(k.w_post, 0, bt) && vec_row(k.w_pre, 0, bt);
   const size_t need = block_norm_backward_workspace(a->rows, h);
@@ -527,7 +725,6 @@ int muon_block_norm_backward(const muon_block_norm_backward_args *a, void *works
       k.partial = static_cast<float *>(owned);
     }
   }
-  void *dg = k.want_gate ? a->dgate : nullptr;
   int st;
   if (rt == MUON_BF16) st = launch_bwd<__nv_bfloat16, __nv_bfloat16>(k, vec, a->dw_pre, a->dw_post, dg, s);
   else if (bt == MUON_BF16) st = launch_bwd<float, __nv_bfloat16>(k, vec, a->dw_pre, a->dw_post, dg, s);
