@@ -25,7 +25,7 @@ OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libmuon.so")
 LIB_CHECKED = os.path.join(OUT_DIR, "libmuon_checked.so")
 SOURCES = ["api.cu", "elementwise.cu", "gemm_tc.cu", "gemm_f32.cu", "ns_static.cu", "host_stream.cu",
-           "ffn.cu", "ffn_tc.cu", "norm.cu", "logprobs.cu"]
+           "ffn.cu", "ffn_tc.cu", "ffn_few.cu", "norm.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

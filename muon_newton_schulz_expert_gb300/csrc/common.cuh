@@ -151,6 +151,16 @@ int ffn_dh(const FfnShape &f, const void *dy, int64_t lddy, const void *w2, cons
            void *du, void *hid, cudaStream_t s);
 int ffn_dx(const FfnShape &f, const void *dg, const void *du, const void *w1, const void *w3, void *dx, int64_t lddx,
            cudaStream_t s);
+// the same products for few rows (ffn_few.cu): hid comes and goes as two
+// halves, bf16(h) and bf16(h - bf16(h))
+int ffn_few_up(const FfnShape &f, const void *x, int64_t ldx, const void *w1, const void *w3, void *hid, void *hid_rest,
+               void *gate, void *up, cudaStream_t s);
+int ffn_few_down(const FfnShape &f, const void *hid, const void *hid_rest, const void *w2, void *y, int64_t ldy,
+                 cudaStream_t s);
+int ffn_few_dh(const FfnShape &f, const void *dy, int64_t lddy, const void *w2, const void *gate, const void *up,
+               void *dg, void *du, void *hid, cudaStream_t s);
+int ffn_few_dx(const FfnShape &f, const void *dg, const void *du, const void *w1, const void *w3, void *dx,
+               int64_t lddx, cudaStream_t s);
 // scratch of ffn_dw, in bf16 elements
 size_t ffn_tail_elems(const FfnShape &f);
 int ffn_dw(const FfnShape &f, const void *x, int64_t ldx, const void *dy, int64_t lddy, const void *dg, const void *du,

@@ -1,5 +1,6 @@
 // C entry points of the gated feed-forward block: argument checks, workspace
 // and the order of the products (ffn_tc.cu).
+#include <algorithm>
 #include <initializer_list>
 
 #include "common.cuh"
@@ -60,8 +61,21 @@ struct Scratch {
   }
 };
 
-size_t fwd_bytes(const FfnShape &f) { return align256((size_t)f.rows * f.ffn * 2); }
-size_t bwd_bytes(const FfnShape &f) { return 3 * fwd_bytes(f) + align256(ffn_tail_elems(f) * 2); }
+// Which kernels take a row product with `cols` output columns (of tiles of
+// `tile`): where 256-row tiles leave pairs of CTAs without one, and an expert's
+// rows fit two row tiles of ffn_few.cu, its smaller tiles and cut K loop.
+// Measured at 6144 x 1792, one expert: 1 row 37 + 19 us against 14 + 10 us.
+// With more rows an expert the smaller tiles read the weights again for each:
+// 1777 rows, 5 experts, 1000 x 328: 21 + 13 us against 97 + 26 us.
+bool few_tiles(const FfnShape &f, int64_t cols, int64_t tile) {
+  const int64_t active = std::min(f.experts, f.rows);
+  return f.rows <= 128 * active && (f.rows / 256 + active) * ((cols + tile - 1) / tile) < num_sms() / 2;
+}
+bool few_up(const FfnShape &f) { return few_tiles(f, f.ffn, 128); }
+
+size_t rows_bytes(const FfnShape &f) { return align256((size_t)f.rows * f.ffn * 2); }
+size_t fwd_bytes(const FfnShape &f) { return 2 * rows_bytes(f); }   // h, and for few rows what its rounding left
+size_t bwd_bytes(const FfnShape &f) { return 3 * rows_bytes(f) + align256(ffn_tail_elems(f) * 2); }
 
 #define MUON_TRY(expr)              \
   do {                              \
@@ -73,9 +87,12 @@ int backward(const FfnShape &f, const void *dy, int64_t lddy, const void *x, int
              const void *up, const void *w1, const void *w3, const void *w2, void *dx, int64_t lddx, void *dw1,
              void *dw3, void *dw2, void *scratch, cudaStream_t s) {
   uint8_t *p = static_cast<uint8_t *>(scratch);
-  void *dg = p, *du = p + fwd_bytes(f), *hid = p + 2 * fwd_bytes(f), *tails = p + 3 * fwd_bytes(f);
-  MUON_TRY(ffn_dh(f, dy, lddy, w2, gate, up, dg, du, hid, s));
-  if (dx) MUON_TRY(ffn_dx(f, dg, du, w1, w3, dx, lddx, s));
+  void *dg = p, *du = p + rows_bytes(f), *hid = p + 2 * rows_bytes(f), *tails = p + 3 * rows_bytes(f);
+  MUON_TRY(few_tiles(f, f.ffn, 256) ? ffn_few_dh(f, dy, lddy, w2, gate, up, dg, du, hid, s)
+                                    : ffn_dh(f, dy, lddy, w2, gate, up, dg, du, hid, s));
+  if (dx)
+    MUON_TRY(few_tiles(f, f.hidden, 256) ? ffn_few_dx(f, dg, du, w1, w3, dx, lddx, s)
+                                         : ffn_dx(f, dg, du, w1, w3, dx, lddx, s));
   if (dw1) MUON_TRY(ffn_dw(f, x, ldx, dy, lddy, dg, du, hid, tails, dw1, dw3, dw2, s));
   return MUON_OK;
 }
@@ -106,8 +123,15 @@ int muon_gated_ffn(const void *x, int64_t x_stride, const void *w1, const void *
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   Scratch ws(s);
   MUON_TRY(ws.take(workspace, workspace_bytes, fwd_bytes(f)));
-  int st = ffn_up(f, x, x_stride, w1, w3, ws.p, gate, up, s);
-  if (st == MUON_OK) st = ffn_down(f, ws.p, w2, y, y_stride, s);
+  void *hid = ws.p, *rest = static_cast<uint8_t *>(ws.p) + rows_bytes(f);
+  int st;
+  if (few_up(f)) {
+    st = ffn_few_up(f, x, x_stride, w1, w3, hid, rest, gate, up, s);
+    if (st == MUON_OK) st = ffn_few_down(f, hid, rest, w2, y, y_stride, s);
+  } else {
+    st = ffn_up(f, x, x_stride, w1, w3, hid, gate, up, s);
+    if (st == MUON_OK) st = ffn_down(f, hid, w2, y, y_stride, s);
+  }
   return ws.done(st);
 }
 

@@ -40,7 +40,7 @@
 // bounded (tc.cuh).
 #include <algorithm>
 
-#include "tc.cuh"
+#include "ffn.cuh"
 
 namespace muon {
 namespace {
@@ -95,58 +95,21 @@ struct Args {
   unsigned long long timeout_ns;
 };
 
-// Walks the tiles in order.  Every role of every CTA walks the same sequence,
-// so the groups' sizes are read from the device and the host needs none.
+// A tile: expert, row tile and column tile, rows of the expert.
 template <int MODE>
-struct Cursor {
-  const Args &p;
-  int e = -1;
-  long long first = 0, count = 0;    // tiles before expert e, tiles of expert e
-  long long lo = 0, hi = 0;          // rows of expert e
-  int ti = 0, tj = 0;
+struct Tile {
+  int e, ti, tj, lo, hi;
 
-  __device__ explicit Cursor(const Args &args) : p(args) {}
-
-  __device__ bool seek(long long t) {
-    while (t >= first + count) {
-      if (++e >= p.experts) return false;
-      first += count;
-      if (p.offsets) {
-        // clamped, so that no offsets can send an access outside the arrays
-        const long long a = __ldg(p.offsets + e), b = __ldg(p.offsets + e + 1);
-        lo = a < 0 ? 0 : a > p.rows ? p.rows : a;
-        hi = b < lo ? lo : b > p.rows ? p.rows : b;
-      } else {
-        hi = p.rows;
-      }
-      count = (long long)(Form<MODE>::dw ? p.tiles_m : (hi - lo + CM - 1) / CM) * p.tiles_n;
-    }
-    const int r = (int)(t - first);
-    const int tm = Form<MODE>::dw ? p.tiles_m : (int)((hi - lo + CM - 1) / CM);
-    tj = r / tm;
-    ti = r - tj * tm;
-    return true;
+  __device__ Tile(const Args &p, const WarpCursor &cur) {
+    e = cur.e, lo = cur.lo, hi = cur.hi;
+    const int tm = Form<MODE>::dw ? p.tiles_m : (hi - lo + CM - 1) / CM;
+    tj = (int)(cur.index / tm);
+    ti = (int)(cur.index - (long long)tj * tm);
   }
-
-  __device__ int num_kb() const {
-    return Form<MODE>::dw ? (int)((hi - lo + BK - 1) / BK) : MODE == DX ? 2 * p.kblocks : p.kblocks;
+  __device__ int num_kb(const Args &p) const {
+    return Form<MODE>::dw ? (hi - lo + BK - 1) / BK : MODE == DX ? 2 * p.kblocks : p.kblocks;
   }
 };
-
-// act(g) and act'(g): both activations are g * sigmoid(v), with v = g (silu)
-// or v = 2 sqrt(2/pi) (g + 0.044715 g^3) (the tanh form of gelu, since
-// (1 + tanh(z))/2 = sigmoid(2z)).
-__device__ __forceinline__ float sigmoid_of(float g, int act, float *dv) {
-  constexpr float c = 1.5957691216057308f, k = 0.044715f;
-  float v = g;
-  *dv = 1.f;
-  if (act == MUON_ACT_GELU) {
-    const float g2 = g * g;
-    v = c * g * fmaf(k, g2, 1.f);
-    *dv = c * fmaf(3.f * k, g2, 1.f);
-  }
-  return __fdividef(1.f, 1.f + __expf(-v));
-}
 
 __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
   __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
@@ -230,17 +193,6 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
     tma_prefetch_desc(&p.a);
     tma_prefetch_desc(&p.b);
     tma_prefetch_desc(&p.out[0]);
-    if (p.offsets && blockIdx.x == 0) {
-      // offsets that do not cut 0..rows into consecutive groups are reported
-      long long last = 0;
-      bool ok = __ldg(p.offsets) == 0;
-      for (int e = 0; e < p.experts; ++e) {
-        const long long v = __ldg(p.offsets + e + 1);
-        ok = ok && v >= last;
-        last = v;
-      }
-      if (!ok || last != p.rows) atomicOr(p.err, kErrDevice);
-    }
   }
   if (warp == 1) {  // one warp in each CTA of the pair allocates the same columns in both
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -255,19 +207,24 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
   const uint32_t tmem = *tmem_slot;
   const Watch w{abort_flag, p.err, p.timeout_ns};
   const unsigned long long drain_ns = p.timeout_ns < 20000000ull ? p.timeout_ns : 20000000ull;
-  Cursor<MODE> cur(p);
+  wait_for_previous_grid();
+  let_next_grid_start();
+  if (warp == 2 && blockIdx.x == 0) report_offsets(p.offsets, p.experts, p.rows, p.err);
+  WarpCursor walk(p.offsets, p.rows, p.experts, Form<MODE>::dw ? 0 : CM,
+                  (long long)(Form<MODE>::dw ? p.tiles_m : 1) * p.tiles_n);
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer (both CTAs)
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      uint32_t issued = 0, issued_parity = 0;  // stages ever filled, and the parity of their last fill
-      bool ok = true;
-      for (long long t = cid; ok && cur.seek(t); t += ncl) {
-        const int num_kb = cur.num_kb();
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t issued = 0, issued_parity = 0;  // stages ever filled, and the parity of their last fill
+    bool ok = true;
+    for (long long t = cid; walk.seek(t); t += ncl) {
+      const Tile<MODE> cur(p, walk);
+      if (lane == 0 && ok) {
+        const int num_kb = cur.num_kb(p);
         const int mn_a = cur.ti * CM + (int)rank * BM;   // DW: first column of A's rows in this CTA
-        const int row_a = (int)cur.lo + mn_a;            // row products: first row
+        const int row_a = cur.lo + mn_a;                 // row products: first row
         const int n_b = Form<MODE>::paired ? cur.tj * BNH : cur.tj * BN + (int)rank * BNH;
         const CUtensorMap *mb = Form<MODE>::paired && rank ? &p.b2 : &p.b;
         for (int kb = 0; kb < num_kb; kb += KSUB) {
@@ -291,8 +248,8 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
             const uint32_t bar = map_to_rank(full(stage, j), 0);
             if (Form<MODE>::dw) {
               // boxes of 64 columns x 64 rows; the group's last rows from the padded copies
-              const bool tail = (cur.hi - cur.lo) - (long long)k * BK < BK;
-              const int kr = tail ? 0 : (int)cur.lo + k * BK, z = tail ? cur.e : 0;
+              const bool tail = cur.hi - cur.lo - k * BK < BK;
+              const int kr = tail ? 0 : cur.lo + k * BK, z = tail ? cur.e : 0;
               const CUtensorMap *ma = tail ? &p.a2 : &p.a;
               const CUtensorMap *mbk = !tail ? mb : Form<MODE>::paired && rank ? &p.bt2 : &p.bt;
 #pragma unroll
@@ -320,64 +277,70 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
           }
         }
       }
-      // After an abort, stages may still be filling: let those copies land.
-      if (*abort_flag && rank == 0)
-        for (int s2 = 0; s2 < STAGES; ++s2)
-          if (issued & (1u << s2))
-            for (int j = 0; j < KSUB; ++j) drain_wait(full(s2, j), (issued_parity >> s2) & 1u, drain_ns);
+      __syncwarp();
     }
+    // After an abort, stages may still be filling: let those copies land.
+    if (*abort_flag && rank == 0 && lane == 0)
+      for (int s2 = 0; s2 < STAGES; ++s2)
+        if (issued & (1u << s2))
+          for (int j = 0; j < KSUB; ++j) drain_wait(full(s2, j), (issued_parity >> s2) & 1u, drain_ns);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (CTA 0 of the pair)
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       constexpr uint32_t idesc = make_idesc(CM, BN, Form<MODE>::a_mn, Form<MODE>::b_mn, kBF16);
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
-      for (long long t = cid; cur.seek(t); t += ncl) {
-        if (!wait_bounded(acce(acc), acc_phase ^ 1u, w)) break;
-        tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
-        const int num_kb = cur.num_kb();
-        for (int kb = 0; kb < num_kb; kb += KSUB) {
-          const int valid = num_kb - kb < KSUB ? num_kb - kb : KSUB;
+      for (long long t = cid; walk.seek(t); t += ncl) {
+        const Tile<MODE> cur(p, walk);
+        if (lane == 0 && ok) ok = wait_bounded(acce(acc), acc_phase ^ 1u, w);
+        if (lane == 0 && ok) {
+          tc_fence_after();
+          const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
+          const int num_kb = cur.num_kb(p);
+          for (int kb = 0; kb < num_kb; kb += KSUB) {
+            const int valid = num_kb - kb < KSUB ? num_kb - kb : KSUB;
 #pragma unroll
-          for (int j = 0; j < KSUB; ++j) {
-            if (j >= valid) break;
-            if (!wait_polled(full(stage, j), phase, w)) {
-              ok = false;
-              break;
+            for (int j = 0; j < KSUB; ++j) {
+              if (j >= valid) break;
+              if (!wait_polled(full(stage, j), phase, w)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t sa = sbase + stage * STAGE_BYTES + j * KB_BYTES, sb = sa + A_STAGE;
+              // K-major: advance 16 K-elements (32 bytes) inside the swizzle row.
+              // MN-major: advance 16 K-rows (two 8-row groups of 1024 bytes);
+              // 8192 bytes between 64-wide atoms, 1024 between 8-row groups.
+#pragma unroll
+              for (int kk = 0; kk < BK / UMMA_K; ++kk) {
+                const uint64_t ad = Form<MODE>::a_mn ? smem_desc(sa + kk * (UMMA_K * 128), 64 * BK * 2, 1024)
+                                               : smem_desc(sa + kk * (UMMA_K * 2), 16, 1024);
+                const uint64_t bd = Form<MODE>::b_mn ? smem_desc(sb + kk * (UMMA_K * 128), 64 * BK * 2, 1024)
+                                               : smem_desc(sb + kk * (UMMA_K * 2), 16, 1024);
+                tc_mma(d, ad, bd, idesc, ((kb + j) | kk) != 0 ? 1u : 0u);
+              }
             }
-            tc_fence_after();
-            const uint32_t sa = sbase + stage * STAGE_BYTES + j * KB_BYTES, sb = sa + A_STAGE;
-            // K-major: advance 16 K-elements (32 bytes) inside the swizzle row.
-            // MN-major: advance 16 K-rows (two 8-row groups of 1024 bytes);
-            // 8192 bytes between 64-wide atoms, 1024 between 8-row groups.
-#pragma unroll
-            for (int kk = 0; kk < BK / UMMA_K; ++kk) {
-              const uint64_t ad = Form<MODE>::a_mn ? smem_desc(sa + kk * (UMMA_K * 128), 64 * BK * 2, 1024)
-                                             : smem_desc(sa + kk * (UMMA_K * 2), 16, 1024);
-              const uint64_t bd = Form<MODE>::b_mn ? smem_desc(sb + kk * (UMMA_K * 128), 64 * BK * 2, 1024)
-                                             : smem_desc(sb + kk * (UMMA_K * 2), 16, 1024);
-              tc_mma(d, ad, bd, idesc, ((kb + j) | kk) != 0 ? 1u : 0u);
+            if (!ok) break;
+            tc_commit_mc(empty(stage), 0x3);  // both CTAs may refill this stage
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
             }
           }
-          if (!ok) break;
-          tc_commit_mc(empty(stage), 0x3);  // both CTAs may refill this stage
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (ok) tc_commit_mc(accf(acc), 0x3);  // both CTAs' accumulators are ready
         }
-        if (!ok) break;
-        tc_commit_mc(accf(acc), 0x3);  // both CTAs' accumulators are ready
+        __syncwarp();
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
-      tc_commit_mc(drain_bar, 0x1);  // flips once all MMAs issued by this thread have completed
-      volatile int no_abort = 0;
-      wait_bounded(drain_bar, 0, Watch{&no_abort, p.err, p.timeout_ns});
+      if (lane == 0) {
+        tc_commit_mc(drain_bar, 0x1);  // flips once all MMAs issued by this thread have completed
+        volatile int no_abort = 0;
+        wait_bounded(drain_bar, 0, Watch{&no_abort, p.err, p.timeout_ns});
+      }
     }
   } else {
     // ---------------------------------------------------------------- epilogue (both CTAs)
@@ -386,13 +349,14 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
     Writer out{epi_smem + ew * (EPI_BOXES * BOX_BYTES), smem_u32(epi_smem) + (uint32_t)(ew * EPI_BOXES * BOX_BYTES)};
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (long long t = cid; cur.seek(t); t += ncl) {
+    for (long long t = cid; walk.seek(t); t += ncl) {
+      const Tile<MODE> cur(p, walk);
       const bool ok = wait_bounded(accf(acc), acc_phase, w);
       if (!__all_sync(0xffffffffu, ok)) break;  // warp-uniform: the TMEM loads below are .sync.aligned
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
       const int rt = cur.ti * CM + (int)rank * BM + q * 32;
-      const long long row0 = Form<MODE>::dw ? rt : cur.lo + rt;
+      const long long row0 = Form<MODE>::dw ? rt : (long long)cur.lo + rt;
       const long long row_end = Form<MODE>::dw ? p.M : cur.hi;
       const int mat = Form<MODE>::dw ? cur.e : 0;
       if (row0 < row_end) {
@@ -454,13 +418,8 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
               float dg[2], du[2], h[2];
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const float g = j ? g2.y : g2.x, u = j ? u2.y : u2.x, d = __uint_as_float(r[2 * i + j]);
-                float dv;
-                const float s = sigmoid_of(g, p.act, &dv);
-                const float a = g * s;
-                h[j] = a * u;
-                du[j] = d * a;
-                dg[j] = d * u * fmaf(a * (1.f - s), dv, s);
+                gated_gradient(__uint_as_float(r[2 * i + j]), j ? g2.y : g2.x, j ? u2.y : u2.x, p.act, &dg[j], &du[j],
+                               &h[j]);
               }
               wg[i] = pack_bf16(dg[0], dg[1]);
               wu[i] = pack_bf16(du[0], du[1]);
@@ -554,13 +513,15 @@ int launch(Args &p, int trace_kind, cudaStream_t s) {
   auto *kernel = ffn_gemm_kernel<MODE>;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(THREADS, 1, 1);
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 1;   // the occupancy query knows clusters only
   cfg.dynamicSmemBytes = SMEM_BYTES;
   std::call_once(attr_once[dev], [&] {
     attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
@@ -581,6 +542,7 @@ int launch(Args &p, int trace_kind, cudaStream_t s) {
       Form<MODE>::dw ? (long long)p.tiles_m * p.experts : p.rows / CM + std::min<long long>(p.experts, p.rows);
   const long long pairs = std::min<long long>(row_tiles * p.tiles_n, max_pairs[dev]);
   cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
+  cfg.numAttrs = 2;
   cfg.stream = s;
   trace_before(trace_kind, s);
   const cudaError_t le = cudaLaunchKernelEx(&cfg, kernel, p);
