@@ -469,6 +469,11 @@ def _one_device(first, *others):
             raise ValueError("all tensors must be on one device")
 
 
+def _new(rows, cols, like):
+    import torch
+    return torch.empty((rows, cols), dtype=like.dtype, device=like.device)
+
+
 def _opt(t):
     return None if t is None else t.data_ptr()
 
@@ -533,11 +538,11 @@ def muon_gated_ffn(x, w1, w3, w2, offsets=None, *, act="silu", keep=False, out=N
     ldx, T, E, H, F, code = _ffn_shapes(x, w1, w3, w2, offsets, act)
     gate = up = gate_ptr = up_ptr = None
     if keep:
-        gate, up = x.new_empty((T, F)), x.new_empty((T, F))
+        gate, up = _new(T, F, x), _new(T, F, x)
         gate_ptr, up_ptr = gate.data_ptr(), up.data_ptr()
     ldy = H
     if out is None:
-        out = x.new_empty((T, H))
+        out = _new(T, H, x)
     else:
         ldy = _rows(out, x.dtype, (T, H), "out")
     ws, ws_bytes = _workspace(workspace)
@@ -568,7 +573,7 @@ def muon_gated_ffn_backward(dy, x, gate, up, w1, w3, w2, offsets=None, *, act="s
     if not need_dx:
         dx = None
     elif dx is None:
-        dx = x.new_empty((T, H))
+        dx = _new(T, H, x)
     else:
         lddx = _rows(dx, bf, (T, H), "dx")
     if need_dw:
@@ -620,7 +625,8 @@ def muon_block_norm(residual, block=None, *, w_post=None, gate=None, w_pre=None,
         raise ValueError("residual must be (rows, hidden)")
     T, H = shape = residual.shape
     rt = residual.dtype
-    branch = next((t for t in (block, w_pre, w_post, gate, normed) if t is not None), residual)
+    branch = (block if block is not None else w_pre if w_pre is not None else
+              normed if normed is not None else residual)
     bt = branch.dtype
     rcode, bcode = _dtype_code(residual, "residual"), _dtype_code(branch, "block")
     ldr = _rows(residual, rt, shape, "residual")
@@ -638,31 +644,29 @@ def muon_block_norm(residual, block=None, *, w_post=None, gate=None, w_pre=None,
         if gate is not None:
             ldg = _gate(gate, bt, T, H)
         if out is None:
-            out, ldo = residual.new_empty(shape), H
+            out, ldo = _new(T, H, residual), H
         else:
             ldo = _rows(out, rt, shape, "out")
     if norm_next:
         if w_pre is not None:
             _dense(w_pre, bt, (H,), "w_pre")
         if normed is None:
-            normed, ldn = branch.new_empty(shape), H
+            normed, ldn = _new(T, H, branch), H
         else:
             ldn = _rows(normed, bt, shape, "normed")
     else:
         if w_pre is not None or normed is not None:
             raise ValueError("w_pre and normed belong to the norm before the next block")
         ldn = 0
-    stats = torch.empty((2, T), dtype=torch.float32, device=residual.device)   # both rows' factors
-    at = stats.data_ptr()
     if block is not None:
-        rstd_post = stats[0]
+        rstd_post = torch.empty((T,), dtype=torch.float32, device=residual.device)
     if norm_next:
-        rstd_pre = stats[1]
+        rstd_pre = torch.empty((T,), dtype=torch.float32, device=residual.device)
     _one_device(residual, block, w_post, gate, w_pre, out, normed)
     _check("muon_block_norm", lib().muon_block_norm(_NORM_ARGS.pack(
         T, H, rcode, bcode, residual.data_ptr(), ldr, *((0, 0) if block is None else (block.data_ptr(), ldb)),
         _opt(w_post) or 0, _opt(gate) or 0, ldg, _opt(w_pre) or 0, scale, eps, _opt(out) or 0, ldo, _opt(normed) or 0,
-        ldn, at if block is not None else 0, at + 4 * T if norm_next else 0), _raw_stream(stream)))
+        ldn, _opt(rstd_post) or 0, _opt(rstd_pre) or 0), _raw_stream(stream)))
     return residual if block is None else out, normed, rstd_post, rstd_pre
 
 
@@ -683,7 +687,7 @@ def muon_block_norm_backward(dresidual, dnormed, residual, block=None, rstd_post
         raise ValueError("residual must be (rows, hidden)")
     T, H = shape = residual.shape
     rt = residual.dtype
-    branch = next((t for t in (dnormed, block, w_pre, w_post, gate) if t is not None), residual)
+    branch = dnormed if dnormed is not None else block if block is not None else residual
     bt = branch.dtype
     rcode, bcode = _dtype_code(residual, "residual"), _dtype_code(branch, "block")
     if dresidual is None and dnormed is None:
@@ -700,7 +704,7 @@ def muon_block_norm_backward(dresidual, dnormed, residual, block=None, rstd_post
         _dense(rstd_pre, f32, (T,), "rstd_pre")
         if w_pre is not None:
             _dense(w_pre, bt, (H,), "w_pre")
-            dw_pre = w_pre.new_empty((H,))
+            dw_pre = torch.empty_like(w_pre)
     else:
         if w_pre is not None:
             raise ValueError("w_pre belongs to the norm before the next block")
@@ -708,18 +712,18 @@ def muon_block_norm_backward(dresidual, dnormed, residual, block=None, rstd_post
     if block is not None:
         ldb = _rows(block, bt, shape, "block")
         _dense(rstd_post, f32, (T,), "rstd_post")
-        dblock = block.new_empty(shape)
+        dblock = _new(T, H, block)
         if w_post is not None:
             _dense(w_post, bt, (H,), "w_post")
-            dw_post = w_post.new_empty((H,))
+            dw_post = torch.empty_like(w_post)
         if gate is not None:
             ldg = _gate(gate, bt, T, H)
-            dgate = gate.new_empty(gate.shape)
+            dgate = torch.empty(gate.shape, dtype=bt, device=gate.device)
     else:
         if w_post is not None or gate is not None:
             raise ValueError("w_post and gate belong to a block")
         rstd_post = None
-    dr = residual.new_empty(shape)
+    dr = _new(T, H, residual)
     ws, ws_bytes = _workspace(workspace)
     _one_device(residual, dresidual, dnormed, block, rstd_post, rstd_pre, w_post, gate, w_pre, workspace)
     _check("muon_block_norm_backward", lib().muon_block_norm_backward(_NORM_BACKWARD_ARGS.pack(
@@ -780,7 +784,7 @@ def muon_token_logprobs_backward(logits, tokens, lse, entropy=None, dlogp=None, 
         if t is not None or n == "lse":
             _dense(t, torch.float32, (T,), n)
     if out is None:
-        out, out_stride = logits.new_empty((T, V)), V
+        out, out_stride = _new(T, V, logits), V
     else:
         out_stride = _rows(out, logits.dtype, (T, V), "out")
     _one_device(logits, tokens, lse, entropy, dlogp, dentropy, out)

@@ -386,12 +386,15 @@ int launch(Args &p, const FfnShape &f, int trace_kind, cudaStream_t s) {
   p.tn = row_tile(f);
   // Shared memory for two blocks of an SM, so that the next product's blocks
   // fetch their first weights beside this one's last; UP with 64 rows (40 KB
-  // stages) takes it whole.  K is cut while the blocks still fit the SMs at once.
+  // stages) takes it whole.  K is cut while the blocks still fit the SMs at
+  // once and each keeps 6 k-blocks or more (6144 x 1792, one row: 53 us uncut,
+  // 34, 24 and 21 us cut in 2, 4 and 8; but a cut costs two cluster barriers: 8
+  // experts of one row, 1024 x 512, take 14 us cut in 2 and 17 us cut in 4).
   const int per_sm = MODE == UP ? 1 : 2;
   const int64_t tiles = (int64_t)p.tiles_m * (f.experts == 1 ? (f.rows + p.tn - 1) / p.tn : active);
   const int all_kb = p.kblocks * p.segments;
   p.split = 1;
-  while (p.split < 8 && 2 * p.split * tiles <= (int64_t)num_sms() * per_sm && 4 * p.split <= all_kb) p.split *= 2;
+  while (p.split < 8 && 2 * p.split * tiles <= (int64_t)num_sms() * per_sm && 12 * p.split <= all_kb) p.split *= 2;
   const size_t stage = MATS * A_BYTES + (size_t)(MODE == DOWN ? 2 : 1) * p.tn * BK * 2;
   const size_t fixed = 1024 + (size_t)MATS * p.tn * BM * 4 + NUM_BARS * 8 + 16;
   const size_t budget = MODE == UP && p.tn == MAX_TN ? 220 * 1024 : 112 * 1024;
