@@ -56,13 +56,12 @@ constexpr int STAGES = 3, KSUB = 2;
 constexpr int STAGE_BYTES = KSUB * KB_BYTES;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
-constexpr int BOX_BYTES = 32 * 32 * 2;    // output staging box of an epilogue warp
-constexpr int EPI_BOXES = 2;              // boxes per warp: one fills while the other's store is read
+constexpr int BOX_BYTES = 32 * 64 * 2;    // output staging box of an epilogue warp: 32 rows x 64 columns
 constexpr int ACC_COLS = BN;
 constexpr int TMEM_COLS = 2 * ACC_COLS;
 constexpr int NFULL = STAGES * KSUB;
 constexpr int NUM_BARS = NFULL + STAGES + 5;
-constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * EPI_BOXES * BOX_BYTES + NUM_BARS * 8 + 16;
+constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * BOX_BYTES + NUM_BARS * 8 + 16;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 
 enum Mode { UP = 0, DOWN, DH, DX, DW13, DW2 };
@@ -80,7 +79,7 @@ struct Args {
   // operands: A and its second K segment (DX) or tail copy (DW); B and its
   // partner (UP: W3, DX: W3, DW13: dU) and their tail copies
   CUtensorMap a, a2, b, b2, bt, bt2;
-  CUtensorMap out[3];                // 32 x 32 boxes
+  CUtensorMap out[3];                // boxes of 32 rows x 64 columns
   void *outp[3];
   long long out_ld[3];               // row strides in elements
   const int64_t *offsets;            // null: one group of all rows
@@ -120,39 +119,47 @@ __device__ __forceinline__ float2 unpack_bf16(uint32_t v) {
   return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&v));
 }
 
-// One epilogue warp's way out: 32 rows x 32 columns of bf16, lane = row.  A
-// full box leaves through shared memory and TMA (clipped at the array's edge);
-// a box that a group ends in is written row by row.
-struct Writer {
-  uint8_t *boxes;
-  uint32_t boxes_s;
-  int next = 0;
+// 32 lanes x 64 consecutive fp32 columns -> 64 registers per thread, waited.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&lo)[32], uint32_t (&hi)[32]) {
+  tmem_ld32_issue(taddr, lo);
+  tmem_ld32_issue(taddr + 32, hi);
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  // the registers are only valid from here on
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(lo[i]), "+r"(hi[i]));
+}
 
-  __device__ void put(const uint32_t (&w)[16], const CUtensorMap *map, void *base, long long ld, int lane, int col0,
+// One epilogue warp's way out: 32 rows x 64 columns of bf16, lane = row.  A
+// full box leaves through shared memory and TMA (clipped at the array's edge):
+// 128-byte rows, since 64-byte ones (32 columns) held the stores of the weight
+// gradients to 2.6 TB/s.  A box that a group ends in is written row by row.
+struct Writer {
+  uint8_t *box;
+  uint32_t box_s;
+
+  __device__ void put(const uint32_t (&w)[32], const CUtensorMap *map, void *base, long long ld, int lane, int col0,
                       int cols, long long row0, long long row_end, bool clip_rows, int mat, unsigned *err) {
     if (clip_rows && row0 + 32 > row_end) {
       const long long row = row0 + lane;
       if (row < row_end) {
         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(base) + row * ld + col0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 8; ++c)
           if (col0 + 8 * c < cols)
             *reinterpret_cast<uint4 *>(dst + 8 * c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
       }
       return;
     }
-    const uint32_t off = (uint32_t)(next * BOX_BYTES);
-    next ^= 1;
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the box's last store has read it
+    if (lane == 0) bulk_wait_read_all();  // the box's last store has read it
     __syncwarp();
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<uint4 *>(boxes + off + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+    for (int c = 0; c < 8; ++c)
+      *reinterpret_cast<uint4 *>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
           make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_3d(map, boxes_s + off, col0, (int)row0, mat, err);
+      tma_store_3d(map, box_s, col0, (int)row0, mat, err);
       bulk_commit();
     }
   }
@@ -163,7 +170,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *epi_smem = smem + STAGES * STAGE_BYTES;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(epi_smem + EPI_WARPS * EPI_BOXES * BOX_BYTES);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(epi_smem + EPI_WARPS * BOX_BYTES);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NUM_BARS);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -346,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
     // ---------------------------------------------------------------- epilogue (both CTAs)
     const int ew = warp - 2;
     const int q = warp & 3, half = ew >> 2;  // TMEM lanes 32q.., and which half of the columns
-    Writer out{epi_smem + ew * (EPI_BOXES * BOX_BYTES), smem_u32(epi_smem) + (uint32_t)(ew * EPI_BOXES * BOX_BYTES)};
+    Writer out{epi_smem + ew * BOX_BYTES, smem_u32(epi_smem) + (uint32_t)(ew * BOX_BYTES)};
     int acc = 0;
     uint32_t acc_phase = 0;
     for (long long t = cid; walk.seek(t); t += ncl) {
@@ -361,69 +368,69 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
       const int mat = Form<MODE>::dw ? cur.e : 0;
       if (row0 < row_end) {
         if (MODE == UP) {
-#pragma unroll 1
-          for (int ch = 0; ch < 2; ++ch) {
-            const int cc = half * 64 + ch * 32, col0 = cur.tj * BNH + cc;
-            if (col0 >= p.N) break;
-            uint32_t g[32], u[32];
-            tmem_ld32(taddr + (uint32_t)cc, g);
-            tmem_ld32(taddr + (uint32_t)(BNH + cc), u);
-            uint32_t wh[16];
+          // this warp's 64 columns of the tile: G from the low half of the accumulator, U from the high one
+          const int cc = half * 64, col0 = cur.tj * BNH + cc;
+          if (col0 < p.N) {
+            uint32_t wg[32], wu[32], wh[32];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float h[2], dv;
+            for (int part = 0; part < 2; ++part) {
+              uint32_t g[32], u[32];
+              tmem_ld32(taddr + (uint32_t)(cc + 32 * part), g);
+              tmem_ld32(taddr + (uint32_t)(BNH + cc + 32 * part), u);
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const float gf = __uint_as_float(g[2 * i + j]);
-                h[j] = gf * sigmoid_of(gf, p.act, &dv) * __uint_as_float(u[2 * i + j]);
+              for (int i = 0; i < 16; ++i) {
+                float h[2], dv;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const float gf = __uint_as_float(g[2 * i + j]);
+                  h[j] = gf * sigmoid_of(gf, p.act, &dv) * __uint_as_float(u[2 * i + j]);
+                }
+                wh[16 * part + i] = pack_bf16(h[0], h[1]);
+                wg[16 * part + i] = pack_bf16(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
+                wu[16 * part + i] = pack_bf16(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
               }
-              wh[i] = pack_bf16(h[0], h[1]);
             }
             out.put(wh, &p.out[0], p.outp[0], p.out_ld[0], lane, col0, p.N, row0, row_end, true, 0, p.err);
             if (p.outp[1]) {
-              uint32_t wp[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) wp[i] = pack_bf16(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
-              out.put(wp, &p.out[1], p.outp[1], p.out_ld[1], lane, col0, p.N, row0, row_end, true, 0, p.err);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) wp[i] = pack_bf16(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-              out.put(wp, &p.out[2], p.outp[2], p.out_ld[2], lane, col0, p.N, row0, row_end, true, 0, p.err);
+              out.put(wg, &p.out[1], p.outp[1], p.out_ld[1], lane, col0, p.N, row0, row_end, true, 0, p.err);
+              out.put(wu, &p.out[2], p.outp[2], p.out_ld[2], lane, col0, p.N, row0, row_end, true, 0, p.err);
             }
           }
         } else if (MODE == DH) {
 #pragma unroll 1
-          for (int ch = 0; ch < 4; ++ch) {
-            const int cc = half * 128 + ch * 32, col0 = cur.tj * BN + cc;
+          for (int ch = 0; ch < 2; ++ch) {
+            const int cc = half * 128 + ch * 64, col0 = cur.tj * BN + cc;
             if (col0 >= p.N) break;
-            uint32_t gw[16], uw[16];
+            uint32_t wg[32], wu[32], wh[32];   // g, u and then dg, du in wg and wu
             const bool in_row = row0 + lane < row_end;
             const long long at = (row0 + lane) * p.N + col0;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 8; ++c) {
               uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
               if (in_row && col0 + 8 * c < p.N) {
                 a = __ldg(reinterpret_cast<const uint4 *>(p.g + at + 8 * c));
                 b = __ldg(reinterpret_cast<const uint4 *>(p.u + at + 8 * c));
               }
-              gw[4 * c] = a.x, gw[4 * c + 1] = a.y, gw[4 * c + 2] = a.z, gw[4 * c + 3] = a.w;
-              uw[4 * c] = b.x, uw[4 * c + 1] = b.y, uw[4 * c + 2] = b.z, uw[4 * c + 3] = b.w;
+              wg[4 * c] = a.x, wg[4 * c + 1] = a.y, wg[4 * c + 2] = a.z, wg[4 * c + 3] = a.w;
+              wu[4 * c] = b.x, wu[4 * c + 1] = b.y, wu[4 * c + 2] = b.z, wu[4 * c + 3] = b.w;
             }
             __syncwarp();
-            uint32_t r[32];
-            tmem_ld32(taddr + (uint32_t)cc, r);
-            uint32_t wg[16], wu[16], wh[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 g2 = unpack_bf16(gw[i]), u2 = unpack_bf16(uw[i]);
-              float dg[2], du[2], h[2];
+            for (int part = 0; part < 2; ++part) {
+              uint32_t r[32];
+              tmem_ld32(taddr + (uint32_t)(cc + 32 * part), r);
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                gated_gradient(__uint_as_float(r[2 * i + j]), j ? g2.y : g2.x, j ? u2.y : u2.x, p.act, &dg[j], &du[j],
-                               &h[j]);
+              for (int i = 0; i < 16; ++i) {
+                const float2 g2 = unpack_bf16(wg[16 * part + i]), u2 = unpack_bf16(wu[16 * part + i]);
+                float dg[2], du[2], h[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  gated_gradient(__uint_as_float(r[2 * i + j]), j ? g2.y : g2.x, j ? u2.y : u2.x, p.act, &dg[j], &du[j],
+                                 &h[j]);
+                wg[16 * part + i] = pack_bf16(dg[0], dg[1]);
+                wu[16 * part + i] = pack_bf16(du[0], du[1]);
+                wh[16 * part + i] = pack_bf16(h[0], h[1]);
               }
-              wg[i] = pack_bf16(dg[0], dg[1]);
-              wu[i] = pack_bf16(du[0], du[1]);
-              wh[i] = pack_bf16(h[0], h[1]);
             }
             out.put(wg, &p.out[0], p.outp[0], p.out_ld[0], lane, col0, p.N, row0, row_end, true, 0, p.err);
             out.put(wu, &p.out[1], p.outp[1], p.out_ld[1], lane, col0, p.N, row0, row_end, true, 0, p.err);
@@ -431,19 +438,21 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
           }
         } else {
           const bool empty_sum = Form<MODE>::dw && cur.hi == cur.lo;  // no MMA ran: the accumulator holds nothing
-          const int which = Form<MODE>::paired ? half : 0;               // DW13: dW1 in the low columns, dW3 in the high
+          const int which = Form<MODE>::paired ? half : 0;            // DW13: dW1 in the low columns, dW3 in the high
 #pragma unroll 1
-          for (int ch = 0; ch < 4; ++ch) {
-            const int cc = half * 128 + ch * 32;
-            const int col0 = Form<MODE>::paired ? cur.tj * BNH + ch * 32 : cur.tj * BN + cc;
+          for (int ch = 0; ch < 2; ++ch) {
+            const int cc = half * 128 + ch * 64;
+            const int col0 = Form<MODE>::paired ? cur.tj * BNH + ch * 64 : cur.tj * BN + cc;
             if (col0 >= p.N) break;
-            uint32_t r[32], wo[16];
-            tmem_ld32(taddr + (uint32_t)cc, r);
+            uint32_t lo[32], hi[32], wo[32];
+            tmem_ld64(taddr + (uint32_t)cc, lo, hi);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              wo[i] = empty_sum ? 0u : pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-            out.put(wo, &p.out[which], p.outp[which], p.out_ld[which], lane, col0, p.N, row0, row_end, !Form<MODE>::dw,
-                    mat, p.err);
+            for (int i = 0; i < 16; ++i) {
+              wo[i] = empty_sum ? 0u : pack_bf16(__uint_as_float(lo[2 * i]), __uint_as_float(lo[2 * i + 1]));
+              wo[16 + i] = empty_sum ? 0u : pack_bf16(__uint_as_float(hi[2 * i]), __uint_as_float(hi[2 * i + 1]));
+            }
+            out.put(wo, &p.out[which], p.outp[which], p.out_ld[which], lane, col0, p.N, row0, row_end,
+                    !Form<MODE>::dw, mat, p.err);
           }
         }
       }
@@ -560,7 +569,7 @@ int map_mn(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_
   return make_map(m, base, kBF16, batch, rows, cols, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, ld);
 }
 int map_out(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols, int64_t ld = 0) {
-  return make_map(m, base, kBF16, batch, rows, cols, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, ld);
+  return make_map(m, base, kBF16, batch, rows, cols, 32, 64, CU_TENSOR_MAP_SWIZZLE_128B, ld);
 }
 
 Args base_args(const FfnShape &f) {
