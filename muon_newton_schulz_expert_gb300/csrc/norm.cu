@@ -41,12 +41,12 @@ constexpr int kRowsPerCta = 4;   // rows of one CTA where a warp holds a whole r
 // instance with wide blocks.
 constexpr int kPlaces = 2;
 constexpr int max_threads(int w, int vpt, bool backward) {
-  if (w == 1) return vpt == 32 ? 512 : backward && vpt == 4 ? 512 : 1024;
+  if (w == 1) return vpt == 4 ? 512 : 1024;
   return vpt == 1 ? 128 : 384;
 }
 constexpr int kWideThreads = 1024;
 constexpr int blocks_per_sm(int w, int threads, bool backward) {
-  const int all = w == 1 ? (backward ? 512 : 1024) : backward ? 768 : 1152;
+  const int all = w == 1 ? 1024 : backward ? 768 : 1152;
   return threads > all / 2 ? 1 : all / (threads < 64 ? 64 : threads);
 }
 
@@ -229,7 +229,7 @@ struct FwdArgs {
 };
 
 template <typename R, typename B, int W, int VPT, int THREADS, int FORM>
-__global__ void __launch_bounds__(THREADS, W == 1 ? 1 : blocks_per_sm(W, THREADS, false))
+__global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, false))
     block_norm_kernel(const __grid_constant__ FwdArgs a) {
   __shared__ float4 red[2][1][8];
   using P = Item<W>;
@@ -328,7 +328,7 @@ struct BwdArgs {
 // For a shared gate, sum over rows of dr b q serves dw_post (times scale gate)
 // and dgate (times scale w_post) alike.
 template <typename R, typename B, int W, int VPT, int THREADS, int FORM>
-__global__ void __launch_bounds__(THREADS, W == 1 ? 1 : blocks_per_sm(W, THREADS, true))
+__global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, true))
     block_norm_backward_kernel(const __grid_constant__ BwdArgs a) {
   __shared__ float4 red[2][3][8];
   using P = Item<W>;
@@ -469,8 +469,8 @@ __global__ void __launch_bounds__(THREADS, W == 1 ? 1 : blocks_per_sm(W, THREADS
 
 // The weights' gradients from the groups' sums: dw_pre = sum of the first,
 // dw_post = scale (shared gate) times the sum of the second, and for a shared
-// gate dgate = scale w_post times it.  16 interleaved partial sums per column,
-// added in a fixed order.
+// gate dgate = scale w_post times it.  16 x 4 interleaved partial sums per
+// column, added in a fixed order.
 template <typename B>
 __global__ void __launch_bounds__(512) norm_weight_sum_kernel(const float *partial, int64_t groups, int hidden,
                                                               float scale, const B *w_post, const B *shared_gate,
@@ -479,22 +479,25 @@ __global__ void __launch_bounds__(512) norm_weight_sum_kernel(const float *parti
   const int which = blockIdx.y;
   if (which == 0 ? !dw_pre : !dw_post && !dgate) return;
   const int c = blockIdx.x * 32 + threadIdx.x;
-  float v = 0.f;
+  float v[4] = {};
   if (c < hidden)
-    for (int64_t g = threadIdx.y; g < groups; g += 16) v += partial[(g * 2 + which) * hidden + c];
-  part[threadIdx.y][threadIdx.x] = v;
+    for (int64_t g = threadIdx.y; g < groups; g += 64)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (g + 16 * k < groups) v[k] += partial[((g + 16 * k) * 2 + which) * hidden + c];
+  part[threadIdx.y][threadIdx.x] = (v[0] + v[1]) + (v[2] + v[3]);
   __syncthreads();
   if (threadIdx.y != 0 || c >= hidden) return;
-  v = 0.f;
+  float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v += part[i][threadIdx.x];
+  for (int i = 0; i < 16; ++i) sum += part[i][threadIdx.x];
   if (which == 0) {
-    from_f(dw_pre + c, v);
+    from_f(dw_pre + c, sum);
     return;
   }
-  v *= scale;
-  if (dw_post) from_f(dw_post + c, shared_gate ? v * to_f(shared_gate[c]) : v);
-  if (dgate) from_f(dgate + c, w_post ? v * to_f(w_post[c]) : v);
+  sum *= scale;
+  if (dw_post) from_f(dw_post + c, shared_gate ? sum * to_f(shared_gate[c]) : sum);
+  if (dgate) from_f(dgate + c, w_post ? sum * to_f(w_post[c]) : sum);
 }
 
 // Threads, and places per thread, of a row.
@@ -509,14 +512,14 @@ Plan plan_rows(int hidden, bool vec, bool backward) {
   if (vec) {
     p.vpt = n <= 128 ? 1 : kPlaces;   // up to 128 places: one each
   } else {
-    p.vpt = n <= 4 * max_threads(1, 4, backward) ? 4 : n <= 8 * max_threads(1, 8, backward) ? 8 : 32;
+    p.vpt = n <= 4 * max_threads(1, 4, backward) ? 4 : n <= 8 * max_threads(1, 8, backward) ? 8 : 16;
   }
   p.threads = (n + p.vpt - 1) / p.vpt;
   p.threads = (p.threads + 31) / 32 * 32;
   p.rows_per_cta = p.threads == 32 ? kRowsPerCta : 1;
   return p;
 }
-static_assert(8 * kPlaces * kWideThreads >= kMaxHidden && 32 * max_threads(1, 32, true) >= kMaxHidden,
+static_assert(8 * kPlaces * kWideThreads >= kMaxHidden && 16 * max_threads(1, 16, true) >= kMaxHidden,
               "every width has a plan");
 
 inline bool vec_row(const void *p, int64_t stride, int type) {
@@ -542,12 +545,11 @@ int launch_rows(Kernel *kernel, const Args &a, const Plan &p, bool backward, int
 template <typename R, typename B, int W, int VPT, int THREADS = max_threads(W, VPT, false)>
 int launch_fwd_as(const FwdArgs &a, const Plan &p, cudaStream_t s) {
   auto go = [&](auto *kernel) { return launch_rows(kernel, a, p, false, kTraceBlockNorm, s); };
-  if constexpr (W == 8)
-    if (a.block.p && a.normed.p && a.w_post && a.w_pre) {
-      if (a.gate.p) return go(block_norm_kernel<R, B, W, VPT, THREADS, FULL_ROW_GATE>);
-      if (a.shared_gate) return go(block_norm_kernel<R, B, W, VPT, THREADS, FULL_SHARED_GATE>);
-      return go(block_norm_kernel<R, B, W, VPT, THREADS, FULL>);
-    }
+  if (a.block.p && a.normed.p && a.w_post && a.w_pre) {
+    if (a.gate.p) return go(block_norm_kernel<R, B, W, VPT, THREADS, FULL_ROW_GATE>);
+    if (a.shared_gate) return go(block_norm_kernel<R, B, W, VPT, THREADS, FULL_SHARED_GATE>);
+    return go(block_norm_kernel<R, B, W, VPT, THREADS, FULL>);
+  }
   return go(block_norm_kernel<R, B, W, VPT, THREADS, ANY>);
 }
 
@@ -559,19 +561,18 @@ int launch_fwd(const FwdArgs &a, bool vec, cudaStream_t s) {
     return p.threads <= max_threads(8, kPlaces, false) ? launch_fwd_as<R, B, 8, kPlaces>(a, p, s)
                                                           : launch_fwd_as<R, B, 8, kPlaces, kWideThreads>(a, p, s);
   if (p.vpt == 4) return launch_fwd_as<R, B, 1, 4>(a, p, s);
-  return p.vpt == 8 ? launch_fwd_as<R, B, 1, 8>(a, p, s) : launch_fwd_as<R, B, 1, 32>(a, p, s);
+  return p.vpt == 8 ? launch_fwd_as<R, B, 1, 8>(a, p, s) : launch_fwd_as<R, B, 1, 16>(a, p, s);
 }
 
 template <typename R, typename B, int W, int VPT, int THREADS = max_threads(W, VPT, true)>
 int launch_bwd_as(const BwdArgs &a, const Plan &p, cudaStream_t s) {
   auto go = [&](auto *kernel) { return launch_rows(kernel, a, p, true, kTraceBlockNormBwd, s); };
-  if constexpr (W == 8)
-    if (a.dresidual_out.p && a.dnormed.p && a.block.p && a.w_post && a.w_pre && a.dresidual.p && a.dblock.p &&
-        !a.gate.p == !a.dgate.p) {
-      if (a.gate.p) return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, FULL_ROW_GATE>);
-      if (a.shared_gate) return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, FULL_SHARED_GATE>);
-      return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, FULL>);
-    }
+  if (a.dresidual_out.p && a.dnormed.p && a.block.p && a.w_post && a.w_pre && a.dresidual.p && a.dblock.p &&
+      !a.gate.p == !a.dgate.p) {
+    if (a.gate.p) return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, FULL_ROW_GATE>);
+    if (a.shared_gate) return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, FULL_SHARED_GATE>);
+    return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, FULL>);
+  }
   return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, ANY>);
 }
 
@@ -584,7 +585,7 @@ int launch_bwd(const BwdArgs &a, bool vec, void *dw_pre, void *dw_post, void *dg
   else if (p.w == 8) st = launch_bwd_as<R, B, 8, kPlaces, kWideThreads>(a, p, s);
   else if (p.vpt == 4) st = launch_bwd_as<R, B, 1, 4>(a, p, s);
   else if (p.vpt == 8) st = launch_bwd_as<R, B, 1, 8>(a, p, s);
-  else st = launch_bwd_as<R, B, 1, 32>(a, p, s);
+  else st = launch_bwd_as<R, B, 1, 16>(a, p, s);
   if (st != MUON_OK || !a.partial) return st;
   trace_before(kTraceNormWeightSum, s);
   norm_weight_sum_kernel<B><<<dim3((unsigned)((a.hidden + 31) / 32), 2), dim3(32, 16), 0, s>>>(
