@@ -15,7 +15,7 @@
 // the rows of the array; several groups on an SM overlap one's reductions with
 // another's loads.  The weights and a shared gate stay in L1, and so does the part of a row that is read a second time
 // after its reduction rather than held in registers.  The weights' gradients
-// stay in registers over a group's rows; each group writes its sums and a
+// stay in registers over a group's rows; each block writes its sums and a
 // second kernel adds them, in a fixed order (no atomics).  All arithmetic is
 // fp32, in pairs (f32x2) where vectors are moved.
 #include <algorithm>
@@ -157,6 +157,16 @@ template <typename T>
 __device__ __forceinline__ void store(T *dst, const float (&v)[1]) {
   from_f(dst, v[0]);
 }
+
+// Plain stores (shared memory).
+__device__ __forceinline__ void keep(float *dst, const F2 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 h = halves(v[i]);
+    dst[2 * i] = h.x, dst[2 * i + 1] = h.y;
+  }
+}
+__device__ __forceinline__ void keep(float *dst, const float (&v)[1]) { dst[0] = v[0]; }
 
 // Sums of N values over the threads of a row (blockDim.x, a multiple of 32);
 // with one warp per row no shared memory and no barrier is used.  Successive
@@ -315,7 +325,7 @@ struct BwdArgs {
   RowOut dresidual, dblock, dgate;                     // dgate: a row for each token
   const void *w_post, *shared_gate, *w_pre;
   const float *rstd_post, *rstd_pre;
-  float *partial;                    // [groups][2][hidden]: sums of dy xh, and of (per-row gate) dr bh
+  float *partial;                    // [blocks][2][hidden]: sums of dy xh, and of (per-row gate) dr bh
   int64_t rows;
   int hidden;
   float scale;
@@ -458,7 +468,29 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, true))
     dr.next(), db.next();
   }
   if (!a.partial) return;
-  float *out = a.partial + group * 2 * a.hidden + c0;
+  // the block's sums: those of its groups where warps hold rows, through shared memory
+  if (blockDim.y > 1) {
+    constexpr int MOST = 32 * VPT * W;   // columns of a warp's row
+    __shared__ float block_sums[VPT * W <= 8 ? kRowsPerCta : 1][2][VPT * W <= 8 ? MOST : 1];
+    if constexpr (VPT * W <= 8) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        keep(&block_sums[threadIdx.y][0][c0 + i * across], dwp[i]);
+        keep(&block_sums[threadIdx.y][1][c0 + i * across], dwq[i]);
+      }
+      __syncthreads();
+      const int tid = threadIdx.x + threadIdx.y * 32;
+      for (int k = tid; k < 2 * a.hidden; k += 32 * kRowsPerCta) {
+        const int which = k >= a.hidden, c = k - which * a.hidden;
+        float v = 0.f;
+#pragma unroll
+        for (int y = 0; y < kRowsPerCta; ++y) v += block_sums[y][which][c];
+        a.partial[(int64_t)blockIdx.x * 2 * a.hidden + k] = v;
+      }
+    }
+    return;
+  }
+  float *out = a.partial + blockIdx.x * (int64_t)2 * a.hidden + c0;
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
     if (c0 + i * across < a.hidden) {
@@ -467,12 +499,12 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, true))
     }
 }
 
-// The weights' gradients from the groups' sums: dw_pre = sum of the first,
+// The weights' gradients from the blocks' sums: dw_pre = sum of the first,
 // dw_post = scale (shared gate) times the sum of the second, and for a shared
 // gate dgate = scale w_post times it.  16 x 4 interleaved partial sums per
 // column, added in a fixed order.
 template <typename B>
-__global__ void __launch_bounds__(512) norm_weight_sum_kernel(const float *partial, int64_t groups, int hidden,
+__global__ void __launch_bounds__(512) norm_weight_sum_kernel(const float *partial, int64_t blocks, int hidden,
                                                               float scale, const B *w_post, const B *shared_gate,
                                                               B *dw_pre, B *dw_post, B *dgate) {
   __shared__ float part[16][33];
@@ -481,10 +513,10 @@ __global__ void __launch_bounds__(512) norm_weight_sum_kernel(const float *parti
   const int c = blockIdx.x * 32 + threadIdx.x;
   float v[4] = {};
   if (c < hidden)
-    for (int64_t g = threadIdx.y; g < groups; g += 64)
+    for (int64_t g = threadIdx.y; g < blocks; g += 64)
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (g + 16 * k < groups) v[k] += partial[((g + 16 * k) * 2 + which) * hidden + c];
+        if (g + 16 * k < blocks) v[k] += partial[((g + 16 * k) * 2 + which) * hidden + c];
   part[threadIdx.y][threadIdx.x] = (v[0] + v[1]) + (v[2] + v[3]);
   __syncthreads();
   if (threadIdx.y != 0 || c >= hidden) return;
@@ -589,7 +621,7 @@ int launch_bwd(const BwdArgs &a, bool vec, void *dw_pre, void *dw_post, void *dg
   if (st != MUON_OK || !a.partial) return st;
   trace_before(kTraceNormWeightSum, s);
   norm_weight_sum_kernel<B><<<dim3((unsigned)((a.hidden + 31) / 32), 2), dim3(32, 16), 0, s>>>(
-      a.partial, groups_of(p, a.rows, true), a.hidden, a.scale, static_cast<const B *>(a.w_post),
+      a.partial, groups_of(p, a.rows, true) / p.rows_per_cta, a.hidden, a.scale, static_cast<const B *>(a.w_post),
       static_cast<const B *>(a.shared_gate), static_cast<B *>(dw_pre), static_cast<B *>(dw_post),
       static_cast<B *>(dgate));
   return trace_after(kTraceNormWeightSum, s);
