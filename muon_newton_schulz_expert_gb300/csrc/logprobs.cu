@@ -16,8 +16,8 @@
 //
 // Top alternatives: the pass also keeps each thread's maximum.  The top-th
 // largest of a block's thread maxima bounds its top-th largest element from
-// below, so a second pass over the slice (from L2) collects the few elements
-// at or above that bound, which are sorted.  Where more than kCandidates reach
+// below, so the vectors of the few threads that reach that bound are read again
+// (from L2) for the elements at or above it, which are sorted.  Where more than kCandidates reach
 // it (ties), warps keep sorted lists of 32 keys instead, one per lane.  A key
 // holds the value's order and the complemented index, so equal values keep the
 // lowest index first, and NaN counts as the largest.
@@ -30,9 +30,13 @@
 namespace muon {
 namespace {
 
-// Threads of a block: 512, or 128 where a row gives each of them 8 vectors or
-// fewer (10218 rows of 1403 fp32 logits with top = 1: 181 us with 512).
-constexpr int kThreads = 512, kFewThreads = 128;
+// Threads of a block: as few as leave each of them 64 vectors of a row at most
+// (several rows on an SM then overlap one's reductions and sorts with another's
+// loads), 512 for long rows and for rows cut over a cluster.  Measured, us:
+//   10218 rows of 1403 fp32, top 1    512 threads 181, 128 threads 45, 64 threads 34
+//   3000 rows of 32003 fp32, top 5    512 threads 111, 128 threads 85
+//   6000 rows of 65000 bf16           512 threads 152, 128 threads 127
+constexpr int kThreads = 512, kMidThreads = 128, kFewThreads = 64;
 constexpr int kMaxSplit = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.402823466e38f;
@@ -343,6 +347,7 @@ __global__ void __launch_bounds__(THREADS) token_logprobs_kernel(const __grid_co
     add_any(acc, f);
     mine.top = fmaxf(mine.top, f[0]);
   }
+  const bool odd = !(acc.s == acc.s);   // this thread met a NaN or +inf
   // the block's sums
 #pragma unroll
   for (int o = 16; o; o >>= 1)
@@ -367,26 +372,29 @@ __global__ void __launch_bounds__(THREADS) token_logprobs_kernel(const __grid_co
     const uint64_t bound = lists[0][a.top - 1];
     const float least = key_value(bound);
     if (bound) {
-      for (int v = v0 + threadIdx.x; v < v1; v += THREADS * U) {
-        uint4 raw[U];
+      // Only a thread whose maximum reaches the bound (or that met a NaN) has
+      // candidates.  Its vectors are read again: by itself where they are few,
+      // else by its warp, 32 at a time.
+      auto candidates = [&](int v) {
+        float f[N];
+        unpack<T>(__ldg(xv + v), f);
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-          if (v + i * THREADS < v1) raw[i] = __ldg(xv + v + i * THREADS);
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          if (v + i * THREADS >= v1) break;
-          float f[N];
-          unpack<T>(raw[i], f);
-          bool some = false;
-#pragma unroll
-          for (int j = 0; j < N; ++j) some |= !(f[j] < least);
-          if (some)
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-              if (!(f[j] < least)) {
-                const int at = atomicAdd(&count, 1);
-                if (at < kCandidates) found[at] = top_key(f[j], (uint32_t)(head + (v + i * THREADS) * N + j));
-              }
+        for (int j = 0; j < N; ++j)
+          if (!(f[j] < least)) {
+            const int at = atomicAdd(&count, 1);
+            if (at < kCandidates) found[at] = top_key(f[j], (uint32_t)(head + v * N + j));
+          }
+      };
+      const bool reaches = any && (!(mine.top < least) || odd);
+      if (v1 - v0 <= 4 * THREADS) {
+        if (reaches)
+          for (int v = v0 + threadIdx.x; v < v1; v += THREADS) candidates(v);
+      } else {
+        uint32_t who = __ballot_sync(0xffffffffu, reaches);
+        while (who && *reinterpret_cast<volatile int *>(&count) <= kCandidates) {
+          const int owner = warp * 32 + __ffs(who) - 1;
+          who &= who - 1;
+          for (int v = v0 + owner + lane * THREADS; v < v1; v += 32 * THREADS) candidates(v);
         }
       }
       if ((int)threadIdx.x < ends) {
@@ -496,6 +504,7 @@ struct Slope {
 template <typename T>
 __global__ void __launch_bounds__(256) token_logprobs_backward_kernel(const __grid_constant__ BwdArgs a) {
   constexpr int N = kVec<T>;
+  const int threads = blockDim.x;
   const int64_t row = blockIdx.y;
   const T *x = static_cast<const T *>(a.logits) + row * a.stride;
   T *out = static_cast<T *>(a.dlogits) + row * a.out_stride;
@@ -519,14 +528,14 @@ __global__ void __launch_bounds__(256) token_logprobs_backward_kernel(const __gr
   const uint4 *xv = reinterpret_cast<const uint4 *>(x + v0);
   uint4 *ov = reinterpret_cast<uint4 *>(out + v0);
   constexpr int U = 4;
-  for (int v = threadIdx.x; v < vecs; v += 256 * U) {
+  for (int v = threadIdx.x; v < vecs; v += threads * U) {
     uint4 raw[U];
 #pragma unroll
     for (int i = 0; i < U; ++i)
-      if (v + i * 256 < vecs) raw[i] = __ldcs(xv + v + i * 256);
+      if (v + i * threads < vecs) raw[i] = __ldcs(xv + v + i * threads);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int k = v + i * 256;
+      const int k = v + i * threads;
       if (k >= vecs) break;
       float e[N];
       unpack<T>(raw[i], e);
@@ -554,7 +563,7 @@ __global__ void __launch_bounds__(256) token_logprobs_backward_kernel(const __gr
   }
   // the elements before the first boundary and after the last vector
   const int rest = head + (c1 - tail0);
-  for (int i = threadIdx.x; i < rest; i += 256) {
+  for (int i = threadIdx.x; i < rest; i += threads) {
     const int k = i < head ? c0 + i : tail0 + (i - head);
     const float v = none ? 0.f : f(to_f(x[k])) + (k == token ? f.dlogp : 0.f);
     from_f(out + k, v);
@@ -567,9 +576,11 @@ int launch_fwd(const FwdArgs &a, int64_t rows, cudaStream_t s) {
   // elements each.
   int split = 1;
   while (split < kMaxSplit && rows * split < 2 * num_sms() && a.vocab >= 2 * split * 8192) split *= 2;
-  const bool few = split == 1 && a.vocab <= 8 * kVec<T> * kFewThreads;
+  const int vecs = a.vocab / kVec<T>;
+  const int threads = split > 1 ? kThreads : vecs <= 16 * kFewThreads ? kFewThreads
+                                         : vecs <= 64 * kMidThreads ? kMidThreads : kThreads;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(few ? kFewThreads : kThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.gridDim = dim3((unsigned)(rows * split));
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -580,8 +591,10 @@ int launch_fwd(const FwdArgs &a, int64_t rows, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = split > 1 ? 1 : 0;
   trace_before(kTraceLogprobs, s);
-  const cudaError_t e = few ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, TOP, kFewThreads>, a, split)
-                            : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, TOP, kThreads>, a, split);
+  const cudaError_t e =
+      threads == kFewThreads   ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, TOP, kFewThreads>, a, split)
+      : threads == kMidThreads ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, TOP, kMidThreads>, a, split)
+                               : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, TOP, kThreads>, a, split);
   const int st = trace_after(kTraceLogprobs, s);
   return e == cudaSuccess ? st : MUON_ERR_CUDA;
 }
@@ -652,6 +665,9 @@ int muon_token_logprobs_backward(const void *logits, int64_t stride, const int64
   if (!a.err) return MUON_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const unsigned chunks = (unsigned)((vocab + a.chunk - 1) / a.chunk);
+  // 4 vectors a thread, so that short rows do not leave most of a block idle
+  const int64_t vecs = std::min<int64_t>(vocab, a.chunk) * (int64_t)es / 16;
+  const unsigned threads = (unsigned)std::clamp<int64_t>((vecs / 4 + 31) / 32 * 32, 64, 256);
   // grid.y holds at most 65535 rows
   for (int64_t r = 0; r < rows; r += 65535) {
     BwdArgs b = a;
@@ -664,8 +680,8 @@ int muon_token_logprobs_backward(const void *logits, int64_t stride, const int64
     b.dentropy = dentropy ? dentropy + r : nullptr;
     const dim3 grid(chunks, (unsigned)std::min<int64_t>(65535, rows - r));
     trace_before(kTraceLogprobsBwd, s);
-    if (type == MUON_BF16) token_logprobs_backward_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(b);
-    else token_logprobs_backward_kernel<float><<<grid, 256, 0, s>>>(b);
+    if (type == MUON_BF16) token_logprobs_backward_kernel<__nv_bfloat16><<<grid, threads, 0, s>>>(b);
+    else token_logprobs_backward_kernel<float><<<grid, threads, 0, s>>>(b);
     const int st = trace_after(kTraceLogprobsBwd, s);
     if (st != MUON_OK) return st;
   }
