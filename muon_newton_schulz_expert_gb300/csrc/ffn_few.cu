@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
       }
     } else if (warp == 1) {
       if (lane == 0 && ok) {
-        const uint32_t idesc = make_idesc(BM, n_rows, A_MN, false, kBF16);
+        const uint32_t idesc = make_idesc(BM, n_rows, A_MN, false);
         ok = wait_bounded(acce(acc), acc_phase ^ 1u, w);
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
@@ -440,10 +440,10 @@ int launch(Args &p, const FfnShape &f, int trace_kind, cudaStream_t s) {
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 int map_weights(CUtensorMap *m, const void *base, const FfnShape &f, int64_t rows, int64_t cols, bool mn) {
-  return make_map(m, base, kBF16, f.experts, rows, cols, mn ? 64 : 128, 64);
+  return make_map(m, base, f.experts, rows, cols, mn ? 64 : 128);
 }
 int map_rows(CUtensorMap *m, const void *base, const FfnShape &f, int64_t cols, int64_t ld) {
-  return make_map(m, base, kBF16, 1, f.rows, cols, row_tile(f), 64, CU_TENSOR_MAP_SWIZZLE_128B, ld);
+  return make_map(m, base, 1, f.rows, cols, row_tile(f), ld);
 }
 
 Args base_args(const FfnShape &f, int64_t M, int64_t K) {

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (CTA 0 of the pair)
     if (rank == 0) {
-      constexpr uint32_t idesc = make_idesc(CM, BN, Form<MODE>::a_mn, Form<MODE>::b_mn, kBF16);
+      constexpr uint32_t idesc = make_idesc(CM, BN, Form<MODE>::a_mn, Form<MODE>::b_mn);
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -563,13 +563,13 @@ int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // operand maps: K-major rows (boxes of 128 rows x 64 columns), MN-major (64 x 64)
 int map_k(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols, int64_t ld = 0) {
-  return make_map(m, base, kBF16, batch, rows, cols, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B, ld);
+  return make_map(m, base, batch, rows, cols, 128, ld);
 }
 int map_mn(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols, int64_t ld = 0) {
-  return make_map(m, base, kBF16, batch, rows, cols, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, ld);
+  return make_map(m, base, batch, rows, cols, 64, ld);
 }
 int map_out(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols, int64_t ld = 0) {
-  return make_map(m, base, kBF16, batch, rows, cols, 32, 64, CU_TENSOR_MAP_SWIZZLE_128B, ld);
+  return make_map(m, base, batch, rows, cols, 32, ld);
 }
 
 Args base_args(const FfnShape &f) {

@@ -211,7 +211,8 @@ __device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t adesc, uint64_t
       : "memory");
 }
 
-// 32 lanes x 32 consecutive fp32 columns -> 32 registers per thread, waited.
+// 32 lanes x 16 or 32 consecutive fp32 columns -> as many registers per thread
+// (the first 16 of r), waited.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -252,11 +253,11 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
 }
 
 // Instruction descriptor of kind::f16: fp32 D (bit 4), A and B both bf16
-// (format 1 at bits 7 and 10) or both fp16 (format 0), each operand K-major
-// or MN-major (bits 15 and 16), N >> 3 at bit 17, M >> 4 at bit 24.
-__host__ __device__ constexpr uint32_t make_idesc(int m, int n, bool a_mn_major, bool b_mn_major, int tin) {
-  return (1u << 4) | (tin == kBF16 ? (1u << 7) | (1u << 10) : 0u) | ((a_mn_major ? 1u : 0u) << 15) |
-         ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+// (format 1 at bits 7 and 10), each operand K-major or MN-major (bits 15 and
+// 16), N >> 3 at bit 17, M >> 4 at bit 24.
+__host__ __device__ constexpr uint32_t make_idesc(int m, int n, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // Bounded wait used on the way out after an abort: waits for the phase of
@@ -287,24 +288,21 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 3-D map over a [batch][rows][cols] stack of elements of format `fmt`
-// (16-bit, or the 8-bit low half), rows `pitch` elements apart (0: dense);
-// box = box_cols columns x box_rows rows x 1 matrix.
-int make_map(CUtensorMap *map, const void *base, int fmt, int64_t batch, int64_t rows, int64_t cols, int box_rows,
-             int box_cols = 64, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B, int64_t pitch = 0) {
+// 3-D map over a [batch][rows][cols] stack of bf16, rows `pitch` elements apart
+// (0: dense); box = box_cols columns x box_rows rows x 1 matrix, whose rows are
+// the 128 bytes that the swizzle spans.
+int make_map(CUtensorMap *map, const void *base, int64_t batch, int64_t rows, int64_t cols, int box_rows,
+             int64_t pitch = 0) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return MUON_ERR_CUDA;
-  const cuuint64_t es = fmt == kE5M2 ? 1 : 2;   // element bytes
   const cuuint64_t ld = (cuuint64_t)(pitch > 0 ? pitch : cols);
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
-  cuuint64_t strides[2] = {ld * es, (cuuint64_t)rows * ld * es};
-  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1u};
+  cuuint64_t strides[2] = {ld * 2, (cuuint64_t)rows * ld * 2};
+  cuuint32_t box[3] = {64u, (cuuint32_t)box_rows, 1u};
   cuuint32_t estr[3] = {1u, 1u, 1u};
-  const CUtensorMapDataType dt = fmt == kE5M2 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                 : fmt == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                               : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  CUresult r = enc(map, dt, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? MUON_OK : MUON_ERR_CUDA;
 }
 

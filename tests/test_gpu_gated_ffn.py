@@ -271,6 +271,47 @@ def test_repeated_calls_give_the_same_bits_on_other_streams_and_workspaces(mk):
             assert torch.equal(got[k], ref[k]), k
 
 
+@pytest.mark.parametrize("sizes,H,F", [([3], 136, 40), ([300, 0, 70], 264, 136)])
+def test_captured_in_a_graph(mk, sizes, H, F):
+    """Captured once, replayed on new inputs and new group sizes (the sizes are read on the device)."""
+    d = inputs(sizes, H, F, seed=12)
+    T, E = d["x"].shape[0], len(sizes)
+    ws = torch.empty(mk.muon_gated_ffn_backward_workspace_bytes(T, E, H, F), dtype=torch.uint8, device="cuda")
+    kept = {k: d[k].clone() for k in ("x", "off", "dy", "gate", "up")}
+    step = {**d, **kept}
+    forward(mk, step, "silu", workspace=ws), backward(mk, step, "silu", workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        f = forward(mk, step, "silu", workspace=ws)
+        b = backward(mk, step, "silu", workspace=ws)
+    new = inputs(sizes[::-1], H, F, seed=13)
+    for k, v in kept.items():
+        v.copy_(new[k])
+    graph.replay()
+    mixed = {**new, "w1": d["w1"], "w3": d["w3"], "w2": d["w2"]}
+    for got, ref in ((f, forward(mk, mixed, "silu")), (b, backward(mk, mixed, "silu"))):
+        for k in ref:
+            assert torch.equal(got[k], ref[k]), k
+    assert mk.muon_get_device_status() == 0
+
+
+def test_rows_past_32_bit_offsets(mk):
+    """rows * ffn past 2^31 elements: the last rows against 64 bits."""
+    T, H, F = 270_000, 64, 8192
+    d = inputs([T], H, F, seed=14)
+    f = forward(mk, d, "silu")
+    tail = {**d, "sizes": [200], **{k: d[k][-200:] for k in ("x", "dy", "gate", "up")}}
+    ref = forward64(tail, "silu")
+    for k in f:
+        check(f[k][-200:], ref[k], k)
+    del f
+    b = backward(mk, d, "silu")
+    check(b["dx"][-200:], backward64(tail, "silu")["dx"], "dx")
+    assert all(bool(b[k].isfinite().all()) for k in b)
+    assert mk.muon_get_device_status() == 0
+
+
 def test_what_is_not_needed_is_left_out(mk):
     d = inputs([30, 35], 136, 72, seed=10)
     ref = backward(mk, d, "silu")
