@@ -2,8 +2,10 @@
 
 Argument marshalling only: every step runs in the CUDA kernels of
 ``_lib/libmuon.so`` (C ABI declared in ``include/muon.h``).  PyTorch supplies
-device memory and the current stream.  There is no fallback: when the library
-has not been built, every call raises ``MuonLibraryMissing``.
+device memory and the current stream.  The operators around the step, whose
+calls last a few microseconds, are marshalled by ``_lib/muon_ops.so``
+(csrc/binding.cpp).  There is no fallback: when the library has not been built,
+every call raises ``MuonLibraryMissing``.
 
 Method: "Training a 1T-Parameter MoE on EU public infrastructure with PyTorch
 and TorchTitan", section "FlexShard: Muon without communication" -- one fp32
@@ -15,14 +17,16 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import importlib.util
 import os
-import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # MUON_CHECKED=1 loads the checked build (device-side checks of the kernels'
 # TMA coordinates, reported as MUON_ERR_DEVICE), for example to run the tests on it
 CHECKED = os.environ.get("MUON_CHECKED") == "1"
 LIB_PATH = os.path.join(_PKG, "_lib", "libmuon_checked.so" if CHECKED else "libmuon.so")
+
+OPS_PATH = os.path.join(_PKG, "_lib", "muon_ops.so")
 
 QUINTIC = (3.4445, -4.7750, 2.0315)
 
@@ -429,53 +433,23 @@ BlockNormGrads = collections.namedtuple("BlockNormGrads", "dresidual dblock dw_p
 TokenLogprobs = collections.namedtuple("TokenLogprobs", "logp entropy lse top_ids top_logp")
 
 
-# The binding's own time counts in calls of a few microseconds: argument structs are packed in one go, and the
-# checks look at each tensor once.
-_NORM_ARGS = struct.Struct("@qqii" "Pq" "Pq" "PPqP" "ff" "Pq" "Pq" "PP")        # muon_block_norm_args
-_NORM_BACKWARD_ARGS = struct.Struct("@qqii" "PqPqPqPq" "PPqP" "PP" "f" "PqPq" "PPqP")   # muon_block_norm_backward_args
+_ops_module = None
 
 
-def _rows(t, dtype, shape, name):
-    """Checks a CUDA tensor of `shape` whose last axis is dense; returns its row stride."""
-    _dense(t, dtype, shape, name, True)
-    if t.is_contiguous():
-        return shape[-1]
-    stride = t.stride()
-    if len(stride) != 2 or (stride[1] != 1 and shape[1] > 1) or (stride[0] < shape[1] and shape[0] > 1):
-        raise ValueError(f"{name} must be dense along its last axis, with rows that do not overlap")
-    return max(stride[0], shape[1])   # the stride of a single row says nothing
-
-
-def _dense(t, dtype, shape, name, any_stride=False):
-    try:
-        if t.is_cuda and t.dtype is dtype and t.shape == shape and (any_stride or t.is_contiguous()):
-            return
-    except AttributeError:
-        pass
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _one_device(first, *others):
-    index = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != index:
-            raise ValueError("all tensors must be on one device")
-
-
-def _new(rows, cols, like):
-    import torch
-    return torch.empty((rows, cols), dtype=like.dtype, device=like.device)
-
-
-def _opt(t):
-    return None if t is None else t.data_ptr()
+def _ops():
+    """The compiled binding of these operators, on the loaded library; raises if it was never built."""
+    global _ops_module
+    if _ops_module is None:
+        handle = lib()
+        if not os.path.exists(OPS_PATH):
+            raise MuonLibraryMissing(f"{OPS_PATH} is missing: build it with muon_newton_schulz_expert_gb300.build.build()")
+        import torch  # noqa: F401  (its libraries first)
+        spec = importlib.util.spec_from_file_location("muon_ops", OPS_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind({n: ctypes.cast(getattr(handle, n), _P).value for n in SIGNATURES})
+        _ops_module = module
+    return _ops_module
 
 
 def _raw_stream(stream):
@@ -486,40 +460,18 @@ def _raw_stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _workspace(workspace):
-    if workspace is None:
-        return None, 0
-    import torch
-    _need(workspace, torch.uint8, "workspace")
-    return workspace.data_ptr(), workspace.numel()
+def _outputs(call, result):
+    """What the binding returned, or an error where it is a status."""
+    if type(result) is int:
+        raise MuonError(call, result)
+    return result
 
 
-def _ffn_shapes(x, w1, w3, w2, offsets, act):
-    """(row stride of x, rows, experts, hidden, ffn, activation), after the checks that both directions share."""
-    import torch
+def _activation(act):
     code = ACTIVATIONS.get(act)
     if code is None:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}")
-    shape = w1.shape
-    if len(shape) == 3:
-        E, H, F = shape
-        w2_shape = (E, F, H)
-    elif len(shape) == 2:
-        E, (H, F) = 1, shape
-        w2_shape = (F, H)
-    else:
-        raise ValueError("w1 must be (experts, hidden, ffn) or (hidden, ffn)")
-    bf = torch.bfloat16
-    T = x.shape[0]
-    ldx = _rows(x, bf, (T, H), "x")
-    _dense(w1, bf, shape, "w1")
-    _dense(w3, bf, shape, "w3")
-    _dense(w2, bf, w2_shape, "w2")
-    if offsets is not None:
-        _dense(offsets, torch.int64, (E + 1,), "offsets")
-    elif E != 1:
-        raise ValueError("offsets are needed with more than one expert")
-    return ldx, T, E, H, F, code
+    return code
 
 
 def muon_gated_ffn_workspace_bytes(rows, experts, hidden, ffn):
@@ -535,22 +487,8 @@ def muon_gated_ffn(x, w1, w3, w2, offsets=None, *, act="silu", keep=False, out=N
     expert and the end (None: one expert with all rows).  Returns y, or with
     ``keep`` (y, gate, up) for the backward pass.
     """
-    ldx, T, E, H, F, code = _ffn_shapes(x, w1, w3, w2, offsets, act)
-    gate = up = gate_ptr = up_ptr = None
-    if keep:
-        gate, up = _new(T, F, x), _new(T, F, x)
-        gate_ptr, up_ptr = gate.data_ptr(), up.data_ptr()
-    ldy = H
-    if out is None:
-        out = _new(T, H, x)
-    else:
-        ldy = _rows(out, x.dtype, (T, H), "out")
-    ws, ws_bytes = _workspace(workspace)
-    _one_device(x, w1, w3, w2, offsets, out, workspace)
-    _check("muon_gated_ffn", lib().muon_gated_ffn(
-        x.data_ptr(), ldx, w1.data_ptr(), w3.data_ptr(), w2.data_ptr(), _opt(offsets), T, E, H, F, code,
-        out.data_ptr(), ldy, gate_ptr, up_ptr, ws, ws_bytes, _raw_stream(stream)))
-    return (out, gate, up) if keep else out
+    return _outputs("muon_gated_ffn", _ops().gated_ffn(
+        x, w1, w3, w2, offsets, _activation(act), keep, out, workspace, _raw_stream(stream)))
 
 
 def muon_gated_ffn_backward_workspace_bytes(rows, experts, hidden, ffn):
@@ -564,50 +502,9 @@ def muon_gated_ffn_backward(dy, x, gate, up, w1, w3, w2, offsets=None, *, act="s
     gate and up are what the forward call kept.  dx and dw = (dw1, dw3, dw2)
     are written (and overwritten) when given; what is not needed is None.
     """
-    ldx, T, E, H, F, code = _ffn_shapes(x, w1, w3, w2, offsets, act)
-    bf = x.dtype
-    lddy = _rows(dy, bf, (T, H), "dy")
-    _dense(gate, bf, (T, F), "gate")
-    _dense(up, bf, (T, F), "up")
-    lddx, dw1, dw3, dw2 = H, None, None, None
-    if not need_dx:
-        dx = None
-    elif dx is None:
-        dx = _new(T, H, x)
-    else:
-        lddx = _rows(dx, bf, (T, H), "dx")
-    if need_dw:
-        if dw is None:
-            dw1, dw3, dw2 = (w.new_empty(w.shape) for w in (w1, w3, w2))
-        else:
-            dw1, dw3, dw2 = dw
-            _dense(dw1, bf, w1.shape, "dw1")
-            _dense(dw3, bf, w3.shape, "dw3")
-            _dense(dw2, bf, w2.shape, "dw2")
-    ws, ws_bytes = _workspace(workspace)
-    _one_device(x, w1, w3, w2, offsets, dy, gate, up, dx, dw1, dw3, dw2, workspace)
-    _check("muon_gated_ffn_backward", lib().muon_gated_ffn_backward(
-        dy.data_ptr(), lddy, x.data_ptr(), ldx, gate.data_ptr(), up.data_ptr(), w1.data_ptr(), w3.data_ptr(),
-        w2.data_ptr(), _opt(offsets), T, E, H, F, code, _opt(dx), lddx, _opt(dw1), _opt(dw3), _opt(dw2), ws, ws_bytes,
+    return _outputs("muon_gated_ffn_backward", _ops().gated_ffn_backward(
+        dy, x, gate, up, w1, w3, w2, offsets, _activation(act), dx, dw, need_dx, need_dw, workspace,
         _raw_stream(stream)))
-    return dx, dw1, dw3, dw2
-
-
-def _dtype_code(t, name):
-    import torch
-    if t.dtype is torch.bfloat16:
-        return 0
-    if t.dtype is torch.float32:
-        return 1
-    raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-
-
-def _gate(gate, dtype, T, H):
-    """A gate's row stride: 0 for one gate for all rows."""
-    if gate.dim() == 1:
-        _dense(gate, dtype, (H,), "gate")
-        return 0
-    return _rows(gate, dtype, (T, H), "gate")
 
 
 def muon_block_norm(residual, block=None, *, w_post=None, gate=None, w_pre=None, scale=1.0, eps=1e-6, norm_next=True,
@@ -620,54 +517,8 @@ def muon_block_norm(residual, block=None, *, w_post=None, gate=None, w_pre=None,
     r' is residual itself; without norm_next there is no y.  Returns
     (r', y, rstd_post, rstd_pre), None in the place of what there is not.
     """
-    import torch
-    if residual.dim() != 2:
-        raise ValueError("residual must be (rows, hidden)")
-    T, H = shape = residual.shape
-    rt = residual.dtype
-    branch = (block if block is not None else w_pre if w_pre is not None else
-              normed if normed is not None else residual)
-    bt = branch.dtype
-    rcode, bcode = _dtype_code(residual, "residual"), _dtype_code(branch, "block")
-    ldr = _rows(residual, rt, shape, "residual")
-    ldb = ldg = ldo = 0
-    rstd_post = rstd_pre = None
-    if block is None:
-        if w_post is not None or gate is not None or out is not None:
-            raise ValueError("w_post, gate and out belong to a block")
-        if not norm_next:
-            raise ValueError("there is nothing to compute without a block and without norm_next")
-    else:
-        ldb = _rows(block, bt, shape, "block")
-        if w_post is not None:
-            _dense(w_post, bt, (H,), "w_post")
-        if gate is not None:
-            ldg = _gate(gate, bt, T, H)
-        if out is None:
-            out, ldo = _new(T, H, residual), H
-        else:
-            ldo = _rows(out, rt, shape, "out")
-    if norm_next:
-        if w_pre is not None:
-            _dense(w_pre, bt, (H,), "w_pre")
-        if normed is None:
-            normed, ldn = _new(T, H, branch), H
-        else:
-            ldn = _rows(normed, bt, shape, "normed")
-    else:
-        if w_pre is not None or normed is not None:
-            raise ValueError("w_pre and normed belong to the norm before the next block")
-        ldn = 0
-    if block is not None:
-        rstd_post = torch.empty((T,), dtype=torch.float32, device=residual.device)
-    if norm_next:
-        rstd_pre = torch.empty((T,), dtype=torch.float32, device=residual.device)
-    _one_device(residual, block, w_post, gate, w_pre, out, normed)
-    _check("muon_block_norm", lib().muon_block_norm(_NORM_ARGS.pack(
-        T, H, rcode, bcode, residual.data_ptr(), ldr, *((0, 0) if block is None else (block.data_ptr(), ldb)),
-        _opt(w_post) or 0, _opt(gate) or 0, ldg, _opt(w_pre) or 0, scale, eps, _opt(out) or 0, ldo, _opt(normed) or 0,
-        ldn, _opt(rstd_post) or 0, _opt(rstd_pre) or 0), _raw_stream(stream)))
-    return residual if block is None else out, normed, rstd_post, rstd_pre
+    return _outputs("muon_block_norm", _ops().block_norm(
+        residual, block, w_post, gate, w_pre, scale, eps, norm_next, out, normed, _raw_stream(stream)))
 
 
 def muon_block_norm_backward_workspace_bytes(rows, hidden):
@@ -683,55 +534,9 @@ def muon_block_norm_backward(dresidual, dnormed, residual, block=None, rstd_post
     returned, the rest what it took and returned.  A gradient is None where
     the forward call had no such input.
     """
-    if residual.dim() != 2:
-        raise ValueError("residual must be (rows, hidden)")
-    T, H = shape = residual.shape
-    rt = residual.dtype
-    branch = dnormed if dnormed is not None else block if block is not None else residual
-    bt = branch.dtype
-    rcode, bcode = _dtype_code(residual, "residual"), _dtype_code(branch, "block")
-    if dresidual is None and dnormed is None:
-        raise ValueError("dresidual or dnormed must be given")
-    import torch
-    f32 = torch.float32
-    ldr = _rows(residual, rt, shape, "residual")
-    ldd = ldn = ldb = ldg = 0
-    dblock = dw_post = dgate = dw_pre = None
-    if dresidual is not None:
-        ldd = _rows(dresidual, rt, shape, "dresidual")
-    if dnormed is not None:
-        ldn = _rows(dnormed, bt, shape, "dnormed")
-        _dense(rstd_pre, f32, (T,), "rstd_pre")
-        if w_pre is not None:
-            _dense(w_pre, bt, (H,), "w_pre")
-            dw_pre = torch.empty_like(w_pre)
-    else:
-        if w_pre is not None:
-            raise ValueError("w_pre belongs to the norm before the next block")
-        rstd_pre = None
-    if block is not None:
-        ldb = _rows(block, bt, shape, "block")
-        _dense(rstd_post, f32, (T,), "rstd_post")
-        dblock = _new(T, H, block)
-        if w_post is not None:
-            _dense(w_post, bt, (H,), "w_post")
-            dw_post = torch.empty_like(w_post)
-        if gate is not None:
-            ldg = _gate(gate, bt, T, H)
-            dgate = torch.empty(gate.shape, dtype=bt, device=gate.device)
-    else:
-        if w_post is not None or gate is not None:
-            raise ValueError("w_post and gate belong to a block")
-        rstd_post = None
-    dr = _new(T, H, residual)
-    ws, ws_bytes = _workspace(workspace)
-    _one_device(residual, dresidual, dnormed, block, rstd_post, rstd_pre, w_post, gate, w_pre, workspace)
-    _check("muon_block_norm_backward", lib().muon_block_norm_backward(_NORM_BACKWARD_ARGS.pack(
-        T, H, rcode, bcode, _opt(dresidual) or 0, ldd, _opt(dnormed) or 0, ldn, residual.data_ptr(), ldr,
-        _opt(block) or 0, ldb, _opt(w_post) or 0, _opt(gate) or 0, ldg, _opt(w_pre) or 0, _opt(rstd_post) or 0,
-        _opt(rstd_pre) or 0, scale, dr.data_ptr(), H, _opt(dblock) or 0, H, _opt(dw_post) or 0, _opt(dgate) or 0, H,
-        _opt(dw_pre) or 0), ws, ws_bytes, _raw_stream(stream)))
-    return BlockNormGrads(dr, dblock, dw_post, dgate, dw_pre)
+    return BlockNormGrads(*_outputs("muon_block_norm_backward", _ops().block_norm_backward(
+        dresidual, dnormed, residual, block, rstd_post, rstd_pre, w_post, gate, w_pre, scale, workspace,
+        _raw_stream(stream))))
 
 
 def muon_token_logprobs(logits, tokens=None, *, top=0, stream=None):
@@ -740,26 +545,8 @@ def muon_token_logprobs(logits, tokens=None, *, top=0, stream=None):
     Returns TokenLogprobs(logp, entropy, lse, top_ids, top_logp), fp32 but the
     int64 ids; logp is None without tokens, the last two without ``top``.
     """
-    import torch
-    if logits.dim() != 2:
-        raise ValueError("logits must be (rows, vocab)")
-    code = _dtype_code(logits, "logits")
-    T, V = logits.shape
-    stride = _rows(logits, logits.dtype, logits.shape, "logits")
-    logp = top_ids = top_logp = None
-    if tokens is not None:
-        _dense(tokens, torch.int64, (T,), "tokens")
-    out = torch.empty((3, T), dtype=torch.float32, device=logits.device)
-    lse, entropy, logp = out.unbind()
-    at = out.data_ptr()
-    if top:
-        top_ids = torch.empty((T, max(0, top)), dtype=torch.int64, device=logits.device)
-        top_logp = torch.empty((T, max(0, top)), dtype=torch.float32, device=logits.device)
-    _one_device(logits, tokens)
-    _check("muon_token_logprobs", lib().muon_token_logprobs(
-        logits.data_ptr(), stride, _opt(tokens), T, V, code, None if tokens is None else at + 8 * T, at + 4 * T, at,
-        top, _opt(top_ids), _opt(top_logp), _raw_stream(stream)))
-    return TokenLogprobs(None if tokens is None else logp, entropy, lse, top_ids, top_logp)
+    return TokenLogprobs(*_outputs("muon_token_logprobs", _ops().token_logprobs(
+        logits, tokens, top, _raw_stream(stream))))
 
 
 def muon_token_logprobs_backward(logits, tokens, lse, entropy=None, dlogp=None, dentropy=None, *, out=None,
@@ -768,30 +555,8 @@ def muon_token_logprobs_backward(logits, tokens, lse, entropy=None, dlogp=None, 
 
     lse and entropy are the forward call's; ``out`` may be the logits themselves.
     """
-    import torch
-    if logits.dim() != 2:
-        raise ValueError("logits must be (rows, vocab)")
-    code = _dtype_code(logits, "logits")
-    T, V = logits.shape
-    stride = _rows(logits, logits.dtype, logits.shape, "logits")
-    if tokens is not None:
-        _dense(tokens, torch.int64, (T,), "tokens")
-    elif dlogp is not None:
-        raise ValueError("dlogp needs tokens")
-    if dentropy is not None and entropy is None:
-        raise ValueError("dentropy needs entropy")
-    for t, n in ((lse, "lse"), (entropy, "entropy"), (dlogp, "dlogp"), (dentropy, "dentropy")):
-        if t is not None or n == "lse":
-            _dense(t, torch.float32, (T,), n)
-    if out is None:
-        out, out_stride = _new(T, V, logits), V
-    else:
-        out_stride = _rows(out, logits.dtype, (T, V), "out")
-    _one_device(logits, tokens, lse, entropy, dlogp, dentropy, out)
-    _check("muon_token_logprobs_backward", lib().muon_token_logprobs_backward(
-        logits.data_ptr(), stride, _opt(tokens), lse.data_ptr(), _opt(entropy), _opt(dlogp), _opt(dentropy), T, V,
-        code, out.data_ptr(), out_stride, _raw_stream(stream)))
-    return out
+    return _outputs("muon_token_logprobs_backward", _ops().token_logprobs_backward(
+        logits, tokens, lse, entropy, dlogp, dentropy, out, _raw_stream(stream)))
 
 
 def muon_default_scale(rows, cols):

@@ -5,8 +5,10 @@ linked into ``_lib/libmuon.so`` next to this file with the CUDA runtime linked
 statically.  ``build(checked=True)`` makes ``_lib/libmuon_checked.so`` from the
 same sources with ``-DMUON_DEVICE_CHECKS``: the kernels then test, before each
 access that would fault if it broke, the invariants they rely on, and report a
-broken one as MUON_ERR_DEVICE instead of making the access.  A rebuild is
-skipped when the library is newer than every source and header.
+broken one as MUON_ERR_DEVICE instead of making the access.  ``_lib/muon_ops.so``
+is the binding of the operators around the step (csrc/binding.cpp, against the
+installed torch).  A rebuild is skipped when the library is newer than every
+source and header.
 """
 
 from __future__ import annotations
@@ -16,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,6 +27,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libmuon.so")
 LIB_CHECKED = os.path.join(OUT_DIR, "libmuon_checked.so")
+BINDING = os.path.join(OUT_DIR, "muon_ops.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = ["api.cu", "elementwise.cu", "gemm_tc.cu", "gemm_f32.cu", "ns_static.cu", "host_stream.cu",
            "ffn.cu", "ffn_tc.cu", "ffn_few.cu", "norm.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -53,9 +58,31 @@ def up_to_date(checked: bool = False) -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def build_binding(force: bool = False) -> str:
+    """Build muon_ops.so if needed and return its path."""
+    inputs = [BINDING_SOURCE, os.path.join(INCLUDE, "muon.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in inputs):
+        return BINDING
+    import torch
+    home = os.path.dirname(torch.__file__)
+    os.makedirs(OUT_DIR, exist_ok=True)
+    tmp = f"{BINDING}.{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, "-isystem", os.path.join(home, "include"),
+           "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"), BINDING_SOURCE, "-o", tmp,
+           "-L", os.path.join(home, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
-    """Build libmuon.so (or, checked, libmuon_checked.so) if needed and return its path."""
+    """Build libmuon.so (or, checked, libmuon_checked.so) and the binding if needed; returns the library's path."""
     lib = LIB_CHECKED if checked else LIB
+    build_binding(force)
     if not force and up_to_date(checked):
         return lib
     nvcc = _nvcc()
@@ -87,7 +114,8 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
 
 
 def build_all(force: bool = False) -> list[str]:
-    """Both libraries, their translation units compiled side by side."""
+    """Both libraries, their translation units compiled side by side, and the binding."""
+    build_binding(force)
     with concurrent.futures.ThreadPoolExecutor(max_workers=2) as ex:
         return list(ex.map(lambda c: build(force=force, checked=c), (False, True)))
 

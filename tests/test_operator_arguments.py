@@ -9,11 +9,28 @@ import muon_newton_schulz_expert_gb300 as mk
 from muon_newton_schulz_expert_gb300 import build as mkbuild
 
 P = ctypes.c_void_p
-NORM = ("rows hidden residual_type branch_type residual residual_stride block block_stride w_post gate gate_stride w_pre "
-        "scale eps residual_out residual_out_stride normed normed_stride rstd_post rstd_pre").split()
-NORM_BACKWARD = ("rows hidden residual_type branch_type dresidual_out dresidual_out_stride dnormed dnormed_stride residual "
-                 "residual_stride block block_stride w_post gate gate_stride w_pre rstd_post rstd_pre scale dresidual "
-                 "dresidual_stride dblock dblock_stride dw_post dgate dgate_stride dw_pre").split()
+
+
+class NormArgs(ctypes.Structure):
+    """muon_block_norm_args"""
+    _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int64), ("residual_type", ctypes.c_int),
+                ("branch_type", ctypes.c_int), ("residual", P), ("residual_stride", ctypes.c_int64), ("block", P),
+                ("block_stride", ctypes.c_int64), ("w_post", P), ("gate", P), ("gate_stride", ctypes.c_int64),
+                ("w_pre", P), ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("residual_out", P),
+                ("residual_out_stride", ctypes.c_int64), ("normed", P), ("normed_stride", ctypes.c_int64),
+                ("rstd_post", P), ("rstd_pre", P)]
+
+
+class NormBackwardArgs(ctypes.Structure):
+    """muon_block_norm_backward_args"""
+    _fields_ = [("rows", ctypes.c_int64), ("hidden", ctypes.c_int64), ("residual_type", ctypes.c_int),
+                ("branch_type", ctypes.c_int), ("dresidual_out", P), ("dresidual_out_stride", ctypes.c_int64),
+                ("dnormed", P), ("dnormed_stride", ctypes.c_int64), ("residual", P),
+                ("residual_stride", ctypes.c_int64), ("block", P), ("block_stride", ctypes.c_int64), ("w_post", P),
+                ("gate", P), ("gate_stride", ctypes.c_int64), ("w_pre", P), ("rstd_post", P), ("rstd_pre", P),
+                ("scale", ctypes.c_float), ("dresidual", P), ("dresidual_stride", ctypes.c_int64), ("dblock", P),
+                ("dblock_stride", ctypes.c_int64), ("dw_post", P), ("dgate", P), ("dgate_stride", ctypes.c_int64),
+                ("dw_pre", P)]
 
 
 def header_fields(name):
@@ -23,15 +40,9 @@ def header_fields(name):
     return [re.sub(r".*[ *]", "", f.strip()) for d in body.split(";") for f in d.split(",") if f.strip()]
 
 
-def packed(layout, names, values):
-    return layout.pack(*[values.get(n) or 0 for n in names])
-
-
-def test_packed_structs_follow_the_header():
-    assert header_fields("muon_block_norm_args") == NORM
-    assert header_fields("muon_block_norm_backward_args") == NORM_BACKWARD
-    # native alignment, every pointer and int64 8 bytes
-    assert mk._NORM_ARGS.size == 2 * 8 + 8 + 14 * 8 + 8 and mk._NORM_BACKWARD_ARGS.size == 2 * 8 + 8 + 22 * 8 + 8
+def test_structs_follow_the_header():
+    assert header_fields("muon_block_norm_args") == [n for n, _ in NormArgs._fields_]
+    assert header_fields("muon_block_norm_backward_args") == [n for n, _ in NormBackwardArgs._fields_]
 
 
 @pytest.fixture(scope="module")
@@ -87,7 +98,7 @@ def test_block_norm(lib):
     def call(**kw):
         base = dict(rows=2, hidden=64, residual=256, residual_stride=64, block=256, block_stride=64, scale=1.0,
                     eps=1e-6, residual_out=256, residual_out_stride=64, normed=256, normed_stride=64)
-        return lib.muon_block_norm(packed(mk._NORM_ARGS, NORM, {**base, **kw}), None)
+        return lib.muon_block_norm(ctypes.byref(NormArgs(**{**base, **kw})), None)
 
     assert lib.muon_block_norm(None, None) == -1
     for bad in (dict(rows=-1), dict(hidden=0), dict(residual_type=2), dict(branch_type=-1), dict(eps=-1.0),
@@ -105,8 +116,7 @@ def test_block_norm_backward(lib):
         base = dict(rows=2, hidden=64, dresidual_out=256, dresidual_out_stride=64, dnormed=256, dnormed_stride=64,
                     residual=256, residual_stride=64, block=256, block_stride=64, rstd_post=256, rstd_pre=256,
                     scale=1.0, dresidual=256, dresidual_stride=64, dblock=256, dblock_stride=64, dw_pre=256)
-        return lib.muon_block_norm_backward(packed(mk._NORM_BACKWARD_ARGS, NORM_BACKWARD, {**base, **kw}), ws, wsb,
-                                            None)
+        return lib.muon_block_norm_backward(ctypes.byref(NormBackwardArgs(**{**base, **kw})), ws, wsb, None)
 
     assert lib.muon_block_norm_backward(None, None, 0, None) == -1
     for bad in (dict(rows=-1), dict(residual_type=7), dict(scale=float("nan")), dict(residual=None),
@@ -140,3 +150,29 @@ def test_token_logprobs(lib):
         assert back(**bad) == -1, bad
     assert back(x=P(257)) == -2
     assert back(rows=0) == 0
+
+
+def test_the_binding_refuses_what_is_no_cuda_tensor(lib):
+    import torch
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    ops = mk._ops()
+    for bad in (None, 3, "x", x):
+        with pytest.raises(TypeError, match="must be a CUDA tensor"):
+            ops.gated_ffn(bad, x, x, x, None, 0, False, None, None, 0)
+        with pytest.raises(TypeError, match="must be a CUDA tensor"):
+            ops.block_norm(bad, None, None, None, None, 1.0, 1e-6, True, None, None, 0)
+        with pytest.raises(TypeError, match="must be a CUDA tensor"):
+            ops.token_logprobs(bad, None, 0, 0)
+    for f in (ops.gated_ffn, ops.gated_ffn_backward, ops.block_norm, ops.block_norm_backward, ops.token_logprobs,
+              ops.token_logprobs_backward):
+        with pytest.raises(TypeError, match="expected"):
+            f()
+    with pytest.raises(ValueError, match="no address"):
+        ops.bind({})
+
+
+def test_missing_binding_fails_loudly(lib, monkeypatch, tmp_path):
+    monkeypatch.setattr(mk, "OPS_PATH", str(tmp_path / "nope.so"))
+    monkeypatch.setattr(mk, "_ops_module", None)
+    with pytest.raises(mk.MuonLibraryMissing):
+        mk._ops()
