@@ -64,6 +64,11 @@ cudaError_t alloc_async(void **ptr, size_t bytes, cudaStream_t s);
 // without any CUDA call: MUON_OK when the call can go ahead.
 int ns_precheck(const void *X, int64_t batch, int64_t m, int64_t n, int steps, const float *coeffs, float eps);
 
+// Programmatic launch: a kernel may start its set-up, or loads of what no
+// kernel before it in the call writes, while the one before it ends.
+__device__ __forceinline__ void wait_for_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---- elementwise / reduction kernels (elementwise.cu) ----
 int launch_momentum_bf16(const __nv_bfloat16 *g, float *buf, __nv_bfloat16 *u, int64_t numel, float mu,
                          int nesterov, cudaStream_t s);

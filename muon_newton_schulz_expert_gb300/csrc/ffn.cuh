@@ -102,10 +102,5 @@ struct WarpCursor {
   }
 };
 
-// Programmatic launch: a kernel may start its set-up, or loads of what no
-// kernel before it in the call writes, while the one before it ends.
-__device__ __forceinline__ void wait_for_previous_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 }  // namespace
 }  // namespace muon

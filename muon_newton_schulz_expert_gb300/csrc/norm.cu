@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, true))
   const int c0 = threadIdx.x * W, across = blockDim.x * W;
   const float inv_h = 1.f / (float)a.hidden;
   constexpr bool full = FORM != ANY;
+  let_next_grid_start();   // norm_weight_sum_kernel, which waits for this one's end
   const bool post = full || a.block.p, pre = full || a.dnormed.p;
   const bool from_above = full || a.dresidual_out.p;
   const bool gate_rows = full ? FORM == FULL_ROW_GATE : a.gate.p != nullptr;
@@ -509,6 +510,7 @@ __global__ void __launch_bounds__(512) norm_weight_sum_kernel(const float *parti
                                                               B *dw_pre, B *dw_post, B *dgate) {
   __shared__ float part[16][33];
   const int which = blockIdx.y;
+  wait_for_previous_grid();
   if (which == 0 ? !dw_pre : !dw_post && !dgate) return;
   const int c = blockIdx.x * 32 + threadIdx.x;
   float v[4] = {};
@@ -620,10 +622,23 @@ int launch_bwd(const BwdArgs &a, bool vec, void *dw_pre, void *dw_post, void *dg
   else st = launch_bwd_as<R, B, 1, 16>(a, p, s);
   if (st != MUON_OK || !a.partial) return st;
   trace_before(kTraceNormWeightSum, s);
-  norm_weight_sum_kernel<B><<<dim3((unsigned)((a.hidden + 31) / 32), 2), dim3(32, 16), 0, s>>>(
-      a.partial, groups_of(p, a.rows, true) / p.rows_per_cta, a.hidden, a.scale, static_cast<const B *>(a.w_post),
-      static_cast<const B *>(a.shared_gate), static_cast<B *>(dw_pre), static_cast<B *>(dw_post),
-      static_cast<B *>(dgate));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.hidden + 31) / 32), 2);
+  cfg.blockDim = dim3(32, 16);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(
+      &cfg, norm_weight_sum_kernel<B>, (const float *)a.partial, groups_of(p, a.rows, true) / p.rows_per_cta, a.hidden,
+      a.scale, static_cast<const B *>(a.w_post), static_cast<const B *>(a.shared_gate), static_cast<B *>(dw_pre),
+      static_cast<B *>(dw_post), static_cast<B *>(dgate));
+  if (e != cudaSuccess) {
+    trace_after(kTraceNormWeightSum, s);
+    return MUON_ERR_CUDA;
+  }
   return trace_after(kTraceNormWeightSum, s);
 }
 
