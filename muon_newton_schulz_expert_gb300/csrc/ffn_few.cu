@@ -7,7 +7,7 @@
 // roles of the operands are exchanged (weights on M, rows on N):
 //   D[128 weight columns, TN rows] = W^T X^T
 // with tcgen05.mma of one CTA (M = 128, N = TN = 16, 32 or 64), and the K loop
-// is cut into S parts (1, 2, 4 or 8) that the CTAs of a cluster take.  Each
+// is cut into S parts (1 to 8) that the CTAs of a cluster take.  Each
 // leaves its part of the sum (fp32) in its shared memory; after a cluster
 // barrier the CTAs read each other's through distributed shared memory, add
 // them in order of rank and finish the tile.  No workspace, no atomics, one
@@ -34,7 +34,6 @@ constexpr int BM = 128, BK = 64, UMMA_K = 16;
 constexpr int A_BYTES = BM * BK * 2;
 constexpr int EPI_THREADS = 128, THREADS = 64 + EPI_THREADS;
 constexpr int MAX_STAGES = 12, MAX_TN = 64;
-constexpr int ACC_COLS = 128, TMEM_COLS = 2 * ACC_COLS;   // two accumulators of up to 128 columns
 constexpr int NUM_BARS = 2 * MAX_STAGES + 4;
 
 enum Mode { UP = 0, DOWN, DH, DX };
@@ -170,6 +169,8 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int n_rows = MODE == DOWN ? 2 * p.tn : p.tn;   // N of one MMA
+  // TMEM: two accumulators, UP's and DOWN's of 2 tn columns (64 to 256 in all, a power of two)
+  const uint32_t acc_cols = (MODE == UP || MODE == DOWN ? 2u : 1u) * p.tn, tmem_cols = max(64u, 2 * acc_cols);
   const uint32_t b_bytes = (uint32_t)n_rows * (BK * 2), stage_bytes = MATS * A_BYTES + b_bytes;
   uint8_t *part = smem + p.stages * stage_bytes;       // [MATS][tn][128] fp32
   uint64_t *bars = reinterpret_cast<uint64_t *>(part + MATS * p.tn * BM * 4);
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
   if (warp == 1) {
     __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(TMEM_COLS)
+                 "r"(tmem_cols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
         const uint32_t idesc = make_idesc(BM, n_rows, A_MN, false);
         ok = wait_bounded(acce(acc), acc_phase ^ 1u, w);
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
+        const uint32_t d = tmem + (uint32_t)acc * acc_cols;
         for (int k = kb0; ok && k < kb1; ++k) {
           if (!wait_polled(full(stage), phase, w)) {
             ok = false;
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
       if (ok) ok = __all_sync(0xffffffffu, wait_bounded(accf(acc), acc_phase, w));
       if (ok) {
         tc_fence_after();
-        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * acc_cols;
         float *mine = reinterpret_cast<float *>(part) + q * 32 + lane;
         const int n = min(cur.hi - cur.row0, p.tn);
 #pragma unroll
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(tmem_cols) : "memory");
   }
 }
 
@@ -384,22 +385,25 @@ int launch(Args &p, const FfnShape &f, int trace_kind, cudaStream_t s) {
   constexpr int MATS = MODE == UP ? 2 : 1;
   const int64_t active = std::min(f.experts, f.rows);
   p.tn = row_tile(f);
-  // Shared memory for two blocks of an SM, so that the next product's blocks
-  // fetch their first weights beside this one's last; UP with 64 rows (40 KB
-  // stages) takes it whole.  K is cut while the blocks still fit the SMs at
-  // once and each keeps 6 k-blocks or more (6144 x 1792, one row: 53 us uncut,
-  // 34, 24 and 21 us cut in 2, 4 and 8; but a cut costs two cluster barriers: 8
-  // experts of one row, 1024 x 512, take 14 us cut in 2 and 17 us cut in 4).
+  // UP takes an SM for itself (34 to 40 KB stages: 4 of 16 rows, 3 of 64), the
+  // others share it between two blocks.  K is cut while the blocks still fit
+  // the SMs at once and each keeps 6 k-blocks or more (6144 x 1792, one row, in
+  // L2: 53 us uncut, 34, 24 and 21 us cut in 2, 4 and 8; but a cut costs two
+  // cluster barriers: 8 experts of one row, 1024 x 512, take 14 us cut in 2 and
+  // 17 us cut in 4).  From HBM, one row takes 24.0 us (26.6 with 2 stages of
+  // UP): 9.8 us of weights at the copy bandwidth, and about 5.5 us per kernel
+  // for its start, first loads, barriers and end.
   const int per_sm = MODE == UP ? 1 : 2;
   const int64_t tiles = (int64_t)p.tiles_m * (f.experts == 1 ? (f.rows + p.tn - 1) / p.tn : active);
   const int all_kb = p.kblocks * p.segments;
   p.split = 1;
-  while (p.split < 8 && 2 * p.split * tiles <= (int64_t)num_sms() * per_sm && 12 * p.split <= all_kb) p.split *= 2;
+  while (p.split < 8 && (p.split + 1) * tiles <= (int64_t)num_sms() * per_sm && 6 * (p.split + 1) <= all_kb) ++p.split;
   const size_t stage = MATS * A_BYTES + (size_t)(MODE == DOWN ? 2 : 1) * p.tn * BK * 2;
   const size_t fixed = 1024 + (size_t)MATS * p.tn * BM * 4 + NUM_BARS * 8 + 16;
-  const size_t budget = MODE == UP && p.tn == MAX_TN ? 220 * 1024 : 112 * 1024;
+  const size_t budget = MODE != UP ? 112 * 1024 : p.tn == MAX_TN ? 220 * 1024 : 160 * 1024;
   p.stages = (int)std::min<size_t>({(size_t)MAX_STAGES, (budget - fixed) / stage,
                                     (size_t)std::max(2, (all_kb + p.split - 1) / p.split)});
+  if (p.stages < 2) return MUON_ERR_UNSUPPORTED;   // cannot be: DOWN has 2 of 64 rows, every other case more
   const size_t smem = fixed + p.stages * stage;
   p.err = device_error_word();
   p.timeout_ns = wait_timeout_ns();
