@@ -81,7 +81,8 @@ struct WarpCursor {
           b = b < a ? a : b > rows ? rows : b;
         }
         lane_lo = (int)a, lane_hi = (int)b;
-        count = (row_tile ? (b - a + row_tile - 1) / row_tile : 1) * col_tiles;
+        // in 32 bits: rows are fewer than 2^31
+        count = (row_tile ? ((unsigned)(b - a) + (unsigned)row_tile - 1u) / (unsigned)row_tile : 1u) * col_tiles;
       }
       upto = count;
 #pragma unroll

@@ -7,11 +7,13 @@
 // roles of the operands are exchanged (weights on M, rows on N):
 //   D[128 weight columns, TN rows] = W^T X^T
 // with tcgen05.mma of one CTA (M = 128, N = TN = 16, 32 or 64), and the K loop
-// is cut into S parts (1 to 8) that the CTAs of a cluster take.  Each
-// leaves its part of the sum (fp32) in its shared memory; after a cluster
-// barrier the CTAs read each other's through distributed shared memory, add
-// them in order of rank and finish the tile.  No workspace, no atomics, one
-// launch per product.
+// is cut into S parts (1 to 8) that the CTAs of a cluster take.  Each CTA
+// finishes a part of the tile's columns: all send it their parts of its sums
+// (fp32, distributed shared memory), and after a cluster barrier it adds them in
+// order of rank.  Stores to the others need no answer: reading the parts where they
+// were made took 1.2 to 3.3 us a tile, this 1.5 us less (one row, 6144 x 1792, from
+// HBM: 23.9 against 22.4 us; 64 rows 32.1 against 27.6 us).  No workspace, no atomics, one launch
+// per product.
 //   UP    two accumulators (W1, W3) over one load of the rows; h = act(g) * u
 //   DOWN  y = h W2; h comes as two bf16 halves (value and remainder), which
 //         are 2 TN rows of one N, so h's rounding costs no accuracy and the
@@ -61,8 +63,8 @@ struct Tile {
   __device__ Tile(const Args &p, const WarpCursor &cur) {
     const int tt = (cur.hi - cur.lo + p.tn - 1) / p.tn;
     e = cur.e;
-    tm = (int)(cur.index / tt);
-    row0 = cur.lo + (int)(cur.index - (long long)tm * tt) * p.tn;
+    tm = (int)((unsigned)cur.index / (unsigned)tt);   // few tiles: 32 bits hold their number
+    row0 = cur.lo + ((int)cur.index - tm * tt) * p.tn;
     hi = cur.hi;
   }
 };
@@ -85,13 +87,8 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
@@ -112,22 +109,29 @@ __device__ __forceinline__ void put4(__nv_bfloat16 *dst, __nv_bfloat16 *rest, co
   }
 }
 
-// Adds the S parts of a tile and finishes it: items of 4 columns of one row.
-// `part` is the shared::cta address of this CTA's parts, [accumulator][row][128].
+// The columns of a tile that a CTA of its cluster finishes: as many as any other,
+// the last CTA possibly fewer, in fours.
+__device__ __forceinline__ int cut_width(int split) { return (32 + split - 1) / split * 4; }
+
+// Adds the S parts of this CTA's columns and finishes them: items of 4 columns of
+// one row.  `part` holds the parts, [rank][accumulator][row][width].
 template <int MODE>
-__device__ __forceinline__ void finish(const Args &p, const Tile &cur, uint32_t part, int thread, int threads) {
+__device__ __forceinline__ void finish(const Args &p, const Tile &cur, const float *part, int rank, int width,
+                                       int thread, int threads) {
   const int n = min(cur.hi - cur.row0, p.tn);
-  const int col_base = cur.tm * BM;
-  for (int i = thread; i < n * 32; i += threads) {
-    const int t = i >> 5, c = (i & 31) * 4, col = col_base + c;
+  const int quads = min(width, BM - rank * width) / 4;
+  const int col_base = cur.tm * BM + rank * width, per_mat = p.tn * width, per_rank = (MODE == UP ? 2 : 1) * per_mat;
+  for (int i = thread; i < n * quads; i += threads) {
+    const int t = i / quads, c = (i - t * quads) * 4, col = col_base + c;
     if (col >= p.M) continue;   // M is a multiple of 8
     float s0[4] = {}, s1[4] = {};
-    for (int r = 0; r < p.split; ++r) {
-      const uint32_t at = (p.split > 1 ? map_to_rank(part, r) : part) + (uint32_t)((t * BM + c) * 4);
-      const float4 x = ld_cluster(at);
+    const float *from = part + t * width + c;
+#pragma unroll 4
+    for (int r = 0; r < p.split; ++r, from += per_rank) {
+      const float4 x = *reinterpret_cast<const float4 *>(from);
       s0[0] += x.x, s0[1] += x.y, s0[2] += x.z, s0[3] += x.w;
       if (MODE == UP) {
-        const float4 y = ld_cluster(at + (uint32_t)(p.tn * BM * 4));
+        const float4 y = *reinterpret_cast<const float4 *>(from + per_mat);
         s1[0] += y.x, s1[1] += y.y, s1[2] += y.z, s1[3] += y.w;
       }
     }
@@ -172,8 +176,9 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
   // TMEM: two accumulators, UP's and DOWN's of 2 tn columns (64 to 256 in all, a power of two)
   const uint32_t acc_cols = (MODE == UP || MODE == DOWN ? 2u : 1u) * p.tn, tmem_cols = max(64u, 2 * acc_cols);
   const uint32_t b_bytes = (uint32_t)n_rows * (BK * 2), stage_bytes = MATS * A_BYTES + b_bytes;
-  uint8_t *part = smem + p.stages * stage_bytes;       // [MATS][tn][128] fp32
-  uint64_t *bars = reinterpret_cast<uint64_t *>(part + MATS * p.tn * BM * 4);
+  const int width = cut_width(p.split);
+  float *part = reinterpret_cast<float *>(smem + p.stages * stage_bytes);   // [split][MATS][tn][width]
+  uint64_t *bars = reinterpret_cast<uint64_t *>(part + p.split * MATS * p.tn * width);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NUM_BARS);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -212,6 +217,7 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (cut) cluster_arrive();   // this CTA runs, and its parts may be written
   // UP and DH read what earlier calls wrote, offsets among it; DOWN and DX run
   // after one of them in the same call, so that only the rows that it makes are
   // waited for, below.
@@ -225,14 +231,17 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
   const unsigned long long drain_ns = p.timeout_ns < 20000000ull ? p.timeout_ns : 20000000ull;
   // this CTA's share of the K loop
   const int all_kb = p.kblocks * p.segments;
-  const int kb0 = (int)((long long)all_kb * rank / p.split), kb1 = (int)((long long)all_kb * (rank + 1) / p.split);
+  const int kb0 = all_kb * rank / p.split, kb1 = all_kb * (rank + 1) / p.split;   // all_kb < 2^26
 
   WarpCursor walk(p.offsets, p.rows, p.experts, p.tn, p.tiles_m);
   int stage = 0, acc = 0;
   uint32_t phase = 0, acc_phase = 0, issued = 0, issued_parity = 0;
   bool ok = true;   // of this warp's role
   bool rows_ready = !SECOND;
-  for (long long t = cid; walk.seek(t); t += ncl) {
+  long long t = cid;
+  bool more = walk.seek(t);
+  if (cut && !more) cluster_wait();
+  while (more) {
     const Tile cur(p, walk);
     if (warp == 0) {
       if (lane == 0 && ok) {
@@ -316,10 +325,15 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
     } else {
       const int q = warp & 3;   // TMEM lanes 32q..
       if (ok) ok = __all_sync(0xffffffffu, wait_bounded(accf(acc), acc_phase, w));
+      if (cut) cluster_wait();   // the parts of the tile before have been added
       if (ok) {
         tc_fence_after();
         const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * acc_cols;
-        float *mine = reinterpret_cast<float *>(part) + q * 32 + lane;
+        // this lane's column: the CTA that finishes it, and its place there
+        const int column = q * 32 + lane, owner = column / width;
+        const uint32_t here = smem_u32(part);
+        const uint32_t there = (cut ? map_to_rank(here, (uint32_t)owner) : here) +
+                               4u * (uint32_t)(rank * MATS * p.tn * width + column - owner * width);
         const int n = min(cur.hi - cur.row0, p.tn);
 #pragma unroll
         for (int i = 0; i < MATS; ++i)
@@ -329,8 +343,9 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
             if (MODE == DOWN) tmem_ld16(taddr + (uint32_t)(p.tn + c), r2);
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-              mine[(i * p.tn + c + j) * BM] =
-                  MODE == DOWN ? __uint_as_float(r[j]) + __uint_as_float(r2[j]) : __uint_as_float(r[j]);
+              if (c + j < n)
+                st_cluster(there + 4u * (uint32_t)((i * p.tn + c + j) * width),
+                           MODE == DOWN ? __uint_as_float(r[j]) + __uint_as_float(r2[j]) : __uint_as_float(r[j]));
           }
         tc_fence_before();
         __syncwarp();
@@ -341,17 +356,19 @@ __global__ void __launch_bounds__(THREADS) ffn_few_kernel(const __grid_constant_
       if (!cut) {
         // the four warps have the whole tile in `part`
         asm volatile("bar.sync 1, %0;" ::"r"(EPI_THREADS) : "memory");
-        if (ok) finish<MODE>(p, cur, smem_u32(part), (int)threadIdx.x - 64, EPI_THREADS);
+        if (ok) finish<MODE>(p, cur, part, 0, width, (int)threadIdx.x - 64, EPI_THREADS);
         asm volatile("bar.sync 1, %0;" ::"r"(EPI_THREADS) : "memory");
       }
     }
     __syncwarp();
     if (cut) {
-      cluster_sync_all();   // every CTA's part is in its shared memory
-      if (!*abort_flag) finish<MODE>(p, cur, smem_u32(part), rank * THREADS + (int)threadIdx.x, p.split * THREADS);
-      __syncwarp();
-      cluster_sync_all();   // and has been read
+      if (warp < 2) cluster_wait();
+      cluster_sync_all();   // all parts of this CTA's columns are here
+      if (!*abort_flag) finish<MODE>(p, cur, part, rank, width, (int)threadIdx.x, THREADS);
     }
+    t += ncl;
+    more = walk.seek(t);
+    if (cut && more) cluster_arrive();   // and have been added
   }
   // a kernel ends after the one it was started early beside, whatever it had to do
   if (!rows_ready) wait_for_previous_grid();
@@ -388,18 +405,19 @@ int launch(Args &p, const FfnShape &f, int trace_kind, cudaStream_t s) {
   // UP takes an SM for itself (34 to 40 KB stages: 4 of 16 rows, 3 of 64), the
   // others share it between two blocks.  K is cut while the blocks still fit
   // the SMs at once and each keeps 6 k-blocks or more (6144 x 1792, one row, in
-  // L2: 53 us uncut, 34, 24 and 21 us cut in 2, 4 and 8; but a cut costs two
-  // cluster barriers: 8 experts of one row, 1024 x 512, take 14 us cut in 2 and
-  // 17 us cut in 4).  From HBM, one row takes 24.0 us (26.6 with 2 stages of
-  // UP): 9.8 us of weights at the copy bandwidth, and about 5.5 us per kernel
-  // for its start, first loads, barriers and end.
+  // L2: 53 us uncut, 34, 24 and 21 us cut in 2, 4 and 8; from HBM 22.4 us, and
+  // 27.4 us if 4 k-blocks are enough, which cuts DOWN in 6 instead of 4 and
+  // leaves its clusters waiting for places; 2048 x 1024 takes 19.6 us with 6
+  // k-blocks, 18.6 us with 4).  Of the 22.4 us the weights' bytes take 9.8 at the
+  // copy bandwidth; each kernel adds about 1.5 us until its first loads leave,
+  // 1 us for their latency, 2 to 3 us for sums, exchange and end.
   const int per_sm = MODE == UP ? 1 : 2;
   const int64_t tiles = (int64_t)p.tiles_m * (f.experts == 1 ? (f.rows + p.tn - 1) / p.tn : active);
   const int all_kb = p.kblocks * p.segments;
   p.split = 1;
   while (p.split < 8 && (p.split + 1) * tiles <= (int64_t)num_sms() * per_sm && 6 * (p.split + 1) <= all_kb) ++p.split;
   const size_t stage = MATS * A_BYTES + (size_t)(MODE == DOWN ? 2 : 1) * p.tn * BK * 2;
-  const size_t fixed = 1024 + (size_t)MATS * p.tn * BM * 4 + NUM_BARS * 8 + 16;
+  const size_t fixed = 1024 + (size_t)p.split * ((32 + p.split - 1) / p.split * 4) * MATS * p.tn * 4 + NUM_BARS * 8 + 16;
   const size_t budget = MODE != UP ? 112 * 1024 : p.tn == MAX_TN ? 220 * 1024 : 160 * 1024;
   p.stages = (int)std::min<size_t>({(size_t)MAX_STAGES, (budget - fixed) / stage,
                                     (size_t)std::max(2, (all_kb + p.split - 1) / p.split)});
