@@ -9,27 +9,35 @@
 //             dW1 = X^T dG, dW3 = X^T dU                       (DW13)
 //             dW2 = Hid^T dY                                   (DW2)
 // One kernel, instantiated for the six products; all are persistent CTA pairs
-// on 256 x 256 output tiles (tcgen05.mma.cta_group::2, M = N = 256, K = 16,
+// on output tiles of up to 256 x 256 (tcgen05.mma.cta_group::2, M = 256, K = 16,
 // bf16 operands, fp32 accumulation in TMEM), fed by TMA through a ring of
 // three stages of two k-blocks of 64.
 //
-// The two halves of a pair tile's N axis are loaded by the two CTAs of the
-// pair.  UP and DW13 use that: the even CTA loads 128 columns of W1 (dG), the
-// odd one the same 128 columns of W3 (dU), so that columns 0..127 of the
-// accumulator hold G (dW1) and 128..255 U (dW3) of the same places.  One
-// kernel forms both products, reads X once for both, and the activation and
-// the product meet in one thread's registers.
+// The row products (UP, DOWN, DH, DX) have the weights on M and the rows on N:
+//   D[256 weight columns, N rows] = W^T X^T
+// since N may be any multiple of 32 up to 256, and groups of rows end anywhere.
+// A group's n rows are ceil(n / 32) units, spread evenly over ceil(n / 256)
+// tiles, so that 16 rows of a group are computed in vain on average and no tile
+// is much shorter than its neighbours.  (With the rows on M every tile counts 256:
+// 16384 rows over 32 experts, 6144 x 1792, fill 83% of those.)  Rows past a
+// group's end belong to the next expert: computed and not stored, since rows do
+// not mix.
 //
-// DX runs one K loop over both products: first dG W1^T, then dU W3^T.
+// UP forms both products of the same places: the M axis of a CTA holds 64
+// columns of W1 and the same 64 of W3, so X is read once for both.  G is then in
+// TMEM lanes 0..63 and U in lanes 64..127; the two warps that hold the same places
+// exchange halves through shared memory.
 //
-// Rows of a group end anywhere.  The row products (UP, DOWN, DH, DX) compute
-// whole tiles: rows past a group's end belong to the next expert and are
-// computed but not stored (rows do not mix).  The weight gradients sum over
-// the group's rows, so there the last, partial k-block must hold zeros past
-// the group's end in both operands: it is read from copies of those rows
-// padded with zeros (`tail` arrays, [experts][64][columns]), which keeps a
-// NaN of one expert's rows out of another's gradient.  An expert without rows
-// gets zeros.
+// DX runs one K loop over both products: first W1 dG^T, then W3 dU^T.
+//
+// DW13 has 128 columns of dG on the even CTA's half of N and of dU on the odd
+// one's, so that X is read once for both gradients.
+//
+// The weight gradients sum over the group's rows, so there the last, partial
+// k-block must hold zeros past the group's end in both operands: it is read
+// from copies of those rows padded with zeros (`tail` arrays,
+// [experts][64][columns]), which keeps a NaN of one expert's rows out of
+// another's gradient.  An expert without rows gets zeros.
 //
 // Rounding: Hid, dG and dU are stored in bf16, the operand type of the product
 // that reads them; everything before that rounding is fp32.
@@ -37,7 +45,7 @@
 // Roles per CTA (320 threads): warp 0 TMA producer, warp 1 MMA issuer (even
 // CTA) and TMEM owner, warps 2..9 epilogue.  Two accumulators, so that the
 // epilogue of one tile overlaps the next tile's products.  Every wait is
-// bounded (tc.cuh).
+// bounded (tc.cuh); an epilogue warp that gave up still meets its partner of UP.
 #include <algorithm>
 
 #include "ffn.cuh"
@@ -45,8 +53,9 @@
 namespace muon {
 namespace {
 
-constexpr int CM = 256, BM = 128;   // rows of a pair tile, rows held by one CTA
-constexpr int BN = 256, BNH = 128;  // columns of a pair tile, columns loaded by one CTA
+constexpr int CM = 256, BM = 128;   // M of a pair tile, M held by one CTA
+constexpr int BN = 256, BNH = 128;  // most N of a pair tile, N loaded by one CTA
+constexpr int UNIT = 32;            // rows by which a row product's N grows
 constexpr int BK = 64;              // one 128-byte swizzle row of bf16
 constexpr int UMMA_K = 16;
 constexpr int A_STAGE = BM * BK * 2;
@@ -62,6 +71,7 @@ constexpr int TMEM_COLS = 2 * ACC_COLS;
 constexpr int NFULL = STAGES * KSUB;
 constexpr int NUM_BARS = NFULL + STAGES + 5;
 constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * BOX_BYTES + NUM_BARS * 8 + 16;
+constexpr int ROW_BOX = 64;          // rows of one load of a row product
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 
 enum Mode { UP = 0, DOWN, DH, DX, DW13, DW2 };
@@ -69,17 +79,17 @@ enum Mode { UP = 0, DOWN, DH, DX, DW13, DW2 };
 template <int MODE>
 struct Form {
   static constexpr bool dw = MODE == DW13 || MODE == DW2;
-  static constexpr bool a_mn = dw;
-  static constexpr bool b_mn = MODE == UP || MODE == DOWN || dw;
+  static constexpr bool a_mn = dw || MODE == UP || MODE == DOWN;
+  static constexpr bool b_mn = dw;
   // two weight matrices side by side in the accumulator's columns
-  static constexpr bool paired = MODE == UP || MODE == DW13;
+  static constexpr bool paired = MODE == DW13;
 };
 
 struct Args {
-  // operands: A and its second K segment (DX) or tail copy (DW); B and its
-  // partner (UP: W3, DX: W3, DW13: dU) and their tail copies
+  // operands: A (row products: weights; UP, DX: a2 = W3; DW: a2 = tail copy)
+  // and B (row products: rows; DX: b2 = dU; DW13: b2 = dU; DW: bt, bt2 tail copies)
   CUtensorMap a, a2, b, b2, bt, bt2;
-  CUtensorMap out[3];                // boxes of 32 rows x 64 columns
+  CUtensorMap out[2];                // DW: boxes of 32 rows x 64 columns
   void *outp[3];
   long long out_ld[3];               // row strides in elements
   const int64_t *offsets;            // null: one group of all rows
@@ -94,16 +104,22 @@ struct Args {
   unsigned long long timeout_ns;
 };
 
-// A tile: expert, row tile and column tile, rows of the expert.
+// A tile: expert, row tile and column tile, rows of the expert; of a row product
+// also the tile's first row and the units of 32 rows it spans.
 template <int MODE>
 struct Tile {
-  int e, ti, tj, lo, hi;
+  int e, ti, tj, lo, hi, row0 = 0, units = BN / UNIT;
 
   __device__ Tile(const Args &p, const WarpCursor &cur) {
     e = cur.e, lo = cur.lo, hi = cur.hi;
-    const int tm = Form<MODE>::dw ? p.tiles_m : (hi - lo + CM - 1) / CM;
+    const int tm = Form<MODE>::dw ? p.tiles_m : (hi - lo + BN - 1) / BN;
     tj = (int)(cur.index / tm);
     ti = (int)(cur.index - (long long)tj * tm);
+    if (!Form<MODE>::dw) {
+      const int all = (hi - lo + UNIT - 1) / UNIT, each = all / tm, more = all - each * tm;
+      units = each + (ti < more ? 1 : 0);
+      row0 = lo + UNIT * (ti * each + min(ti, more));
+    }
   }
   __device__ int num_kb(const Args &p) const {
     return Form<MODE>::dw ? (hi - lo + BK - 1) / BK : MODE == DX ? 2 * p.kblocks : p.kblocks;
@@ -129,27 +145,15 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&lo)[32], ui
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(lo[i]), "+r"(hi[i]));
 }
 
-// One epilogue warp's way out: 32 rows x 64 columns of bf16, lane = row.  A
-// full box leaves through shared memory and TMA (clipped at the array's edge):
-// 128-byte rows, since 64-byte ones (32 columns) held the stores of the weight
-// gradients to 2.6 TB/s.  A box that a group ends in is written row by row.
+// Weight gradients: one epilogue warp's way out, 32 rows x 64 columns of bf16,
+// lane = row, through shared memory and TMA, which clips at the array's edge:
+// 128-byte rows, since 64-byte ones (32 columns) held the stores to 2.6 TB/s.
 struct Writer {
   uint8_t *box;
   uint32_t box_s;
 
-  __device__ void put(const uint32_t (&w)[32], const CUtensorMap *map, void *base, long long ld, int lane, int col0,
-                      int cols, long long row0, long long row_end, bool clip_rows, int mat, unsigned *err) {
-    if (clip_rows && row0 + 32 > row_end) {
-      const long long row = row0 + lane;
-      if (row < row_end) {
-        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(base) + row * ld + col0;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (col0 + 8 * c < cols)
-            *reinterpret_cast<uint4 *>(dst + 8 * c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-      }
-      return;
-    }
+  __device__ void put(const uint32_t (&w)[32], const CUtensorMap *map, int lane, int col0, int row0, int mat,
+                      unsigned *err) {
     if (lane == 0) bulk_wait_read_all();  // the box's last store has read it
     __syncwarp();
 #pragma unroll
@@ -159,11 +163,37 @@ struct Writer {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_3d(map, box_s, col0, (int)row0, mat, err);
+      tma_store_3d(map, box_s, col0, row0, mat, err);
       bulk_commit();
     }
   }
 };
+
+// Row products: a lane holds one column's sums for 32 rows of the output.
+// Lanes 2i and 2i + 1 exchange halves, so that each has both columns, c[j][0]
+// and c[j][1], of the 16 rows 2j + (lane & 1): 4-byte accesses, a warp's 64 bytes
+// of two rows, whole 32-byte sectors.
+__device__ __forceinline__ void pair_columns(const uint32_t (&v)[32], float (&c)[16][2], int lane) {
+  const bool odd = lane & 1;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float mine = __uint_as_float(odd ? v[2 * j + 1] : v[2 * j]);
+    const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(odd ? v[2 * j] : v[2 * j + 1]), 1);
+    c[j][0] = odd ? other : mine;
+    c[j][1] = odd ? mine : other;
+  }
+}
+
+// rows first + 2 j, j in [0, N), of a lane's two columns
+template <int N>
+__device__ __forceinline__ void put_pairs(void *base, long long ld, long long first, long long row_end, int col,
+                                          int cols, const uint32_t (&w)[N]) {
+  if (col >= cols) return;
+  __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(base) + first * ld + col;
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    if (first + 2 * j < row_end) *reinterpret_cast<uint32_t *>(dst + 2 * j * ld) = w[j];
+}
 
 template <int MODE>
 __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_constant__ Args p) {
@@ -199,7 +229,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&p.a);
     tma_prefetch_desc(&p.b);
-    tma_prefetch_desc(&p.out[0]);
+    if (Form<MODE>::dw) tma_prefetch_desc(&p.out[0]);
   }
   if (warp == 1) {  // one warp in each CTA of the pair allocates the same columns in both
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -217,7 +247,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
   wait_for_previous_grid();
   let_next_grid_start();
   if (warp == 2 && blockIdx.x == 0) report_offsets(p.offsets, p.experts, p.rows, p.err);
-  WarpCursor walk(p.offsets, p.rows, p.experts, Form<MODE>::dw ? 0 : CM,
+  WarpCursor walk(p.offsets, p.rows, p.experts, Form<MODE>::dw ? 0 : BN,
                   (long long)(Form<MODE>::dw ? p.tiles_m : 1) * p.tiles_n);
 
   if (warp == 0) {
@@ -230,9 +260,14 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
       const Tile<MODE> cur(p, walk);
       if (lane == 0 && ok) {
         const int num_kb = cur.num_kb(p);
-        const int mn_a = cur.ti * CM + (int)rank * BM;   // DW: first column of A's rows in this CTA
-        const int row_a = cur.lo + mn_a;                 // row products: first row
+        // first of this CTA's places on M and N
+        const int mn_a = Form<MODE>::dw ? cur.ti * CM + (int)rank * BM
+                         : MODE == UP   ? cur.tj * BM + (int)rank * (BM / 2)
+                                        : cur.tj * CM + (int)rank * BM;
         const int n_b = Form<MODE>::paired ? cur.tj * BNH : cur.tj * BN + (int)rank * BNH;
+        const int half_rows = cur.units * (UNIT / 2), row_b = cur.row0 + (int)rank * half_rows;
+        const uint32_t kb_bytes =
+            Form<MODE>::dw ? KB_BYTES : A_STAGE + (half_rows + ROW_BOX - 1) / ROW_BOX * (ROW_BOX * BK * 2);
         const CUtensorMap *mb = Form<MODE>::paired && rank ? &p.b2 : &p.b;
         for (int kb = 0; kb < num_kb; kb += KSUB) {
           if (!wait_polled(empty(stage), phase ^ 1u, w)) {
@@ -244,7 +279,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
           // end of K still completes its phase, with no bytes
           if (rank == 0)
 #pragma unroll
-            for (int j = 0; j < KSUB; ++j) mbar_expect_tx(full(stage, j), j < valid ? 2 * KB_BYTES : 0);
+            for (int j = 0; j < KSUB; ++j) mbar_expect_tx(full(stage, j), j < valid ? 2 * kb_bytes : 0);
           issued |= 1u << stage;
           issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
 #pragma unroll
@@ -268,14 +303,15 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
             } else {
               const bool second = MODE == DX && k >= p.kblocks;
               const int kc = (second ? k - p.kblocks : k) * BK;
-              tma_load_3d_pair(sa, second ? &p.a2 : &p.a, bar, kc, row_a, 0, p.err);
-              if (Form<MODE>::b_mn) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-                  tma_load_3d_pair(sb + q * (64 * BK * 2), mb, bar, n_b + q * 64, kc, cur.e, p.err);
-              } else {
-                tma_load_3d_pair(sb, second ? &p.b2 : &p.b, bar, kc, n_b, cur.e, p.err);
+              if (Form<MODE>::a_mn) {   // boxes of 64 weight columns x 64 K-rows
+                tma_load_3d_pair(sa, &p.a, bar, mn_a, kc, cur.e, p.err);
+                tma_load_3d_pair(sa + 64 * BK * 2, MODE == UP ? &p.a2 : &p.a, bar, MODE == UP ? mn_a : mn_a + 64, kc,
+                                 cur.e, p.err);
+              } else {                  // one box of 128 weight rows x 64 K-columns
+                tma_load_3d_pair(sa, second ? &p.a2 : &p.a, bar, kc, mn_a, cur.e, p.err);
               }
+              for (int r = 0; r < half_rows; r += ROW_BOX)
+                tma_load_3d_pair(sb + r * (BK * 2), second ? &p.b2 : &p.b, bar, kc, row_b + r, 0, p.err);
             }
           }
           if (++stage == STAGES) {
@@ -294,7 +330,6 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (CTA 0 of the pair)
     if (rank == 0) {
-      constexpr uint32_t idesc = make_idesc(CM, BN, Form<MODE>::a_mn, Form<MODE>::b_mn);
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -307,6 +342,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
           tc_fence_after();
           const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
           const int num_kb = cur.num_kb(p);
+          const uint32_t idesc = make_idesc(CM, UNIT * cur.units, Form<MODE>::a_mn, Form<MODE>::b_mn);
           for (int kb = 0; kb < num_kb; kb += KSUB) {
             const int valid = num_kb - kb < KSUB ? num_kb - kb : KSUB;
 #pragma unroll
@@ -353,92 +389,104 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
     // ---------------------------------------------------------------- epilogue (both CTAs)
     const int ew = warp - 2;
     const int q = warp & 3, half = ew >> 2;  // TMEM lanes 32q.., and which half of the columns
-    Writer out{epi_smem + ew * BOX_BYTES, smem_u32(epi_smem) + (uint32_t)(ew * BOX_BYTES)};
+    uint8_t *box = epi_smem + ew * BOX_BYTES;
+    Writer out{box, smem_u32(box)};
     int acc = 0;
-    uint32_t acc_phase = 0;
+    uint32_t acc_phase = 0, flip = 0;
+    bool ok = true;
     for (long long t = cid; walk.seek(t); t += ncl) {
       const Tile<MODE> cur(p, walk);
-      const bool ok = wait_bounded(accf(acc), acc_phase, w);
-      if (!__all_sync(0xffffffffu, ok)) break;  // warp-uniform: the TMEM loads below are .sync.aligned
+      if (ok) ok = __all_sync(0xffffffffu, wait_bounded(accf(acc), acc_phase, w));   // warp-uniform
+      if (!ok && MODE != UP) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
-      const int rt = cur.ti * CM + (int)rank * BM + q * 32;
-      const long long row0 = Form<MODE>::dw ? rt : (long long)cur.lo + rt;
-      const long long row_end = Form<MODE>::dw ? p.M : cur.hi;
-      const int mat = Form<MODE>::dw ? cur.e : 0;
-      if (row0 < row_end) {
-        if (MODE == UP) {
-          // this warp's 64 columns of the tile: G from the low half of the accumulator, U from the high one
-          const int cc = half * 64, col0 = cur.tj * BNH + cc;
-          if (col0 < p.N) {
-            uint32_t wg[32], wu[32], wh[32];
+      if (MODE == UP) {
+        // lanes of q = 0, 1 hold G of 32 columns each, those of q = 2, 3 U of the same
+        const bool has_u = q >= 2;
+        const int col = cur.tj * BM + (int)rank * (BM / 2) + (q & 1) * 32 + (lane & ~1);
+        float2 *mine = reinterpret_cast<float2 *>(box) + lane;
+        const float2 *partner = reinterpret_cast<const float2 *>(epi_smem + (ew ^ 2) * BOX_BYTES) + lane;
+        for (int ch = half; ch < cur.units; ch += 2) {
+          float c[16][2];
+          if (ok) {
+            uint32_t v[32];
+            tmem_ld32(taddr + (uint32_t)(UNIT * ch), v);
+            pair_columns(v, c, lane);
+            // each of the two warps finishes 16 of the 32 rows: it hands over its sums of the others
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              uint32_t g[32], u[32];
-              tmem_ld32(taddr + (uint32_t)(cc + 32 * part), g);
-              tmem_ld32(taddr + (uint32_t)(BNH + cc + 32 * part), u);
+            for (int j = 0; j < 8; ++j)
+              mine[(flip * 8 + j) * 32] = has_u ? make_float2(c[j][0], c[j][1]) : make_float2(c[8 + j][0], c[8 + j][1]);
+          }
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + half * 2 + (q & 1)) : "memory");
+          if (ok) {
+            const long long first = (long long)cur.row0 + UNIT * ch + (lane & 1);
+            uint32_t wh[8], w16[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float h[2], dv;
+            for (int j = 0; j < 8; ++j) {
+              const float2 o = partner[(flip * 8 + j) * 32];
+              float h[2], dv;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  const float gf = __uint_as_float(g[2 * i + j]);
-                  h[j] = gf * sigmoid_of(gf, p.act, &dv) * __uint_as_float(u[2 * i + j]);
-                }
-                wh[16 * part + i] = pack_bf16(h[0], h[1]);
-                wg[16 * part + i] = pack_bf16(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
-                wu[16 * part + i] = pack_bf16(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+              for (int i = 0; i < 2; ++i) {
+                const float ov = i ? o.y : o.x, mv = has_u ? c[8 + j][i] : c[j][i];
+                const float g = has_u ? ov : mv, u = has_u ? mv : ov;
+                h[i] = g * sigmoid_of(g, p.act, &dv) * u;
               }
+              wh[j] = pack_bf16(h[0], h[1]);
             }
-            out.put(wh, &p.out[0], p.outp[0], p.out_ld[0], lane, col0, p.N, row0, row_end, true, 0, p.err);
+            put_pairs<8>(p.outp[0], p.out_ld[0], first + (has_u ? 16 : 0), cur.hi, col, p.N, wh);
             if (p.outp[1]) {
-              out.put(wg, &p.out[1], p.outp[1], p.out_ld[1], lane, col0, p.N, row0, row_end, true, 0, p.err);
-              out.put(wu, &p.out[2], p.outp[2], p.out_ld[2], lane, col0, p.N, row0, row_end, true, 0, p.err);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w16[j] = pack_bf16(c[j][0], c[j][1]);
+              put_pairs<16>(p.outp[has_u ? 2 : 1], p.out_ld[1], first, cur.hi, col, p.N, w16);
             }
           }
-        } else if (MODE == DH) {
-#pragma unroll 1
-          for (int ch = 0; ch < 2; ++ch) {
-            const int cc = half * 128 + ch * 64, col0 = cur.tj * BN + cc;
-            if (col0 >= p.N) break;
-            uint32_t wg[32], wu[32], wh[32];   // g, u and then dg, du in wg and wu
-            const bool in_row = row0 + lane < row_end;
-            const long long at = (row0 + lane) * p.N + col0;
+          flip ^= 1u;   // the partner may still be reading this half of the box
+        }
+      } else if (!Form<MODE>::dw) {
+        const int col = cur.tj * CM + (int)rank * BM + q * 32 + (lane & ~1);
+        for (int ch = half; ch < cur.units; ch += 2) {
+          const long long first = (long long)cur.row0 + UNIT * ch + (lane & 1);
+          uint32_t wg[16], wu[16], wh[16];
+          if (MODE == DH) {
+            const long long at = first * p.N + col;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-              if (in_row && col0 + 8 * c < p.N) {
-                a = __ldg(reinterpret_cast<const uint4 *>(p.g + at + 8 * c));
-                b = __ldg(reinterpret_cast<const uint4 *>(p.u + at + 8 * c));
-              }
-              wg[4 * c] = a.x, wg[4 * c + 1] = a.y, wg[4 * c + 2] = a.z, wg[4 * c + 3] = a.w;
-              wu[4 * c] = b.x, wu[4 * c + 1] = b.y, wu[4 * c + 2] = b.z, wu[4 * c + 3] = b.w;
+            for (int j = 0; j < 16; ++j) {
+              const bool in = col < p.N && first + 2 * j < cur.hi;
+              wg[j] = in ? __ldg(reinterpret_cast<const unsigned *>(p.g + at + 2 * j * (long long)p.N)) : 0u;
+              wu[j] = in ? __ldg(reinterpret_cast<const unsigned *>(p.u + at + 2 * j * (long long)p.N)) : 0u;
             }
             __syncwarp();
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              uint32_t r[32];
-              tmem_ld32(taddr + (uint32_t)(cc + 32 * part), r);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float2 g2 = unpack_bf16(wg[16 * part + i]), u2 = unpack_bf16(wu[16 * part + i]);
-                float dg[2], du[2], h[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                  gated_gradient(__uint_as_float(r[2 * i + j]), j ? g2.y : g2.x, j ? u2.y : u2.x, p.act, &dg[j], &du[j],
-                                 &h[j]);
-                wg[16 * part + i] = pack_bf16(dg[0], dg[1]);
-                wu[16 * part + i] = pack_bf16(du[0], du[1]);
-                wh[16 * part + i] = pack_bf16(h[0], h[1]);
-              }
-            }
-            out.put(wg, &p.out[0], p.outp[0], p.out_ld[0], lane, col0, p.N, row0, row_end, true, 0, p.err);
-            out.put(wu, &p.out[1], p.outp[1], p.out_ld[1], lane, col0, p.N, row0, row_end, true, 0, p.err);
-            out.put(wh, &p.out[2], p.outp[2], p.out_ld[2], lane, col0, p.N, row0, row_end, true, 0, p.err);
           }
-        } else {
-          const bool empty_sum = Form<MODE>::dw && cur.hi == cur.lo;  // no MMA ran: the accumulator holds nothing
-          const int which = Form<MODE>::paired ? half : 0;            // DW13: dW1 in the low columns, dW3 in the high
+          uint32_t v[32];
+          tmem_ld32(taddr + (uint32_t)(UNIT * ch), v);
+          float c[16][2];
+          pair_columns(v, c, lane);
+          if (MODE == DH) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float2 g2 = unpack_bf16(wg[j]), u2 = unpack_bf16(wu[j]);
+              float dg[2], du[2], h[2];
+              gated_gradient(c[j][0], g2.x, u2.x, p.act, &dg[0], &du[0], &h[0]);
+              gated_gradient(c[j][1], g2.y, u2.y, p.act, &dg[1], &du[1], &h[1]);
+              wg[j] = pack_bf16(dg[0], dg[1]);
+              wu[j] = pack_bf16(du[0], du[1]);
+              wh[j] = pack_bf16(h[0], h[1]);
+            }
+            put_pairs<16>(p.outp[0], p.out_ld[0], first, cur.hi, col, p.N, wg);
+            put_pairs<16>(p.outp[1], p.out_ld[1], first, cur.hi, col, p.N, wu);
+            put_pairs<16>(p.outp[2], p.out_ld[2], first, cur.hi, col, p.N, wh);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) wh[j] = pack_bf16(c[j][0], c[j][1]);
+            put_pairs<16>(p.outp[0], p.out_ld[0], first, cur.hi, col, p.N, wh);
+          }
+          __syncwarp();
+        }
+      } else {
+        const int row0 = cur.ti * CM + (int)rank * BM + q * 32;
+        if (row0 < p.M) {
+          const bool empty_sum = cur.hi == cur.lo;           // no MMA ran: the accumulator holds nothing
+          const int which = Form<MODE>::paired ? half : 0;   // DW13: dW1 in the low columns, dW3 in the high
 #pragma unroll 1
           for (int ch = 0; ch < 2; ++ch) {
             const int cc = half * 128 + ch * 64;
@@ -451,14 +499,13 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
               wo[i] = empty_sum ? 0u : pack_bf16(__uint_as_float(lo[2 * i]), __uint_as_float(lo[2 * i + 1]));
               wo[16 + i] = empty_sum ? 0u : pack_bf16(__uint_as_float(hi[2 * i]), __uint_as_float(hi[2 * i + 1]));
             }
-            out.put(wo, &p.out[which], p.outp[which], p.out_ld[which], lane, col0, p.N, row0, row_end,
-                    !Form<MODE>::dw, mat, p.err);
+            out.put(wo, &p.out[which], lane, col0, row0, cur.e, p.err);
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(map_to_rank(acce(acc), 0));
+      if (lane == 0 && ok) mbar_arrive_cluster(map_to_rank(acce(acc), 0));
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
@@ -548,7 +595,7 @@ int launch(Args &p, int trace_kind, cudaStream_t s) {
   if (!p.err) return MUON_ERR_CUDA;
   // at most this many tiles, whatever the groups' sizes are
   const long long row_tiles =
-      Form<MODE>::dw ? (long long)p.tiles_m * p.experts : p.rows / CM + std::min<long long>(p.experts, p.rows);
+      Form<MODE>::dw ? (long long)p.tiles_m * p.experts : p.rows / BN + std::min<long long>(p.experts, p.rows);
   const long long pairs = std::min<long long>(row_tiles * p.tiles_n, max_pairs[dev]);
   cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
   cfg.numAttrs = 2;
@@ -561,12 +608,15 @@ int launch(Args &p, int trace_kind, cudaStream_t s) {
 
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// operand maps: K-major rows (boxes of 128 rows x 64 columns), MN-major (64 x 64)
-int map_k(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols, int64_t ld = 0) {
-  return make_map(m, base, batch, rows, cols, 128, ld);
+// operand maps: K-major weights and rows (boxes of 128 and 64 rows x 64 columns), MN-major (64 x 64)
+int map_k(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols) {
+  return make_map(m, base, batch, rows, cols, BM);
 }
 int map_mn(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols, int64_t ld = 0) {
   return make_map(m, base, batch, rows, cols, 64, ld);
+}
+int map_rows(CUtensorMap *m, const void *base, const FfnShape &f, int64_t cols, int64_t ld = 0) {
+  return make_map(m, base, 1, f.rows, cols, ROW_BOX, ld);
 }
 int map_out(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols, int64_t ld = 0) {
   return make_map(m, base, batch, rows, cols, 32, ld);
@@ -587,10 +637,10 @@ Args base_args(const FfnShape &f) {
     if (_st != MUON_OK) return _st; \
   } while (0)
 
-int set_out(Args &p, int i, void *base, int64_t batch, int64_t rows, int64_t cols, int64_t ld) {
-  p.outp[i] = base;
-  p.out_ld[i] = ld;
-  return base ? map_out(&p.out[i], base, batch, rows, cols, ld) : MUON_OK;
+// an output of a row product, and of a weight gradient
+void set_rows(Args &p, int i, void *base, int64_t ld) { p.outp[i] = base, p.out_ld[i] = ld; }
+int set_dw(Args &p, int i, void *base, const FfnShape &f, int64_t rows, int64_t cols) {
+  return map_out(&p.out[i], base, f.experts, rows, cols);
 }
 
 }  // namespace
@@ -598,56 +648,56 @@ int set_out(Args &p, int i, void *base, int64_t batch, int64_t rows, int64_t col
 int ffn_up(const FfnShape &f, const void *x, int64_t ldx, const void *w1, const void *w3, void *hid, void *gate,
            void *up, cudaStream_t s) {
   Args p = base_args(f);
-  FFN_TRY(map_k(&p.a, x, 1, f.rows, f.hidden, ldx));
-  FFN_TRY(map_mn(&p.b, w1, f.experts, f.hidden, f.ffn));
-  FFN_TRY(map_mn(&p.b2, w3, f.experts, f.hidden, f.ffn));
-  FFN_TRY(set_out(p, 0, hid, 1, f.rows, f.ffn, f.ffn));
-  FFN_TRY(set_out(p, 1, gate, 1, f.rows, f.ffn, f.ffn));
-  FFN_TRY(set_out(p, 2, up, 1, f.rows, f.ffn, f.ffn));
+  FFN_TRY(map_rows(&p.b, x, f, f.hidden, ldx));
+  FFN_TRY(map_mn(&p.a, w1, f.experts, f.hidden, f.ffn));
+  FFN_TRY(map_mn(&p.a2, w3, f.experts, f.hidden, f.ffn));
+  set_rows(p, 0, hid, f.ffn);
+  set_rows(p, 1, gate, f.ffn);
+  set_rows(p, 2, up, f.ffn);
   p.N = (int)f.ffn;
   p.kblocks = cdiv(f.hidden, BK);
-  p.tiles_n = cdiv(f.ffn, BNH);
+  p.tiles_n = cdiv(f.ffn, BM);
   return launch<UP>(p, kTraceFfnUp, s);
 }
 
 int ffn_down(const FfnShape &f, const void *hid, const void *w2, void *y, int64_t ldy, cudaStream_t s) {
   Args p = base_args(f);
-  FFN_TRY(map_k(&p.a, hid, 1, f.rows, f.ffn));
-  FFN_TRY(map_mn(&p.b, w2, f.experts, f.ffn, f.hidden));
-  FFN_TRY(set_out(p, 0, y, 1, f.rows, f.hidden, ldy));
+  FFN_TRY(map_rows(&p.b, hid, f, f.ffn));
+  FFN_TRY(map_mn(&p.a, w2, f.experts, f.ffn, f.hidden));
+  set_rows(p, 0, y, ldy);
   p.N = (int)f.hidden;
   p.kblocks = cdiv(f.ffn, BK);
-  p.tiles_n = cdiv(f.hidden, BN);
+  p.tiles_n = cdiv(f.hidden, CM);
   return launch<DOWN>(p, kTraceFfnDown, s);
 }
 
 int ffn_dh(const FfnShape &f, const void *dy, int64_t lddy, const void *w2, const void *gate, const void *up, void *dg,
            void *du, void *hid, cudaStream_t s) {
   Args p = base_args(f);
-  FFN_TRY(map_k(&p.a, dy, 1, f.rows, f.hidden, lddy));
-  FFN_TRY(map_k(&p.b, w2, f.experts, f.ffn, f.hidden));
-  FFN_TRY(set_out(p, 0, dg, 1, f.rows, f.ffn, f.ffn));
-  FFN_TRY(set_out(p, 1, du, 1, f.rows, f.ffn, f.ffn));
-  FFN_TRY(set_out(p, 2, hid, 1, f.rows, f.ffn, f.ffn));
+  FFN_TRY(map_rows(&p.b, dy, f, f.hidden, lddy));
+  FFN_TRY(map_k(&p.a, w2, f.experts, f.ffn, f.hidden));
+  set_rows(p, 0, dg, f.ffn);
+  set_rows(p, 1, du, f.ffn);
+  set_rows(p, 2, hid, f.ffn);
   p.g = static_cast<const __nv_bfloat16 *>(gate);
   p.u = static_cast<const __nv_bfloat16 *>(up);
   p.N = (int)f.ffn;
   p.kblocks = cdiv(f.hidden, BK);
-  p.tiles_n = cdiv(f.ffn, BN);
+  p.tiles_n = cdiv(f.ffn, CM);
   return launch<DH>(p, kTraceFfnDh, s);
 }
 
 int ffn_dx(const FfnShape &f, const void *dg, const void *du, const void *w1, const void *w3, void *dx, int64_t lddx,
            cudaStream_t s) {
   Args p = base_args(f);
-  FFN_TRY(map_k(&p.a, dg, 1, f.rows, f.ffn));
-  FFN_TRY(map_k(&p.a2, du, 1, f.rows, f.ffn));
-  FFN_TRY(map_k(&p.b, w1, f.experts, f.hidden, f.ffn));
-  FFN_TRY(map_k(&p.b2, w3, f.experts, f.hidden, f.ffn));
-  FFN_TRY(set_out(p, 0, dx, 1, f.rows, f.hidden, lddx));
+  FFN_TRY(map_rows(&p.b, dg, f, f.ffn));
+  FFN_TRY(map_rows(&p.b2, du, f, f.ffn));
+  FFN_TRY(map_k(&p.a, w1, f.experts, f.hidden, f.ffn));
+  FFN_TRY(map_k(&p.a2, w3, f.experts, f.hidden, f.ffn));
+  set_rows(p, 0, dx, lddx);
   p.N = (int)f.hidden;
   p.kblocks = cdiv(f.ffn, BK);
-  p.tiles_n = cdiv(f.hidden, BN);
+  p.tiles_n = cdiv(f.hidden, CM);
   return launch<DX>(p, kTraceFfnDx, s);
 }
 
@@ -680,8 +730,8 @@ int ffn_dw(const FfnShape &f, const void *x, int64_t ldx, const void *dy, int64_
     FFN_TRY(map_mn(&p.b2, du, 1, f.rows, f.ffn));
     FFN_TRY(map_mn(&p.bt, ta.dst[2], f.experts, BK, f.ffn));
     FFN_TRY(map_mn(&p.bt2, ta.dst[3], f.experts, BK, f.ffn));
-    FFN_TRY(set_out(p, 0, dw1, f.experts, f.hidden, f.ffn, f.ffn));
-    FFN_TRY(set_out(p, 1, dw3, f.experts, f.hidden, f.ffn, f.ffn));
+    FFN_TRY(set_dw(p, 0, dw1, f, f.hidden, f.ffn));
+    FFN_TRY(set_dw(p, 1, dw3, f, f.hidden, f.ffn));
     p.M = (int)f.hidden;
     p.N = (int)f.ffn;
     p.tiles_m = cdiv(f.hidden, CM);
@@ -693,7 +743,7 @@ int ffn_dw(const FfnShape &f, const void *x, int64_t ldx, const void *dy, int64_
   FFN_TRY(map_mn(&p.a2, ta.dst[4], f.experts, BK, f.ffn));
   FFN_TRY(map_mn(&p.b, dy, 1, f.rows, f.hidden, lddy));
   FFN_TRY(map_mn(&p.bt, ta.dst[1], f.experts, BK, f.hidden));
-  FFN_TRY(set_out(p, 0, dw2, f.experts, f.ffn, f.hidden, f.hidden));
+  FFN_TRY(set_dw(p, 0, dw2, f, f.ffn, f.hidden));
   p.M = (int)f.ffn;
   p.N = (int)f.hidden;
   p.tiles_m = cdiv(f.ffn, CM);
