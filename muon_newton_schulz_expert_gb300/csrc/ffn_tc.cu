@@ -71,7 +71,6 @@ constexpr int TMEM_COLS = 2 * ACC_COLS;
 constexpr int NFULL = STAGES * KSUB;
 constexpr int NUM_BARS = NFULL + STAGES + 5;
 constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * BOX_BYTES + NUM_BARS * 8 + 16;
-constexpr int ROW_BOX = 64;          // rows of one load of a row product
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 
 enum Mode { UP = 0, DOWN, DH, DX, DW13, DW2 };
@@ -86,9 +85,14 @@ struct Form {
 };
 
 struct Args {
-  // operands: A (row products: weights; UP, DX: a2 = W3; DW: a2 = tail copy)
-  // and B (row products: rows; DX: b2 = dU; DW13: b2 = dU; DW: bt, bt2 tail copies)
-  CUtensorMap a, a2, b, b2, bt, bt2;
+  // weights of the row products (UP, DX: a2 = W3), A of the gradients (a2 = tail copy)
+  CUtensorMap a, a2;
+  union {
+    CUtensorMap rows_of[2][BN / UNIT];   // row products: boxes of 16, 32, .. 128 rows; DX: of dG and of dU
+    struct {
+      CUtensorMap b, b2, bt, bt2;        // gradients: B (DW13: dG, dU) and its tail copies
+    };
+  };
   CUtensorMap out[2];                // DW: boxes of 32 rows x 64 columns
   void *outp[3];
   long long out_ld[3];               // row strides in elements
@@ -99,6 +103,7 @@ struct Args {
   int kblocks;                       // row products: k-blocks of one K segment
   int tiles_m, tiles_n;              // DW: row tiles; all: column tiles
   int act;
+  bool wide;                         // 128-column operands load in one piece
   const __nv_bfloat16 *g, *u;        // DH: saved pre-activations [rows][N]
   unsigned *err;
   unsigned long long timeout_ns;
@@ -143,6 +148,18 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&lo)[32], ui
   // the registers are only valid from here on
 #pragma unroll
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(lo[i]), "+r"(hi[i]));
+}
+
+// 128 columns x 64 K-rows into two atoms of 64 columns: one load where the columns
+// are whole blocks of 64, two boxes otherwise.
+__device__ __forceinline__ void load_columns(uint32_t dst, const CUtensorMap *map, uint32_t bar, int col, int row, int z,
+                                             bool wide, unsigned *err) {
+  if (wide) {
+    tma_load_4d_pair(dst, map, bar, 0, row, col / 64, z, err);
+  } else {
+    tma_load_3d_pair(dst, map, bar, col, row, z, err);
+    tma_load_3d_pair(dst + 64 * BK * 2, map, bar, col + 64, row, z, err);
+  }
 }
 
 // Weight gradients: one epilogue warp's way out, 32 rows x 64 columns of bf16,
@@ -228,7 +245,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&p.a);
-    tma_prefetch_desc(&p.b);
+    if (Form<MODE>::dw) tma_prefetch_desc(&p.b);
     if (Form<MODE>::dw) tma_prefetch_desc(&p.out[0]);
   }
   if (warp == 1) {  // one warp in each CTA of the pair allocates the same columns in both
@@ -266,8 +283,8 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
                                         : cur.tj * CM + (int)rank * BM;
         const int n_b = Form<MODE>::paired ? cur.tj * BNH : cur.tj * BN + (int)rank * BNH;
         const int half_rows = cur.units * (UNIT / 2), row_b = cur.row0 + (int)rank * half_rows;
-        const uint32_t kb_bytes =
-            Form<MODE>::dw ? KB_BYTES : A_STAGE + (half_rows + ROW_BOX - 1) / ROW_BOX * (ROW_BOX * BK * 2);
+        const uint32_t kb_bytes = Form<MODE>::dw ? KB_BYTES : A_STAGE + half_rows * (BK * 2);
+        const CUtensorMap *row_maps = p.rows_of[0] + (cur.units - 1);   // boxes of half_rows rows
         const CUtensorMap *mb = Form<MODE>::paired && rank ? &p.b2 : &p.b;
         for (int kb = 0; kb < num_kb; kb += KSUB) {
           if (!wait_polled(empty(stage), phase ^ 1u, w)) {
@@ -294,24 +311,20 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
               const int kr = tail ? 0 : cur.lo + k * BK, z = tail ? cur.e : 0;
               const CUtensorMap *ma = tail ? &p.a2 : &p.a;
               const CUtensorMap *mbk = !tail ? mb : Form<MODE>::paired && rank ? &p.bt2 : &p.bt;
-#pragma unroll
-              for (int q = 0; q < 2; ++q)
-                tma_load_3d_pair(sa + q * (64 * BK * 2), ma, bar, mn_a + q * 64, kr, z, p.err);
-#pragma unroll
-              for (int q = 0; q < 2; ++q)
-                tma_load_3d_pair(sb + q * (64 * BK * 2), mbk, bar, n_b + q * 64, kr, z, p.err);
+              load_columns(sa, ma, bar, mn_a, kr, z, p.wide, p.err);
+              load_columns(sb, mbk, bar, n_b, kr, z, p.wide, p.err);
             } else {
               const bool second = MODE == DX && k >= p.kblocks;
               const int kc = (second ? k - p.kblocks : k) * BK;
-              if (Form<MODE>::a_mn) {   // boxes of 64 weight columns x 64 K-rows
+              if (MODE == UP) {         // boxes of 64 weight columns x 64 K-rows
                 tma_load_3d_pair(sa, &p.a, bar, mn_a, kc, cur.e, p.err);
-                tma_load_3d_pair(sa + 64 * BK * 2, MODE == UP ? &p.a2 : &p.a, bar, MODE == UP ? mn_a : mn_a + 64, kc,
-                                 cur.e, p.err);
+                tma_load_3d_pair(sa + 64 * BK * 2, &p.a2, bar, mn_a, kc, cur.e, p.err);
+              } else if (MODE == DOWN) {
+                load_columns(sa, &p.a, bar, mn_a, kc, cur.e, p.wide, p.err);
               } else {                  // one box of 128 weight rows x 64 K-columns
                 tma_load_3d_pair(sa, second ? &p.a2 : &p.a, bar, kc, mn_a, cur.e, p.err);
               }
-              for (int r = 0; r < half_rows; r += ROW_BOX)
-                tma_load_3d_pair(sb + r * (BK * 2), second ? &p.b2 : &p.b, bar, kc, row_b + r, 0, p.err);
+              tma_load_3d_pair(sb, second ? row_maps + BN / UNIT : row_maps, bar, kc, row_b, 0, p.err);
             }
           }
           if (++stage == STAGES) {
@@ -608,15 +621,21 @@ int launch(Args &p, int trace_kind, cudaStream_t s) {
 
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// operand maps: K-major weights and rows (boxes of 128 and 64 rows x 64 columns), MN-major (64 x 64)
+// operand maps: K-major weights (boxes of 128 rows x 64 columns), MN-major (64 x 64)
 int map_k(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols) {
   return make_map(m, base, batch, rows, cols, BM);
+}
+int map_cols(CUtensorMap *m, const Args &p, const void *base, int64_t batch, int64_t rows, int64_t cols, int64_t ld = 0) {
+  return p.wide ? make_map_blocks(m, base, batch, rows, cols, BK, 2, ld) : make_map(m, base, batch, rows, cols, BK, ld);
 }
 int map_mn(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols, int64_t ld = 0) {
   return make_map(m, base, batch, rows, cols, 64, ld);
 }
-int map_rows(CUtensorMap *m, const void *base, const FfnShape &f, int64_t cols, int64_t ld = 0) {
-  return make_map(m, base, 1, f.rows, cols, ROW_BOX, ld);
+// one box of exactly the rows that a tile's half has
+int map_rows(CUtensorMap (&m)[BN / UNIT], const void *base, const FfnShape &f, int64_t cols, int64_t ld = 0) {
+  for (int u = 0; u < BN / UNIT; ++u)
+    if (const int st = make_map(&m[u], base, 1, f.rows, cols, (u + 1) * UNIT / 2, ld)) return st;
+  return MUON_OK;
 }
 int map_out(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols, int64_t ld = 0) {
   return make_map(m, base, batch, rows, cols, 32, ld);
@@ -628,6 +647,7 @@ Args base_args(const FfnShape &f) {
   p.rows = f.rows;
   p.experts = (int)f.experts;
   p.act = f.act;
+  p.wide = f.hidden % 64 == 0 && f.ffn % 64 == 0;
   return p;
 }
 
@@ -648,7 +668,7 @@ int set_dw(Args &p, int i, void *base, const FfnShape &f, int64_t rows, int64_t 
 int ffn_up(const FfnShape &f, const void *x, int64_t ldx, const void *w1, const void *w3, void *hid, void *gate,
            void *up, cudaStream_t s) {
   Args p = base_args(f);
-  FFN_TRY(map_rows(&p.b, x, f, f.hidden, ldx));
+  FFN_TRY(map_rows(p.rows_of[0], x, f, f.hidden, ldx));
   FFN_TRY(map_mn(&p.a, w1, f.experts, f.hidden, f.ffn));
   FFN_TRY(map_mn(&p.a2, w3, f.experts, f.hidden, f.ffn));
   set_rows(p, 0, hid, f.ffn);
@@ -662,8 +682,8 @@ int ffn_up(const FfnShape &f, const void *x, int64_t ldx, const void *w1, const 
 
 int ffn_down(const FfnShape &f, const void *hid, const void *w2, void *y, int64_t ldy, cudaStream_t s) {
   Args p = base_args(f);
-  FFN_TRY(map_rows(&p.b, hid, f, f.ffn));
-  FFN_TRY(map_mn(&p.a, w2, f.experts, f.ffn, f.hidden));
+  FFN_TRY(map_rows(p.rows_of[0], hid, f, f.ffn));
+  FFN_TRY(map_cols(&p.a, p, w2, f.experts, f.ffn, f.hidden));
   set_rows(p, 0, y, ldy);
   p.N = (int)f.hidden;
   p.kblocks = cdiv(f.ffn, BK);
@@ -674,7 +694,7 @@ int ffn_down(const FfnShape &f, const void *hid, const void *w2, void *y, int64_
 int ffn_dh(const FfnShape &f, const void *dy, int64_t lddy, const void *w2, const void *gate, const void *up, void *dg,
            void *du, void *hid, cudaStream_t s) {
   Args p = base_args(f);
-  FFN_TRY(map_rows(&p.b, dy, f, f.hidden, lddy));
+  FFN_TRY(map_rows(p.rows_of[0], dy, f, f.hidden, lddy));
   FFN_TRY(map_k(&p.a, w2, f.experts, f.ffn, f.hidden));
   set_rows(p, 0, dg, f.ffn);
   set_rows(p, 1, du, f.ffn);
@@ -690,8 +710,8 @@ int ffn_dh(const FfnShape &f, const void *dy, int64_t lddy, const void *w2, cons
 int ffn_dx(const FfnShape &f, const void *dg, const void *du, const void *w1, const void *w3, void *dx, int64_t lddx,
            cudaStream_t s) {
   Args p = base_args(f);
-  FFN_TRY(map_rows(&p.b, dg, f, f.ffn));
-  FFN_TRY(map_rows(&p.b2, du, f, f.ffn));
+  FFN_TRY(map_rows(p.rows_of[0], dg, f, f.ffn));
+  FFN_TRY(map_rows(p.rows_of[1], du, f, f.ffn));
   FFN_TRY(map_k(&p.a, w1, f.experts, f.hidden, f.ffn));
   FFN_TRY(map_k(&p.a2, w3, f.experts, f.hidden, f.ffn));
   set_rows(p, 0, dx, lddx);
@@ -724,12 +744,12 @@ int ffn_dw(const FfnShape &f, const void *x, int64_t ldx, const void *dy, int64_
   FFN_TRY(trace_after(kTraceFfnTail, s));
   {
     Args p = base_args(f);
-    FFN_TRY(map_mn(&p.a, x, 1, f.rows, f.hidden, ldx));
-    FFN_TRY(map_mn(&p.a2, ta.dst[0], f.experts, BK, f.hidden));
-    FFN_TRY(map_mn(&p.b, dg, 1, f.rows, f.ffn));
-    FFN_TRY(map_mn(&p.b2, du, 1, f.rows, f.ffn));
-    FFN_TRY(map_mn(&p.bt, ta.dst[2], f.experts, BK, f.ffn));
-    FFN_TRY(map_mn(&p.bt2, ta.dst[3], f.experts, BK, f.ffn));
+    FFN_TRY(map_cols(&p.a, p, x, 1, f.rows, f.hidden, ldx));
+    FFN_TRY(map_cols(&p.a2, p, ta.dst[0], f.experts, BK, f.hidden));
+    FFN_TRY(map_cols(&p.b, p, dg, 1, f.rows, f.ffn));
+    FFN_TRY(map_cols(&p.b2, p, du, 1, f.rows, f.ffn));
+    FFN_TRY(map_cols(&p.bt, p, ta.dst[2], f.experts, BK, f.ffn));
+    FFN_TRY(map_cols(&p.bt2, p, ta.dst[3], f.experts, BK, f.ffn));
     FFN_TRY(set_dw(p, 0, dw1, f, f.hidden, f.ffn));
     FFN_TRY(set_dw(p, 1, dw3, f, f.hidden, f.ffn));
     p.M = (int)f.hidden;
@@ -739,10 +759,10 @@ int ffn_dw(const FfnShape &f, const void *x, int64_t ldx, const void *dy, int64_
     FFN_TRY(launch<DW13>(p, kTraceFfnDw13, s));
   }
   Args p = base_args(f);
-  FFN_TRY(map_mn(&p.a, hid, 1, f.rows, f.ffn));
-  FFN_TRY(map_mn(&p.a2, ta.dst[4], f.experts, BK, f.ffn));
-  FFN_TRY(map_mn(&p.b, dy, 1, f.rows, f.hidden, lddy));
-  FFN_TRY(map_mn(&p.bt, ta.dst[1], f.experts, BK, f.hidden));
+  FFN_TRY(map_cols(&p.a, p, hid, 1, f.rows, f.ffn));
+  FFN_TRY(map_cols(&p.a2, p, ta.dst[4], f.experts, BK, f.ffn));
+  FFN_TRY(map_cols(&p.b, p, dy, 1, f.rows, f.hidden, lddy));
+  FFN_TRY(map_cols(&p.bt, p, ta.dst[1], f.experts, BK, f.hidden));
   FFN_TRY(set_dw(p, 0, dw2, f, f.ffn, f.hidden));
   p.M = (int)f.ffn;
   p.N = (int)f.hidden;

@@ -140,6 +140,16 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1,
+                                                 int c2, int c3, unsigned *err) {
+  if (!dcheck((c0 & 15) == 0 && c2 >= 0 && c3 >= 0, err)) return;
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, "
+      "%6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -309,6 +319,23 @@ int make_map(CUtensorMap *map, const void *base, int64_t batch, int64_t rows, in
   cuuint32_t box[3] = {64u, (cuuint32_t)box_rows, 1u};
   cuuint32_t estr[3] = {1u, 1u, 1u};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MUON_OK : MUON_ERR_CUDA;
+}
+
+// The same array by blocks of 64 columns (cols is a multiple of 64): a box of
+// `blocks` of them is that many atoms, one after the other.
+int make_map_blocks(CUtensorMap *map, const void *base, int64_t batch, int64_t rows, int64_t cols, int box_rows,
+                    int blocks, int64_t pitch = 0) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return MUON_ERR_CUDA;
+  const cuuint64_t ld = (cuuint64_t)(pitch > 0 ? pitch : cols);
+  cuuint64_t dims[4] = {64u, (cuuint64_t)rows, (cuuint64_t)cols / 64, (cuuint64_t)batch};
+  cuuint64_t strides[3] = {ld * 2, 128u, (cuuint64_t)rows * ld * 2};
+  cuuint32_t box[4] = {64u, (cuuint32_t)box_rows, (cuuint32_t)blocks, 1u};
+  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? MUON_OK : MUON_ERR_CUDA;
