@@ -750,7 +750,7 @@ int ffn_dw(const FfnShape &f, const void *x, int64_t ldx, const void *dy, int64_
   ta.offsets = f.offsets;
   ta.rows = f.rows;
   trace_before(kTraceFfnTail, s);
-  ffn_tail_kernel<<<dim3((unsigned)f.experts, 8, 5), 256, 0, s>>>(ta);
+  ffn_tail_kernel<<<dim3((unsigned)f.experts, 24, 5), 256, 0, s>>>(ta);
   FFN_TRY(trace_after(kTraceFfnTail, s));
   {
     Args p = base_args(f);
