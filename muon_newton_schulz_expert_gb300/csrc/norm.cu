@@ -13,15 +13,17 @@
 //
 // One pass over memory.  A group of threads takes one row at a time and walks
 // the rows of the array; several groups on an SM overlap one's reductions with
-// another's loads.  The weights and a shared gate stay in L1, and so does the part of a row that is read a second time
-// after its reduction rather than held in registers.  The weights' gradients
+// another's loads.  The weights and a shared gate stay in L1, and so does the
+// part of a row that is read a second time after its reduction rather than held
+// in registers; the backward pass of wide rows has them in shared memory, copied
+// ahead (Stages), and the weights in registers.  The weights' gradients
 // stay in registers over a group's rows; each block writes its sums and a
 // second kernel adds them, in a fixed order (no atomics).  All arithmetic is
 // fp32, in pairs (f32x2) where vectors are moved.
 #include <algorithm>
 #include <type_traits>
 
-#include "common.cuh"
+#include "tc.cuh"
 
 namespace muon {
 namespace {
@@ -32,13 +34,9 @@ constexpr int kRowsPerCta = 4;   // rows of one CTA where a warp holds a whole r
 // Rows of more than 128 vectors give each thread kPlaces of them.  The largest
 // block of an instance and how many of them an SM has to hold fix its
 // registers: 56 a thread forward, 80 backward, where two sums per column are
-// kept besides.  Measured at 16384 x 6144: forward 240 us (86% of the measured
-// copy bandwidth; 245 us with 4 places and 4 blocks of 192 threads), backward
-// 300 us (59%; 315 us with 3 places and 2 blocks of 256, 332 us with one block
-// of 384 that keeps more in registers, 324 us with the next rows copied to
-// shared memory by cp.async): it is bound by the instructions it issues, about
-// 40 an element for 12 bytes.  Rows that need more threads than that take an
-// instance with wide blocks.
+// kept besides.  Measured at 16384 x 6144: forward 237 us (88% of the measured
+// copy bandwidth; 245 us with 4 places and 4 blocks of 192 threads).  Rows that
+// need more threads than that take an instance with wide blocks.
 constexpr int kPlaces = 2;
 constexpr int max_threads(int w, int vpt, bool backward) {
   if (w == 1) return vpt == 4 ? 512 : 1024;
@@ -329,6 +327,87 @@ struct BwdArgs {
   int64_t rows;
   int hidden;
   float scale;
+  // staged rows
+  int stages, stage_bytes;
+  unsigned *err;
+  unsigned long long timeout_ns;
+};
+
+// Rows on their way in: the four or five rows that one token's gradients read
+// (dr_out, r', dy, b and a gate of its own) are copied to shared memory whole,
+// by one thread and the copy engine, up to `stages` tokens ahead.  The threads
+// then spend no instructions and hold no registers on loads in flight, so that
+// few of them suffice and each has registers for the weights: the kernel was
+// bound by the instructions it issued (about 40 an element, 5 of every 8 vector
+// loads being of weights).  16384 x 6144 in bf16: 232 us (77% of the measured
+// copy bandwidth) against 301 us with plain loads, 2 blocks of 384 threads; 272 us
+// with the weights re-read and 512 threads, 317 us with 768 threads of one place,
+// 225 us with 256 threads of three, which takes 165 us where this takes 125 (30000 x
+// 2048).  8192 columns, fp32 stream: 334 against 493 us.
+// Every wait is bounded; after one that ran out the block goes on without
+// waiting, on whatever it has, and the error word says so.
+constexpr int kMaxStages = 8;
+template <typename R, typename B, bool GATE>
+struct Stages {
+  const BwdArgs &a;
+  unsigned long long *full;   // shared: a barrier for each slot
+  int *abort;
+  int slot = 0;
+  uint32_t phase = 0, issued = 0, parity = 0;   // thread 0: slots ever filled, and their last fill's parity
+
+  __device__ Stages(const BwdArgs &args, unsigned long long *bars, int *flag) : a(args), full(bars), abort(flag) {}
+  __device__ static uint8_t *rows_in() {
+    extern __shared__ __align__(128) uint8_t staged_rows[];
+    return staged_rows;
+  }
+  __device__ void fetch(int64_t row, int to_slot, uint32_t ph) {
+    issued |= 1u << to_slot;
+    parity = (parity & ~(1u << to_slot)) | (ph << to_slot);
+    const uint32_t bar = smem_u32(full + to_slot);
+    const uint32_t wide = (uint32_t)a.hidden * sizeof(R), narrow = (uint32_t)a.hidden * sizeof(B);
+    uint32_t to = smem_u32(rows_in()) + (uint32_t)(to_slot * a.stage_bytes);
+    mbar_expect_tx(bar, 2 * wide + (GATE ? 3 : 2) * narrow);
+    auto copy = [&](const Row &r, uint32_t bytes, int each) {
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+                   "l"(static_cast<const uint8_t *>(r.p) + row * r.stride * each), "r"(bytes), "r"(bar)
+                   : "memory");
+      to += bytes;
+    };
+    copy(a.dresidual_out, wide, sizeof(R));
+    copy(a.residual, wide, sizeof(R));
+    copy(a.dnormed, narrow, sizeof(B));
+    copy(a.block, narrow, sizeof(B));
+    if (GATE) copy(a.gate, narrow, sizeof(B));
+  }
+  // before a __syncthreads
+  __device__ void start(int64_t first, int64_t step) {
+    if (threadIdx.x != 0) return;
+    *abort = 0;
+    for (int i = 0; i < a.stages; ++i) mbar_init(smem_u32(full + i), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int i = 0; i < a.stages && first + i * step < a.rows; ++i) fetch(first + i * step, i, 0);
+  }
+  // the row at hand, complete
+  __device__ const uint8_t *wait() {
+    volatile int *flag = abort;
+    if (!*flag) wait_bounded(smem_u32(full + slot), phase, Watch{flag, a.err, a.timeout_ns});
+    return rows_in() + slot * a.stage_bytes;
+  }
+  // after a __syncthreads that follows wait(): every thread is done with the
+  // row before, whose slot takes the next one due
+  __device__ void next(int64_t row, int64_t first, int64_t step) {
+    const int64_t due = row + (a.stages - 1) * step;
+    if (threadIdx.x == 0 && row != first && due < a.rows && !*static_cast<volatile int *>(abort))
+      fetch(due, slot ? slot - 1 : a.stages - 1, slot ? phase ^ 1u : phase);
+    if (++slot == a.stages) slot = 0, phase ^= 1u;
+  }
+  // after the last row: if a wait ran out, copies may still be landing
+  __device__ void finish() {
+    if (threadIdx.x != 0 || !*static_cast<volatile int *>(abort)) return;
+    const unsigned long long limit = a.timeout_ns < 20000000ull ? a.timeout_ns : 20000000ull;
+    for (int i = 0; i < a.stages; ++i)
+      if (issued & (1u << i)) drain_wait(smem_u32(full + i), (parity >> i) & 1u, limit);
+  }
 };
 
 // The two means of a row come from one reduction of three sums over the raw
@@ -337,8 +416,8 @@ struct BwdArgs {
 //   db = q k dr - c2 b,       c2 = q^3 (S2 - c1 S3) / H,  S2 = sum k b z,  S3 = sum k b r'
 // For a shared gate, sum over rows of dr b q serves dw_post (times scale gate)
 // and dgate (times scale w_post) alike.
-template <typename R, typename B, int W, int VPT, int THREADS, int FORM>
-__global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, true))
+template <typename R, typename B, int W, int VPT, int THREADS, int FORM, bool STAGED = false>
+__global__ void __launch_bounds__(THREADS, STAGED ? 1 : blocks_per_sm(W, THREADS, true))
     block_norm_backward_kernel(const __grid_constant__ BwdArgs a) {
   __shared__ float4 red[2][3][8];
   using P = Item<W>;
@@ -352,6 +431,11 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, true))
   const bool from_above = full || a.dresidual_out.p;
   const bool gate_rows = full ? FORM == FULL_ROW_GATE : a.gate.p != nullptr;
   const bool gate_shared = full ? FORM == FULL_SHARED_GATE : a.shared_gate != nullptr;
+  // staged: rows come in through shared memory
+  __shared__ unsigned long long bars[STAGED ? kMaxStages : 1];
+  __shared__ int aborted;
+  Stages<R, B, FORM == FULL_ROW_GATE> staged(a, bars, &aborted);
+  if (STAGED) staged.start(group, groups);
   clear_sums<3>(red);
   P dwp[VPT][N], dwq[VPT][N];
 #pragma unroll
@@ -366,22 +450,74 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, true))
   Walk<B> db(a.dblock.p, a.dblock.stride, group, groups, c0);
   const B *w_post = static_cast<const B *>(a.w_post), *w_pre = static_cast<const B *>(a.w_pre);
   const B *shared_gate = static_cast<const B *>(a.shared_gate);
+  const R *dres_at = nullptr, *res_at = nullptr;   // this thread's columns of the row at hand
+  const B *dnorm_at = nullptr, *blk_at = nullptr, *gate_at = nullptr;
+  // staged: the weights stay in registers: w_pre, and w_post times a shared gate
+  P keep_pre[STAGED ? VPT : 1][N], keep_post[STAGED ? VPT : 1][N];
+  if constexpr (STAGED) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = c0 + i * across;
+#pragma unroll
+      for (int j = 0; j < N; ++j) keep_pre[i][j] = keep_post[i][j] = both<P>(0.f);
+      if (c < a.hidden) {
+        load(w_pre + c, keep_pre[i]);
+        load(w_post + c, keep_post[i]);
+        if (gate_shared) times<B, W>(shared_gate + c, keep_post[i]);
+      }
+    }
+  }
+  auto times_pre = [&](int i, P (&v)[N]) {
+    if constexpr (STAGED) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = mul(v[j], keep_pre[i][j]);
+    } else if (full || w_pre) {
+      times<B, W>(w_pre + c0 + i * across, v);
+    }
+  };
+  auto times_post = [&](int i, P (&v)[N]) {
+    if constexpr (STAGED) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = mul(v[j], keep_post[i][j]);
+    } else if (full || w_post) {
+      times<B, W>(w_post + c0 + i * across, v);
+    }
+  };
   // k / scale = gate w_post, in g
   auto factors = [&](int i, P (&g)[N]) {
     const int c = c0 + i * across;
+    if (STAGED && !gate_rows) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) g[j] = keep_post[STAGED ? i : 0][j];
+      return;
+    }
     if (gate_rows) {
-      load(gate.p + i * across, g);
+      load(gate_at + i * across, g);
     } else if (gate_shared) {
       load(shared_gate + c, g);
     } else {
 #pragma unroll
       for (int j = 0; j < N; ++j) g[j] = both<P>(1.f);
     }
-    if (full || w_post) times<B, W>(w_post + c, g);
+    times_post(i, g);
   };
   int turn = 0;
+  float p_next = 0.f, q_next = 0.f;   // staged: read a row ahead
+  if (STAGED) p_next = a.rstd_pre[group], q_next = a.rstd_post[group];
   for (int64_t row = group; row < a.rows; row += groups) {
-    const float p = pre ? a.rstd_pre[row] : 0.f, q = post ? a.rstd_post[row] : 0.f;
+    const float p = STAGED ? p_next : pre ? a.rstd_pre[row] : 0.f;
+    const float q = STAGED ? q_next : post ? a.rstd_post[row] : 0.f;
+    if constexpr (STAGED) {
+      if (row + groups < a.rows) p_next = a.rstd_pre[row + groups], q_next = a.rstd_post[row + groups];
+      const uint8_t *at = staged.wait();
+      dres_at = reinterpret_cast<const R *>(at) + c0;
+      res_at = dres_at + a.hidden;
+      dnorm_at = reinterpret_cast<const B *>(at + 2 * sizeof(R) * a.hidden) + c0;
+      blk_at = dnorm_at + a.hidden;
+      gate_at = blk_at + a.hidden;
+    } else {
+      dres_at = dres.p, res_at = res.p, dnorm_at = dnorm.p, blk_at = blk.p, gate_at = gate.p;
+    }
     P z[VPT][N];
     P s1 = both<P>(0.f), s2 = s1, s3 = s1;
     const P p2 = both<P>(p);
@@ -390,21 +526,21 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, true))
       if (c0 + i * across < a.hidden) {
         P r[N];
         if (from_above) {
-          load(dres.p + i * across, z[i]);
+          load(dres_at + i * across, z[i]);
         } else {
 #pragma unroll
           for (int j = 0; j < N; ++j) z[i][j] = both<P>(0.f);
         }
         if (pre) {
           P t[N];
-          load(res.p + i * across, r);
-          load(dnorm.p + i * across, t);
+          load(res_at + i * across, r);
+          load(dnorm_at + i * across, t);
 #pragma unroll
           for (int j = 0; j < N; ++j) {
             t[j] = mul(t[j], p2);
             dwp[i][j] = fma(t[j], r[j], dwp[i][j]);
           }
-          if (full || w_pre) times<B, W>(w_pre + c0 + i * across, t);
+          times_pre(i, t);
 #pragma unroll
           for (int j = 0; j < N; ++j) {
             s1 = fma(t[j], r[j], s1);
@@ -413,7 +549,7 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, true))
         }
         if (post) {
           P b[N], g[N];
-          load(blk.p + i * across, b);
+          load(blk_at + i * across, b);
           factors(i, g);
 #pragma unroll
           for (int j = 0; j < N; ++j) {
@@ -425,6 +561,7 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, true))
       }
     float sum[3] = {total(s1), total(s2), total(s3)};
     row_sums(sum, red[turn]);
+    if (STAGED) staged.next(row, group, groups);
     turn ^= 1;
     // s2 and s3 lack the factor scale
     const float c1 = p * p * sum[0] * inv_h, c2 = q * q * q * a.scale * (sum[1] - c1 * sum[2]) * inv_h;
@@ -434,25 +571,25 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, true))
       if (c0 + i * across < a.hidden) {
         if (pre) {
           P r[N];
-          load(res.p + i * across, r);
+          load(res_at + i * across, r);
 #pragma unroll
           for (int j = 0; j < N; ++j) z[i][j] = fma(c1n, r[j], z[i][j]);
         }
         if (full || dr.p) store(dr.p + i * across, z[i]);
         if (post) {
           P b[N], g[N];
-          load(blk.p + i * across, b);
+          load(blk_at + i * across, b);
 #pragma unroll
           for (int j = 0; j < N; ++j) z[i][j] = mul(z[i][j], q2);   // dr q
           if (full ? gate_rows : a.dgate.p != nullptr) {
             P v[N];
 #pragma unroll
             for (int j = 0; j < N; ++j) v[j] = mul(mul(z[i][j], b[j]), scale);
-            if (full || w_post) times<B, W>(w_post + c0 + i * across, v);
+            times_post(i, v);
             store(static_cast<B *>(a.dgate.p) + row * a.dgate.stride + c0 + i * across, v);
           }
           if (gate_rows) {
-            load(gate.p + i * across, g);
+            load(gate_at + i * across, g);
 #pragma unroll
             for (int j = 0; j < N; ++j) dwq[i][j] = fma(mul(z[i][j], g[j]), b[j], dwq[i][j]);
           } else {
@@ -468,6 +605,7 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, true))
     dres.next(), res.next(), dnorm.next(), blk.next(), gate.next();
     dr.next(), db.next();
   }
+  if (STAGED) staged.finish();
   if (!a.partial) return;
   // the block's sums: those of its groups where warps hold rows, through shared memory
   if (blockDim.y > 1) {
@@ -598,23 +736,83 @@ int launch_fwd(const FwdArgs &a, bool vec, cudaStream_t s) {
   return p.vpt == 8 ? launch_fwd_as<R, B, 1, 8>(a, p, s) : launch_fwd_as<R, B, 1, 16>(a, p, s);
 }
 
+// everything present: the forms other than ANY
+bool full_backward(const BwdArgs &a) {
+  return a.dresidual_out.p && a.dnormed.p && a.block.p && a.w_post && a.w_pre && a.dresidual.p && a.dblock.p &&
+         !a.gate.p == !a.dgate.p;
+}
+
 template <typename R, typename B, int W, int VPT, int THREADS = max_threads(W, VPT, true)>
 int launch_bwd_as(const BwdArgs &a, const Plan &p, cudaStream_t s) {
   auto go = [&](auto *kernel) { return launch_rows(kernel, a, p, true, kTraceBlockNormBwd, s); };
-  if (a.dresidual_out.p && a.dnormed.p && a.block.p && a.w_post && a.w_pre && a.dresidual.p && a.dblock.p &&
-      !a.gate.p == !a.dgate.p) {
-    if (a.gate.p) return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, FULL_ROW_GATE>);
-    if (a.shared_gate) return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, FULL_SHARED_GATE>);
-    return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, FULL>);
-  }
+  // bf16 branches of two places a thread and up to 384 threads are always staged
+  constexpr bool all_forms = !(W == 8 && VPT == kPlaces && THREADS == max_threads(W, VPT, true) && sizeof(B) == 2);
+  if constexpr (all_forms)
+    if (full_backward(a)) {
+      if (a.gate.p) return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, FULL_ROW_GATE>);
+      if (a.shared_gate) return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, FULL_SHARED_GATE>);
+      return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, FULL>);
+    }
   return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, ANY>);
 }
 
+// Backward, rows of more than 128 vectors with everything present: through
+// shared memory, where two rows or more fit.  Few threads with many registers:
+// 384 of 168 an SM with two places each, in as many blocks as that gives, or
+// one block of 256 with four places for rows that need it.
+constexpr int kStagedBytes = 216 * 1024;
+constexpr int staged_threads(int places) { return places == 2 ? 384 : 256; }
+
 template <typename R, typename B>
-int launch_bwd(const BwdArgs &a, bool vec, void *dw_pre, void *dw_post, void *dgate, cudaStream_t s) {
-  const Plan p = plan_rows(a.hidden, vec, true);
-  int st;
-  if (p.w == 8 && p.vpt == 1) st = launch_bwd_as<R, B, 8, 1>(a, p, s);
+bool stage_rows(BwdArgs &a, Plan &p, int *blocks) {
+  if (p.w != 8 || p.vpt != kPlaces || !full_backward(a)) return false;
+  const int places = a.hidden <= 8 * 2 * staged_threads(2) ? 2 : 4;
+  const int threads = (a.hidden / 8 + 32 * places - 1) / (32 * places) * 32;
+  const int bytes = a.hidden * (int)(2 * sizeof(R) + (a.gate.p ? 3 : 2) * sizeof(B));
+  a.stage_bytes = (bytes + 127) / 128 * 128;
+  const int per_sm = std::max(1, std::min(staged_threads(places) / threads, kStagedBytes / (2 * a.stage_bytes)));
+  a.stages = std::min(kMaxStages, kStagedBytes / per_sm / a.stage_bytes);
+  if (threads > staged_threads(places) || a.stages < 2) return false;
+  a.err = device_error_word();
+  a.timeout_ns = wait_timeout_ns();
+  if (!a.err) return false;
+  p.vpt = places, p.threads = threads;
+  *blocks = (int)std::min<int64_t>(a.rows, (int64_t)num_sms() * per_sm);
+  return true;
+}
+
+template <auto kernel>
+int launch_staged(const BwdArgs &a, const Plan &p, int blocks, cudaStream_t s) {
+  static std::once_flag attr_once[64];
+  static cudaError_t attr_err[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MUON_ERR_CUDA;
+  std::call_once(attr_once[dev], [&] {
+    attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedBytes);
+    cudaGetLastError();
+  });
+  if (attr_err[dev] != cudaSuccess) return MUON_ERR_CUDA;
+  trace_before(kTraceBlockNormBwd, s);
+  kernel<<<blocks, p.threads, a.stages * a.stage_bytes, s>>>(a);
+  return trace_after(kTraceBlockNormBwd, s);
+}
+
+template <typename R, typename B, int PLACES, int THREADS = staged_threads(PLACES)>
+int launch_staged_as(const BwdArgs &a, const Plan &p, int blocks, cudaStream_t s) {
+  if (a.gate.p)
+    return launch_staged<block_norm_backward_kernel<R, B, 8, PLACES, THREADS, FULL_ROW_GATE, true>>(a, p, blocks, s);
+  if (a.shared_gate)
+    return launch_staged<block_norm_backward_kernel<R, B, 8, PLACES, THREADS, FULL_SHARED_GATE, true>>(a, p, blocks, s);
+  return launch_staged<block_norm_backward_kernel<R, B, 8, PLACES, THREADS, FULL, true>>(a, p, blocks, s);
+}
+
+template <typename R, typename B>
+int launch_bwd(BwdArgs &a, bool vec, void *dw_pre, void *dw_post, void *dgate, cudaStream_t s) {
+  Plan p = plan_rows(a.hidden, vec, true);
+  int st, blocks = (int)(groups_of(p, a.rows, true) / p.rows_per_cta);
+  if (stage_rows<R, B>(a, p, &blocks)) {
+    st = p.vpt == 2 ? launch_staged_as<R, B, 2>(a, p, blocks, s) : launch_staged_as<R, B, 4>(a, p, blocks, s);
+  } else if (p.w == 8 && p.vpt == 1) st = launch_bwd_as<R, B, 8, 1>(a, p, s);
   else if (p.w == 8 && p.threads <= max_threads(8, kPlaces, true)) st = launch_bwd_as<R, B, 8, kPlaces>(a, p, s);
   else if (p.w == 8) st = launch_bwd_as<R, B, 8, kPlaces, kWideThreads>(a, p, s);
   else if (p.vpt == 4) st = launch_bwd_as<R, B, 1, 4>(a, p, s);
@@ -632,7 +830,7 @@ int launch_bwd(const BwdArgs &a, bool vec, void *dw_pre, void *dw_post, void *dg
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(
-      &cfg, norm_weight_sum_kernel<B>, (const float *)a.partial, groups_of(p, a.rows, true) / p.rows_per_cta, a.hidden,
+      &cfg, norm_weight_sum_kernel<B>, (const float *)a.partial, (int64_t)blocks, a.hidden,
       a.scale, static_cast<const B *>(a.w_post), static_cast<const B *>(a.shared_gate), static_cast<B *>(dw_pre),
       static_cast<B *>(dw_post), static_cast<B *>(dgate));
   if (e != cudaSuccess) {

@@ -260,3 +260,36 @@ def test_no_rows_and_refusals(mk):
         mk.muon_block_norm_backward(d["dr"], d["dy"], d["r"], None, None, torch.ones(4, device="cuda"),
                                     w_pre=d["w_pre"])
     assert err.value.status == -4 and mk.muon_inject_alloc_failures(0) == 0
+
+
+@pytest.mark.parametrize("T, H, types, gate", [
+    (9001, 1032, ("f32", "f32"), "rows"),      # several blocks of one SM, every slot filled several times
+    (5000, 2056, ("bf16", "bf16"), "shared"),
+    (2500, 6144, ("f32", "bf16"), "rows"),
+    (2500, 6144, ("bf16", "bf16"), "none"),
+    (1500, 6144, ("f32", "f32"), "rows"),      # too wide for two rows at once
+    (1500, 6152, ("f32", "bf16"), "shared"),
+    (1700, 8192, ("bf16", "bf16"), "rows"),
+    (900, 8200, ("bf16", "bf16"), "shared"),
+])
+def test_backward_of_rows_that_stream_in(mk, T, H, types, gate):
+    """Many rows a block, of arrays with gaps between the rows, which no copy may write to."""
+    rt, bt = (DT[t] for t in types)
+    d = inputs(T, H, rt, bt, gate, seed=5)
+    r, _, q, p = mk.muon_block_norm(d["r"], d["b"], w_post=d["w_post"], gate=d["gate"], w_pre=d["w_pre"])
+    wide = {}
+
+    def spread(t):   # the same rows, 16 elements apart
+        if t is None or t.dim() == 1:
+            return t
+        w = torch.full((T, H + 16), 3.0, dtype=t.dtype, device="cuda")
+        w[:, 8:H + 8] = t
+        wide[len(wide)] = w
+        return w[:, 8:H + 8]
+
+    got = mk.muon_block_norm_backward(spread(d["dr"]), spread(d["dy"]), spread(r), spread(d["b"]), q, p,
+                                      w_post=d["w_post"], gate=spread(d["gate"]), w_pre=d["w_pre"])
+    for k, (value, mags) in backward64(d, r, q, p, 1.0).items():
+        within(getattr(got, k), value, mags, k, extra=T * 2.0 ** -24)
+    for w in wide.values():
+        assert bool((w[:, :8] == 3).all()) and bool((w[:, H + 8:] == 3).all())
