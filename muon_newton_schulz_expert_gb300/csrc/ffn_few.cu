@@ -10,10 +10,10 @@
 // is cut into S parts (1 to 8) that the CTAs of a cluster take.  Each CTA
 // finishes a part of the tile's columns: all send it their parts of its sums
 // (fp32, distributed shared memory), and after a cluster barrier it adds them in
-// order of rank.  Stores to the others need no answer: reading the parts where they
-// were made took 1.2 to 3.3 us a tile, this 1.5 us less (one row, 6144 x 1792, from
-// HBM: 23.9 against 22.4 us; 64 rows 32.1 against 27.6 us).  No workspace, no atomics, one launch
-// per product.
+// order of rank.  Stores to the others need no answer: reading the parts where
+// they were made took 1.2 to 3.3 us a tile, this 1.5 us less (one row, 6144 x 1792,
+// from HBM: 23.9 against 22.4 us; 64 rows 32.1 against 27.6 us).  No workspace, no
+// atomics, one launch per product.
 //   UP    two accumulators (W1, W3) over one load of the rows; h = act(g) * u
 //   DOWN  y = h W2; h comes as two bf16 halves (value and remainder), which
 //         are 2 TN rows of one N, so h's rounding costs no accuracy and the
@@ -417,7 +417,8 @@ int launch(Args &p, const FfnShape &f, int trace_kind, cudaStream_t s) {
   p.split = 1;
   while (p.split < 8 && (p.split + 1) * tiles <= (int64_t)num_sms() * per_sm && 6 * (p.split + 1) <= all_kb) ++p.split;
   const size_t stage = MATS * A_BYTES + (size_t)(MODE == DOWN ? 2 : 1) * p.tn * BK * 2;
-  const size_t fixed = 1024 + (size_t)p.split * ((32 + p.split - 1) / p.split * 4) * MATS * p.tn * 4 + NUM_BARS * 8 + 16;
+  const size_t parts = (size_t)p.split * ((32 + p.split - 1) / p.split * 4) * MATS * p.tn * 4;
+  const size_t fixed = 1024 + parts + NUM_BARS * 8 + 16;
   const size_t budget = MODE != UP ? 112 * 1024 : p.tn == MAX_TN ? 220 * 1024 : 160 * 1024;
   p.stages = (int)std::min<size_t>({(size_t)MAX_STAGES, (budget - fixed) / stage,
                                     (size_t)std::max(2, (all_kb + p.split - 1) / p.split)});
@@ -432,7 +433,8 @@ int launch(Args &p, const FfnShape &f, int trace_kind, cudaStream_t s) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MUON_ERR_CUDA;
   std::call_once(attr_once[dev], [&] {
-    attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MODE == UP ? 220 * 1024 : 112 * 1024);
+    attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         MODE == UP ? 220 * 1024 : 112 * 1024);
     cudaGetLastError();
   });
   if (attr_err[dev] != cudaSuccess) return MUON_ERR_CUDA;

@@ -151,9 +151,10 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&lo)[32], ui
 }
 
 // 128 columns x 64 K-rows into two atoms of 64 columns: one load where the columns
-// are whole blocks of 64, two boxes otherwise.
-__device__ __forceinline__ void load_columns(uint32_t dst, const CUtensorMap *map, uint32_t bar, int col, int row, int z,
-                                             bool wide, unsigned *err) {
+// are whole blocks of 64, two boxes otherwise (16384 rows, 32 experts, 6144 x 1792:
+// dW1 and dW3 530 us with one, 555 us with two; dW2 281 and 291; DOWN the same).
+__device__ __forceinline__ void load_columns(uint32_t dst, const CUtensorMap *map, uint32_t bar, int col, int row,
+                                             int z, bool wide, unsigned *err) {
   if (wide) {
     tma_load_4d_pair(dst, map, bar, 0, row, col / 64, z, err);
   } else {
@@ -635,13 +636,16 @@ int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 int map_k(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols) {
   return make_map(m, base, batch, rows, cols, BM);
 }
-int map_cols(CUtensorMap *m, const Args &p, const void *base, int64_t batch, int64_t rows, int64_t cols, int64_t ld = 0) {
+int map_cols(CUtensorMap *m, const Args &p, const void *base, int64_t batch, int64_t rows, int64_t cols,
+             int64_t ld = 0) {
   return p.wide ? make_map_blocks(m, base, batch, rows, cols, BK, 2, ld) : make_map(m, base, batch, rows, cols, BK, ld);
 }
 int map_mn(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols, int64_t ld = 0) {
   return make_map(m, base, batch, rows, cols, 64, ld);
 }
-// one box of exactly the rows that a tile's half has
+// One box of exactly the rows that a tile's half has: boxes are paid for by the
+// piece and by the bytes (16384 rows, 32 experts, forward: 797 us; 816 with boxes of
+// 64 rows, 906 with exactly the rows in boxes of 64 and 16).
 int map_rows(CUtensorMap (&m)[BN / UNIT], const void *base, const FfnShape &f, int64_t cols, int64_t ld = 0) {
   for (int u = 0; u < BN / UNIT; ++u)
     if (const int st = make_map(&m[u], base, 1, f.rows, cols, (u + 1) * UNIT / 2, ld)) return st;

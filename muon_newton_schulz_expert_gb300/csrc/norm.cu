@@ -15,8 +15,8 @@
 // the rows of the array; several groups on an SM overlap one's reductions with
 // another's loads.  The weights and a shared gate stay in L1, and so does the
 // part of a row that is read a second time after its reduction rather than held
-// in registers; the backward pass of wide rows has them in shared memory, copied
-// ahead (Stages), and the weights in registers.  The weights' gradients
+// in registers; where rows have many bytes they come through shared memory, copied
+// ahead (Stages), and the weights are in registers.  The weights' gradients
 // stay in registers over a group's rows; each block writes its sums and a
 // second kernel adds them, in a fixed order (no atomics).  All arithmetic is
 // fp32, in pairs (f32x2) where vectors are moved.
@@ -34,9 +34,9 @@ constexpr int kRowsPerCta = 4;   // rows of one CTA where a warp holds a whole r
 // Rows of more than 128 vectors give each thread kPlaces of them.  The largest
 // block of an instance and how many of them an SM has to hold fix its
 // registers: 56 a thread forward, 80 backward, where two sums per column are
-// kept besides.  Measured at 16384 x 6144: forward 237 us (88% of the measured
-// copy bandwidth; 245 us with 4 places and 4 blocks of 192 threads).  Rows that
-// need more threads than that take an instance with wide blocks.
+// kept besides.  Measured at 16384 x 6144: forward in bf16 154 us (77% of the
+// measured copy bandwidth).  Rows that need more threads than that take an
+// instance with wide blocks.
 constexpr int kPlaces = 2;
 constexpr int max_threads(int w, int vpt, bool backward) {
   if (w == 1) return vpt == 4 ? 512 : 1024;
@@ -226,6 +226,88 @@ __device__ __forceinline__ void times(const T *w, Item<W> (&v)[kItems<W>]) {
   for (int j = 0; j < kItems<W>; ++j) v[j] = mul(v[j], x[j]);
 }
 
+// Rows on their way in: the rows that one token reads (backward: dr_out, r', dy, b
+// and a gate of its own; forward: r, b and the gate) are copied to shared memory
+// whole, by one thread and the copy engine, up to `stages` tokens ahead.  The threads
+// then spend no instructions and hold no registers on loads in flight, so that
+// few of them suffice and each has registers for the weights: the kernel was
+// bound by the instructions it issued (about 40 an element, 5 of every 8 vector
+// loads being of weights).  16384 x 6144 in bf16: 232 us (77% of the measured
+// copy bandwidth) against 301 us with plain loads, 2 blocks of 384 threads; 272 us
+// with the weights re-read and 512 threads, 317 us with 768 threads of one place,
+// 225 us with 256 threads of three, which takes 165 us where this takes 125 (30000 x
+// 2048).  8192 columns, fp32 stream: 334 against 493 us.
+// Every wait is bounded; after one that ran out the block goes on without
+// waiting, on whatever it has, and the error word says so.
+constexpr int kMaxStages = 8;
+struct Staging {
+  const uint8_t *src[5];     // in the order of their places in a slot
+  int64_t pitch[5];          // bytes from row to row
+  uint32_t bytes[5];
+  int count, stages, slot_bytes;
+  unsigned *err;
+  unsigned long long timeout_ns;
+};
+
+struct Stages {
+  const Staging &in;
+  const int64_t rows;
+  unsigned long long *full;   // shared: a barrier for each slot
+  int *abort;
+  int slot = 0;
+  uint32_t phase = 0, issued = 0, parity = 0;   // thread 0: slots ever filled, and their last fill's parity
+
+  __device__ Stages(const Staging &s, int64_t n, unsigned long long *bars, int *flag)
+      : in(s), rows(n), full(bars), abort(flag) {}
+  __device__ static uint8_t *rows_in() {
+    extern __shared__ __align__(128) uint8_t staged_rows[];
+    return staged_rows;
+  }
+  __device__ void fetch(int64_t row, int to_slot, uint32_t ph) {
+    issued |= 1u << to_slot;
+    parity = (parity & ~(1u << to_slot)) | (ph << to_slot);
+    const uint32_t bar = smem_u32(full + to_slot);
+    uint32_t to = smem_u32(rows_in()) + (uint32_t)(to_slot * in.slot_bytes), all = 0;
+    for (int i = 0; i < in.count; ++i) all += in.bytes[i];
+    mbar_expect_tx(bar, all);
+    for (int i = 0; i < in.count; ++i) {
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+                   "l"(in.src[i] + row * in.pitch[i]), "r"(in.bytes[i]), "r"(bar)
+                   : "memory");
+      to += in.bytes[i];
+    }
+  }
+  // before a __syncthreads
+  __device__ void start(int64_t first, int64_t step) {
+    if (threadIdx.x != 0) return;
+    *abort = 0;
+    for (int i = 0; i < in.stages; ++i) mbar_init(smem_u32(full + i), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int i = 0; i < in.stages && first + i * step < rows; ++i) fetch(first + i * step, i, 0);
+  }
+  // the row at hand, complete
+  __device__ const uint8_t *wait() {
+    volatile int *flag = abort;
+    if (!*flag) wait_bounded(smem_u32(full + slot), phase, Watch{flag, in.err, in.timeout_ns});
+    return rows_in() + slot * in.slot_bytes;
+  }
+  // after a __syncthreads that follows wait(): every thread is done with the
+  // row before, whose slot takes the next one due
+  __device__ void next(int64_t row, int64_t first, int64_t step) {
+    const int64_t due = row + (in.stages - 1) * step;
+    if (threadIdx.x == 0 && row != first && due < rows && !*static_cast<volatile int *>(abort))
+      fetch(due, slot ? slot - 1 : in.stages - 1, slot ? phase ^ 1u : phase);
+    if (++slot == in.stages) slot = 0, phase ^= 1u;
+  }
+  // after the last row: if a wait ran out, copies may still be landing
+  __device__ void finish() {
+    if (threadIdx.x != 0 || !*static_cast<volatile int *>(abort)) return;
+    const unsigned long long limit = in.timeout_ns < 20000000ull ? in.timeout_ns : 20000000ull;
+    for (int i = 0; i < in.stages; ++i)
+      if (issued & (1u << i)) drain_wait(smem_u32(full + i), (parity >> i) & 1u, limit);
+  }
+};
+
 struct FwdArgs {
   Row residual, block, gate;   // gate: a row for each token (a shared gate is a column factor)
   RowOut residual_out, normed;
@@ -234,10 +316,11 @@ struct FwdArgs {
   int64_t rows;
   int hidden;
   float scale, eps;
+  Staging in;
 };
 
-template <typename R, typename B, int W, int VPT, int THREADS, int FORM>
-__global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, false))
+template <typename R, typename B, int W, int VPT, int THREADS, int FORM, bool STAGED = false>
+__global__ void __launch_bounds__(THREADS, STAGED ? 1 : blocks_per_sm(W, THREADS, false))
     block_norm_kernel(const __grid_constant__ FwdArgs a) {
   __shared__ float4 red[2][1][8];
   using P = Item<W>;
@@ -249,6 +332,10 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, false))
   const bool post = full || a.block.p, pre = full || a.normed.p;
   const bool gate_rows = full ? FORM == FULL_ROW_GATE : a.gate.p != nullptr;
   const bool gate_shared = full ? FORM == FULL_SHARED_GATE : a.shared_gate != nullptr;
+  __shared__ unsigned long long bars[STAGED ? kMaxStages : 1];
+  __shared__ int aborted;
+  Stages staged(a.in, a.rows, bars, &aborted);
+  if (STAGED) staged.start(group, groups);
   clear_sums<1>(red);
   Walk<R> res(a.residual.p, a.residual.stride, group, groups, c0);
   Walk<B> blk(a.block.p, a.block.stride, group, groups, c0), gate(a.gate.p, a.gate.stride, group, groups, c0);
@@ -256,24 +343,48 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, false))
   Walk<B> y(a.normed.p, a.normed.stride, group, groups, c0);
   const B *w_post = static_cast<const B *>(a.w_post), *w_pre = static_cast<const B *>(a.w_pre);
   const B *shared_gate = static_cast<const B *>(a.shared_gate);
+  // staged: the weights stay in registers: w_pre, and w_post times a shared gate
+  P keep_pre[STAGED ? VPT : 1][N], keep_post[STAGED ? VPT : 1][N];
+  if constexpr (STAGED) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = c0 + i * across;
+#pragma unroll
+      for (int j = 0; j < N; ++j) keep_pre[i][j] = keep_post[i][j] = both<P>(0.f);
+      if (c < a.hidden) {
+        load(w_pre + c, keep_pre[i]);
+        load(w_post + c, keep_post[i]);
+        if (gate_shared) times<B, W>(shared_gate + c, keep_post[i]);
+      }
+    }
+  }
   int turn = 0;
   for (int64_t row = group; row < a.rows; row += groups) {
+    const R *res_at = res.p;   // this thread's columns of the row at hand
+    const B *blk_at = blk.p, *gate_at = gate.p;
+    if constexpr (STAGED) {
+      const uint8_t *at = staged.wait();
+      res_at = reinterpret_cast<const R *>(at) + c0;
+      blk_at = reinterpret_cast<const B *>(at + sizeof(R) * a.hidden) + c0;
+      gate_at = blk_at + a.hidden;
+    }
     P r[VPT][N], ss = both<P>(0.f);
     float q = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
-      if (c0 + i * across < a.hidden) load(res.p + i * across, r[i]);
+      if (c0 + i * across < a.hidden) load(res_at + i * across, r[i]);
     if (post) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
         if (c0 + i * across < a.hidden) {
           P b[N];
-          load(blk.p + i * across, b);
+          load(blk_at + i * across, b);
 #pragma unroll
           for (int j = 0; j < N; ++j) ss = fma(b[j], b[j], ss);
         }
       float sum[1] = {total(ss)};
       row_sums(sum, red[turn]);
+      if (STAGED) staged.next(row, group, groups);
       turn ^= 1;
       q = rsqrtf(fmaf(sum[0], inv_h, a.eps));
       if (threadIdx.x == 0 && a.rstd_post) a.rstd_post[row] = q;
@@ -286,10 +397,15 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, false))
         const int c = c0 + i * across;
         if (post) {
           P b[N];
-          load(blk.p + i * across, b);   // again, from L1
-          if (full || w_post) times<B, W>(w_post + c, b);
-          if (gate_rows) times<B, W>(gate.p + i * across, b);
-          else if (gate_shared) times<B, W>(shared_gate + c, b);
+          load(blk_at + i * across, b);   // again, from L1 or shared memory
+          if constexpr (STAGED) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) b[j] = mul(b[j], keep_post[i][j]);
+          } else if (full || w_post) {
+            times<B, W>(w_post + c, b);
+          }
+          if (gate_rows) times<B, W>(gate_at + i * across, b);
+          else if (gate_shared && !STAGED) times<B, W>(shared_gate + c, b);
 #pragma unroll
           for (int j = 0; j < N; ++j) r[i][j] = fma(b[j], qs, r[i][j]);
           store(out.p + i * across, r[i]);
@@ -310,12 +426,18 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(W, THREADS, false))
         if (c0 + i * across < a.hidden) {
 #pragma unroll
           for (int j = 0; j < N; ++j) r[i][j] = mul(r[i][j], p2);
-          if (full || w_pre) times<B, W>(w_pre + c0 + i * across, r[i]);
+          if constexpr (STAGED) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) r[i][j] = mul(r[i][j], keep_pre[i][j]);
+          } else if (full || w_pre) {
+            times<B, W>(w_pre + c0 + i * across, r[i]);
+          }
           store(y.p + i * across, r[i]);
         }
     }
     res.next(), blk.next(), gate.next(), out.next(), y.next();
   }
+  if (STAGED) staged.finish();
 }
 
 struct BwdArgs {
@@ -327,87 +449,7 @@ struct BwdArgs {
   int64_t rows;
   int hidden;
   float scale;
-  // staged rows
-  int stages, stage_bytes;
-  unsigned *err;
-  unsigned long long timeout_ns;
-};
-
-// Rows on their way in: the four or five rows that one token's gradients read
-// (dr_out, r', dy, b and a gate of its own) are copied to shared memory whole,
-// by one thread and the copy engine, up to `stages` tokens ahead.  The threads
-// then spend no instructions and hold no registers on loads in flight, so that
-// few of them suffice and each has registers for the weights: the kernel was
-// bound by the instructions it issued (about 40 an element, 5 of every 8 vector
-// loads being of weights).  16384 x 6144 in bf16: 232 us (77% of the measured
-// copy bandwidth) against 301 us with plain loads, 2 blocks of 384 threads; 272 us
-// with the weights re-read and 512 threads, 317 us with 768 threads of one place,
-// 225 us with 256 threads of three, which takes 165 us where this takes 125 (30000 x
-// 2048).  8192 columns, fp32 stream: 334 against 493 us.
-// Every wait is bounded; after one that ran out the block goes on without
-// waiting, on whatever it has, and the error word says so.
-constexpr int kMaxStages = 8;
-template <typename R, typename B, bool GATE>
-struct Stages {
-  const BwdArgs &a;
-  unsigned long long *full;   // shared: a barrier for each slot
-  int *abort;
-  int slot = 0;
-  uint32_t phase = 0, issued = 0, parity = 0;   // thread 0: slots ever filled, and their last fill's parity
-
-  __device__ Stages(const BwdArgs &args, unsigned long long *bars, int *flag) : a(args), full(bars), abort(flag) {}
-  __device__ static uint8_t *rows_in() {
-    extern __shared__ __align__(128) uint8_t staged_rows[];
-    return staged_rows;
-  }
-  __device__ void fetch(int64_t row, int to_slot, uint32_t ph) {
-    issued |= 1u << to_slot;
-    parity = (parity & ~(1u << to_slot)) | (ph << to_slot);
-    const uint32_t bar = smem_u32(full + to_slot);
-    const uint32_t wide = (uint32_t)a.hidden * sizeof(R), narrow = (uint32_t)a.hidden * sizeof(B);
-    uint32_t to = smem_u32(rows_in()) + (uint32_t)(to_slot * a.stage_bytes);
-    mbar_expect_tx(bar, 2 * wide + (GATE ? 3 : 2) * narrow);
-    auto copy = [&](const Row &r, uint32_t bytes, int each) {
-      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
-                   "l"(static_cast<const uint8_t *>(r.p) + row * r.stride * each), "r"(bytes), "r"(bar)
-                   : "memory");
-      to += bytes;
-    };
-    copy(a.dresidual_out, wide, sizeof(R));
-    copy(a.residual, wide, sizeof(R));
-    copy(a.dnormed, narrow, sizeof(B));
-    copy(a.block, narrow, sizeof(B));
-    if (GATE) copy(a.gate, narrow, sizeof(B));
-  }
-  // before a __syncthreads
-  __device__ void start(int64_t first, int64_t step) {
-    if (threadIdx.x != 0) return;
-    *abort = 0;
-    for (int i = 0; i < a.stages; ++i) mbar_init(smem_u32(full + i), 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    for (int i = 0; i < a.stages && first + i * step < a.rows; ++i) fetch(first + i * step, i, 0);
-  }
-  // the row at hand, complete
-  __device__ const uint8_t *wait() {
-    volatile int *flag = abort;
-    if (!*flag) wait_bounded(smem_u32(full + slot), phase, Watch{flag, a.err, a.timeout_ns});
-    return rows_in() + slot * a.stage_bytes;
-  }
-  // after a __syncthreads that follows wait(): every thread is done with the
-  // row before, whose slot takes the next one due
-  __device__ void next(int64_t row, int64_t first, int64_t step) {
-    const int64_t due = row + (a.stages - 1) * step;
-    if (threadIdx.x == 0 && row != first && due < a.rows && !*static_cast<volatile int *>(abort))
-      fetch(due, slot ? slot - 1 : a.stages - 1, slot ? phase ^ 1u : phase);
-    if (++slot == a.stages) slot = 0, phase ^= 1u;
-  }
-  // after the last row: if a wait ran out, copies may still be landing
-  __device__ void finish() {
-    if (threadIdx.x != 0 || !*static_cast<volatile int *>(abort)) return;
-    const unsigned long long limit = a.timeout_ns < 20000000ull ? a.timeout_ns : 20000000ull;
-    for (int i = 0; i < a.stages; ++i)
-      if (issued & (1u << i)) drain_wait(smem_u32(full + i), (parity >> i) & 1u, limit);
-  }
+  Staging in;
 };
 
 // The two means of a row come from one reduction of three sums over the raw
@@ -434,7 +476,7 @@ __global__ void __launch_bounds__(THREADS, STAGED ? 1 : blocks_per_sm(W, THREADS
   // staged: rows come in through shared memory
   __shared__ unsigned long long bars[STAGED ? kMaxStages : 1];
   __shared__ int aborted;
-  Stages<R, B, FORM == FULL_ROW_GATE> staged(a, bars, &aborted);
+  Stages staged(a.in, a.rows, bars, &aborted);
   if (STAGED) staged.start(group, groups);
   clear_sums<3>(red);
   P dwp[VPT][N], dwq[VPT][N];
@@ -725,9 +767,82 @@ int launch_fwd_as(const FwdArgs &a, const Plan &p, cudaStream_t s) {
   return go(block_norm_kernel<R, B, W, VPT, THREADS, ANY>);
 }
 
+// Rows of more than 128 vectors with everything present go through shared
+// memory, where two rows or more fit.  Few threads with many registers: backward 384
+// of 168 an SM with two places each, in as many blocks as that gives, or one block of
+// 256 with four places for rows that need it; forward 512 of 128.
+constexpr int kStagedBytes = 216 * 1024;
+constexpr int staged_threads(int places, bool backward) { return places == 4 ? 256 : backward ? 384 : 512; }
+
+// Forward, which waits for two sums a row, it takes rows of many bytes, or ones that
+// need wide blocks otherwise: 16384 x 6144 with an fp32 stream and a gate of its own
+// for each row (48 KB) 219 us staged, 237 us not; the shared gate (36 KB) 210 and 202;
+// bf16 (24 KB) 173 and 154; 8192 columns of bf16 (32 KB) 192 and 215.  And rows enough
+// to fill the slots more than once: 1200 rows of 48 KB take 22 us staged, 19 us not,
+// 2400 rows 41 and 44.
+constexpr int kStagedRowBytes = 40 * 1024;
+constexpr int64_t kStagedRows = 2048;
+
+// Adds the rows of one input to a slot.
+void stage_input(Staging &in, const Row &r, int hidden, int each) {
+  const int i = in.count++;
+  in.src[i] = static_cast<const uint8_t *>(r.p);
+  in.pitch[i] = r.stride * each;
+  in.bytes[i] = (uint32_t)(hidden * each);
+  in.slot_bytes += hidden * each;
+}
+
+bool stage_rows(Staging &in, Plan &p, int hidden, int64_t rows, bool backward, int *blocks) {
+  const int places = !backward || hidden <= 8 * 2 * staged_threads(2, true) ? 2 : 4;
+  const int most = staged_threads(places, backward);
+  const int threads = (hidden / 8 + 32 * places - 1) / (32 * places) * 32;
+  in.slot_bytes = (in.slot_bytes + 127) / 128 * 128;
+  const int per_sm = std::max(1, std::min(most / threads, kStagedBytes / (2 * in.slot_bytes)));
+  in.stages = std::min(kMaxStages, kStagedBytes / per_sm / in.slot_bytes);
+  if (threads > most || in.stages < 2) return false;
+  in.err = device_error_word();
+  in.timeout_ns = wait_timeout_ns();
+  if (!in.err) return false;
+  p.vpt = places, p.threads = threads;
+  *blocks = (int)std::min<int64_t>(rows, (int64_t)num_sms() * per_sm);
+  return true;
+}
+
+template <auto kernel, typename Args>
+int launch_staged(const Args &a, const Plan &p, int blocks, int trace, cudaStream_t s) {
+  static std::once_flag attr_once[64];
+  static cudaError_t attr_err[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MUON_ERR_CUDA;
+  std::call_once(attr_once[dev], [&] {
+    attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedBytes);
+    cudaGetLastError();
+  });
+  if (attr_err[dev] != cudaSuccess) return MUON_ERR_CUDA;
+  trace_before(trace, s);
+  kernel<<<blocks, p.threads, a.in.stages * a.in.slot_bytes, s>>>(a);
+  return trace_after(trace, s);
+}
+
 template <typename R, typename B>
-int launch_fwd(const FwdArgs &a, bool vec, cudaStream_t s) {
+int launch_fwd(FwdArgs &a, bool vec, cudaStream_t s) {
   const Plan p = plan_rows(a.hidden, vec, false);
+  if (p.w == 8 && p.vpt == kPlaces && a.block.p && a.normed.p && a.w_post && a.w_pre && a.rows >= kStagedRows) {
+    stage_input(a.in, a.residual, a.hidden, sizeof(R));
+    stage_input(a.in, a.block, a.hidden, sizeof(B));
+    if (a.gate.p) stage_input(a.in, a.gate, a.hidden, sizeof(B));
+    Plan q = p;
+    int blocks = 0;
+    if ((a.in.slot_bytes >= kStagedRowBytes || p.threads > max_threads(8, kPlaces, false)) &&
+        stage_rows(a.in, q, a.hidden, a.rows, false, &blocks)) {
+      constexpr int T = staged_threads(2, false), trace = kTraceBlockNorm;
+      if (a.gate.p)
+        return launch_staged<block_norm_kernel<R, B, 8, 2, T, FULL_ROW_GATE, true>>(a, q, blocks, trace, s);
+      if (a.shared_gate)
+        return launch_staged<block_norm_kernel<R, B, 8, 2, T, FULL_SHARED_GATE, true>>(a, q, blocks, trace, s);
+      return launch_staged<block_norm_kernel<R, B, 8, 2, T, FULL, true>>(a, q, blocks, trace, s);
+    }
+  }
   if (p.w == 8 && p.vpt == 1) return launch_fwd_as<R, B, 8, 1>(a, p, s);
   if (p.w == 8)
     return p.threads <= max_threads(8, kPlaces, false) ? launch_fwd_as<R, B, 8, kPlaces>(a, p, s)
@@ -756,61 +871,30 @@ int launch_bwd_as(const BwdArgs &a, const Plan &p, cudaStream_t s) {
   return go(block_norm_backward_kernel<R, B, W, VPT, THREADS, ANY>);
 }
 
-// Backward, rows of more than 128 vectors with everything present: through
-// shared memory, where two rows or more fit.  Few threads with many registers:
-// 384 of 168 an SM with two places each, in as many blocks as that gives, or
-// one block of 256 with four places for rows that need it.
-constexpr int kStagedBytes = 216 * 1024;
-constexpr int staged_threads(int places) { return places == 2 ? 384 : 256; }
-
-template <typename R, typename B>
-bool stage_rows(BwdArgs &a, Plan &p, int *blocks) {
-  if (p.w != 8 || p.vpt != kPlaces || !full_backward(a)) return false;
-  const int places = a.hidden <= 8 * 2 * staged_threads(2) ? 2 : 4;
-  const int threads = (a.hidden / 8 + 32 * places - 1) / (32 * places) * 32;
-  const int bytes = a.hidden * (int)(2 * sizeof(R) + (a.gate.p ? 3 : 2) * sizeof(B));
-  a.stage_bytes = (bytes + 127) / 128 * 128;
-  const int per_sm = std::max(1, std::min(staged_threads(places) / threads, kStagedBytes / (2 * a.stage_bytes)));
-  a.stages = std::min(kMaxStages, kStagedBytes / per_sm / a.stage_bytes);
-  if (threads > staged_threads(places) || a.stages < 2) return false;
-  a.err = device_error_word();
-  a.timeout_ns = wait_timeout_ns();
-  if (!a.err) return false;
-  p.vpt = places, p.threads = threads;
-  *blocks = (int)std::min<int64_t>(a.rows, (int64_t)num_sms() * per_sm);
-  return true;
-}
-
-template <auto kernel>
-int launch_staged(const BwdArgs &a, const Plan &p, int blocks, cudaStream_t s) {
-  static std::once_flag attr_once[64];
-  static cudaError_t attr_err[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MUON_ERR_CUDA;
-  std::call_once(attr_once[dev], [&] {
-    attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedBytes);
-    cudaGetLastError();
-  });
-  if (attr_err[dev] != cudaSuccess) return MUON_ERR_CUDA;
-  trace_before(kTraceBlockNormBwd, s);
-  kernel<<<blocks, p.threads, a.stages * a.stage_bytes, s>>>(a);
-  return trace_after(kTraceBlockNormBwd, s);
-}
-
-template <typename R, typename B, int PLACES, int THREADS = staged_threads(PLACES)>
+template <typename R, typename B, int PLACES, int T = staged_threads(PLACES, true)>
 int launch_staged_as(const BwdArgs &a, const Plan &p, int blocks, cudaStream_t s) {
+  constexpr int trace = kTraceBlockNormBwd;
   if (a.gate.p)
-    return launch_staged<block_norm_backward_kernel<R, B, 8, PLACES, THREADS, FULL_ROW_GATE, true>>(a, p, blocks, s);
+    return launch_staged<block_norm_backward_kernel<R, B, 8, PLACES, T, FULL_ROW_GATE, true>>(a, p, blocks, trace, s);
   if (a.shared_gate)
-    return launch_staged<block_norm_backward_kernel<R, B, 8, PLACES, THREADS, FULL_SHARED_GATE, true>>(a, p, blocks, s);
-  return launch_staged<block_norm_backward_kernel<R, B, 8, PLACES, THREADS, FULL, true>>(a, p, blocks, s);
+    return launch_staged<block_norm_backward_kernel<R, B, 8, PLACES, T, FULL_SHARED_GATE, true>>(a, p, blocks, trace, s);
+  return launch_staged<block_norm_backward_kernel<R, B, 8, PLACES, T, FULL, true>>(a, p, blocks, trace, s);
 }
 
 template <typename R, typename B>
 int launch_bwd(BwdArgs &a, bool vec, void *dw_pre, void *dw_post, void *dgate, cudaStream_t s) {
   Plan p = plan_rows(a.hidden, vec, true);
   int st, blocks = (int)(groups_of(p, a.rows, true) / p.rows_per_cta);
-  if (stage_rows<R, B>(a, p, &blocks)) {
+  bool staged = p.w == 8 && p.vpt == kPlaces && full_backward(a);
+  if (staged) {
+    stage_input(a.in, a.dresidual_out, a.hidden, sizeof(R));
+    stage_input(a.in, a.residual, a.hidden, sizeof(R));
+    stage_input(a.in, a.dnormed, a.hidden, sizeof(B));
+    stage_input(a.in, a.block, a.hidden, sizeof(B));
+    if (a.gate.p) stage_input(a.in, a.gate, a.hidden, sizeof(B));
+    staged = stage_rows(a.in, p, a.hidden, a.rows, true, &blocks);
+  }
+  if (staged) {
     st = p.vpt == 2 ? launch_staged_as<R, B, 2>(a, p, blocks, s) : launch_staged_as<R, B, 4>(a, p, blocks, s);
   } else if (p.w == 8 && p.vpt == 1) st = launch_bwd_as<R, B, 8, 1>(a, p, s);
   else if (p.w == 8 && p.threads <= max_threads(8, kPlaces, true)) st = launch_bwd_as<R, B, 8, kPlaces>(a, p, s);

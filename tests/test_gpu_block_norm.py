@@ -293,3 +293,38 @@ def test_backward_of_rows_that_stream_in(mk, T, H, types, gate):
         within(getattr(got, k), value, mags, k, extra=T * 2.0 ** -24)
     for w in wide.values():
         assert bool((w[:, :8] == 3).all()) and bool((w[:, H + 8:] == 3).all())
+
+
+@pytest.mark.parametrize("T, H, types, gate", [
+    (9001, 1032, ("f32", "f32"), "rows"),
+    (5000, 2056, ("bf16", "bf16"), "shared"),
+    (2500, 6144, ("f32", "bf16"), "rows"),
+    (2500, 6144, ("bf16", "bf16"), "none"),
+    (1500, 6152, ("f32", "f32"), "shared"),
+    (1700, 8192, ("f32", "f32"), "rows"),
+    (900, 16384, ("bf16", "bf16"), "none"),
+])
+def test_forward_of_rows_that_stream_in(mk, T, H, types, gate):
+    """Many rows a block, of arrays with gaps between the rows; the stream is updated in place."""
+    rt, bt = (DT[t] for t in types)
+    d = inputs(T, H, rt, bt, gate, seed=6)
+    R, mR, Y, mY, Q, P = forward64(d, -0.6, 1e-6)
+    wide = {}
+
+    def spread(t):
+        if t is None or t.dim() == 1:
+            return t
+        w = torch.full((T, H + 16), 3.0, dtype=t.dtype, device="cuda")
+        w[:, 8:H + 8] = t
+        wide[len(wide)] = w
+        return w[:, 8:H + 8]
+
+    stream, y = spread(d["r"]), spread(torch.zeros(T, H, dtype=bt, device="cuda"))
+    r, got, q, p = mk.muon_block_norm(stream, spread(d["b"]), w_post=d["w_post"], gate=spread(d["gate"]),
+                                      w_pre=d["w_pre"], scale=-0.6, out=stream, normed=y)
+    within(stream, R, mR, "r")
+    within(y, Y, mY, "y")
+    within(q, Q, Q, "rstd_post")
+    within(p, P, P, "rstd_pre", extra=2 * E32)
+    for w in wide.values():
+        assert bool((w[:, :8] == 3).all()) and bool((w[:, H + 8:] == 3).all())
