@@ -64,9 +64,9 @@ struct Scratch {
 // Which kernels take a row product with `cols` output columns (of tiles of
 // `tile`): where 256-row tiles leave pairs of CTAs without one, and an expert's
 // rows fit two row tiles of ffn_few.cu, its smaller tiles and cut K loop.
-// Measured at 6144 x 1792, one expert: 1 row 37 + 19 us against 14 + 10 us.
+// Measured at 6144 x 1792, one expert: 1 row 33 + 17 us against 17 + 15 us.
 // With more rows an expert the smaller tiles read the weights again for each:
-// 1777 rows, 5 experts, 1000 x 328: 21 + 13 us against 97 + 26 us.
+// 1777 rows, 5 experts, 1000 x 328: 19 + 13 us against 32 + 17 us.
 bool few_tiles(const FfnShape &f, int64_t cols, int64_t tile) {
   const int64_t active = std::min(f.experts, f.rows);
   return f.rows <= 128 * active && (f.rows / 256 + active) * ((cols + tile - 1) / tile) < num_sms() / 2;
