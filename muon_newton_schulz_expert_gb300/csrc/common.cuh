@@ -166,10 +166,11 @@ int ffn_few_dh(const FfnShape &f, const void *dy, int64_t lddy, const void *w2, 
                void *dg, void *du, void *hid, cudaStream_t s);
 int ffn_few_dx(const FfnShape &f, const void *dg, const void *du, const void *w1, const void *w3, void *dx,
                int64_t lddx, cudaStream_t s);
-// scratch of ffn_dw, in bf16 elements
+// scratch of ffn_dw: bf16 elements and fp32 elements
 size_t ffn_tail_elems(const FfnShape &f);
+size_t ffn_parts_elems(const FfnShape &f);
 int ffn_dw(const FfnShape &f, const void *x, int64_t ldx, const void *dy, int64_t lddy, const void *dg, const void *du,
-           const void *hid, void *tails, void *dw1, void *dw3, void *dw2, cudaStream_t s);
+           const void *hid, void *tails, float *parts, void *dw1, void *dw3, void *dw2, cudaStream_t s);
 
 // ---- fp32 SIMT GEMMs for the verification mode (gemm_f32.cu) ----
 // mode 0: C = s2 * P P^T (P m x k);  mode 1: C = b*P + c*P P (P m x m);

@@ -75,7 +75,9 @@ bool few_up(const FfnShape &f) { return few_tiles(f, f.ffn, 128); }
 
 size_t rows_bytes(const FfnShape &f) { return align256((size_t)f.rows * f.ffn * 2); }
 size_t fwd_bytes(const FfnShape &f) { return 2 * rows_bytes(f); }   // h, and for few rows what its rounding left
-size_t bwd_bytes(const FfnShape &f) { return 3 * rows_bytes(f) + align256(ffn_tail_elems(f) * 2); }
+size_t bwd_bytes(const FfnShape &f) {
+  return 3 * rows_bytes(f) + align256(ffn_tail_elems(f) * 2) + align256(ffn_parts_elems(f) * 4);
+}
 
 #define MUON_TRY(expr)              \
   do {                              \
@@ -88,12 +90,13 @@ int backward(const FfnShape &f, const void *dy, int64_t lddy, const void *x, int
              void *dw3, void *dw2, void *scratch, cudaStream_t s) {
   uint8_t *p = static_cast<uint8_t *>(scratch);
   void *dg = p, *du = p + rows_bytes(f), *hid = p + 2 * rows_bytes(f), *tails = p + 3 * rows_bytes(f);
+  float *parts = reinterpret_cast<float *>(p + 3 * rows_bytes(f) + align256(ffn_tail_elems(f) * 2));
   MUON_TRY(few_tiles(f, f.ffn, 256) ? ffn_few_dh(f, dy, lddy, w2, gate, up, dg, du, hid, s)
                                     : ffn_dh(f, dy, lddy, w2, gate, up, dg, du, hid, s));
   if (dx)
     MUON_TRY(few_tiles(f, f.hidden, 256) ? ffn_few_dx(f, dg, du, w1, w3, dx, lddx, s)
                                          : ffn_dx(f, dg, du, w1, w3, dx, lddx, s));
-  if (dw1) MUON_TRY(ffn_dw(f, x, ldx, dy, lddy, dg, du, hid, tails, dw1, dw3, dw2, s));
+  if (dw1) MUON_TRY(ffn_dw(f, x, ldx, dy, lddy, dg, du, hid, tails, parts, dw1, dw3, dw2, s));
   return MUON_OK;
 }
 

@@ -368,3 +368,26 @@ def test_refusals(mk):
         mk.muon_gated_ffn(x, w1, w3, w2, off)
     assert e.value.status == -4 and mk.muon_inject_alloc_failures(0) == 0
     assert mk.muon_get_device_status() == 0
+
+
+@pytest.mark.parametrize("sizes,H,F", [
+    ([9001], 136, 72),               # 16 parts, the last k-block of 41 rows
+    ([3000, 0, 211], 264, 136),      # an expert without rows, one with fewer k-blocks than it has parts
+    ([0, 2, 5500, 1], 256, 264),
+    ([4096, 4096], 520, 392),
+])
+def test_weight_gradients_of_long_cut_sums(mk, sizes, H, F):
+    """Few tiles and many rows: the rows are cut into parts."""
+    d = inputs(sizes, H, F, seed=11)
+    dw = tuple(torch.full_like(d[k], float("nan")) for k in ("w1", "w3", "w2"))
+    got = backward(mk, d, "silu", dw=dw)
+    assert mk.muon_get_device_status() == 0
+    ref = backward64(d, "silu")
+    for k in got:
+        check(got[k], ref[k], k)
+    again = backward(mk, d, "silu")
+    for k in got:
+        assert torch.equal(got[k], again[k])
+    for i, n in enumerate(sizes):
+        if n == 0:
+            assert all(not bool(t[i].any()) for t in dw)
