@@ -4,7 +4,8 @@ Argument marshalling only: every step runs in the CUDA kernels of
 ``_lib/libmuon.so`` (C ABI declared in ``include/muon.h``).  PyTorch supplies
 device memory and the current stream.  The operators around the step, whose
 calls last a few microseconds, are marshalled by ``_lib/muon_ops.so``
-(csrc/binding.cpp).  There is no fallback: when the library has not been built,
+(csrc/binding.cpp); the outputs that they make belong to the stream that the
+call runs on, as if it were the current one.  There is no fallback: when the library has not been built,
 every call raises ``MuonLibraryMissing``.
 
 Method: "Training a 1T-Parameter MoE on EU public infrastructure with PyTorch

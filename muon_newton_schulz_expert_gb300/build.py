@@ -70,8 +70,9 @@ def build_binding(force: bool = False) -> str:
     cmd = [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, "-isystem", os.path.join(home, "include"),
-           "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"), BINDING_SOURCE, "-o", tmp,
-           "-L", os.path.join(home, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
+           "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"), BINDING_SOURCE, "-o", tmp,
+           "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on binding.cpp:\n{r.stdout}\n{r.stderr}")

@@ -6,12 +6,19 @@
 // The C functions are handed over by address (bind), so that whichever build of
 // the library is loaded is the one that runs.  Every function returns its
 // outputs, or the muon_status as an integer when the call was refused.
+//
+// Outputs are allocated with the call's stream as PyTorch's current one: its
+// allocator hands a block out again to the stream that it was made for without
+// waiting, so a block made for any other stream could still be read by that
+// stream's work, or be handed on while this call writes it.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <optional>
 #include <string>
 
 #include "muon.h"
@@ -41,9 +48,38 @@ std::string shape_text(at::IntArrayRef s) {
   return r + ")";
 }
 
-// One call's tensors: all on the device of the first.
+double number(PyObject *o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Error{nullptr, ""};
+  return v;
+}
+long long integer(PyObject *o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Error{nullptr, ""};
+  return v;
+}
+
+// One call's tensors, all on the device of the first, and its stream.
 struct Call {
   int device = -1;
+  cudaStream_t handle;
+  std::optional<c10::cuda::CUDAStreamGuard> guard;
+  bool entered = false;
+
+  explicit Call(PyObject *stream) : handle(reinterpret_cast<cudaStream_t>((uintptr_t)integer(stream))) {}
+
+  // From here to the call's end its stream is PyTorch's current one.
+  void enter() {
+    if (entered) return;
+    entered = true;
+    if (c10::cuda::getCurrentCUDAStream().stream() != handle)
+      guard.emplace(c10::cuda::getStreamFromExternal(handle, c10::cuda::current_device()));
+  }
+  at::Tensor empty(at::IntArrayRef sizes, const at::TensorOptions &options) {
+    enter();
+    return at::empty(sizes, options);
+  }
+  muon_stream_t stream() const { return reinterpret_cast<muon_stream_t>(handle); }
 
   const at::Tensor &tensor(PyObject *o, const char *name) {
     if (!THPVariable_Check(o)) type_error(std::string(name) + " must be a CUDA tensor");
@@ -117,7 +153,7 @@ struct Out {
 Out out_rows(Call &c, PyObject *o, const char *name, const at::Tensor &like, int64_t n, int64_t cols, int64_t *stride) {
   Out r;
   if (o == Py_None) {
-    r.t = at::empty({n, cols}, like.options());
+    r.t = c.empty({n, cols}, like.options());
     *stride = cols;
   } else {
     r.t = c.rows(o, name, like.scalar_type(), n, cols, stride);
@@ -140,18 +176,6 @@ PyObject *tuple_of(std::initializer_list<const Out *> outs) {
   }
   return r;
 }
-
-double number(PyObject *o) {
-  const double v = PyFloat_AsDouble(o);
-  if (v == -1.0 && PyErr_Occurred()) throw Error{nullptr, ""};
-  return v;
-}
-long long integer(PyObject *o) {
-  const long long v = PyLong_AsLongLong(o);
-  if (v == -1 && PyErr_Occurred()) throw Error{nullptr, ""};
-  return v;
-}
-muon_stream_t stream_of(PyObject *o) { return reinterpret_cast<muon_stream_t>((uintptr_t)integer(o)); }
 
 // Runs a function's body; its exceptions become Python's.
 template <typename F>
@@ -197,21 +221,21 @@ struct Ffn {
 // (x, w1, w3, w2, offsets, act, keep, out, workspace, stream)
 PyObject *gated_ffn(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded(n, 10, [&]() -> PyObject * {
-    Call c;
+    Call c(a[9]);
     const Ffn f(c, a[0], a[1], a[2], a[3], a[4]);
     const bool keep = PyObject_IsTrue(a[6]);
     int64_t ldy;
     const Out y = out_rows(c, a[7], "out", *f.x, f.T, f.H, &ldy);
     Out gate, up;
     if (keep) {
-      gate.t = at::empty({f.T, f.F}, f.x->options());
-      up.t = at::empty({f.T, f.F}, f.x->options());
+      gate.t = c.empty({f.T, f.F}, f.x->options());
+      up.t = c.empty({f.T, f.F}, f.x->options());
     }
     size_t bytes;
     void *ws = c.workspace(a[8], &bytes);
     const int st = p_gated_ffn(f.x->data_ptr(), f.ldx, f.w1->data_ptr(), f.w3->data_ptr(), f.w2->data_ptr(), f.offsets,
                                f.T, f.E, f.H, f.F, (int)integer(a[5]), y.t.data_ptr(), ldy, opt(gate.t), opt(up.t), ws,
-                               bytes, stream_of(a[9]));
+                               bytes, c.stream());
     if (st != MUON_OK) return PyLong_FromLong(st);
     return keep ? tuple_of({&y, &gate, &up}) : y.object();
   });
@@ -220,7 +244,7 @@ PyObject *gated_ffn(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // (dy, x, gate, up, w1, w3, w2, offsets, act, dx, dw, need_dx, need_dw, workspace, stream)
 PyObject *gated_ffn_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded(n, 15, [&]() -> PyObject * {
-    Call c;
+    Call c(a[14]);
     const Ffn f(c, a[1], a[4], a[5], a[6], a[7]);
     int64_t lddy, lddx = f.H;
     const at::Tensor &dy = c.rows(a[0], "dy", at::kBFloat16, f.T, f.H, &lddy);
@@ -232,7 +256,7 @@ PyObject *gated_ffn_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (PyObject_IsTrue(a[12])) {
       static const char *names[3] = {"dw1", "dw3", "dw2"};
       if (a[10] == Py_None) {
-        for (int i = 0; i < 3; ++i) dw[i].t = at::empty(w[i]->sizes(), w[i]->options());
+        for (int i = 0; i < 3; ++i) dw[i].t = c.empty(w[i]->sizes(), w[i]->options());
       } else {
         if (!PyTuple_Check(a[10]) || PyTuple_GET_SIZE(a[10]) != 3) value_error("dw must be (dw1, dw3, dw2)");
         for (int i = 0; i < 3; ++i) {
@@ -246,7 +270,7 @@ PyObject *gated_ffn_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int st = p_gated_ffn_backward(dy.data_ptr(), lddy, f.x->data_ptr(), f.ldx, gate.data_ptr(), up.data_ptr(),
                                         f.w1->data_ptr(), f.w3->data_ptr(), f.w2->data_ptr(), f.offsets, f.T, f.E, f.H,
                                         f.F, (int)integer(a[8]), opt(dx.t), lddx, opt(dw[0].t), opt(dw[1].t),
-                                        opt(dw[2].t), ws, bytes, stream_of(a[14]));
+                                        opt(dw[2].t), ws, bytes, c.stream());
     if (st != MUON_OK) return PyLong_FromLong(st);
     return tuple_of({&dx, &dw[0], &dw[1], &dw[2]});
   });
@@ -265,7 +289,7 @@ bool given(PyObject *o) { return o != Py_None; }
 // (residual, block, w_post, gate, w_pre, scale, eps, norm_next, out, normed, stream)
 PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded(n, 11, [&]() -> PyObject * {
-    Call c;
+    Call c(a[10]);
     const at::Tensor &res = c.tensor(a[0], "residual");
     if (res.dim() != 2) value_error("residual must be (rows, hidden)");
     const int64_t T = res.size(0), H = res.size(1);
@@ -286,7 +310,7 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
       if (given(a[3])) k.gate = gate_of(c, a[3], bt, T, H, &k.gate_stride).data_ptr();
       out = out_rows(c, a[8], "out", res, T, H, &k.residual_out_stride);
       k.residual_out = out.t.data_ptr();
-      rstd_post.t = at::empty({T}, f32);
+      rstd_post.t = c.empty({T}, f32);
       k.rstd_post = rstd_post.t.data_ptr<float>();
     } else {
       if (given(a[2]) || given(a[3]) || given(a[8])) value_error("w_post, gate and out belong to a block");
@@ -297,12 +321,12 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
       if (given(a[4])) k.w_pre = c.dense(a[4], "w_pre", bt, {H}).data_ptr();
       normed = out_rows(c, a[9], "normed", branch, T, H, &k.normed_stride);
       k.normed = normed.t.data_ptr();
-      rstd_pre.t = at::empty({T}, f32);
+      rstd_pre.t = c.empty({T}, f32);
       k.rstd_pre = rstd_pre.t.data_ptr<float>();
     } else if (given(a[4]) || given(a[9])) {
       value_error("w_pre and normed belong to the norm before the next block");
     }
-    const int st = p_block_norm(&k, stream_of(a[10]));
+    const int st = p_block_norm(&k, c.stream());
     if (st != MUON_OK) return PyLong_FromLong(st);
     return tuple_of({&out, &normed, &rstd_post, &rstd_pre});
   });
@@ -311,7 +335,7 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // (dresidual, dnormed, residual, block, rstd_post, rstd_pre, w_post, gate, w_pre, scale, workspace, stream)
 PyObject *block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded(n, 12, [&]() -> PyObject * {
-    Call c;
+    Call c(a[11]);
     const at::Tensor &res = c.tensor(a[2], "residual");
     if (res.dim() != 2) value_error("residual must be (rows, hidden)");
     const int64_t T = res.size(0), H = res.size(1);
@@ -331,7 +355,7 @@ PyObject *block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
       k.rstd_pre = static_cast<const float *>(c.dense(a[5], "rstd_pre", at::kFloat, {T}).data_ptr());
       if (given(a[8])) {
         k.w_pre = c.dense(a[8], "w_pre", bt, {H}).data_ptr();
-        dw_pre.t = at::empty({H}, branch.options());
+        dw_pre.t = c.empty({H}, branch.options());
         k.dw_pre = dw_pre.t.data_ptr();
       }
     } else if (given(a[8])) {
@@ -340,27 +364,27 @@ PyObject *block_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (post) {
       k.block = c.rows(a[3], "block", bt, T, H, &k.block_stride).data_ptr();
       k.rstd_post = static_cast<const float *>(c.dense(a[4], "rstd_post", at::kFloat, {T}).data_ptr());
-      dblock.t = at::empty({T, H}, branch.options());
+      dblock.t = c.empty({T, H}, branch.options());
       k.dblock = dblock.t.data_ptr(), k.dblock_stride = H;
       if (given(a[6])) {
         k.w_post = c.dense(a[6], "w_post", bt, {H}).data_ptr();
-        dw_post.t = at::empty({H}, branch.options());
+        dw_post.t = c.empty({H}, branch.options());
         k.dw_post = dw_post.t.data_ptr();
       }
       if (given(a[7])) {
         const at::Tensor &g = gate_of(c, a[7], bt, T, H, &k.gate_stride);
         k.gate = g.data_ptr();
-        dgate.t = at::empty(g.sizes(), branch.options());
+        dgate.t = c.empty(g.sizes(), branch.options());
         k.dgate = dgate.t.data_ptr(), k.dgate_stride = H;
       }
     } else if (given(a[6]) || given(a[7])) {
       value_error("w_post and gate belong to a block");
     }
-    dr.t = at::empty({T, H}, res.options());
+    dr.t = c.empty({T, H}, res.options());
     k.dresidual = dr.t.data_ptr(), k.dresidual_stride = H;
     size_t bytes;
     void *ws = c.workspace(a[10], &bytes);
-    const int st = p_block_norm_backward(&k, ws, bytes, stream_of(a[11]));
+    const int st = p_block_norm_backward(&k, ws, bytes, c.stream());
     if (st != MUON_OK) return PyLong_FromLong(st);
     return tuple_of({&dr, &dblock, &dw_post, &dgate, &dw_pre});
   });
@@ -383,7 +407,7 @@ const int64_t *tokens_of(Call &c, PyObject *o, int64_t T) {
 // (logits, tokens, top, stream)
 PyObject *token_logprobs(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded(n, 4, [&]() -> PyObject * {
-    Call c;
+    Call c(a[3]);
     int64_t T, V, stride;
     int code;
     const at::Tensor &x = logits_of(c, a[0], &T, &V, &stride, &code);
@@ -392,17 +416,17 @@ PyObject *token_logprobs(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (top < -1000000 || top > 1000000) value_error("top is out of range");
     const auto f32 = x.options().dtype(at::kFloat);
     Out logp, entropy, lse, ids, values;
-    if (given(a[1])) logp.t = at::empty({T}, f32);
-    entropy.t = at::empty({T}, f32);
-    lse.t = at::empty({T}, f32);
+    if (given(a[1])) logp.t = c.empty({T}, f32);
+    entropy.t = c.empty({T}, f32);
+    lse.t = c.empty({T}, f32);
     if (top > 0) {
-      ids.t = at::empty({T, top}, x.options().dtype(at::kLong));
-      values.t = at::empty({T, top}, f32);
+      ids.t = c.empty({T, top}, x.options().dtype(at::kLong));
+      values.t = c.empty({T, top}, f32);
     }
     const int st = p_token_logprobs(x.data_ptr(), stride, tokens, T, V, code, static_cast<float *>(opt(logp.t)),
                                     entropy.t.data_ptr<float>(), lse.t.data_ptr<float>(), (int)top,
                                     static_cast<int64_t *>(opt(ids.t)), static_cast<float *>(opt(values.t)),
-                                    stream_of(a[3]));
+                                    c.stream());
     if (st != MUON_OK) return PyLong_FromLong(st);
     return tuple_of({&logp, &entropy, &lse, &ids, &values});
   });
@@ -411,7 +435,7 @@ PyObject *token_logprobs(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // (logits, tokens, lse, entropy, dlogp, dentropy, out, stream)
 PyObject *token_logprobs_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded(n, 8, [&]() -> PyObject * {
-    Call c;
+    Call c(a[7]);
     int64_t T, V, stride, out_stride;
     int code;
     const at::Tensor &x = logits_of(c, a[0], &T, &V, &stride, &code);
@@ -425,7 +449,7 @@ PyObject *token_logprobs_backward(PyObject *, PyObject *const *a, Py_ssize_t n) 
         in[i] = static_cast<const float *>(c.dense(a[2 + i], names[i], at::kFloat, {T}).data_ptr());
     const Out out = out_rows(c, a[6], "out", x, T, V, &out_stride);
     const int st = p_token_logprobs_backward(x.data_ptr(), stride, tokens, in[0], in[1], in[2], in[3], T, V, code,
-                                             out.t.data_ptr(), out_stride, stream_of(a[7]));
+                                             out.t.data_ptr(), out_stride, c.stream());
     if (st != MUON_OK) return PyLong_FromLong(st);
     return out.object();
   });
