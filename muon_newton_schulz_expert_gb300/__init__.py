@@ -454,11 +454,14 @@ def _ops():
 
 
 def _raw_stream(stream):
-    """The stream's handle; None is the current stream of the current device."""
+    """The stream's handle and device; None is the current stream of the current device, which a bare handle is on too."""
+    from torch import _C
     if stream is None:
-        from torch import _C
-        return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        device = _C._cuda_getDevice()
+        return _C._cuda_getCurrentRawStream(device), device
+    if hasattr(stream, "cuda_stream"):
+        return stream.cuda_stream, stream.device_index
+    return int(stream), _C._cuda_getDevice()
 
 
 def _outputs(call, result):

@@ -59,34 +59,44 @@ long long integer(PyObject *o) {
   return v;
 }
 
-// One call's tensors, all on the device of the first, and its stream.
+// One call's stream and tensors, all on one device.
 struct Call {
-  int device = -1;
+  int device;
   cudaStream_t handle;
   std::optional<c10::cuda::CUDAStreamGuard> guard;
   bool entered = false;
 
-  explicit Call(PyObject *stream) : handle(reinterpret_cast<cudaStream_t>((uintptr_t)integer(stream))) {}
+  // the stream's handle and its device, or the handle alone: of the current device
+  explicit Call(PyObject *stream) {
+    const bool both = PyTuple_Check(stream) && PyTuple_GET_SIZE(stream) == 2;
+    handle = reinterpret_cast<cudaStream_t>((uintptr_t)integer(both ? PyTuple_GET_ITEM(stream, 0) : stream));
+    device = both ? (int)integer(PyTuple_GET_ITEM(stream, 1)) : -1;
+  }
 
-  // From here to the call's end its stream is PyTorch's current one.
+  // From here to the call's end its stream and device are PyTorch's current ones.
   void enter() {
     if (entered) return;
     entered = true;
-    if (c10::cuda::getCurrentCUDAStream().stream() != handle)
-      guard.emplace(c10::cuda::getStreamFromExternal(handle, c10::cuda::current_device()));
+    if (c10::cuda::current_device() != device || c10::cuda::getCurrentCUDAStream(device).stream() != handle)
+      guard.emplace(c10::cuda::getStreamFromExternal(handle, device));
   }
   at::Tensor empty(at::IntArrayRef sizes, const at::TensorOptions &options) {
     enter();
     return at::empty(sizes, options);
   }
-  muon_stream_t stream() const { return reinterpret_cast<muon_stream_t>(handle); }
+  muon_stream_t stream() {
+    enter();
+    return reinterpret_cast<muon_stream_t>(handle);
+  }
 
   const at::Tensor &tensor(PyObject *o, const char *name) {
     if (!THPVariable_Check(o)) type_error(std::string(name) + " must be a CUDA tensor");
     const at::Tensor &t = THPVariable_Unpack(o);
     if (!t.is_cuda()) type_error(std::string(name) + " must be a CUDA tensor");
-    if (device < 0) device = t.get_device();
-    if (t.get_device() != device) value_error("all tensors must be on one device");
+    if (device < 0) device = c10::cuda::current_device();
+    if (t.get_device() != device)   // a launch on one device with another's memory
+      value_error(std::string(name) + " is on cuda:" + std::to_string(t.get_device()) + ", the call's stream on cuda:" +
+                  std::to_string(device));
     return t;
   }
 

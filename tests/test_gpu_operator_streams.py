@@ -88,3 +88,22 @@ def test_outputs_given_by_the_caller_are_left_where_they_are(mk):
     assert mk.muon_gated_ffn(d["x"], d["w1"], d["w3"], d["w2"], d["off"], out=out, stream=side) is out
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(out, want)
+
+
+class Elsewhere:
+    """A stream of another device."""
+    def __init__(self):
+        self.cuda_stream = torch.cuda.current_stream().cuda_stream
+        self.device_index = torch.cuda.current_device() + 1
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_tensors_of_another_device_than_the_streams_are_refused(mk, name, monkeypatch):
+    d = inputs(4)
+    with pytest.raises(ValueError, match="cuda:0, the call's stream on cuda:1"):
+        CALLS[name](mk, d, Elsewhere())
+    # the current stream of a current device that is not the tensors'
+    elsewhere = (torch.cuda.current_stream().cuda_stream, torch.cuda.current_device() + 1)
+    monkeypatch.setattr(mk, "_raw_stream", lambda stream: elsewhere)
+    with pytest.raises(ValueError, match="cuda:0, the call's stream on cuda:1"):
+        CALLS[name](mk, d, None)
