@@ -372,8 +372,8 @@ int muon_gated_ffn_backward(const void *dy, int64_t dy_stride, const void *x, in
  * gives one gate row for all rows.  rstd_post and rstd_pre (fp32, rows; may be
  * NULL) are what the backward pass takes.  All arithmetic is fp32; normed is
  * formed from r' before r' is rounded to its type.  residual_out may be
- * residual.  hidden <= 16384, else MUON_ERR_UNSUPPORTED; any alignment of the
- * element type (hidden and strides multiples of 8 and 16-byte aligned
+ * residual.  hidden <= 16384 and every pointer aligned to its element, else
+ * MUON_ERR_UNSUPPORTED (hidden and strides multiples of 8 and 16-byte aligned
  * pointers take the vector path).  rows == 0 is a no-op.
  */
 typedef enum { MUON_BF16 = 0, MUON_F32 = 1 } muon_dtype;

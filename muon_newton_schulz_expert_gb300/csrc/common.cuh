@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "muon.h"
 
 namespace muon {
@@ -63,6 +65,13 @@ cudaError_t alloc_async(void **ptr, size_t bytes, cudaStream_t s);
 // The argument, shape and coefficient checks of muon_ns_batched, in its order,
 // without any CUDA call: MUON_OK when the call can go ahead.
 int ns_precheck(const void *X, int64_t batch, int64_t m, int64_t n, int steps, const float *coeffs, float eps);
+
+// Every pointer on an element's boundary (a null one is).
+inline bool on_elements(std::initializer_list<const void *> ptrs, uintptr_t size) {
+  for (const void *p : ptrs)
+    if (reinterpret_cast<uintptr_t>(p) % size) return false;
+  return true;
+}
 
 // Programmatic launch: a kernel may start its set-up, or loads of what no
 // kernel before it in the call writes, while the one before it ends.

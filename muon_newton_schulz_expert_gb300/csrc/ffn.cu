@@ -122,7 +122,7 @@ int muon_gated_ffn(const void *x, int64_t x_stride, const void *w1, const void *
   if (rows == 0) return MUON_OK;
   if (!x || !w1 || !w3 || !w2 || !y || !gate != !up || x_stride < hidden || y_stride < hidden)
     return MUON_ERR_INVALID_ARG;
-  if (!takes({x, w1, w3, w2, y, gate, up}, {x_stride, y_stride})) return MUON_ERR_UNSUPPORTED;
+  if (!on_elements({offsets}, 8) || !takes({x, w1, w3, w2, y, gate, up}, {x_stride, y_stride})) return MUON_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   Scratch ws(s);
   MUON_TRY(ws.take(workspace, workspace_bytes, fwd_bytes(f)));
@@ -163,7 +163,8 @@ int muon_gated_ffn_backward(const void *dy, int64_t dy_stride, const void *x, in
   if (!dy || !gate || !up || !w2 || (!dx && !dw1) || (dx && (!w1 || !w3)) || (dw1 && !x) || dy_stride < hidden ||
       (dw1 && x_stride < hidden) || (dx && dx_stride < hidden))
     return MUON_ERR_INVALID_ARG;
-  if (!takes({dy, x, gate, up, w1, w3, w2, dx, dw1, dw3, dw2}, {dy_stride, dw1 ? x_stride : 0, dx ? dx_stride : 0}))
+  if (!on_elements({offsets}, 8) ||
+      !takes({dy, x, gate, up, w1, w3, w2, dx, dw1, dw3, dw2}, {dy_stride, dw1 ? x_stride : 0, dx ? dx_stride : 0}))
     return MUON_ERR_UNSUPPORTED;
   Scratch ws(s);
   MUON_TRY(ws.take(workspace, workspace_bytes, bwd_bytes(f)));

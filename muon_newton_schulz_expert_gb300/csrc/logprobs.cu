@@ -618,6 +618,9 @@ int muon_token_logprobs(const void *logits, int64_t stride, const int64_t *token
   if (rows == 0) return MUON_OK;
   if ((top > 0 && !top_ids) || (top == 0 && (top_ids || top_logp))) return MUON_ERR_INVALID_ARG;
   if (!logits || (logp && !tokens) || (!logp && !entropy && !lse && !top)) return MUON_ERR_INVALID_ARG;
+  if (!on_elements({logits}, type == MUON_BF16 ? 2 : 4) || !on_elements({logp, entropy, lse, top_logp}, 4) ||
+      !on_elements({tokens, top_ids}, 8))
+    return MUON_ERR_UNSUPPORTED;
   FwdArgs a{};
   a.logits = logits;
   a.tokens = tokens;
@@ -631,7 +634,6 @@ int muon_token_logprobs(const void *logits, int64_t stride, const int64_t *token
   a.top = top;
   a.err = device_error_word();
   if (!a.err) return MUON_ERR_CUDA;
-  if (reinterpret_cast<uintptr_t>(logits) % (type == MUON_BF16 ? 2 : 4)) return MUON_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (type == MUON_BF16)
     return top ? launch_fwd<__nv_bfloat16, true>(a, rows, s) : launch_fwd<__nv_bfloat16, false>(a, rows, s);
@@ -647,7 +649,8 @@ int muon_token_logprobs_backward(const void *logits, int64_t stride, const int64
   if (!logits || !lse || !dlogits || (!dlogp && !dentropy) || (dlogp && !tokens) || (dentropy && !entropy))
     return MUON_ERR_INVALID_ARG;
   const uintptr_t es = type == MUON_BF16 ? 2 : 4;
-  if (reinterpret_cast<uintptr_t>(logits) % es || reinterpret_cast<uintptr_t>(dlogits) % es)
+  if (!on_elements({logits, dlogits}, es) || !on_elements({lse, entropy, dlogp, dentropy}, 4) ||
+      !on_elements({tokens}, 8))
     return MUON_ERR_UNSUPPORTED;
   BwdArgs a{};
   a.logits = logits;

@@ -925,6 +925,7 @@ int launch_bwd(BwdArgs &a, bool vec, void *dw_pre, void *dw_post, void *dgate, c
 }
 
 bool bad_type(int t) { return t != MUON_BF16 && t != MUON_F32; }
+uintptr_t size_of(int t) { return t == MUON_BF16 ? 2 : 4; }
 
 }  // namespace
 
@@ -954,6 +955,10 @@ int muon_block_norm(const muon_block_norm_args *a, muon_stream_t stream) {
   if (a->residual_stride < h || (a->block && (a->block_stride < h || a->residual_out_stride < h)) ||
       (a->normed && a->normed_stride < h) || (a->block && a->gate && a->gate_stride != 0 && a->gate_stride < h))
     return MUON_ERR_INVALID_ARG;
+  if (!on_elements({a->residual, a->residual_out}, size_of(a->residual_type)) ||
+      !on_elements({a->block, a->w_post, a->gate, a->w_pre, a->normed}, size_of(a->branch_type)) ||
+      !on_elements({a->rstd_post, a->rstd_pre}, 4))
+    return MUON_ERR_UNSUPPORTED;
   FwdArgs k{};
   k.residual = {a->residual, a->residual_stride};
   k.block = {a->block, a->block_stride};
@@ -1015,6 +1020,11 @@ int muon_block_norm_backward(const muon_block_norm_backward_args *a, void *works
       (gate_rows && a->gate_stride < h) || (a->dresidual && a->dresidual_stride < h) ||
       (a->dblock && a->dblock_stride < h) || (gate_rows && a->dgate && a->dgate_stride < h))
     return MUON_ERR_INVALID_ARG;
+  if (!on_elements({a->dresidual_out, a->residual, a->dresidual}, size_of(rt)) ||
+      !on_elements({a->dnormed, a->block, a->w_post, a->gate, a->w_pre, a->dblock, a->dw_post, a->dgate, a->dw_pre},
+                   size_of(bt)) ||
+      !on_elements({a->rstd_post, a->rstd_pre}, 4))
+    return MUON_ERR_UNSUPPORTED;
   BwdArgs k{};
   k.dresidual_out = {a->dresidual_out, a->dresidual_out_stride};
   k.dnormed = {a->dnormed, a->dnormed_stride};

@@ -176,3 +176,32 @@ def test_missing_binding_fails_loudly(lib, monkeypatch, tmp_path):
     monkeypatch.setattr(mk, "_ops_module", None)
     with pytest.raises(mk.MuonLibraryMissing):
         mk._ops()
+
+
+def test_pointers_off_their_elements_are_refused(lib):
+    """On the host: a kernel's access through one would be a misaligned address."""
+    assert ffn(lib, off=P(256 + 4)) == -2
+    assert lib.muon_gated_ffn_backward(P(256), 64, P(256), 64, P(256), P(256), P(256), P(256), P(256), P(256 + 4), 4, 2,
+                                       64, 72, 0, P(256), 64, P(256), P(256), P(256), P(256), 0, None) == -2
+    for rt, bt in ((0, 0), (1, 0), (1, 1)):
+        for name, fields in (("muon_block_norm", NormArgs), ("muon_block_norm_backward", NormBackwardArgs)):
+            base = dict(rows=2, hidden=64, residual_type=rt, branch_type=bt, scale=1.0)
+            base |= {f: 256 for f, t in fields._fields_ if t is P}
+            base |= {f: 64 for f, _ in fields._fields_ if f.endswith("_stride")}
+            for f in (f for f, t in fields._fields_ if t is P):
+                size = 4 if f.startswith("rstd") else 4 if (rt if "residual" in f else bt) else 2
+                args = fields(**{**base, f: 256 + size // 2})
+                extra = (P(256), 0) if "backward" in name else ()   # a workspace of no bytes: no call gets further
+                assert getattr(lib, name)(ctypes.byref(args), *extra, None) == -2, (name, f, rt, bt)
+    for type_ in (0, 1):
+        base = dict(logits=256, tokens=256, logp=256, entropy=256, lse=256, ids=256, values=256)
+        size = {"logits": 4 if type_ else 2, "tokens": 8, "ids": 8}
+        for k in base:
+            v = {**base, k: 256 + size.get(k, 4) // 2}
+            assert lib.muon_token_logprobs(v["logits"], 100, v["tokens"], 2, 100, type_, v["logp"], v["entropy"],
+                                           v["lse"], 5, v["ids"], v["values"], None) == -2, (k, type_)
+        base = dict(logits=256, tokens=256, lse=256, entropy=256, dlogp=256, dentropy=256, out=256)
+        for k in base:
+            v = {**base, k: 256 + (size["logits"] if k == "out" else size.get(k, 4)) // 2}
+            assert lib.muon_token_logprobs_backward(v["logits"], 100, v["tokens"], v["lse"], v["entropy"], v["dlogp"],
+                                                    v["dentropy"], 2, 100, type_, v["out"], 100, None) == -2, (k, type_)
