@@ -163,9 +163,10 @@ int muon_gated_ffn_backward(const void *dy, int64_t dy_stride, const void *x, in
   if (!dy || !gate || !up || !w2 || (!dx && !dw1) || (dx && (!w1 || !w3)) || (dw1 && !x) || dy_stride < hidden ||
       (dw1 && x_stride < hidden) || (dx && dx_stride < hidden))
     return MUON_ERR_INVALID_ARG;
-  if (!on_elements({offsets}, 8) ||
-      !takes({dy, x, gate, up, w1, w3, w2, dx, dw1, dw3, dw2}, {dy_stride, dw1 ? x_stride : 0, dx ? dx_stride : 0}))
-    return MUON_ERR_UNSUPPORTED;
+  // what is not read or written may lie anywhere
+  const bool aligned = takes({dy, gate, up, w2}, {dy_stride}) && (!dx || takes({w1, w3, dx}, {dx_stride})) &&
+                       (!dw1 || takes({x, dw1, dw3, dw2}, {x_stride}));
+  if (!aligned || !on_elements({offsets}, 8)) return MUON_ERR_UNSUPPORTED;
   Scratch ws(s);
   MUON_TRY(ws.take(workspace, workspace_bytes, bwd_bytes(f)));
   return ws.done(backward(f, dy, dy_stride, x, x_stride, gate, up, w1, w3, w2, dx, dx_stride, dw1, dw3, dw2, ws.p, s));

@@ -391,3 +391,14 @@ def test_weight_gradients_of_long_cut_sums(mk, sizes, H, F):
     for i, n in enumerate(sizes):
         if n == 0:
             assert all(not bool(t[i].any()) for t in dw)
+
+
+def test_an_unaligned_x_is_no_hindrance_where_only_dx_is_wanted(mk):
+    d = inputs([30, 35], 136, 72, seed=10)
+    ref = backward(mk, d, "silu")
+    wide = torch.zeros(65, 139, dtype=torch.bfloat16, device="cuda")
+    d["x"] = wide[:, 3:]
+    assert torch.equal(backward(mk, d, "silu", need_dw=False)["dx"], ref["dx"])
+    with pytest.raises(mk.MuonError) as e:
+        backward(mk, d, "silu")
+    assert e.value.status == -2

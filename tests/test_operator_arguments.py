@@ -205,3 +205,15 @@ def test_pointers_off_their_elements_are_refused(lib):
             v = {**base, k: 256 + (size["logits"] if k == "out" else size.get(k, 4)) // 2}
             assert lib.muon_token_logprobs_backward(v["logits"], 100, v["tokens"], v["lse"], v["entropy"], v["dlogp"],
                                                     v["dentropy"], 2, 100, type_, v["out"], 100, None) == -2, (k, type_)
+
+
+def test_what_a_backward_call_does_not_read_may_lie_anywhere(lib):
+    def call(x=P(256), xs=64, w=P(256), dx=P(256), dw=P(256), dxs=64):
+        return lib.muon_gated_ffn_backward(P(256), 64, x, xs, P(256), P(256), w, w, P(256), P(256), 4, 2, 64, 72, 0, dx,
+                                           dxs, dw, dw, dw, P(256), 0, None)
+
+    # past every check of the arguments a workspace of no bytes is what is refused
+    assert call(x=P(258)) == call(xs=67) == call(w=P(258)) == call(dxs=67) == -2
+    assert call(x=P(258), xs=67, dw=None) == -4
+    assert call(w=P(258), dx=None, dxs=67) == -4
+    assert call(x=P(258), dx=None) == -2 and call(w=P(258), dw=None) == -2
