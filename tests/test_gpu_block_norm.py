@@ -328,3 +328,23 @@ def test_forward_of_rows_that_stream_in(mk, T, H, types, gate):
     within(p, P, P, "rstd_pre", extra=2 * E32)
     for w in wide.values():
         assert bool((w[:, :8] == 3).all()) and bool((w[:, H + 8:] == 3).all())
+
+
+@pytest.mark.parametrize("size", [1e-17, 1e-15, 1e14, 1e17])
+@pytest.mark.parametrize("T, H, types", [(5, 264, ("f32", "f32")), (300, 2056, ("f32", "bf16")),
+                                         (7, 1001, ("f32", "f32"))])
+def test_gradient_keeps_the_range_of_the_forward_pass(mk, T, H, types, size):
+    """Blocks whose mean square is in fp32's range while the cube of their reciprocal norm is not."""
+    rt, bt = (DT[t] for t in types)
+    d = inputs(T, H, rt, bt, "shared", seed=7)
+    d["b"] = (d["b"].float() * (2 * size)).to(bt)
+    r, y, q, p = mk.muon_block_norm(d["r"], d["b"], w_post=d["w_post"], gate=d["gate"], w_pre=d["w_pre"], scale=0.8,
+                                    eps=0.0)
+    R, mR, Y, mY, Q, _ = forward64(d, 0.8, 0.0)
+    within(r, R, mR, "r")
+    within(y, Y, mY, "y")
+    within(q, Q, Q, "rstd_post")
+    got = mk.muon_block_norm_backward(d["dr"], d["dy"], r, d["b"], q, p, w_post=d["w_post"], gate=d["gate"],
+                                      w_pre=d["w_pre"], scale=0.8)
+    for k, (value, mags) in backward64(d, r, q, p, 0.8).items():
+        within(getattr(got, k), value, mags, k, extra=T * 2.0 ** -24)
