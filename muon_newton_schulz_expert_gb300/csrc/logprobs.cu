@@ -73,6 +73,7 @@ struct Sums {
 };
 
 constexpr float kFar = 1e30f;   // a difference beyond which exp(-kFar) is 0 whatever it is
+constexpr float kVeryLow = -0.9f * kFar;   // elements above it are as they were after clamp_vector
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -169,7 +170,7 @@ __device__ __forceinline__ float clamp_vector(uint4 &x) {
 // A thread's sums over vectors: two halves of s and w, and the reference.
 template <typename T>
 struct VectorSums {
-  float m = kLowest, top = -INFINITY;   // top: the largest element, or less (masked ones and NaN left out)
+  float m = kLowest, top = -INFINITY;   // top: the largest element above kVeryLow (NaN left out), -inf if there is none
   f32x2 s = 0, w = 0;
 
   __device__ Sums total() const {
@@ -187,11 +188,11 @@ struct VectorSums {
   __device__ __forceinline__ void add(uint4 raw) {
     uint4 x = raw;
     const float most = clamp_vector<T>(x);
-    if (most > -0.9f * kFar) top = fmaxf(top, most);   // else all it says is that they lie below
+    if (most > kVeryLow) top = fmaxf(top, most);   // else all it says is that they lie below
     if (!(most <= m + 11.f) || m < -0.5f * kFar) {
       // a new reference, a NaN or infinity, or nothing but masked elements so far
       Sums a = total();
-      if (most > -0.9f * kFar && most < INFINITY) {
+      if (most > kVeryLow && most < INFINITY) {
         if (most > m) rebase(a, most);
         set(a);
       } else {
@@ -345,7 +346,9 @@ __global__ void __launch_bounds__(THREADS) token_logprobs_kernel(const __grid_co
   if ((int)threadIdx.x < ends) {
     const float f[1] = {to_f(x[end_at])};
     add_any(acc, f);
-    mine.top = fmaxf(mine.top, f[0]);
+    // by the vectors' rule: an exact maximum beside theirs, which leave very low elements
+    // out, could put the bound below above elements of threads that do not reach it
+    if (f[0] > kVeryLow) mine.top = fmaxf(mine.top, f[0]);
   }
   const bool odd = !(acc.s == acc.s);   // this thread met a NaN or +inf
   // the block's sums

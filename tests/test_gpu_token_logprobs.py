@@ -238,3 +238,29 @@ def test_no_rows_and_refusals(mk):
     with pytest.raises(mk.MuonError) as e:
         mk.muon_token_logprobs_backward(x, tok, f.lse)
     assert e.value.status == -1
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("V, shift", [(33, 0), (40, 3), (999, 0), (50003, 0), (50003, 5), (131075, 1)])
+def test_top_alternatives_of_rows_far_below_zero(mk, dt, V, shift):
+    """Nothing but very low finite values, some of them before or after the row's whole vectors."""
+    t = DT[dt]
+    low = torch.finfo(t).min
+    g = torch.Generator(device="cuda").manual_seed(V + shift)
+    wide = torch.zeros(5, (V + shift + 7) // 8 * 8, dtype=t, device="cuda")   # rows start alike
+    x = wide[:, shift:shift + V]
+    x[0] = low                                  # one mask of the type's lowest value: ties to the lowest index
+    x[1] = -2e30                                # two masks, the larger of them in the middle, the lower one last
+    x[1, V // 2] = -1e30
+    x[1, V - 1] = -1e35
+    x[2] = -1e35
+    x[2, V // 3] = -0.95e30
+    x[2, 0] = x[2, V - 1] = -3e30
+    x[3] = -(10.0 ** (29.7 + 8.5 * torch.rand(V, generator=g, device="cuda"))).to(t)
+    x[4] = -INF
+    x[4, 1], x[4, V - 2], x[4, V - 1] = -1e33, -1e32, low
+    for top in (1, 3, 20):
+        got = mk.muon_token_logprobs(x, top=top)
+        assert mk.muon_get_device_status() == 0
+        assert torch.equal(got.top_ids, torch.sort(x.float(), dim=1, descending=True, stable=True).indices[:, :top])
+        assert torch.equal(got.lse[1:], x.float().amax(1)[1:])   # exp of any other difference is 0
