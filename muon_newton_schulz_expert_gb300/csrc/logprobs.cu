@@ -499,8 +499,9 @@ struct Slope {
   float lse, dlogp, dent, ent;
   __device__ float operator()(float x) const {
     const float t = x - lse, p = ex2(t * kLog2e);
-    // p (x - lse + entropy) is zero where p is (x = -inf)
-    return -p * fmaf(dent, fmaxf(t, -kFar) + ent, dlogp);
+    // p (x - lse + entropy) is zero where p is: below t = -88 p is, and a t no lower than -128
+    // keeps the other factor finite, whatever dentropy is scaled by
+    return -p * fmaf(dent, fmaxf(t, -128.f) + ent, dlogp);
   }
 };
 

@@ -264,3 +264,20 @@ def test_top_alternatives_of_rows_far_below_zero(mk, dt, V, shift):
         assert mk.muon_get_device_status() == 0
         assert torch.equal(got.top_ids, torch.sort(x.float(), dim=1, descending=True, stable=True).indices[:, :top])
         assert torch.equal(got.lse[1:], x.float().amax(1)[1:])   # exp of any other difference is 0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 30, 2.0 ** 60, 2.0 ** 100])
+def test_gradient_of_masked_entries_under_large_factors(mk, dt, scale):
+    """dlogp and dentropy scaled (as a scaled loss sends them): masked entries still get 0."""
+    x, tok, dl, de = inputs(6, 1003, DT[dt], seed=8)
+    low = torch.rand(x.shape, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda") < 0.1
+    low[torch.arange(6, device="cuda"), tok.clamp(min=0)] = False
+    x[low] = torch.finfo(x.dtype).min
+    masked = low | (x == -INF)
+    f = mk.muon_token_logprobs(x, tok)
+    plain = mk.muon_token_logprobs_backward(x, tok, f.lse, f.entropy, dl, de).float()
+    got = mk.muon_token_logprobs_backward(x, tok, f.lse, f.entropy, dl * scale, de * scale).float()
+    assert bool((got[masked] == 0).all()) and bool((plain[masked] == 0).all())
+    # a power of two moves the exponent of every step and rounds nothing otherwise (no entry is near either limit)
+    assert torch.equal(got, plain * scale)
