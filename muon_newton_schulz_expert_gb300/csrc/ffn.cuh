@@ -15,7 +15,9 @@ __device__ __forceinline__ float sigmoid_of(float g, int act, float *dv) {
   float v = g;
   *dv = 1.f;
   if (act == MUON_ACT_GELU) {
-    const float g2 = g * g;
+    // held where sigmoid(v) has long been 0 or 1 in fp32, so that dv stays finite: the
+    // derivative has it times 0 there
+    const float g2 = fminf(g * g, 1e6f);
     v = c * g * fmaf(k, g2, 1.f);
     *dv = c * fmaf(3.f * k, g2, 1.f);
   }

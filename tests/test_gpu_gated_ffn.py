@@ -402,3 +402,15 @@ def test_an_unaligned_x_is_no_hindrance_where_only_dx_is_wanted(mk):
     with pytest.raises(mk.MuonError) as e:
         backward(mk, d, "silu")
     assert e.value.status == -2
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("rows", [4, 300])   # the kernels of few rows and of many
+def test_pre_activations_whose_square_overflows(mk, rows, act):
+    """act'(g) is 1 or 0 there, in the gradient as in the forward pass."""
+    d = inputs([rows], 64, 64, seed=15)
+    d["gate"][0], d["gate"][1], d["gate"][2], d["gate"][3] = 1e20, -1e20, 1e25, -1e25
+    got, ref = backward(mk, d, act), backward64(d, act)
+    for k in got:
+        assert bool(got[k].isfinite().all()), k
+        check(got[k], ref[k], k)
