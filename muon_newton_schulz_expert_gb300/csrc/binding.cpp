@@ -58,6 +58,11 @@ long long integer(PyObject *o) {
   if (v == -1 && PyErr_Occurred()) throw Error{nullptr, ""};
   return v;
 }
+bool truth(PyObject *o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Error{nullptr, ""};
+  return v != 0;
+}
 
 // One call's stream and tensors, all on one device.
 struct Call {
@@ -233,7 +238,7 @@ PyObject *gated_ffn(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded(n, 10, [&]() -> PyObject * {
     Call c(a[9]);
     const Ffn f(c, a[0], a[1], a[2], a[3], a[4]);
-    const bool keep = PyObject_IsTrue(a[6]);
+    const bool keep = truth(a[6]);
     int64_t ldy;
     const Out y = out_rows(c, a[7], "out", *f.x, f.T, f.H, &ldy);
     Out gate, up;
@@ -261,9 +266,9 @@ PyObject *gated_ffn_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::Tensor &gate = c.dense(a[2], "gate", at::kBFloat16, {f.T, f.F});
     const at::Tensor &up = c.dense(a[3], "up", at::kBFloat16, {f.T, f.F});
     Out dx, dw[3];
-    if (PyObject_IsTrue(a[11])) dx = out_rows(c, a[9], "dx", *f.x, f.T, f.H, &lddx);
+    if (truth(a[11])) dx = out_rows(c, a[9], "dx", *f.x, f.T, f.H, &lddx);
     const at::Tensor *w[3] = {f.w1, f.w3, f.w2};
-    if (PyObject_IsTrue(a[12])) {
+    if (truth(a[12])) {
       static const char *names[3] = {"dw1", "dw3", "dw2"};
       if (a[10] == Py_None) {
         for (int i = 0; i < 3; ++i) dw[i].t = c.empty(w[i]->sizes(), w[i]->options());
@@ -303,7 +308,7 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::Tensor &res = c.tensor(a[0], "residual");
     if (res.dim() != 2) value_error("residual must be (rows, hidden)");
     const int64_t T = res.size(0), H = res.size(1);
-    const bool post = given(a[1]), pre = PyObject_IsTrue(a[7]);
+    const bool post = given(a[1]), pre = truth(a[7]);
     const at::Tensor &branch = post ? c.tensor(a[1], "block") : given(a[4]) ? c.tensor(a[4], "w_pre")
                                : given(a[9]) ? c.tensor(a[9], "normed") : res;
     const at::ScalarType bt = branch.scalar_type();

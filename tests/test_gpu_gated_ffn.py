@@ -414,3 +414,11 @@ def test_pre_activations_whose_square_overflows(mk, rows, act):
     for k in got:
         assert bool(got[k].isfinite().all()), k
         check(got[k], ref[k], k)
+
+
+def test_an_argument_without_a_truth_value(mk):
+    d = inputs([4, 4], 64, 72)
+    with pytest.raises(RuntimeError, match="[Bb]oolean value of Tensor"):
+        mk.muon_gated_ffn(d["x"], d["w1"], d["w3"], d["w2"], d["off"], keep=d["off"])
+    with pytest.raises(RuntimeError, match="[Bb]oolean value of Tensor"):
+        backward(mk, d, "silu", need_dx=d["off"])
