@@ -7,13 +7,15 @@ same sources with ``-DMUON_DEVICE_CHECKS``: the kernels then test, before each
 access that would fault if it broke, the invariants they rely on, and report a
 broken one as MUON_ERR_DEVICE instead of making the access.  ``_lib/muon_ops.so``
 is the binding of the operators around the step (csrc/binding.cpp, against the
-installed torch).  A rebuild is skipped when the library is newer than every
+installed torch; not made where there is none, since the library does not need
+it).  A rebuild is skipped when the library is newer than every
 source and header.
 """
 
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -58,8 +60,10 @@ def up_to_date(checked: bool = False) -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
-def build_binding(force: bool = False) -> str:
-    """Build muon_ops.so if needed and return its path."""
+def build_binding(force: bool = False) -> str | None:
+    """Build muon_ops.so if needed and return its path; None without PyTorch, whose tensors it binds."""
+    if importlib.util.find_spec("torch") is None:
+        return None
     inputs = [BINDING_SOURCE, os.path.join(INCLUDE, "muon.h"), os.path.abspath(__file__)]
     if not force and os.path.exists(BINDING) and all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in inputs):
         return BINDING
@@ -83,9 +87,13 @@ def build_binding(force: bool = False) -> str:
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
     """Build libmuon.so (or, checked, libmuon_checked.so) and the binding if needed; returns the library's path."""
     lib = LIB_CHECKED if checked else LIB
+    if force or not up_to_date(checked):
+        _build_library(lib, verbose, checked)
     build_binding(force)
-    if not force and up_to_date(checked):
-        return lib
+    return lib
+
+
+def _build_library(lib: str, verbose: bool, checked: bool) -> None:
     nvcc = _nvcc()
     obj_dir = os.path.join(OUT_DIR, "obj_checked" if checked else "obj")
     os.makedirs(obj_dir, exist_ok=True)
@@ -111,7 +119,6 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
-    return lib
 
 
 def build_all(force: bool = False) -> list[str]:
