@@ -86,14 +86,15 @@ def build_binding(force: bool = False) -> str | None:
 
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
     """Build libmuon.so (or, checked, libmuon_checked.so) and the binding if needed; returns the library's path."""
-    lib = LIB_CHECKED if checked else LIB
-    if force or not up_to_date(checked):
-        _build_library(lib, verbose, checked)
+    lib = _library(force, verbose, checked)
     build_binding(force)
     return lib
 
 
-def _build_library(lib: str, verbose: bool, checked: bool) -> None:
+def _library(force: bool, verbose: bool, checked: bool) -> str:
+    lib = LIB_CHECKED if checked else LIB
+    if not force and up_to_date(checked):
+        return lib
     nvcc = _nvcc()
     obj_dir = os.path.join(OUT_DIR, "obj_checked" if checked else "obj")
     os.makedirs(obj_dir, exist_ok=True)
@@ -119,13 +120,17 @@ def _build_library(lib: str, verbose: bool, checked: bool) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
+    return lib
 
 
 def build_all(force: bool = False) -> list[str]:
     """Both libraries, their translation units compiled side by side, and the binding."""
-    build_binding(force)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=2) as ex:
-        return list(ex.map(lambda c: build(force=force, checked=c), (False, True)))
+    with concurrent.futures.ThreadPoolExecutor(max_workers=3) as ex:
+        libs = [ex.submit(_library, force, False, checked) for checked in (False, True)]
+        binding = ex.submit(build_binding, force)
+        made = [f.result() for f in libs]
+        binding.result()   # its errors, once both libraries are there
+    return made
 
 
 if __name__ == "__main__":

@@ -55,3 +55,14 @@ def test_a_binding_that_does_not_compile_is_an_error_after_the_library(elsewhere
     with pytest.raises(RuntimeError, match="not today"):
         mkbuild.build()
     assert made(tmp_path) == {"libmuon.so"}
+
+
+@pytest.mark.parametrize("force", [False, True])
+def test_build_all_makes_each_thing_once(elsewhere, tmp_path, force):
+    assert mkbuild.build_all(force=force) == [mkbuild.LIB, mkbuild.LIB_CHECKED]
+    assert made(tmp_path) == {"libmuon.so", "libmuon_checked.so", "muon_ops.so"}
+    assert len(elsewhere.of("binding.cpp")) == 1
+    assert all(len(elsewhere.of(s)) == 2 for s in mkbuild.SOURCES)
+    elsewhere.commands.clear()
+    mkbuild.build_all()
+    assert not elsewhere.commands
