@@ -8,13 +8,15 @@ access that would fault if it broke, the invariants they rely on, and report a
 broken one as MUON_ERR_DEVICE instead of making the access.  ``_lib/muon_ops.so``
 is the binding of the operators around the step (csrc/binding.cpp, against the
 installed torch; not made where there is none, since the library does not need
-it).  A rebuild is skipped when the library is newer than every
-source and header.
+it).  A rebuild is skipped when the library is newer than every source and
+header, and for the binding when it was made for the torch and Python that are
+installed.
 """
 
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -65,7 +67,11 @@ def build_binding(force: bool = False) -> str | None:
     if importlib.util.find_spec("torch") is None:
         return None
     inputs = [BINDING_SOURCE, os.path.join(INCLUDE, "muon.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in inputs):
+    # what its ABI depends on besides, kept beside it
+    stamp, built_for = BINDING + ".for", "torch %s, python %d.%d" % (importlib.metadata.version("torch"),
+                                                                     *sys.version_info[:2])
+    if not force and os.path.exists(BINDING) and os.path.exists(stamp) and open(stamp).read() == built_for and \
+            all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in inputs):
         return BINDING
     import torch
     home = os.path.dirname(torch.__file__)
@@ -81,6 +87,8 @@ def build_binding(force: bool = False) -> str | None:
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(stamp, "w") as f:
+        f.write(built_for)
     return BINDING
 
 

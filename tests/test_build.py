@@ -66,3 +66,16 @@ def test_build_all_makes_each_thing_once(elsewhere, tmp_path, force):
     elsewhere.commands.clear()
     mkbuild.build_all()
     assert not elsewhere.commands
+
+
+def test_the_binding_is_made_again_for_another_torch(elsewhere, monkeypatch):
+    mkbuild.build()
+    mkbuild.build()
+    assert len(elsewhere.of("binding.cpp")) == 1
+    monkeypatch.setattr(mkbuild.importlib.metadata, "version", lambda name: "99.0")
+    mkbuild.build()
+    mkbuild.build()
+    assert len(elsewhere.of("binding.cpp")) == 2
+    monkeypatch.setattr(mkbuild.sys, "version_info", (3, 99, 0))
+    mkbuild.build()
+    assert len(elsewhere.of("binding.cpp")) == 3 and len(elsewhere.of(mkbuild.SOURCES[0])) == 1
