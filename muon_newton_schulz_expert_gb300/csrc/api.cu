@@ -38,7 +38,8 @@ const char *kTraceNames[kTraceKinds] = {"momentum_bf16", "momentum_f32", "norm_p
                                         "copy",          "selftest_wait", "adamw",       "momentum_norm_bf16",
                                         "ns_axpy_apply_tc", "ffn_up_tc",   "ffn_down_tc",  "ffn_dh_tc",
                                         "ffn_dx_tc",     "ffn_tail",     "ffn_dw13_tc",  "ffn_dw2_tc",
-                                        "block_norm",    "block_norm_backward", "norm_weight_sum",
+                                        "block_norm",    "block_norm_staged", "block_norm_backward",
+                                        "block_norm_backward_staged", "norm_weight_sum",
                                         "token_logprobs", "token_logprobs_backward"};
 
 struct TraceRec {

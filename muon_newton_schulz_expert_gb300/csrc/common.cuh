@@ -42,7 +42,9 @@ enum TraceKind : int {
   kTraceFfnDw13,       // dW1 = X^T dG, dW3 = X^T dU
   kTraceFfnDw2,        // dW2 = Hid^T dY
   kTraceBlockNorm,
+  kTraceBlockNormStaged,     // rows through shared memory
   kTraceBlockNormBwd,
+  kTraceBlockNormBwdStaged,
   kTraceNormWeightSum,
   kTraceLogprobs,
   kTraceLogprobsBwd,

@@ -836,7 +836,7 @@ int launch_fwd(FwdArgs &a, bool vec, cudaStream_t s) {
     int blocks = 0;
     if ((a.in.slot_bytes >= kStagedRowBytes || p.threads > max_threads(8, kPlaces, false)) &&
         stage_rows(a.in, q, a.hidden, a.rows, false, &blocks)) {
-      constexpr int T = staged_threads(2, false), trace = kTraceBlockNorm;
+      constexpr int T = staged_threads(2, false), trace = kTraceBlockNormStaged;
       if (a.gate.p)
         return launch_staged<block_norm_kernel<R, B, 8, 2, T, FULL_ROW_GATE, true>>(a, q, blocks, trace, s);
       if (a.shared_gate)
@@ -874,7 +874,7 @@ int launch_bwd_as(const BwdArgs &a, const Plan &p, cudaStream_t s) {
 
 template <typename R, typename B, int PLACES, int T = staged_threads(PLACES, true)>
 int launch_staged_as(const BwdArgs &a, const Plan &p, int blocks, cudaStream_t s) {
-  constexpr int trace = kTraceBlockNormBwd;
+  constexpr int trace = kTraceBlockNormBwdStaged;
   if (a.gate.p)
     return launch_staged<block_norm_backward_kernel<R, B, 8, PLACES, T, FULL_ROW_GATE, true>>(a, p, blocks, trace, s);
   if (a.shared_gate)

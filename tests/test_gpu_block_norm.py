@@ -348,3 +348,48 @@ def test_gradient_keeps_the_range_of_the_forward_pass(mk, T, H, types, size):
                                       w_pre=d["w_pre"], scale=0.8)
     for k, (value, mags) in backward64(d, r, q, p, 0.8).items():
         within(getattr(got, k), value, mags, k, extra=T * 2.0 ** -24)
+
+
+def kernels_of(mk, call):
+    mk.muon_trace_begin()
+    out = call()
+    return out, set(mk.muon_trace_end())
+
+
+@pytest.mark.parametrize("gate", ["none", "shared", "rows"])
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("H", [3416, 5120, 6144, 6152, 7000, 8192])
+def test_forward_of_staged_rows(mk, H, types, gate):
+    """Rows enough to go through shared memory, where their bytes or their width ask for it: which did is looked at."""
+    rt, bt = (DT[t] for t in types)
+    T = 2100                                     # about 14 rows a block: every slot is filled again
+    row = H * (rt.itemsize + bt.itemsize * (2 if gate == "rows" else 1))
+    staged = row >= 40 * 1024 or H > 6144        # bytes, or more threads than the plain form's blocks have
+    d = inputs(T, H, rt, bt, gate, seed=8)
+    (r, y, q, p), names = kernels_of(mk, lambda: mk.muon_block_norm(
+        d["r"], d["b"], w_post=d["w_post"], gate=d["gate"], w_pre=d["w_pre"], scale=0.9))
+    assert names == {"block_norm_staged" if staged else "block_norm"}
+    R, mR, Y, mY, Q, P = forward64(d, 0.9, 1e-6)
+    within(r, R, mR, "r")
+    within(y, Y, mY, "y")
+    within(q, Q, Q, "rstd_post")
+    within(p, P, P, "rstd_pre", extra=2 * E32)
+    again = mk.muon_block_norm(d["r"], d["b"], w_post=d["w_post"], gate=d["gate"], w_pre=d["w_pre"], scale=0.9)
+    assert all(torch.equal(a, b) for a, b in zip((r, y, q, p), again))
+
+
+@pytest.mark.parametrize("gate", ["none", "shared", "rows"])
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("H", [1032, 6144, 6152, 8192, 8200])
+def test_backward_of_staged_rows(mk, H, types, gate):
+    rt, bt = (DT[t] for t in types)
+    T = 1900                                     # 3 or 12 rows a block
+    row = (H * (2 * rt.itemsize + bt.itemsize * (3 if gate == "rows" else 2)) + 127) // 128 * 128
+    staged = 2 * row <= 216 * 1024 and H <= 8192
+    d = inputs(T, H, rt, bt, gate, seed=9)
+    r, _, q, p = mk.muon_block_norm(d["r"], d["b"], w_post=d["w_post"], gate=d["gate"], w_pre=d["w_pre"], scale=0.9)
+    got, names = kernels_of(mk, lambda: mk.muon_block_norm_backward(
+        d["dr"], d["dy"], r, d["b"], q, p, w_post=d["w_post"], gate=d["gate"], w_pre=d["w_pre"], scale=0.9))
+    assert names == {"block_norm_backward_staged" if staged else "block_norm_backward", "norm_weight_sum"}
+    for k, (value, mags) in backward64(d, r, q, p, 0.9).items():
+        within(getattr(got, k), value, mags, k, extra=T * 2.0 ** -24)
