@@ -422,3 +422,54 @@ def test_an_argument_without_a_truth_value(mk):
         mk.muon_gated_ffn(d["x"], d["w1"], d["w3"], d["w2"], d["off"], keep=d["off"])
     with pytest.raises(RuntimeError, match="[Bb]oolean value of Tensor"):
         backward(mk, d, "silu", need_dx=d["off"])
+
+
+LONG = [700, 100, 1900, 64, 2500, 1283, 0, 3000]   # 41 row tiles, whole and partial k-blocks of 64
+
+
+@pytest.mark.parametrize("H,F", [(1024, 1536),    # both multiples of 64: 128-column operands load in one piece
+                                 (1000, 1320)])   # neither
+def test_many_tiles_a_pair(mk, H, F):
+    """More than two tiles for each of the 76 pairs in all six products: 492 and more of UP, 164 of DOWN and DX,
+    246 of DH, 192 of dW2, 384 of dW1 and dW3.  The accumulators, the ring and the output boxes go round."""
+    d = inputs(LONG, H, F, seed=16)
+    got_f = forward(mk, d, "silu")
+    got_b = backward(mk, d, "silu", dw=tuple(torch.full_like(d[k], float("nan")) for k in ("w1", "w3", "w2")))
+    assert mk.muon_get_device_status() == 0
+    for got, ref in ((got_f, forward64(d, "silu")), (got_b, backward64(d, "silu"))):
+        for k in got:
+            check(got[k], ref[k], k)
+    for got, again in ((got_f, forward(mk, d, "silu")), (got_b, backward(mk, d, "silu"))):
+        for k in got:
+            assert torch.equal(got[k], again[k]), k
+
+
+def test_one_experts_nan_stays_with_it_in_wide_loads(mk):
+    """Widths that are multiples of 64 and several k-blocks an expert: the last, partial one next to the NaNs."""
+    sizes = [300, 3, 470, 129]
+    d = inputs(sizes, 128, 256, seed=17)
+    ref = backward(mk, d, "silu")
+    for k in ("x", "dy", "gate", "up"):
+        d[k] = d[k].clone()
+        d[k][300:303] = float("nan")
+    got = backward(mk, d, "silu")
+    rows = torch.ones(sum(sizes), dtype=torch.bool, device="cuda")
+    rows[300:303] = False
+    assert torch.equal(got["dx"][rows], ref["dx"][rows])
+    for k in ("dw1", "dw3", "dw2"):
+        assert torch.equal(got[k][[0, 2, 3]], ref[k][[0, 2, 3]]), k
+        assert not bool(got[k][1].isfinite().any()), k
+
+
+def test_weight_gradients_of_rows_past_32_bit_offsets(mk):
+    """rows * ffn past 2^31 elements and a gradient in the last rows alone: their sums against 64 bits."""
+    T, H, F = 270_000, 64, 8192
+    d = inputs([T], H, F, seed=18)
+    d["dy"][:-200] = 0
+    got = backward(mk, d, "silu")
+    assert mk.muon_get_device_status() == 0
+    ref = backward64({**d, "sizes": [200], **{k: d[k][-200:] for k in ("x", "dy", "gate", "up")}}, "silu")
+    for k in ("dw1", "dw3", "dw2"):
+        check(got[k], ref[k], k)
+    assert not bool(got["dx"][:-200].any())
+    check(got["dx"][-200:], ref["dx"], "dx")
