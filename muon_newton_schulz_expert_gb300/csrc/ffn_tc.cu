@@ -793,12 +793,12 @@ int ffn_dx(const FfnShape &f, const void *dg, const void *du, const void *w1, co
 namespace {
 
 // A weight gradient of few tiles sums long columns of rows: the rows are cut into
-// parts while they fit the 76 pairs of CTAs, each of 8 k-blocks or more by the
-// groups' average.  30000 rows of one expert, 512 x 512: dW1 and dW3 43 us against
+// parts while they fit the SMs' pairs of CTAs (76), each of 8 k-blocks or more by
+// the groups' average.  30000 rows of one expert, 512 x 512: dW1 and dW3 43 us against
 // 141 uncut, dW2 35 against 142; 28429 rows of 2, 264 x 984: 66 against 105, 44
 // against 105.
 int dw_split(const FfnShape &f, int64_t tiles) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>({16, 76 / std::max<int64_t>(tiles * f.experts, 1),
+  return (int)std::max<int64_t>(1, std::min<int64_t>({16, num_sms() / 2 / std::max<int64_t>(tiles * f.experts, 1),
                                                       f.rows / (f.experts * BK * 8)}));
 }
 int split13(const FfnShape &f) { return dw_split(f, (int64_t)cdiv(f.hidden, CM) * cdiv(f.ffn, BNH)); }

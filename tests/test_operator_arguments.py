@@ -217,3 +217,18 @@ def test_what_a_backward_call_does_not_read_may_lie_anywhere(lib):
     assert call(x=P(258), xs=67, dw=None) == -4
     assert call(w=P(258), dx=None, dxs=67) == -4
     assert call(x=P(258), dx=None) == -2 and call(w=P(258), dw=None) == -2
+
+
+def test_parts_of_a_cut_sum_go_by_the_device(lib):
+    """Scratch of the cut weight gradients: as many parts as pairs of SMs hold, not a fixed number."""
+    # one block a SM of 8192 columns, two fp32 sums each
+    sms = lib.muon_block_norm_backward_workspace_bytes(1 << 20, 8192) // (2 * 8192 * 4)
+    rows, H, F = 1 << 20, 19 * 256, 256
+
+    def up(n):   # regions start on 256 bytes
+        return (n + 255) // 256 * 256
+
+    dw13, dw2 = sms // 2 // (19 * 2), sms // 2 // 19   # tiles of 256 x 128 of dW1 and dW3, of 256 x 256 of dW2
+    sums = max(2 * dw13 if dw13 > 1 else 0, dw2) * H * F * 4
+    want = 3 * up(rows * F * 2) + up(64 * (2 * H + 3 * F) * 2) + up(sums)
+    assert lib.muon_gated_ffn_backward_workspace_bytes(rows, 1, H, F) == want
