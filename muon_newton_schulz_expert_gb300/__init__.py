@@ -454,14 +454,17 @@ def _ops():
 
 
 def _raw_stream(stream):
-    """The stream's handle and device; None is the current stream of the current device, which a bare handle is on too."""
+    """The stream's handle, its device and whether they are the current ones for certain.
+
+    None is the current stream of the current device, which a bare handle is on too.
+    """
     from torch import _C
     if stream is None:
         device = _C._cuda_getDevice()
-        return _C._cuda_getCurrentRawStream(device), device
+        return _C._cuda_getCurrentRawStream(device), device, True
     if hasattr(stream, "cuda_stream"):
-        return stream.cuda_stream, stream.device_index
-    return int(stream), _C._cuda_getDevice()
+        return stream.cuda_stream, stream.device_index, False
+    return int(stream), _C._cuda_getDevice(), False
 
 
 def _outputs(call, result):

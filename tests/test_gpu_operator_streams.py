@@ -103,7 +103,7 @@ def test_tensors_of_another_device_than_the_streams_are_refused(mk, name, monkey
     with pytest.raises(ValueError, match="cuda:0, the call's stream on cuda:1"):
         CALLS[name](mk, d, Elsewhere())
     # the current stream of a current device that is not the tensors'
-    elsewhere = (torch.cuda.current_stream().cuda_stream, torch.cuda.current_device() + 1)
+    elsewhere = (torch.cuda.current_stream().cuda_stream, torch.cuda.current_device() + 1, True)
     monkeypatch.setattr(mk, "_raw_stream", lambda stream: elsewhere)
     with pytest.raises(ValueError, match="cuda:0, the call's stream on cuda:1"):
         CALLS[name](mk, d, None)
