@@ -15,9 +15,9 @@ __device__ __forceinline__ float sigmoid_of(float g, int act, float *dv) {
   float v = g;
   *dv = 1.f;
   if (act == MUON_ACT_GELU) {
-    // held where sigmoid(v) has long been 0 or 1 in fp32, so that dv stays finite: the
-    // derivative has it times 0 there
-    const float g2 = fminf(g * g, 1e6f);
+    // rounded towards zero, so that a square past fp32's range is its largest value: dv stays
+    // finite, and the derivative has it times 0 there
+    const float g2 = __fmul_rz(g, g);
     v = c * g * fmaf(k, g2, 1.f);
     *dv = c * fmaf(3.f * k, g2, 1.f);
   }
