@@ -605,9 +605,10 @@ __global__ void __launch_bounds__(THREADS, STAGED ? 1 : blocks_per_sm(W, THREADS
     row_sums(sum, red[turn]);
     if (STAGED) staged.next(row, group, groups);
     turn ^= 1;
-    // s2 and s3 lack the factor scale.  They carry one b, so a q on them first: q^3
+    // s2 and s3 lack the factor scale.  They carry one b, so one q goes onto them first: q^3
     // alone leaves fp32's range for blocks (rms 1e-13, 1e13) whose mean square does not.
-    const float c1 = p * p * sum[0] * inv_h, c2 = q * (q * (q * (sum[1] - c1 * sum[2]))) * a.scale * inv_h;
+    const float c1 = p * p * sum[0] * inv_h;
+    const float c2 = (q * inv_h * a.scale) * (sum[1] - c1 * sum[2]) * (q * q);
     const P c1n = both<P>(-c1), c2n = both<P>(-c2), q2 = both<P>(q), scale = both<P>(a.scale);
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
