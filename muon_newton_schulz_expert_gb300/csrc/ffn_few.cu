@@ -464,10 +464,10 @@ int launch(Args &p, const FfnShape &f, int trace_kind, cudaStream_t s) {
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 int map_weights(CUtensorMap *m, const void *base, const FfnShape &f, int64_t rows, int64_t cols, bool mn) {
-  return make_map_bf16(m, base, f.experts, rows, cols, mn ? 64 : 128);
+  return make_map(m, base, f.experts, rows, cols, mn ? 64 : 128);
 }
 int map_rows(CUtensorMap *m, const void *base, const FfnShape &f, int64_t cols, int64_t ld) {
-  return make_map_bf16(m, base, 1, f.rows, cols, row_tile(f), ld);
+  return make_map(m, base, 1, f.rows, cols, row_tile(f), ld);
 }
 
 Args base_args(const FfnShape &f, int64_t M, int64_t K) {

@@ -687,25 +687,25 @@ int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // operand maps: K-major weights (boxes of 128 rows x 64 columns), MN-major (64 x 64)
 int map_k(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols) {
-  return make_map_bf16(m, base, batch, rows, cols, BM);
+  return make_map(m, base, batch, rows, cols, BM);
 }
 int map_cols(CUtensorMap *m, const Args &p, const void *base, int64_t batch, int64_t rows, int64_t cols,
              int64_t ld = 0) {
-  return p.wide ? make_map_blocks(m, base, batch, rows, cols, BK, 2, ld) : make_map_bf16(m, base, batch, rows, cols, BK, ld);
+  return p.wide ? make_map_blocks(m, base, batch, rows, cols, BK, 2, ld) : make_map(m, base, batch, rows, cols, BK, ld);
 }
 int map_mn(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols, int64_t ld = 0) {
-  return make_map_bf16(m, base, batch, rows, cols, 64, ld);
+  return make_map(m, base, batch, rows, cols, 64, ld);
 }
 // One box of exactly the rows that a tile's half has: boxes are paid for by the
 // piece and by the bytes (16384 rows, 32 experts, forward: 797 us; 816 with boxes of
 // 64 rows, 906 with exactly the rows in boxes of 64 and 16).
 int map_rows(CUtensorMap (&m)[BN / UNIT], const void *base, const FfnShape &f, int64_t cols, int64_t ld = 0) {
   for (int u = 0; u < BN / UNIT; ++u)
-    if (const int st = make_map_bf16(&m[u], base, 1, f.rows, cols, (u + 1) * UNIT / 2, ld)) return st;
+    if (const int st = make_map(&m[u], base, 1, f.rows, cols, (u + 1) * UNIT / 2, ld)) return st;
   return MUON_OK;
 }
 int map_out(CUtensorMap *m, const void *base, int64_t batch, int64_t rows, int64_t cols, int64_t ld = 0) {
-  return make_map_bf16(m, base, batch, rows, cols, 32, ld);
+  return make_map(m, base, batch, rows, cols, 32, ld);
 }
 
 Args base_args(const FfnShape &f) {

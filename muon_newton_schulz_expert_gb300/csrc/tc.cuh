@@ -1,4 +1,4 @@
-// The sm_103a pieces that the tensor-core kernels are made of: bounded
+// The sm_103a pieces that the grouped tensor-core kernels are made of: bounded
 // mbarrier waits, TMA copies, tcgen05 instructions and descriptors, tensor maps.
 #pragma once
 
@@ -242,21 +242,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[32]) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-
-// The same without the wait: r holds nothing before a tcgen05.wait::ld.
 __device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -270,6 +255,14 @@ __device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  tmem_ld32_issue(taddr, r);
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  // the registers are only valid from here on
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
 // Shared-memory matrix descriptor: start address, leading and stride byte
 // offsets, descriptor version 1, 128-byte swizzle.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
@@ -278,12 +271,11 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
 }
 
 // Instruction descriptor of kind::f16: fp32 D (bit 4), A and B both bf16
-// (format 1 at bits 7 and 10) or both fp16 (format 0), each operand K-major
-// or MN-major (bits 15 and 16), N >> 3 at bit 17, M >> 4 at bit 24.
-__host__ __device__ constexpr uint32_t make_idesc(int m, int n, bool a_mn_major, bool b_mn_major,
-                                                  int tin = kBF16) {
-  return (1u << 4) | (tin == kBF16 ? (1u << 7) | (1u << 10) : 0u) | ((a_mn_major ? 1u : 0u) << 15) |
-         ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+// (format 1 at bits 7 and 10), each operand K-major or MN-major (bits 15 and
+// 16), N >> 3 at bit 17, M >> 4 at bit 24.
+__host__ __device__ constexpr uint32_t make_idesc(int m, int n, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // Bounded wait used on the way out after an abort: waits for the phase of
@@ -314,35 +306,25 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 3-D map over a [batch][rows][cols] stack of elements of format `fmt`
-// (16-bit, or the 8-bit low half), rows `pitch` elements apart (0: dense);
-// box = box_cols columns x box_rows rows x 1 matrix.
-int make_map(CUtensorMap *map, const void *base, int fmt, int64_t batch, int64_t rows, int64_t cols, int box_rows,
-             int box_cols = 64, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B, int64_t pitch = 0) {
+// 3-D map over a [batch][rows][cols] stack of bf16, rows `pitch` elements apart
+// (0: dense); box = box_cols columns x box_rows rows x 1 matrix, whose rows are
+// the 128 bytes that the swizzle spans.
+int make_map(CUtensorMap *map, const void *base, int64_t batch, int64_t rows, int64_t cols, int box_rows,
+             int64_t pitch = 0) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return MUON_ERR_CUDA;
-  const cuuint64_t es = fmt == kE5M2 ? 1 : 2;   // element bytes
   const cuuint64_t ld = (cuuint64_t)(pitch > 0 ? pitch : cols);
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
-  cuuint64_t strides[2] = {ld * es, (cuuint64_t)rows * ld * es};
-  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1u};
+  cuuint64_t strides[2] = {ld * 2, (cuuint64_t)rows * ld * 2};
+  cuuint32_t box[3] = {64u, (cuuint32_t)box_rows, 1u};
   cuuint32_t estr[3] = {1u, 1u, 1u};
-  const CUtensorMapDataType dt = fmt == kE5M2 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                 : fmt == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                               : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  CUresult r = enc(map, dt, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? MUON_OK : MUON_ERR_CUDA;
 }
 
-// The operands of the bf16 products: boxes of 64 columns, the 128 bytes that the
-// swizzle spans.
-int make_map_bf16(CUtensorMap *map, const void *base, int64_t batch, int64_t rows, int64_t cols, int box_rows,
-                  int64_t pitch = 0) {
-  return make_map(map, base, kBF16, batch, rows, cols, box_rows, 64, CU_TENSOR_MAP_SWIZZLE_128B, pitch);
-}
-
-// Such an array by blocks of 64 columns (cols is a multiple of 64): a box of
+// The same array by blocks of 64 columns (cols is a multiple of 64): a box of
 // `blocks` of them is that many atoms, one after the other.
 int make_map_blocks(CUtensorMap *map, const void *base, int64_t batch, int64_t rows, int64_t cols, int box_rows,
                     int blocks, int64_t pitch = 0) {
