@@ -1,5 +1,8 @@
 // The sm_103a pieces that the grouped tensor-core kernels are made of: bounded
 // mbarrier waits, TMA copies, tcgen05 instructions and descriptors, tensor maps.
+// gemm_tc.cu has the pieces that it uses itself, since bench.py reports DRAM counters
+// only for the very bytes of that file that they were taken from;
+// tests/test_tensor_core_pieces.py holds what is in both alike.
 #pragma once
 
 #include <cuda.h>
@@ -83,8 +86,7 @@ __device__ __noinline__ bool wait_bounded(uint32_t bar, uint32_t parity, Watch w
 // suspended, so it sees the phase flip without a wake-up delay, at the price
 // of the issue slots its spinning takes from warps on the same scheduler.
 // The producer and the MMA issuer wait on the operand ring this way: measured
-// 1-2.5% faster per kernel than suspending in try_wait (and it lets the
-// update-fused kernel and X X^T profit from single-k-block stages).
+// 1-2.5% faster than suspending in try_wait on the Newton-Schulz kernels.
 __device__ __forceinline__ bool wait_polled(uint32_t bar, uint32_t parity, Watch w) {
   if (mbar_test_wait(bar, parity)) return true;
   const unsigned long long t0 = global_ns();
