@@ -321,10 +321,12 @@ int muon_adamw_update_f32(float *param, const float *grad, float *exp_avg, float
  *   y         device, bf16, rows x hidden, y_stride elements apart (written)
  *   gate, up  device, bf16, [rows][ffn] dense: g and u for the backward pass;
  *             NULL (both) when it will not run (serving)
- * Arithmetic: bf16 operands, fp32 accumulation; h is rounded to bf16 between
- * the products, y, gate and up once at the end.  x, y and the rest must not
- * overlap.  A row's result depends on that row alone; the kernel that
- * computes it, and with it the order of its sums, is chosen by the sizes.
+ * Arithmetic: bf16 operands, fp32 accumulation; y, gate and up are rounded once
+ * at the end.  Between the products h is rounded to bf16, or, where so few rows
+ * of so few experts are given that the kernels of few rows run, carried as two
+ * bf16 halves (value and remainder).  x, y and the rest must not overlap.  A
+ * row's result depends on that row alone; the kernel that computes it, and with
+ * it the rounding of h and the order of its sums, is chosen by the sizes.
  * Requirements: hidden, ffn and the strides multiples of 8, pointers 16-byte
  * aligned (offsets: 8), else MUON_ERR_UNSUPPORTED.  rows == 0 is a no-op.
  * workspace: device, 256-byte aligned, muon_gated_ffn_workspace_bytes() bytes,
@@ -466,8 +468,11 @@ int muon_token_logprobs(const void *logits, int64_t stride, const int64_t *token
 
 /* The gradient of sum_rows dlogp logp + dentropy entropy in the logits:
  *   dlogits_v = dlogp (1[v = token] - p_v) - dentropy p_v (x_v - lse + entropy)
- * lse and entropy are the forward call's (entropy may be NULL when dentropy
- * is); dlogp or dentropy may be NULL (zero).  A row that is not scored
+ * with p_v = exp(x_v - lse).  lse and entropy are the forward call's (entropy may
+ * be NULL when dentropy is); the rounding of an lse of large magnitude is in
+ * p_v (2^-24 |lse|; where a mask of the type's lowest value covers a whole row
+ * nothing smaller is left, and every p_v is 1).  dlogp or dentropy may be NULL
+ * (zero).  A row that is not scored
  * (negative token) takes no part in dlogp.  A row with lse = -inf, or with both
  * factors zero, gets zeros.  dlogits has `type`, rows dlogits_stride apart, and
  * may be the logits themselves (same stride). */
@@ -508,8 +513,9 @@ int64_t muon_launch_count(void);
 
 /* Fault injection on the host, for testing callers' error paths: the next
  * `count` device allocations the library makes for itself (the workspaces of
- * muon_ns_batched, muon_ns_batched_f32, the schedule variants and
- * muon_step_batched, and the slots of muon_step_host) fail as if the memory
+ * muon_ns_batched, muon_ns_batched_f32, the schedule variants,
+ * muon_step_batched, muon_gated_ffn, its backward call and
+ * muon_block_norm_backward, and the slots of muon_step_host) fail as if the memory
  * pool were exhausted, without calling CUDA: the call returns
  * MUON_ERR_NO_MEMORY before it launches anything or touches its buffers.
  * count = 0 switches it off; count < 0 is MUON_ERR_INVALID_ARG.  Returns the

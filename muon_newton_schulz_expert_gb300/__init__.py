@@ -5,8 +5,11 @@ Argument marshalling only: every step runs in the CUDA kernels of
 device memory and the current stream.  The operators around the step, whose
 calls last a few microseconds, are marshalled by ``_lib/muon_ops.so``
 (csrc/binding.cpp); the outputs that they make belong to the stream that the
-call runs on, as if it were the current one.  There is no fallback: when the library has not been built,
-every call raises ``MuonLibraryMissing``.
+call runs on, as if it were the current one.  None of the calls is known to
+autograd: outputs carry no history, also where an input requires a gradient,
+and tensors that are written in place keep their version.  There is no
+fallback: when the library has not been built, every call raises
+``MuonLibraryMissing``.
 
 Method: "Training a 1T-Parameter MoE on EU public infrastructure with PyTorch
 and TorchTitan", section "FlexShard: Muon without communication" -- one fp32
@@ -492,7 +495,8 @@ def muon_gated_ffn(x, w1, w3, w2, offsets=None, *, act="silu", keep=False, out=N
     w2 (experts, ffn, hidden) as the Muon step holds them (or one expert's 2-D
     matrices); offsets int64 (experts + 1) on the GPU, the first row of each
     expert and the end (None: one expert with all rows).  Returns y, or with
-    ``keep`` (y, gate, up) for the backward pass.
+    ``keep`` (y, gate, up) for the backward pass, muon_gated_ffn_backward
+    (autograd records nothing).
     """
     return _outputs("muon_gated_ffn", _ops().gated_ffn(
         x, w1, w3, w2, offsets, _activation(act), keep, out, workspace, _raw_stream(stream)))
@@ -522,7 +526,8 @@ def muon_block_norm(residual, block=None, *, w_post=None, gate=None, w_pre=None,
     w_pre.  residual (rows, hidden) bf16 or fp32; block, gate ((hidden,) for
     all rows or (rows, hidden)), weights and y share one type.  Without block
     r' is residual itself; without norm_next there is no y.  Returns
-    (r', y, rstd_post, rstd_pre), None in the place of what there is not.
+    (r', y, rstd_post, rstd_pre), None in the place of what there is not.  The
+    gradients are muon_block_norm_backward's (autograd records nothing).
     """
     return _outputs("muon_block_norm", _ops().block_norm(
         residual, block, w_post, gate, w_pre, scale, eps, norm_next, out, normed, _raw_stream(stream)))
@@ -550,7 +555,8 @@ def muon_token_logprobs(logits, tokens=None, *, top=0, stream=None):
     """Log probabilities of tokens (int64, rows) under logits (rows, vocab), bf16 or fp32; see muon.h.
 
     Returns TokenLogprobs(logp, entropy, lse, top_ids, top_logp), fp32 but the
-    int64 ids; logp is None without tokens, the last two without ``top``.
+    int64 ids; logp is None without tokens, the last two without ``top``.  The
+    gradient is muon_token_logprobs_backward's (autograd records nothing).
     """
     return TokenLogprobs(*_outputs("muon_token_logprobs", _ops().token_logprobs(
         logits, tokens, top, _raw_stream(stream))))

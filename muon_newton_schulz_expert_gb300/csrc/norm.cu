@@ -34,8 +34,11 @@ constexpr int kRowsPerCta = 4;   // rows of one CTA where a warp holds a whole r
 // Rows of more than 128 vectors give each thread kPlaces of them.  The largest
 // block of an instance and how many of them an SM has to hold fix its
 // registers: 56 a thread forward, 80 backward, where two sums per column are
-// kept besides.  Measured at 16384 x 6144: forward in bf16 154 us (77% of the
-// measured copy bandwidth).  Rows that need more threads than that take an
+// kept besides.  A backward thread of two places keeps 370 to 520 bytes in local
+// memory all the same, one of a wide block, with 64 registers, 460 to 680: these forms
+// take 1.6 to 2.5 times what their bytes do (6144 and 9216 columns).  Measured at
+// 16384 x 6144: forward in bf16 150 us (79% of the measured copy bandwidth).  Rows
+// that need more threads than that take an
 // instance with wide blocks.
 constexpr int kPlaces = 2;
 constexpr int max_threads(int w, int vpt, bool backward) {
@@ -232,8 +235,8 @@ __device__ __forceinline__ void times(const T *w, Item<W> (&v)[kItems<W>]) {
 // then spend no instructions and hold no registers on loads in flight, so that
 // few of them suffice and each has registers for the weights: the kernel was
 // bound by the instructions it issued (about 40 an element, 5 of every 8 vector
-// loads being of weights).  16384 x 6144 in bf16: 232 us (77% of the measured
-// copy bandwidth) against 301 us with plain loads, 2 blocks of 384 threads; 272 us
+// loads being of weights).  16384 x 6144 in bf16: 232 us, by now 226 to 229 (78% of the
+// measured copy bandwidth), against 301 us with plain loads, 2 blocks of 384 threads; 272 us
 // with the weights re-read and 512 threads, 317 us with 768 threads of one place,
 // 225 us with 256 threads of three, which takes 165 us where this takes 125 (30000 x
 // 2048).  8192 columns, fp32 stream: 334 against 493 us.
