@@ -430,8 +430,8 @@ LONG = [700, 100, 1900, 64, 2500, 1283, 0, 3000]   # 41 row tiles, whole and par
 @pytest.mark.parametrize("H,F", [(1024, 1536),    # both multiples of 64: 128-column operands load in one piece
                                  (1000, 1320)])   # neither
 def test_many_tiles_a_pair(mk, H, F):
-    """More than two tiles for each of the 76 pairs in all six products: 492 and more of UP, 164 of DOWN and DX,
-    246 of DH, 192 of dW2, 384 of dW1 and dW3.  The accumulators, the ring and the output boxes go round."""
+    """More than two tiles for each of the 76 pairs in all six products: 451 or more of UP, 164 of DOWN and DX, 246 of
+    DH, 192 of dW2, 352 or more of dW1 and dW3.  The accumulators, the ring and the output boxes go round."""
     d = inputs(LONG, H, F, seed=16)
     got_f = forward(mk, d, "silu")
     got_b = backward(mk, d, "silu", dw=tuple(torch.full_like(d[k], float("nan")) for k in ("w1", "w3", "w2")))
