@@ -481,6 +481,118 @@ int muon_token_logprobs_backward(const void *logits, int64_t stride, const int64
                                  int64_t vocab, int type, void *dlogits, int64_t dlogits_stride,
                                  muon_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * A router's choice of experts and their weights, and its gradient.  For a row of
+ * logits x:
+ *   s = softmax(x) (MUON_SCORE_SOFTMAX) or sigmoid(x) (MUON_SCORE_SIGMOID)
+ *   the `top` experts with the largest s + bias, or without a bias the largest x;
+ *   equal ones by ascending index
+ *   weight_i = scale * s_i, or with `normalize` scale * s_i / (sum of the chosen s)
+ *   logits    device, rows x experts of `type` (bf16 or fp32), rows `stride`
+ *             elements apart
+ *   bias      device, fp32, experts: takes part in the choice alone (load
+ *             balance); may be NULL.  Sums s + bias that fp32 cannot tell apart
+ *             are compared in 64 bits.
+ *   ids       device, int64, [rows][top]; weights  device, fp32, [rows][top]
+ * An expert whose logit or bias is -inf is never chosen: where fewer than `top`
+ * are left, the last ids are -1 with weight 0.  A NaN counts as the largest and
+ * makes its row's weights NaN (its own alone where weights are single sigmoids), as
+ * +inf does under a softmax; ids stay in range and other rows as they are.  Sums
+ * are fp32.  No workspace.  MUON_ERR_INVALID_ARG: top < 1 or > experts;
+ * MUON_ERR_UNSUPPORTED: top > 32, experts > 1024, rows > 2^27, or a pointer not
+ * aligned to its element.
+ */
+typedef enum { MUON_SCORE_SOFTMAX = 0, MUON_SCORE_SIGMOID = 1 } muon_score;
+
+int muon_route(const void *logits, int64_t stride, const float *bias, int64_t rows, int64_t experts, int type,
+               int top, int score, int normalize, float scale, int64_t *ids, float *weights, muon_stream_t stream);
+
+/* The gradient of sum dweights weight in the logits, the choice held fixed (a
+ * bias has none).  ids are the forward call's; negative ones take no part, one >=
+ * experts takes none and is reported as MUON_ERR_DEVICE.  dlogits has `type`, rows
+ * dlogits_stride apart, is written whole, and may be the logits themselves (same
+ * stride). */
+int muon_route_backward(const float *dweights, const void *logits, int64_t stride, const int64_t *ids, int64_t rows,
+                        int64_t experts, int type, int top, int score, int normalize, float scale, void *dlogits,
+                        int64_t dlogits_stride, muon_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Tokens to rows sorted by expert, as muon_gated_ffn takes them, and back with
+ * weights.  Token t has `top` slots; slot (t, j) goes to expert ids[t][j].
+ *   x         device, tokens x hidden of `type` (bf16 or fp32), rows x_stride apart
+ *   ids       device, int64, [tokens][top]; a negative id is a slot that is not
+ *             routed (padding), one >= experts is treated so and reported as
+ *             MUON_ERR_DEVICE
+ *   rows      device, [tokens * top][hidden] dense, of `type`: the tokens' rows by
+ *             ascending expert, within an expert in the order of the slots; then a
+ *             row of zeros for each slot that is not routed
+ *   offsets   device, int64, experts + 1: each expert's first row and the end,
+ *             tokens * top.  The rows of zeros are the last expert's (their
+ *             results are zeros, and add nothing to gradients).
+ *   place     device, int64, [tokens][top]: each slot's row; -1 - row for a slot
+ *             that is not routed
+ * The order is the same for equal calls.  No workspace, no synchronisation.
+ * tokens == 0 writes zero offsets.  top <= 32, experts <= 1024, tokens * top <=
+ * 2^30, hidden <= 2^20 and pointers aligned to their element, else
+ * MUON_ERR_UNSUPPORTED (16-byte aligned rows take the widest accesses).
+ */
+int muon_dispatch(const void *x, int64_t x_stride, const int64_t *ids, int64_t tokens, int64_t top, int64_t experts,
+                  int64_t hidden, int type, void *rows, int64_t *offsets, int64_t *place, muon_stream_t stream);
+
+/* Its gradient: dx[t] = sum of drows[place[t][j]] over the slots that are routed. */
+int muon_dispatch_backward(const void *drows, const int64_t *place, int64_t tokens, int64_t top, int64_t hidden,
+                           int type, void *dx, int64_t dx_stride, muon_stream_t stream);
+
+/* out[t] = sum of weights[t][j] y[place[t][j]] over the slots that are routed, in the
+ * order of the slots and in fp32; y is [tokens * top][hidden] dense, out has y's type.
+ * weights: device, fp32, [tokens][top]; NULL stands for ones.  The rows of slots
+ * that are not routed are not read.  A place outside 0 .. tokens * top - 1 takes no part and
+ * is reported as MUON_ERR_DEVICE. */
+int muon_combine(const void *y, const int64_t *place, const float *weights, int64_t tokens, int64_t top,
+                 int64_t hidden, int type, void *out, int64_t out_stride, muon_stream_t stream);
+
+/* Its gradients: dy[place[t][j]] = weights[t][j] dout[t] (zeros in rows of slots that are
+ * not routed) and dweights[t][j] = <dout[t], y[place[t][j]]> (fp32 sums; 0 for such a slot).
+ * Either may be NULL; y is read for dweights alone. */
+int muon_combine_backward(const void *dout, int64_t dout_stride, const void *y, const int64_t *place,
+                          const float *weights, int64_t tokens, int64_t top, int64_t hidden, int type, void *dy,
+                          float *dweights, muon_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Softmax cross entropy of hidden states under a head matrix; the logits z = x
+ * weight^T are never stored:
+ *   lse = log sum_v exp z_v;  loss = lse - z[target]
+ *   x         device, bf16, rows x hidden, rows x_stride elements apart
+ *   weight    device, bf16, [vocab][hidden]
+ *   targets   device, int64, rows.  A negative target is not scored (loss 0);
+ *             one >= vocab gives NaN and MUON_ERR_DEVICE.
+ *   loss, lse device, fp32, rows (either may be NULL)
+ * bf16 operands, fp32 accumulation; z is not rounded.  A NaN or infinity stays in
+ * its row.  A row's result depends on that row and the weight alone, but for the
+ * order of its sums, which the sizes choose.  hidden and x_stride
+ * multiples of 8, x and weight 16-byte aligned, vocab <= 2^30, rows <= 2^24, else
+ * MUON_ERR_UNSUPPORTED.  workspace as muon_gated_ffn; rows == 0 is a no-op.
+ */
+size_t muon_head_loss_workspace_bytes(int64_t rows, int64_t vocab, int64_t hidden);
+int muon_head_loss(const void *x, int64_t x_stride, const void *weight, const int64_t *targets, int64_t rows,
+                   int64_t vocab, int64_t hidden, float *loss, float *lse, void *workspace, size_t workspace_bytes,
+                   muon_stream_t stream);
+
+/* The gradients of sum_rows dloss loss + dlse lse, by pieces of the vocabulary: z is
+ * formed again, piece by piece, and with p_v = exp(z_v - lse)
+ *   d_v = (dloss + dlse) p_v - dloss 1[v = target];   dx = d weight;   dweight = d^T x
+ * lse is the forward call's; dlse (fp32, rows) may be NULL (zero).  A row with a
+ * negative target takes no part, whatever else it holds, and its dx is zeros; one
+ * >= vocab is treated so and reported as MUON_ERR_DEVICE.  dx (rows dx_stride apart) and
+ * dweight ([vocab][hidden]) are bf16, written whole, and either may be NULL.  d is rounded to
+ * bf16 before the products that read it, sums are fp32 and in a fixed order.
+ * Requirements and workspace as muon_head_loss; rows == 0 writes a zero dweight. */
+size_t muon_head_loss_backward_workspace_bytes(int64_t rows, int64_t vocab, int64_t hidden);
+int muon_head_loss_backward(const float *dloss, const float *dlse, const void *x, int64_t x_stride,
+                            const void *weight, const int64_t *targets, const float *lse, int64_t rows, int64_t vocab,
+                            int64_t hidden, void *dx, int64_t dx_stride, void *dweight, void *workspace,
+                            size_t workspace_bytes, muon_stream_t stream);
+
 /* The default shape scale sqrt(max(1, rows/cols)). */
 float muon_default_scale(int64_t rows, int64_t cols);
 
@@ -491,8 +603,8 @@ float muon_default_scale(int64_t rows, int64_t cols);
  * word: MUON_ERR_TIMEOUT if a bounded wait ran out, MUON_ERR_DEVICE if a
  * Newton-Schulz input (or fused step's u) had a Frobenius norm that is not
  * finite in fp32 (an Inf or NaN entry, or entries beyond ~1.8e19; its output
- * is then zero or NaN) or a feed-forward or log-probability call met offsets or
- * a token out of range, MUON_ERR_CUDA for a CUDA error, else MUON_OK. */
+ * is then zero or NaN) or an operator beside the step met offsets, a token, a target,
+ * an expert's id or a place out of range, MUON_ERR_CUDA for a CUDA error, else MUON_OK. */
 int muon_get_device_status(muon_stream_t stream);
 
 /* Human-readable name of a muon_status value (static string). */
@@ -514,7 +626,7 @@ int64_t muon_launch_count(void);
 /* Fault injection on the host, for testing callers' error paths: the next
  * `count` device allocations the library makes for itself (the workspaces of
  * muon_ns_batched, muon_ns_batched_f32, the schedule variants,
- * muon_step_batched, muon_gated_ffn, its backward call and
+ * muon_step_batched, muon_gated_ffn, muon_head_loss, their backward calls and
  * muon_block_norm_backward, and the slots of muon_step_host) fail as if the memory
  * pool were exhausted, without calling CUDA: the call returns
  * MUON_ERR_NO_MEMORY before it launches anything or touches its buffers.

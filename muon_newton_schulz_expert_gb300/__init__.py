@@ -100,6 +100,16 @@ SIGNATURES = {
     "muon_block_norm_backward": (_INT, [_P, _P, _SIZE, _P]),
     "muon_token_logprobs": (_INT, [_P, _I64, _P, _I64, _I64, _INT, _P, _P, _P, _INT, _P, _P, _P]),
     "muon_token_logprobs_backward": (_INT, [_P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _INT, _P, _I64, _P]),
+    "muon_route": (_INT, [_P, _I64, _P, _I64, _I64, _INT, _INT, _INT, _INT, _F, _P, _P, _P]),
+    "muon_route_backward": (_INT, [_P, _P, _I64, _P, _I64, _I64, _INT, _INT, _INT, _INT, _F, _P, _I64, _P]),
+    "muon_dispatch": (_INT, [_P, _I64, _P, _I64, _I64, _I64, _I64, _INT, _P, _P, _P, _P]),
+    "muon_dispatch_backward": (_INT, [_P, _P, _I64, _I64, _I64, _INT, _P, _I64, _P]),
+    "muon_combine": (_INT, [_P, _P, _P, _I64, _I64, _I64, _INT, _P, _I64, _P]),
+    "muon_combine_backward": (_INT, [_P, _I64, _P, _P, _P, _I64, _I64, _I64, _INT, _P, _P, _P]),
+    "muon_head_loss_workspace_bytes": (_SIZE, [_I64, _I64, _I64]),
+    "muon_head_loss": (_INT, [_P, _I64, _P, _P, _I64, _I64, _I64, _P, _P, _P, _SIZE, _P]),
+    "muon_head_loss_backward_workspace_bytes": (_SIZE, [_I64, _I64, _I64]),
+    "muon_head_loss_backward": (_INT, [_P, _P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _SIZE, _P]),
     "muon_get_device_status": (_INT, [_P]),
     "muon_status_string": (ctypes.c_char_p, [_INT]),
     "muon_set_wait_timeout_ns": (_U64, [_U64]),
@@ -435,6 +445,10 @@ def muon_step_host_grouped(groups, *, mu=0.95, nesterov=True, steps=5, coeffs=QU
 ACTIVATIONS = {"silu": 0, "gelu": 1}
 BlockNormGrads = collections.namedtuple("BlockNormGrads", "dresidual dblock dw_post dgate dw_pre")
 TokenLogprobs = collections.namedtuple("TokenLogprobs", "logp entropy lse top_ids top_logp")
+SCORES = {"softmax": 0, "sigmoid": 1}
+Route = collections.namedtuple("Route", "ids weights")
+Dispatch = collections.namedtuple("Dispatch", "rows offsets place")
+HeadLoss = collections.namedtuple("HeadLoss", "loss lse")
 
 
 _ops_module = None
@@ -572,6 +586,104 @@ def muon_token_logprobs_backward(logits, tokens, lse, entropy=None, dlogp=None, 
         logits, tokens, lse, entropy, dlogp, dentropy, out, _raw_stream(stream)))
 
 
+def _score(score):
+    code = SCORES.get(score)
+    if code is None:
+        raise ValueError(f"score must be one of {sorted(SCORES)}")
+    return code
+
+
+def muon_route(logits, top, *, bias=None, score="softmax", normalize=True, scale=1.0, stream=None):
+    """A router's ``top`` experts of each row of logits (rows, experts), bf16 or fp32, and their weights; see muon.h.
+
+    score is "softmax" or "sigmoid"; bias (fp32, (experts,)) takes part in the
+    choice alone; with ``normalize`` a row's weights add up to ``scale``.
+    Returns Route(ids, weights): int64 and fp32, (rows, top); an id is -1
+    where fewer experts are left (logit or bias -inf).  The gradient is
+    muon_route_backward's (autograd records nothing).
+    """
+    return Route(*_outputs("muon_route", _ops().route(
+        logits, top, bias, _score(score), normalize, scale, _raw_stream(stream))))
+
+
+def muon_route_backward(dweights, logits, ids, *, score="softmax", normalize=True, scale=1.0, out=None, stream=None):
+    """The gradient of sum(dweights * weights) in the logits, in their type; ids are the forward call's.
+
+    ``out`` may be the logits themselves.
+    """
+    return _outputs("muon_route_backward", _ops().route_backward(
+        dweights, logits, ids, _score(score), normalize, scale, out, _raw_stream(stream)))
+
+
+def muon_dispatch(x, ids, experts, *, out=None, stream=None):
+    """The rows of tokens x (tokens, hidden), bf16 or fp32, sorted by expert, for muon_gated_ffn; see muon.h.
+
+    ids (int64, (tokens, slots)) are the experts of each token's slots; a
+    negative one is a slot that is not routed, whose row is zeros and comes
+    last.  Returns Dispatch(rows, offsets, place): (tokens * slots, hidden),
+    int64 (experts + 1,) and int64 (tokens, slots), each slot's row (-1 - row
+    where it is not routed).  muon_combine brings rows back.  The gradient is
+    muon_dispatch_backward's (autograd records nothing).
+    """
+    return Dispatch(*_outputs("muon_dispatch", _ops().dispatch(x, ids, experts, out, _raw_stream(stream))))
+
+
+def muon_dispatch_backward(drows, place, *, out=None, stream=None):
+    """The gradient of muon_dispatch in x: each token's sum over its routed slots' rows, in their type."""
+    return _outputs("muon_dispatch_backward", _ops().dispatch_backward(drows, place, out, _raw_stream(stream)))
+
+
+def muon_combine(y, place, weights=None, *, out=None, stream=None):
+    """Rows y (tokens * slots, hidden) brought back to their tokens: sum over slots of weights * y[place]; see muon.h.
+
+    place is muon_dispatch's, weights fp32 (tokens, slots) as muon_route gives
+    them (None: ones).  The gradients are muon_combine_backward's (autograd
+    records nothing).
+    """
+    return _outputs("muon_combine", _ops().combine(y, place, weights, out, _raw_stream(stream)))
+
+
+def muon_combine_backward(dout, y, place, weights=None, *, dy=None, need_dy=True, need_dweights=True, stream=None):
+    """Gradients of muon_combine: (dy, dweights); zeros in rows and slots that are not routed.
+
+    dy is written whole when given.  What is not needed is None, and dweights
+    also where there are no weights; y may be None when dweights are not needed.
+    """
+    return _outputs("muon_combine_backward", _ops().combine_backward(
+        dout, y, place, weights, dy, need_dy, need_dweights, _raw_stream(stream)))
+
+
+def muon_head_loss_workspace_bytes(rows, vocab, hidden):
+    return int(lib().muon_head_loss_workspace_bytes(rows, vocab, hidden))
+
+
+def muon_head_loss(x, weight, targets, *, workspace=None, stream=None):
+    """Softmax cross entropy of x (rows, hidden) under a head matrix (vocab, hidden), bf16, without logits; see muon.h.
+
+    targets int64 (rows,), negative where a row is not scored (loss 0).
+    Returns HeadLoss(loss, lse), fp32.  The gradients are
+    muon_head_loss_backward's (autograd records nothing).
+    """
+    return HeadLoss(*_outputs("muon_head_loss", _ops().head_loss(
+        x, weight, targets, workspace, _raw_stream(stream))))
+
+
+def muon_head_loss_backward_workspace_bytes(rows, vocab, hidden):
+    return int(lib().muon_head_loss_backward_workspace_bytes(rows, vocab, hidden))
+
+
+def muon_head_loss_backward(dloss, x, weight, targets, lse, *, dlse=None, dx=None, dweight=None, need_dx=True,
+                            need_dweight=True, workspace=None, stream=None):
+    """Gradients of sum(dloss * loss + dlse * lse): (dx, dweight), bf16, dweight what muon_adamw_update takes.
+
+    lse is the forward call's.  Rows with a negative target take no part (dx
+    zeros).  dx and dweight are written whole when given; what is not needed
+    is None.
+    """
+    return _outputs("muon_head_loss_backward", _ops().head_loss_backward(
+        dloss, x, weight, targets, lse, dlse, dx, dweight, need_dx, need_dweight, workspace, _raw_stream(stream)))
+
+
 def muon_default_scale(rows, cols):
     """The library's default shape scale for a stored rows x cols matrix (muon.h)."""
     return float(lib().muon_default_scale(int(rows), int(cols)))
@@ -612,11 +724,11 @@ def muon_trace_begin():
 
 def muon_trace_end():
     """{kernel name: (launches, total_ms)} for the traced region."""
-    entries = (TraceEntry * 32)()
-    k = lib().muon_trace_end(entries, 32)
+    entries = (TraceEntry * 64)()
+    k = lib().muon_trace_end(entries, 64)
     if k < 0:
         raise MuonError("muon_trace_end", k)
-    return {entries[i].kernel.decode(): (int(entries[i].launches), float(entries[i].total_ms)) for i in range(min(k, 32))}
+    return {entries[i].kernel.decode(): (int(entries[i].launches), float(entries[i].total_ms)) for i in range(min(k, 64))}
 
 
 # ---------------------------------------------------------------------------- one whole step

@@ -34,7 +34,8 @@ LIB_CHECKED = os.path.join(OUT_DIR, "libmuon_checked.so")
 BINDING = os.path.join(OUT_DIR, "muon_ops.so")
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = ["api.cu", "elementwise.cu", "gemm_tc.cu", "gemm_f32.cu", "ns_static.cu", "host_stream.cu",
-           "ffn.cu", "ffn_tc.cu", "ffn_few.cu", "norm.cu", "logprobs.cu"]
+           "ffn.cu", "ffn_tc.cu", "ffn_few.cu", "norm.cu", "logprobs.cu",
+           "route.cu", "dispatch.cu", "head_loss.cu", "head_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -40,7 +40,10 @@ const char *kTraceNames[kTraceKinds] = {"momentum_bf16", "momentum_f32", "norm_p
                                         "ffn_dx_tc",     "ffn_tail",     "ffn_dw13_tc",  "ffn_dw2_tc",
                                         "block_norm",    "block_norm_staged", "block_norm_backward",
                                         "block_norm_backward_staged", "norm_weight_sum",
-                                        "token_logprobs", "token_logprobs_backward"};
+                                        "token_logprobs", "token_logprobs_backward",
+                                        "route",         "route_backward", "expert_order", "dispatch_rows",
+                                        "combine",       "combine_backward", "head_stats_tc", "head_join",
+                                        "head_rows",     "head_dlogits_tc", "head_grads_tc", "head_dx"};
 
 struct TraceRec {
   int kind;

@@ -39,6 +39,14 @@ decltype(&muon_block_norm) p_block_norm;
 decltype(&muon_block_norm_backward) p_block_norm_backward;
 decltype(&muon_token_logprobs) p_token_logprobs;
 decltype(&muon_token_logprobs_backward) p_token_logprobs_backward;
+decltype(&muon_route) p_route;
+decltype(&muon_route_backward) p_route_backward;
+decltype(&muon_dispatch) p_dispatch;
+decltype(&muon_dispatch_backward) p_dispatch_backward;
+decltype(&muon_combine) p_combine;
+decltype(&muon_combine_backward) p_combine_backward;
+decltype(&muon_head_loss) p_head_loss;
+decltype(&muon_head_loss_backward) p_head_loss_backward;
 
 using Sizes = std::initializer_list<int64_t>;
 
@@ -472,6 +480,241 @@ PyObject *token_logprobs_backward(PyObject *, PyObject *const *a, Py_ssize_t n) 
   });
 }
 
+// ---------------------------------------------------------------------------- routing
+// a size or count that has to fit an int (what it may be beyond that is the library's to say)
+int small_integer(PyObject *o, const char *name) {
+  const long long v = integer(o);
+  if (v < -1000000 || v > 1000000) value_error(std::string(name) + " is out of range");
+  return (int)v;
+}
+
+const at::Tensor &route_logits(Call &c, PyObject *o, int64_t *T, int64_t *E, int64_t *stride, int *code) {
+  const at::Tensor &x = c.tensor(o, "logits");
+  if (x.dim() != 2) value_error("logits must be (rows, experts)");
+  *code = type_code(x, "logits");
+  *T = x.size(0), *E = x.size(1);
+  return c.rows(o, "logits", x.scalar_type(), *T, *E, stride);
+}
+
+// (logits, top, bias, score, normalize, scale, stream)
+PyObject *route(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 7, [&]() -> PyObject * {
+    Call c(a[6]);
+    int64_t T, E, stride;
+    int code;
+    const at::Tensor &x = route_logits(c, a[0], &T, &E, &stride, &code);
+    const int top = small_integer(a[1], "top");
+    const float *bias =
+        given(a[2]) ? static_cast<const float *>(c.dense(a[2], "bias", at::kFloat, {E}).data_ptr()) : nullptr;
+    const int score = (int)integer(a[3]), normalize = truth(a[4]);
+    const float scale = (float)number(a[5]);
+    Out ids, weights;
+    ids.t = c.empty({T, std::max(top, 0)}, x.options().dtype(at::kLong));
+    weights.t = c.empty({T, std::max(top, 0)}, x.options().dtype(at::kFloat));
+    const int st = p_route(x.data_ptr(), stride, bias, T, E, code, top, score, normalize, scale,
+                           ids.t.data_ptr<int64_t>(), weights.t.data_ptr<float>(), c.stream());
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    return tuple_of({&ids, &weights});
+  });
+}
+
+// (dweights, logits, ids, score, normalize, scale, out, stream)
+PyObject *route_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> PyObject * {
+    Call c(a[7]);
+    int64_t T, E, stride, out_stride;
+    int code;
+    const at::Tensor &x = route_logits(c, a[1], &T, &E, &stride, &code), &ids = c.tensor(a[2], "ids");
+    if (ids.dim() != 2) value_error("ids must be (rows, top)");
+    const int64_t top = ids.size(1);
+    if (top > 1000000) value_error("top is out of range");
+    c.dense(a[2], "ids", at::kLong, {T, top});
+    const at::Tensor &dw = c.dense(a[0], "dweights", at::kFloat, {T, top});
+    const int score = (int)integer(a[3]), normalize = truth(a[4]);
+    const float scale = (float)number(a[5]);
+    const Out out = out_rows(c, a[6], "out", x, T, E, &out_stride);
+    const int st = p_route_backward(dw.data_ptr<float>(), x.data_ptr(), stride, ids.data_ptr<int64_t>(), T, E, code,
+                                    (int)top, score, normalize, scale, out.t.data_ptr(), out_stride, c.stream());
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    return out.object();
+  });
+}
+
+// ---------------------------------------------------------------------------- tokens by expert and back
+// (tokens, slots), int64
+const at::Tensor &slots_of(Call &c, PyObject *o, const char *name, int64_t *T, int64_t *k) {
+  const at::Tensor &t = c.tensor(o, name);
+  if (t.dim() != 2) value_error(std::string(name) + " must be (tokens, slots)");
+  *T = t.size(0), *k = t.size(1);
+  return c.dense(o, name, at::kLong, {*T, *k});
+}
+
+// rows by expert, dense
+const at::Tensor &sorted_rows(Call &c, PyObject *o, const char *name, int64_t n, int64_t *H, int *code) {
+  const at::Tensor &t = c.tensor(o, name);
+  if (t.dim() != 2) value_error(std::string(name) + " must be (tokens * slots, hidden)");
+  *code = type_code(t, name);
+  *H = t.size(1);
+  return c.dense(o, name, t.scalar_type(), {n, *H});
+}
+
+// (x, ids, experts, out, stream)
+PyObject *dispatch(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 5, [&]() -> PyObject * {
+    Call c(a[4]);
+    int64_t T, k, ldx;
+    const at::Tensor &ids = slots_of(c, a[1], "ids", &T, &k), &xt = c.tensor(a[0], "x");
+    if (xt.dim() != 2) value_error("x must be (tokens, hidden)");
+    const int code = type_code(xt, "x");
+    const int64_t H = xt.size(1);
+    const at::Tensor &x = c.rows(a[0], "x", xt.scalar_type(), T, H, &ldx);
+    const int experts = small_integer(a[2], "experts");
+    Out rows, offsets, place;
+    if (given(a[3])) {
+      rows.t = c.dense(a[3], "out", x.scalar_type(), {T * k, H});
+      rows.given = a[3];
+    } else {
+      rows.t = c.empty({T * k, H}, x.options());
+    }
+    offsets.t = c.empty({std::max(experts, 0) + 1}, ids.options());
+    place.t = c.empty({T, k}, ids.options());
+    const int st = p_dispatch(x.data_ptr(), ldx, ids.data_ptr<int64_t>(), T, k, experts, H, code, rows.t.data_ptr(),
+                              offsets.t.data_ptr<int64_t>(), place.t.data_ptr<int64_t>(), c.stream());
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    return tuple_of({&rows, &offsets, &place});
+  });
+}
+
+// (drows, place, out, stream)
+PyObject *dispatch_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 4, [&]() -> PyObject * {
+    Call c(a[3]);
+    int64_t T, k, H, ldo;
+    int code;
+    const at::Tensor &place = slots_of(c, a[1], "place", &T, &k);
+    const at::Tensor &drows = sorted_rows(c, a[0], "drows", T * k, &H, &code);
+    const Out out = out_rows(c, a[2], "out", drows, T, H, &ldo);
+    const int st = p_dispatch_backward(drows.data_ptr(), place.data_ptr<int64_t>(), T, k, H, code, out.t.data_ptr(), ldo,
+                                       c.stream());
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    return out.object();
+  });
+}
+
+// (y, place, weights, out, stream)
+PyObject *combine(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 5, [&]() -> PyObject * {
+    Call c(a[4]);
+    int64_t T, k, H, ldo;
+    int code;
+    const at::Tensor &place = slots_of(c, a[1], "place", &T, &k);
+    const at::Tensor &y = sorted_rows(c, a[0], "y", T * k, &H, &code);
+    const float *w =
+        given(a[2]) ? static_cast<const float *>(c.dense(a[2], "weights", at::kFloat, {T, k}).data_ptr()) : nullptr;
+    const Out out = out_rows(c, a[3], "out", y, T, H, &ldo);
+    const int st = p_combine(y.data_ptr(), place.data_ptr<int64_t>(), w, T, k, H, code, out.t.data_ptr(), ldo, c.stream());
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    return out.object();
+  });
+}
+
+// (dout, y, place, weights, dy, need_dy, need_dweights, stream)
+PyObject *combine_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> PyObject * {
+    Call c(a[7]);
+    int64_t T, k, ldd;
+    const at::Tensor &place = slots_of(c, a[2], "place", &T, &k), &dt = c.tensor(a[0], "dout");
+    if (dt.dim() != 2) value_error("dout must be (tokens, hidden)");
+    const int code = type_code(dt, "dout");
+    const int64_t H = dt.size(1);
+    const at::Tensor &dout = c.rows(a[0], "dout", dt.scalar_type(), T, H, &ldd);
+    const float *w =
+        given(a[3]) ? static_cast<const float *>(c.dense(a[3], "weights", at::kFloat, {T, k}).data_ptr()) : nullptr;
+    Out dy, dweights;
+    const void *y = nullptr;
+    if (truth(a[5])) {
+      if (given(a[4])) {
+        dy.t = c.dense(a[4], "dy", dout.scalar_type(), {T * k, H});
+        dy.given = a[4];
+      } else {
+        dy.t = c.empty({T * k, H}, dout.options());
+      }
+    }
+    if (given(a[3]) && truth(a[6])) {
+      y = c.dense(a[1], "y", dout.scalar_type(), {T * k, H}).data_ptr();
+      dweights.t = c.empty({T, k}, dout.options().dtype(at::kFloat));
+    }
+    const int st = p_combine_backward(dout.data_ptr(), ldd, y, place.data_ptr<int64_t>(), w, T, k, H, code, opt(dy.t),
+                                      static_cast<float *>(opt(dweights.t)), c.stream());
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    return tuple_of({&dy, &dweights});
+  });
+}
+
+// ---------------------------------------------------------------------------- loss over a head matrix
+struct Head {
+  int64_t T, V, H, ldx;
+  const at::Tensor *x, *w;
+  const int64_t *targets;
+
+  Head(Call &c, PyObject *x_, PyObject *w_, PyObject *t_) {
+    const at::Tensor &xt = c.tensor(x_, "x"), &wt = c.tensor(w_, "weight");
+    if (xt.dim() != 2) value_error("x must be (rows, hidden)");
+    if (wt.dim() != 2) value_error("weight must be (vocab, hidden)");
+    T = xt.size(0), H = xt.size(1), V = wt.size(0);
+    x = &c.rows(x_, "x", at::kBFloat16, T, H, &ldx);
+    w = &c.dense(w_, "weight", at::kBFloat16, {V, H});
+    targets = static_cast<const int64_t *>(c.dense(t_, "targets", at::kLong, {T}).data_ptr());
+  }
+};
+
+// (x, weight, targets, workspace, stream)
+PyObject *head_loss(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 5, [&]() -> PyObject * {
+    Call c(a[4]);
+    const Head h(c, a[0], a[1], a[2]);
+    size_t bytes;
+    void *ws = c.workspace(a[3], &bytes);
+    const auto f32 = h.x->options().dtype(at::kFloat);
+    Out loss, lse;
+    loss.t = c.empty({h.T}, f32);
+    lse.t = c.empty({h.T}, f32);
+    const int st = p_head_loss(h.x->data_ptr(), h.ldx, h.w->data_ptr(), h.targets, h.T, h.V, h.H,
+                               loss.t.data_ptr<float>(), lse.t.data_ptr<float>(), ws, bytes, c.stream());
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    return tuple_of({&loss, &lse});
+  });
+}
+
+// (dloss, x, weight, targets, lse, dlse, dx, dweight, need_dx, need_dweight, workspace, stream)
+PyObject *head_loss_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 12, [&]() -> PyObject * {
+    Call c(a[11]);
+    const Head h(c, a[1], a[2], a[3]);
+    const float *dloss = static_cast<const float *>(c.dense(a[0], "dloss", at::kFloat, {h.T}).data_ptr());
+    const float *lse = static_cast<const float *>(c.dense(a[4], "lse", at::kFloat, {h.T}).data_ptr());
+    const float *dlse =
+        given(a[5]) ? static_cast<const float *>(c.dense(a[5], "dlse", at::kFloat, {h.T}).data_ptr()) : nullptr;
+    int64_t lddx = h.H;
+    Out dx, dw;
+    if (truth(a[8])) dx = out_rows(c, a[6], "dx", *h.x, h.T, h.H, &lddx);
+    if (truth(a[9])) {
+      if (given(a[7])) {
+        dw.t = c.dense(a[7], "dweight", at::kBFloat16, {h.V, h.H});
+        dw.given = a[7];
+      } else {
+        dw.t = c.empty({h.V, h.H}, h.w->options());
+      }
+    }
+    size_t bytes;
+    void *ws = c.workspace(a[10], &bytes);
+    const int st = p_head_loss_backward(dloss, dlse, h.x->data_ptr(), h.ldx, h.w->data_ptr(), h.targets, lse, h.T, h.V,
+                                        h.H, opt(dx.t), lddx, opt(dw.t), ws, bytes, c.stream());
+    if (st != MUON_OK) return PyLong_FromLong(st);
+    return tuple_of({&dx, &dw});
+  });
+}
+
 // bind({name: address}): the library's entry points
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded(n, 1, [&]() -> PyObject * {
@@ -487,6 +730,14 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     MUON_BIND(block_norm_backward);
     MUON_BIND(token_logprobs);
     MUON_BIND(token_logprobs_backward);
+    MUON_BIND(route);
+    MUON_BIND(route_backward);
+    MUON_BIND(dispatch);
+    MUON_BIND(dispatch_backward);
+    MUON_BIND(combine);
+    MUON_BIND(combine_backward);
+    MUON_BIND(head_loss);
+    MUON_BIND(head_loss_backward);
 #undef MUON_BIND
     Py_RETURN_NONE;
   });
@@ -500,6 +751,14 @@ PyMethodDef methods[] = {MUON_METHOD(bind),
                          MUON_METHOD(block_norm_backward),
                          MUON_METHOD(token_logprobs),
                          MUON_METHOD(token_logprobs_backward),
+                         MUON_METHOD(route),
+                         MUON_METHOD(route_backward),
+                         MUON_METHOD(dispatch),
+                         MUON_METHOD(dispatch_backward),
+                         MUON_METHOD(combine),
+                         MUON_METHOD(combine_backward),
+                         MUON_METHOD(head_loss),
+                         MUON_METHOD(head_loss_backward),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "muon_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

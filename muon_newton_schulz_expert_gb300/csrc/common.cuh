@@ -48,6 +48,18 @@ enum TraceKind : int {
   kTraceNormWeightSum,
   kTraceLogprobs,
   kTraceLogprobsBwd,
+  kTraceRoute,
+  kTraceRouteBwd,
+  kTraceExpertOrder,   // the sort of a dispatch
+  kTraceDispatchRows,
+  kTraceCombine,       // and the gradient of a dispatch
+  kTraceCombineBwd,
+  kTraceHeadStats,     // maxima and sums of tiles of x W^T (tensor cores)
+  kTraceHeadJoin,
+  kTraceHeadRows,
+  kTraceHeadDlogits,   // a piece of the logits' gradient (tensor cores)
+  kTraceHeadGrads,     // dx and dW from it (tensor cores)
+  kTraceHeadDx,
   kTraceKinds
 };
 

@@ -1,0 +1,671 @@
+// Tensor-core products of the loss over a head matrix W [V][H] and rows x [T][H]:
+//   z = x W^T  (T x V), lse = log sum_v exp z_v, loss = lse - z_target
+//   d_v = g p_v - hit [v = target],  dx = d W,  dW = d^T x
+// z and d exist as tiles only: STATS reduces a tile of z to a maximum and a sum per
+// row in its epilogue; the backward pass recomputes z by pieces of the vocabulary,
+// DLOGITS stores a piece of d in bf16 and GRADS forms both products that read it.
+//
+// One kernel, instantiated for the three; persistent CTA pairs on output tiles of
+// 256 x up to 256 (tcgen05.mma.cta_group::2, M = 256, K = 16, bf16 operands, fp32
+// accumulation in TMEM), fed by TMA through a ring of three stages of two k-blocks
+// of 64.
+//
+// Rows of x are on M, the vocabulary on N: a thread of the epilogue then holds 32
+// columns of one row at a time, so the softmax's maximum and sum need no exchange
+// between threads; each half of a tile's columns leaves one (m, s) per row.  Tiles
+// walk the vocabulary with the row tiles of a group fastest, a group being as many row
+// tiles as keep their x in L2 (kGroupBytes), so that W is read once per group.
+// With few tiles N is 128 or 64, so that more pairs of CTAs have one.
+//
+// GRADS runs dx's and dW's tiles in one launch: dx has few tiles with long sums (K =
+// the piece), dW many with short ones (K = rows), and the short ones fill what the long
+// ones leave of the last wave (Schedule).  Where dx's tiles are so few that one is more
+// than a pair's share of the work, its K is cut and the parts are added in order.
+//
+// Rounding: d is stored in bf16, the operand type of the products that read it, once
+// (the feed-forward products round h, dg and du the same way); the rest is fp32.
+//
+// Roles per CTA (320 threads): warp 0 TMA producer, warp 1 MMA issuer (even CTA) and
+// TMEM owner, warps 2..9 epilogue.  Two accumulators, so that the epilogue of one tile
+// overlaps the next tile's products.  Every wait is bounded (tc.cuh).
+#include <math.h>
+
+#include <algorithm>
+
+#include "head_loss.cuh"
+#include "tiles.cuh"
+
+namespace muon {
+namespace {
+
+constexpr int CM = 256, BM = 128;   // M of a pair tile, M held by one CTA
+constexpr int BN = 256, BNH = 128;  // most N of a pair tile, N loaded by one CTA
+constexpr int UMMA_K = 16;
+constexpr int A_STAGE = BM * BK * 2;
+constexpr int B_STAGE = BNH * BK * 2;
+constexpr int KB_BYTES = A_STAGE + B_STAGE;
+constexpr int STAGES = 3, KSUB = 2;
+constexpr int STAGE_BYTES = KSUB * KB_BYTES;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int ACC_COLS = BN;
+constexpr int TMEM_COLS = 2 * ACC_COLS;
+constexpr int NFULL = STAGES * KSUB;
+constexpr int NUM_BARS = NFULL + STAGES + 5;
+constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * BOX_BYTES + NUM_BARS * 8 + 16;
+static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int64_t kGroupBytes = 48 << 20;   // of x that is used again and again, beside W's stream through 129 MB of L2
+
+enum Mode { STATS = 0, DLOGITS, GRADS };
+
+// GRADS: dx's tiles (`longs` of them) and then dW's (`shorts`), dealt to the pairs one after the
+// other.  Where dx's do not come out even, the pairs without the last one take `extra` of dW's
+// meanwhile.
+struct Schedule {
+  int longs, shorts, extra;
+
+  __host__ __device__ int before(int ncl) const { return longs % ncl ? extra * (ncl - longs % ncl) : 0; }
+  // the i-th tile of pair c of ncl: < longs a dx tile, else longs + a dW tile; -1: none
+  __device__ int tile(int i, int c, int ncl) const {
+    const int full = longs / ncl, rem = longs % ncl;
+    const int mine = full + (c < rem ? 1 : 0);
+    if (i < mine) return i * ncl + c;
+    i -= mine;
+    int at;
+    if (rem && c >= rem) {
+      if (i < extra) at = i * (ncl - rem) + (c - rem);
+      else at = before(ncl) + (i - extra) * ncl + c;
+    } else {
+      at = before(ncl) + i * ncl + c;
+    }
+    return at < shorts ? longs + at : -1;
+  }
+};
+
+struct Args {
+  CUtensorMap a, b;        // STATS, DLOGITS: x and W, K-major;  GRADS: dx's d (K-major) and W (MN-major)
+  CUtensorMap a2, b2;      // GRADS: dW's d and x, MN-major
+  CUtensorMap out, out2;   // DLOGITS: d;  GRADS: dx or its sums, and dW
+  long long rows, vocab, v0;
+  int hidden;
+  int kblocks, kblocks2;   // of K;  GRADS: of dx's K (the piece) and of dW's (the rows)
+  int tiles_m, tiles_n;    // row tiles and vocabulary tiles (of bn);  GRADS: row tiles and tiles of H
+  int bn, group;           // columns of a tile, row tiles of a group
+  int tiles_v, splits;     // GRADS: vocabulary tiles of the piece, parts of dx's K
+  Schedule schedule;
+  bool wide;               // GRADS: W's 128 columns load in one piece
+  int out_kind;            // GRADS: 0 dx in bf16, 1 sums written, 2 sums added to
+  const int64_t *targets;  // STATS
+  float2 *parts;
+  float *target_logit;
+  const HeadRow *row;      // DLOGITS
+  unsigned *err;
+  unsigned long long timeout_ns;
+};
+
+// A tile: its places on M and N in tiles, first k-block and their number.
+template <int MODE>
+struct Tile {
+  int tm, tn, kb0 = 0, num_kb;
+  int part = 0;       // GRADS, dx: of a cut sum
+  bool dw = false;    // GRADS: a tile of dW (M = the piece's vocabulary entries, N = H)
+
+  __device__ Tile(const Args &p, int t) {
+    if (MODE != GRADS) {
+      const int per = p.group * p.tiles_n, g = t / per, r = t - g * per;
+      const int gm = min(p.group, p.tiles_m - g * p.group);
+      tn = r / gm;
+      tm = g * p.group + (r - tn * gm);
+      num_kb = p.kblocks;
+      return;
+    }
+    dw = t >= p.schedule.longs;
+    if (dw) {
+      t -= p.schedule.longs;
+      tm = t / p.tiles_n;
+      tn = t - tm * p.tiles_n;
+      num_kb = p.kblocks2;
+    } else {
+      const int per = p.tiles_m * p.tiles_n;
+      part = t / per;
+      t -= part * per;
+      tm = t / p.tiles_n;
+      tn = t - tm * p.tiles_n;
+      kb0 = (int)((long long)p.kblocks * part / p.splits);
+      num_kb = (int)((long long)p.kblocks * (part + 1) / p.splits) - kb0;
+    }
+  }
+};
+
+// the i-th tile of this pair, or -1
+template <int MODE>
+__device__ __forceinline__ int tile_of(const Args &p, int i) {
+  const int c = (int)(blockIdx.x >> 1), ncl = (int)(gridDim.x >> 1);
+  if (MODE == GRADS) return p.schedule.tile(i, c, ncl);
+  const long long t = (long long)i * ncl + c;
+  return t < (long long)p.tiles_m * p.tiles_n ? (int)t : -1;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap *map, uint32_t src, int c0, int c1, int c2,
+                                           unsigned *err) {
+  if (!dcheck((c0 & 15) == 0 && c0 >= 0 && c1 >= 0 && c2 >= 0, err)) return;
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
+// 32 rows x 32 columns of fp32 out of a warp (lane = row), written or added
+__device__ __forceinline__ void put_sums(const Writer &out, const uint32_t (&v)[32], const CUtensorMap *map, bool add,
+                                         int lane, int col0, int row0, int part, unsigned *err) {
+  if (lane == 0) bulk_wait_read_all();  // the box's last store has read it
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4 *>(out.box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+        make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (add) tma_add_3d(map, out.box_s, col0, row0, part, err);
+    else tma_store_3d(map, out.box_s, col0, row0, part, err);
+    bulk_commit();
+  }
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_constant__ Args p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *epi_smem = smem + STAGES * STAGE_BYTES;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(epi_smem + EPI_WARPS * BOX_BYTES);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NUM_BARS);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = smem_u32(bars);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();  // 0: issues the MMAs; 1: its peer
+  auto full = [&](int s, int j) { return bar0 + 8u * (uint32_t)(s * KSUB + j); };
+  auto empty = [&](int s) { return bar0 + 8u * (uint32_t)(NFULL + s); };
+  auto accf = [&](int a) { return bar0 + 8u * (uint32_t)(NFULL + STAGES + a); };
+  auto acce = [&](int a) { return bar0 + 8u * (uint32_t)(NFULL + STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (uint32_t)(NFULL + STAGES + 4);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NFULL; ++s) mbar_init(bar0 + 8u * s, 1);   // used in CTA 0: expect_tx for both halves
+    for (int s = 0; s < STAGES; ++s) mbar_init(empty(s), 1);       // multicast commit
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(accf(a), 1);               // multicast commit
+      mbar_init(acce(a), 2 * EPI_WARPS);   // used in CTA 0: every epilogue warp of the pair
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&p.a);
+    tma_prefetch_desc(&p.b);
+    if (MODE != STATS) tma_prefetch_desc(&p.out);
+  }
+  if (warp == 1) {  // one warp in each CTA of the pair allocates the same columns in both
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the peer's barriers are initialised before anyone signals them
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Watch w{abort_flag, p.err, p.timeout_ns};
+  const unsigned long long drain_ns = p.timeout_ns < 20000000ull ? p.timeout_ns : 20000000ull;
+  wait_for_previous_grid();
+  let_next_grid_start();
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer (both CTAs)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t issued = 0, issued_parity = 0;  // stages ever filled, and the parity of their last fill
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        const int t = tile_of<MODE>(p, i);
+        if (t < 0) break;
+        const Tile<MODE> cur(p, t);
+        const int bnh = MODE == GRADS ? BNH : p.bn / 2;
+        const int m_a = cur.tm * CM + (int)rank * BM;                  // first of this CTA's places on M and N
+        const int n_b = cur.tn * (2 * bnh) + (int)rank * bnh;
+        const uint32_t kb_bytes = (uint32_t)(A_STAGE + bnh * (BK * 2));
+        for (int kb = 0; kb < cur.num_kb; kb += KSUB) {
+          if (!wait_polled(empty(stage), phase ^ 1u, w)) {
+            ok = false;
+            break;
+          }
+          const int valid = cur.num_kb - kb < KSUB ? cur.num_kb - kb : KSUB;
+          // CTA 0's barrier counts the bytes of both CTAs; a k-block past the
+          // end of K still completes its phase, with no bytes
+          if (rank == 0)
+#pragma unroll
+            for (int j = 0; j < KSUB; ++j) mbar_expect_tx(full(stage, j), j < valid ? 2 * kb_bytes : 0);
+          issued |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+#pragma unroll
+          for (int j = 0; j < KSUB; ++j) {
+            if (j >= valid) break;
+            const int k = (cur.kb0 + kb + j) * BK;
+            const uint32_t sa = sbase + stage * STAGE_BYTES + j * KB_BYTES, sb = sa + A_STAGE;
+            const uint32_t bar = map_to_rank(full(stage, j), 0);
+            if (MODE != GRADS) {
+              tma_load_3d_pair(sa, &p.a, bar, k, m_a, 0, p.err);
+              tma_load_3d_pair(sb, &p.b, bar, k, (int)p.v0 + n_b, 0, p.err);
+            } else if (!cur.dw) {
+              tma_load_3d_pair(sa, &p.a, bar, k, m_a, 0, p.err);
+              load_columns(sb, &p.b, bar, n_b, (int)p.v0 + k, 0, p.wide, p.err);
+            } else {
+              load_columns(sa, &p.a2, bar, m_a, k, 0, true, p.err);
+              load_columns(sb, &p.b2, bar, n_b, k, 0, true, p.err);
+            }
+          }
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // After an abort, stages may still be filling: let those copies land.
+      if (*abort_flag && rank == 0)
+        for (int s2 = 0; s2 < STAGES; ++s2)
+          if (issued & (1u << s2))
+            for (int j = 0; j < KSUB; ++j) drain_wait(full(s2, j), (issued_parity >> s2) & 1u, drain_ns);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer (CTA 0 of the pair)
+    if (rank == 0 && lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        const int t = tile_of<MODE>(p, i);
+        if (t < 0) break;
+        const Tile<MODE> cur(p, t);
+        ok = wait_bounded(acce(acc), acc_phase ^ 1u, w);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
+        const bool a_mn = MODE == GRADS && cur.dw;
+        constexpr bool b_mn = MODE == GRADS;
+        const uint32_t idesc = make_idesc(CM, MODE == GRADS ? BN : p.bn, a_mn, b_mn);
+        for (int kb = 0; kb < cur.num_kb; kb += KSUB) {
+          const int valid = cur.num_kb - kb < KSUB ? cur.num_kb - kb : KSUB;
+#pragma unroll
+          for (int j = 0; j < KSUB; ++j) {
+            if (j >= valid) break;
+            if (!wait_polled(full(stage, j), phase, w)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = sbase + stage * STAGE_BYTES + j * KB_BYTES, sb = sa + A_STAGE;
+            // K-major: advance 16 K-elements (32 bytes) inside the swizzle row.
+            // MN-major: advance 16 K-rows (two 8-row groups of 1024 bytes);
+            // 8192 bytes between 64-wide atoms, 1024 between 8-row groups.
+#pragma unroll
+            for (int kk = 0; kk < BK / UMMA_K; ++kk) {
+              const uint64_t ad = a_mn ? smem_desc(sa + kk * (UMMA_K * 128), 64 * BK * 2, 1024)
+                                       : smem_desc(sa + kk * (UMMA_K * 2), 16, 1024);
+              const uint64_t bd = b_mn ? smem_desc(sb + kk * (UMMA_K * 128), 64 * BK * 2, 1024)
+                                       : smem_desc(sb + kk * (UMMA_K * 2), 16, 1024);
+              tc_mma(d, ad, bd, idesc, ((kb + j) | kk) != 0 ? 1u : 0u);
+            }
+          }
+          if (!ok) break;
+          tc_commit_mc(empty(stage), 0x3);  // both CTAs may refill this stage
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok) tc_commit_mc(accf(acc), 0x3);  // both CTAs' accumulators are ready
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      tc_commit_mc(drain_bar, 0x1);  // flips once all MMAs issued by this thread have completed
+      volatile int no_abort = 0;
+      wait_bounded(drain_bar, 0, Watch{&no_abort, p.err, p.timeout_ns});
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- epilogue (both CTAs)
+    const int ew = warp - 2;
+    const int q = warp & 3, half = ew >> 2;  // TMEM lanes 32q.., and which half of the columns
+    uint8_t *box = epi_smem + ew * BOX_BYTES;
+    Writer out{box, smem_u32(box)};
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int i = 0;; ++i) {
+      const int t = tile_of<MODE>(p, i);
+      if (t < 0) break;
+      const Tile<MODE> cur(p, t);
+      const int row0 = cur.tm * CM + (int)rank * BM + q * 32, row = row0 + lane;
+      HeadRow hr{0.f, 0.f, 0.f, -1};
+      long long target = -1;
+      if (MODE == DLOGITS && row < p.rows) hr = p.row[row];
+      if (MODE == STATS && row < p.rows) target = __ldg(p.targets + row);
+      if (!__all_sync(0xffffffffu, wait_bounded(accf(acc), acc_phase, w))) break;   // warp-uniform
+      tc_fence_after();
+      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
+      if (MODE == STATS) {
+        if (row0 < p.rows) {
+          const int each = p.bn / 2;
+          float m = -INFINITY, s = 0.f;
+#pragma unroll 1
+          for (int cc = half * each; cc < half * each + each; cc += 32) {
+            const long long n0 = (long long)cur.tn * p.bn + cc;
+            if (n0 >= p.vocab) break;
+            uint32_t v[32];
+            tmem_ld32(taddr + (uint32_t)cc, v);
+            float z[32];
+            const int left = (int)min(p.vocab - n0, 32ll);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) z[c] = c < left ? __uint_as_float(v[c]) : -INFINITY;
+            const long long hit = target - n0;
+            if (__any_sync(0xffffffffu, hit >= 0 && hit < left)) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (hit == c && c < left) p.target_logit[row] = z[c];
+            }
+            float most = z[0];
+#pragma unroll
+            for (int c = 1; c < 32; ++c) most = fmaxf(most, z[c]);
+            if (most > m) {
+              s *= ex2((m - most) * kLog2e);   // m = -inf: s is 0, and so is the factor
+              m = most;
+            }
+            // a NaN, +inf or a whole chunk of -inf makes the differences NaN, and the row's sum with them
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              s0 += ex2((z[c] - m) * kLog2e);
+              s1 += ex2((z[c + 1] - m) * kLog2e);
+            }
+            s += s0 + s1;
+          }
+          if (row < p.rows) p.parts[((long long)cur.tn * 2 + half) * p.rows + row] = make_float2(m, s);
+        }
+      } else if (MODE == DLOGITS) {
+        if (row0 < p.rows) {
+#pragma unroll 1
+          for (int cc = half * (p.bn / 2); cc < (half + 1) * (p.bn / 2); cc += 64) {
+            const int col0 = cur.tn * p.bn + cc;     // in the piece
+            uint32_t lo[32], hi[32], wo[32];
+            tmem_ld64(taddr + (uint32_t)cc, lo, hi);
+            const int left = (int)max(0ll, min(p.vocab - p.v0 - col0, 64ll));
+            float d[64];
+#pragma unroll
+            for (int c = 0; c < 64; ++c) {
+              const float z = __uint_as_float(c < 32 ? lo[c & 31] : hi[c & 31]);
+              d[c] = hr.g * ex2((z - hr.lse) * kLog2e);
+            }
+            const int hit = hr.target < 0 ? -1 : (int)(hr.target - p.v0) - col0;
+            if (__any_sync(0xffffffffu, hit >= 0 && hit < 64)) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                if (hit == c) d[c] -= hr.hit;
+            }
+            // a row that takes no part, whatever its z are, and columns past the vocabulary
+            const int keep = hr.target < 0 ? 0 : left;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              wo[c] = pack_bf16(2 * c < keep ? d[2 * c] : 0.f, 2 * c + 1 < keep ? d[2 * c + 1] : 0.f);
+            out.put(wo, &p.out, lane, col0, row0, 0, p.err);
+          }
+        }
+      } else {
+        const long long rows_m = cur.dw ? p.vocab - p.v0 : p.rows;
+        // a part without k-blocks (of a last piece that is short) has nothing to add
+        if (row0 < rows_m && cur.num_kb > 0) {
+          const bool sums = !cur.dw && p.out_kind != 0;
+          const CUtensorMap *map = cur.dw ? &p.out2 : &p.out;
+          const int row_at = row0 + (cur.dw ? (int)p.v0 : 0);
+#pragma unroll 1
+          for (int cc = half * 128; cc < half * 128 + 128; cc += 64) {
+            const int col0 = cur.tn * BN + cc;
+            if (col0 >= p.hidden) break;
+            uint32_t lo[32], hi[32];
+            tmem_ld64(taddr + (uint32_t)cc, lo, hi);
+            if (sums) {
+              put_sums(out, lo, map, p.out_kind == 2, lane, col0, row_at, cur.part, p.err);
+              if (col0 + 32 < p.hidden)
+                put_sums(out, hi, map, p.out_kind == 2, lane, col0 + 32, row_at, cur.part, p.err);
+            } else {
+              uint32_t wo[32];
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                wo[c] = pack_bf16(__uint_as_float(lo[2 * c]), __uint_as_float(lo[2 * c + 1]));
+                wo[16 + c] = pack_bf16(__uint_as_float(hi[2 * c]), __uint_as_float(hi[2 * c + 1]));
+              }
+              out.put(wo, map, lane, col0, row_at, 0, p.err);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_to_rank(acce(acc), 0));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no CTA frees TMEM or exits while its peer may still use them
+  if (*abort_flag) {
+    // after an abort: a copy that only CTA 1 issued is not covered by the
+    // drain above; it lands within microseconds
+    const unsigned long long t0 = global_ns();
+    while (global_ns() - t0 < 200000ull) __nanosleep(1000);
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+  }
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// 3-D map over [parts][rows][cols] of fp32, boxes of 32 x 32
+int make_map_sums(CUtensorMap *map, const void *base, int64_t parts, int64_t rows, int64_t cols) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return MUON_ERR_CUDA;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * 4, (cuuint64_t)rows * cols * 4};
+  cuuint32_t box[3] = {32u, 32u, 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MUON_OK : MUON_ERR_CUDA;
+}
+
+template <int MODE>
+int launch(Args &p, int64_t tiles, int trace_kind, cudaStream_t s) {
+  static std::once_flag attr_once[64];
+  static int max_pairs[64];
+  static cudaError_t attr_err[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MUON_ERR_CUDA;
+  auto *kernel = head_gemm_kernel<MODE>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;   // the occupancy query knows clusters only
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  std::call_once(attr_once[dev], [&] {
+    attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    int n = 0;
+    cfg.gridDim = dim3(2 * (unsigned)std::max(1, num_sms() / 2), 1, 1);
+    if (attr_err[dev] == cudaSuccess && cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0)
+      max_pairs[dev] = n;
+    else
+      max_pairs[dev] = std::max(1, num_sms() / 2);
+    cudaGetLastError();
+  });
+  if (attr_err[dev] != cudaSuccess) return MUON_ERR_CUDA;
+  p.err = device_error_word();
+  p.timeout_ns = wait_timeout_ns();
+  if (!p.err) return MUON_ERR_CUDA;
+  const int64_t pairs = std::min<int64_t>(tiles, max_pairs[dev]);
+  cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
+  cfg.numAttrs = 2;
+  cfg.stream = s;
+  if (MODE == GRADS && p.schedule.longs % pairs) {
+    // dW tiles that take as long as one of dx; an epilogue costs about as much as 4 k-blocks
+    const int64_t rest = pairs - p.schedule.longs % pairs, each = p.kblocks / p.splits / (p.kblocks2 + 4);
+    p.schedule.extra = (int)std::min<int64_t>(each, p.schedule.shorts / rest);
+  }
+  trace_before(trace_kind, s);
+  const cudaError_t le = cudaLaunchKernelEx(&cfg, kernel, p);
+  const int st = trace_after(trace_kind, s);
+  return le == cudaSuccess ? st : MUON_ERR_CUDA;
+}
+
+#define HEAD_TRY(expr)              \
+  do {                              \
+    const int _st = (expr);         \
+    if (_st != MUON_OK) return _st; \
+  } while (0)
+
+int pairs_of_sms() { return std::max(1, num_sms() / 2); }
+
+// columns of a tile of z: the most that leave a tile for each pair of CTAs
+int columns(const HeadShape &h, int64_t vocab, int least) {
+  int bn = BN;
+  while (bn > least && cdiv(h.rows, CM) * cdiv(vocab, bn) < pairs_of_sms()) bn /= 2;
+  return bn;
+}
+
+int group_of(const HeadShape &h) { return (int)std::clamp<int64_t>(kGroupBytes / (CM * h.hidden * 2), 4, 1 << 20); }
+
+}  // namespace
+
+int head_stats_columns(const HeadShape &h) { return columns(h, h.vocab, 64); }
+int64_t head_parts(const HeadShape &h) { return 2 * cdiv(h.vocab, head_stats_columns(h)); }
+
+int head_stats(const HeadShape &h, const void *x, int64_t ldx, const void *w, const int64_t *targets, float2 *parts,
+               float *target_logit, cudaStream_t s) {
+  Args p{};
+  p.bn = head_stats_columns(h);
+  HEAD_TRY(make_map(&p.a, x, 1, h.rows, h.hidden, BM, ldx));
+  HEAD_TRY(make_map(&p.b, w, 1, h.vocab, h.hidden, p.bn / 2));
+  p.rows = h.rows;
+  p.vocab = h.vocab;
+  p.hidden = (int)h.hidden;
+  p.kblocks = (int)cdiv(h.hidden, BK);
+  p.tiles_m = (int)cdiv(h.rows, CM);
+  p.tiles_n = (int)cdiv(h.vocab, p.bn);
+  p.group = std::min(group_of(h), p.tiles_m);
+  p.targets = targets;
+  p.parts = parts;
+  p.target_logit = target_logit;
+  return launch<STATS>(p, (int64_t)p.tiles_m * p.tiles_n, kTraceHeadStats, s);
+}
+
+// A piece is at most as wide as makes d 128 MB (or 8192 columns, which keep the additions to dx's sums cheap),
+// and of those widths from three quarters of that on the one that leaves the least of the last wave empty.
+HeadPlan head_plan(const HeadShape &h, bool need_dx, bool need_dw) {
+  const int64_t all = cdiv(h.vocab, CM), tm = cdiv(h.rows, CM), pairs = pairs_of_sms();
+  const int64_t most = std::min(all, std::max<int64_t>(32, (int64_t(128) << 20) / (h.rows * CM * 2)));
+  HeadPlan plan{most, 1, 1};
+  if (most < all) {
+    double best = 0;
+    for (int64_t n = most; n >= std::max<int64_t>(1, most * 3 / 4); --n) {
+      const double used = (double)(tm * n) / (double)(cdiv(tm * n, pairs) * pairs);
+      if (used > best + 1e-9) best = used, plan.piece_tiles = n;
+    }
+    plan.pieces = cdiv(all, plan.piece_tiles);
+  }
+  if (need_dx) {
+    // a dx tile no longer than a pair's share of the whole
+    const int64_t th = cdiv(h.hidden, BN), kb = plan.piece_tiles * (CM / BK);
+    const int64_t work = tm * th * kb + (need_dw ? plan.piece_tiles * th * (cdiv(h.rows, BK) + 4) : 0);
+    plan.splits = (int)std::clamp<int64_t>(kb * pairs / std::max<int64_t>(work, 1), 1, std::min<int64_t>(16, std::max<int64_t>(1, kb / 8)));
+  }
+  return plan;
+}
+
+int head_dlogits(const HeadShape &h, const HeadPlan &plan, int64_t v0, const void *x, int64_t ldx, const void *w,
+                 const HeadRow *row, void *d, cudaStream_t s) {
+  Args p{};
+  p.bn = columns(h, plan.width(), 128);
+  HEAD_TRY(make_map(&p.a, x, 1, h.rows, h.hidden, BM, ldx));
+  HEAD_TRY(make_map(&p.b, w, 1, h.vocab, h.hidden, p.bn / 2));
+  HEAD_TRY(make_map(&p.out, d, 1, h.rows, plan.width(), 32));
+  p.rows = h.rows;
+  p.vocab = h.vocab;
+  p.hidden = (int)h.hidden;
+  p.v0 = v0;
+  p.kblocks = (int)cdiv(h.hidden, BK);
+  p.tiles_m = (int)cdiv(h.rows, CM);
+  // the last piece ends with the vocabulary's last 256 columns
+  p.tiles_n = (int)(std::min(plan.piece_tiles, cdiv(h.vocab - v0, CM)) * (CM / p.bn));
+  p.group = std::min(group_of(h), p.tiles_m);
+  p.row = row;
+  return launch<DLOGITS>(p, (int64_t)p.tiles_m * p.tiles_n, kTraceHeadDlogits, s);
+}
+
+int head_grads(const HeadShape &h, const HeadPlan &plan, int64_t v0, bool first, const void *d, const void *w,
+               const void *xc, int64_t xc_cols, void *dx, int64_t lddx, float *acc, void *dweight, cudaStream_t s) {
+  Args p{};
+  const int64_t tiles_v = std::min(plan.piece_tiles, cdiv(h.vocab - v0, CM));
+  p.wide = h.hidden % 64 == 0;
+  p.rows = h.rows;
+  p.vocab = h.vocab;
+  p.hidden = (int)h.hidden;
+  p.v0 = v0;
+  p.tiles_m = (int)cdiv(h.rows, CM);
+  p.tiles_n = (int)cdiv(h.hidden, BN);
+  p.tiles_v = (int)tiles_v;
+  p.kblocks = (int)(tiles_v * (CM / BK));
+  p.kblocks2 = (int)cdiv(h.rows, BK);
+  p.splits = plan.splits;
+  if (dx) {
+    HEAD_TRY(make_map(&p.a, d, 1, h.rows, plan.width(), BM));
+    HEAD_TRY(p.wide ? make_map_blocks(&p.b, w, 1, h.vocab, h.hidden, BK, 2) : make_map(&p.b, w, 1, h.vocab, h.hidden, BK));
+    p.out_kind = plan.pieces == 1 && plan.splits == 1 ? 0 : first ? 1 : 2;
+    HEAD_TRY(p.out_kind == 0 ? make_map(&p.out, dx, 1, h.rows, h.hidden, 32, lddx)
+                             : make_map_sums(&p.out, acc, plan.splits, h.rows, h.hidden));
+    p.schedule.longs = p.tiles_m * p.tiles_n * p.splits;
+  }
+  if (dweight) {
+    HEAD_TRY(make_map_blocks(&p.a2, d, 1, h.rows, plan.width(), BK, 2));
+    HEAD_TRY(make_map_blocks(&p.b2, xc, 1, h.rows, xc_cols, BK, 2));
+    HEAD_TRY(make_map(&p.out2, dweight, 1, h.vocab, h.hidden, 32));
+    p.schedule.shorts = p.tiles_v * p.tiles_n;
+  }
+  return launch<GRADS>(p, (int64_t)p.schedule.longs + p.schedule.shorts, kTraceHeadGrads, s);
+}
+
+}  // namespace muon

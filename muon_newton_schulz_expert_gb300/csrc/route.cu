@@ -1,0 +1,432 @@
+// A router's choice of experts from its logits x [T][E], and the gradient of the
+// weights in the logits.
+//
+//   s = softmax(x) or sigmoid(x); the k experts with the largest s + bias (of x
+//   without a bias: both scores grow with x), ties to the lowest index; their
+//   weights w_i = scale s_i, or scale s_i / sum of the chosen s
+//
+// A warp takes a row and keeps it in registers (lane l: experts l, l + 32, ..), so the
+// logits are read once.  A choice is the warp's largest key (redux.sync on a 32-bit
+// order-preserving key) and, among equal ones, its lowest index; only the winning lane
+// looks at its values again.  The kernel is bound by those k rounds, not by the
+// bytes; shorter rows hold fewer values a lane (kPerLane).
+//
+// With a bias the keys are sums of two numbers, and fp32 may not tell two of them apart
+// that 64 bits do.  Where two neighbours in the order are closer than the keys' error
+// bound, and not equal logits with equal biases, the choice is made again from keys in
+// 64 bits: of the candidates only (sigmoid: a key needs its own logit), or of the whole
+// row (softmax, whose sum needs every logit; or more than 32 candidates).
+#include <math.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "common.cuh"
+
+namespace muon {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kMaxTop = 32;
+constexpr int64_t kMaxExperts = 1024, kMaxRows = int64_t(1) << 27;
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_f(float *d, float v) { *d = v; }
+__device__ __forceinline__ void from_f(__nv_bfloat16 *d, float v) { *d = __float2bfloat16_rn(v); }
+
+// Keys in the values' order: 0 for -inf (never chosen), the largest for NaN; -0 is 0.
+__device__ __forceinline__ uint32_t order_of(float v) {
+  if (v == -INFINITY) return 0u;
+  if (v != v) return 0xffffffffu;
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+__device__ __forceinline__ unsigned long long order_of(double v) {
+  if (v == -INFINITY) return 0ull;
+  if (v != v) return ~0ull;
+  const unsigned long long b = (unsigned long long)__double_as_longlong(v + 0.0);
+  return b >> 63 ? ~b : b | (1ull << 63);
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+template <typename F>
+__device__ __forceinline__ F warp_sum(F v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+
+struct Args {
+  const void *logits;
+  int64_t stride;
+  const float *bias;
+  int64_t rows;
+  int experts, top;
+  bool softmax, normalize;
+  float scale;
+  int64_t *ids;
+  float *weights;
+};
+
+// The choice in 64 bits over a whole row: lane j leaves with the j-th expert's id.
+template <typename T, int R>
+__device__ __noinline__ int choose_in_64(const T *x, const float *bias, int experts, int top, bool softmax) {
+  const int lane = threadIdx.x & 31;
+  double most = -INFINITY, sum = 1.0;
+  if (softmax) {
+    for (int e = lane; e < experts; e += 32) most = fmax(most, (double)to_f(x[e]));
+    for (int o = 16; o; o >>= 1) most = fmax(most, __shfl_xor_sync(kAll, most, o));
+    sum = 0.0;
+    for (int e = lane; e < experts; e += 32) sum += exp((double)to_f(x[e]) - most);
+    sum = warp_sum(sum);
+  }
+  auto key_of = [&](int e) {
+    const double v = to_f(x[e]);
+    return order_of(v == -INFINITY ? v : (softmax ? exp(v - most) / sum : 1.0 / (1.0 + exp(-v))) + (double)bias[e]);
+  };
+  unsigned long long key[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) key[i] = i * 32 + lane < experts ? key_of(i * 32 + lane) : 0ull;
+  int mine = -1;
+  for (int j = 0; j < top; ++j) {
+    unsigned long long best = 0ull;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (key[i] > best) best = key[i], at = i;
+    int e = at * 32 + lane;
+    for (int o = 16; o; o >>= 1) {
+      const unsigned long long k = __shfl_xor_sync(kAll, best, o);
+      const int f = __shfl_xor_sync(kAll, e, o);
+      if (k > best || (k == best && f < e)) best = k, e = f;
+    }
+    if (best == 0ull) break;
+    if (lane == j) mine = e;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (i * 32 + lane == e) key[i] = 0ull;
+  }
+  return mine;
+}
+
+template <typename T, int R, bool BIAS>
+__global__ void __launch_bounds__(kThreads) route_kernel(const Args p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = blockIdx.x * (int64_t)kWarps + (threadIdx.x >> 5);
+  if (row >= p.rows) return;   // a warp together
+  const T *x = static_cast<const T *>(p.logits) + row * p.stride;
+  uint32_t key[R];
+  float m = -INFINITY, sum = 1.f;
+  {
+    float v[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) v[i] = i * 32 + lane < p.experts ? to_f(x[i * 32 + lane]) : -INFINITY;
+    // the softmax's sum, where keys or weights need it
+    if (p.softmax && (BIAS || !p.normalize)) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) m = fmaxf(m, v[i]);
+      m = warp_max(m);
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < R; ++i) sum += v[i] == -INFINITY ? 0.f : expf(v[i] - m);
+      sum = warp_sum(sum);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (BIAS && v[i] != -INFINITY)
+        v[i] = (p.softmax ? expf(v[i] - m) / sum : sigmoid(v[i])) + __ldg(p.bias + i * 32 + lane);
+      key[i] = order_of(v[i]);
+    }
+  }
+  uint32_t best = 0u;
+  int at = 0;
+  auto look = [&] {
+    best = 0u;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (key[i] > best) best = key[i], at = i;
+  };
+  look();
+  int mine = -1;            // lane j: the j-th candidate
+  int count = 0;            // candidates
+  bool unsure = false;
+  float last = 0.f;         // the key before, and the one at the border
+  int last_e = -1;
+  for (;;) {
+    const uint32_t k = __reduce_max_sync(kAll, best);
+    if (k == 0u) break;
+    const int e = (int)__reduce_min_sync(kAll, best == k ? (unsigned)(at * 32 + lane) : ~0u);
+    if (BIAS) {
+      const float v = value_of(k);
+      if (count > 0) {
+        // Either key is within 2^-18 of its score and 2^-23 of itself: an exponential and a division
+        // within 2^-21, a softmax's sum of up to 1024 terms within 36 roundings.  A score is at most |key| + |bias|.
+        const float eps = (fabsf(last) + fabsf(v) + fabsf(__ldg(p.bias + last_e)) + fabsf(__ldg(p.bias + e))) * 0x1p-18f;
+        const bool close = last - v <= eps;
+        if (count >= p.top && !close) break;          // the rest is surely below
+        if (close && (to_f(x[last_e]) != to_f(x[e]) || __ldg(p.bias + last_e) != __ldg(p.bias + e))) unsure = true;
+      }
+      last = v, last_e = e;
+    }
+    if (count == kMaxTop) {                           // more candidates than lanes
+      count = kMaxTop + 1;
+      break;
+    }
+    if (lane == count) mine = e;
+    ++count;
+    if (!BIAS && count == p.top) break;
+    if (lane == (e & 31)) {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (i == at) key[i] = 0u;
+      look();
+    }
+  }
+  if (BIAS && unsure) {
+    if (p.softmax || count > kMaxTop) {
+      mine = choose_in_64<T, R>(x, p.bias, p.experts, p.top, p.softmax);
+    } else {
+      // the candidates' places among themselves
+      const double v = mine >= 0 ? 1.0 / (1.0 + exp(-(double)to_f(x[mine]))) + (double)__ldg(p.bias + mine) : 0.0;
+      const unsigned long long k = mine >= 0 ? order_of(v) : 0ull;
+      int before = 0;
+      for (int j = 0; j < count; ++j) {
+        const unsigned long long o = __shfl_sync(kAll, k, j);
+        const int e = __shfl_sync(kAll, mine, j);
+        before += o > k || (o == k && e < mine);
+      }
+      int next = -1;
+      for (int j = 0; j < count; ++j) {
+        const int to = __shfl_sync(kAll, before, j), e = __shfl_sync(kAll, mine, j);
+        if (to == lane) next = e;
+      }
+      mine = next;
+    }
+  }
+  if (lane >= p.top) mine = -1;
+  float s = 0.f;
+  const float c = mine >= 0 ? to_f(x[mine]) : -INFINITY;
+  if (p.softmax) {
+    if (p.normalize) {
+      m = warp_max(c);
+      // a NaN or +inf that was not chosen is in the choice's sum all the same
+      s = mine < 0 ? 0.f : BIAS && sum != sum ? sum : expf(c - m);
+    } else {
+      s = mine >= 0 ? expf(c - m) / sum : 0.f;
+    }
+  } else if (mine >= 0) {
+    s = sigmoid(c);
+  }
+  if (p.normalize) {
+    const float total = warp_sum(s);
+    s = total == 0.f ? 0.f : s / total;   // sigmoids that are all 0 in fp32
+  }
+  if (lane < p.top) {
+    p.ids[row * p.top + lane] = mine;
+    p.weights[row * p.top + lane] = p.scale * s;
+  }
+}
+
+// ---------------------------------------------------------------------------- gradient
+//   with g_i = scale dw_i, and for a normalised call share_i = s_i / sum of the chosen s:
+//   softmax, normalised:  dx_i = share_i h_i;         h_i = sum_j share_j (g_i - g_j)
+//   sigmoid, normalised:  dx_i = share_i (1 - s_i) h_i
+//   sigmoid:              dx_i = g_i s_i (1 - s_i)
+//   softmax:              dx_e = p_e (sum of g at e - G), G = sum_j g_j p_j; for a chosen expert as
+//                         p_e (g_e rest + sum over the chosen c of p_c (g_e - g_c)), rest = the p of the others
+// Differences of the g and sums of what is left out, so that nothing cancels where one score is nearly all.  A slot's
+// value is added at its expert; an id that comes twice counts twice.
+struct BwdArgs {
+  const float *dweights;
+  const void *logits;
+  int64_t stride;
+  const int64_t *ids;
+  int64_t rows;
+  int experts, top;
+  bool softmax, normalize;
+  float scale;
+  void *dlogits;
+  int64_t out_stride;
+  unsigned *err;
+};
+
+template <typename T, int R>
+__global__ void __launch_bounds__(kThreads) route_backward_kernel(const BwdArgs p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = blockIdx.x * (int64_t)kWarps + (threadIdx.x >> 5);
+  if (row >= p.rows) return;   // a warp together
+  const T *x = static_cast<const T *>(p.logits) + row * p.stride;
+  int id = -1;
+  float g = 0.f, c = -INFINITY;
+  if (lane < p.top) {
+    const int64_t v = p.ids[row * p.top + lane];
+    if (v >= p.experts) atomicOr(p.err, kErrDevice);
+    else if (v >= 0) id = (int)v;
+    if (id >= 0) g = p.scale * p.dweights[row * p.top + lane], c = to_f(x[id]);
+  }
+  float out[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) out[i] = 0.f;
+  float value = 0.f;                       // what this lane's slot adds at its expert
+  const bool whole = p.softmax && !p.normalize;
+  if (!p.softmax && !p.normalize) {
+    if (id >= 0) value = g * sigmoid(c) * (1.f / (1.f + expf(c)));
+  } else if (!whole) {
+    const float m = p.softmax ? warp_max(c) : 0.f;
+    const float s = id < 0 || c == -INFINITY ? 0.f : p.softmax ? expf(c - m) : sigmoid(c);
+    const float total = warp_sum(s), share = total == 0.f ? 0.f : s / total;
+    float h = 0.f;
+    for (int j = 0; j < p.top; ++j) h = fmaf(__shfl_sync(kAll, share, j), g - __shfl_sync(kAll, g, j), h);
+    if (id >= 0) value = share * h * (p.softmax ? 1.f : 1.f / (1.f + expf(c)));
+  } else {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      out[i] = i * 32 + lane < p.experts ? to_f(x[i * 32 + lane]) : -INFINITY;
+      m = fmaxf(m, out[i]);
+    }
+    m = warp_max(m);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      out[i] = out[i] == -INFINITY ? 0.f : expf(out[i] - m);
+      sum += out[i];
+    }
+    sum = warp_sum(sum);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;   // a row with nothing but -inf
+    // slots of one expert count as one, with their g added: the first of them stands for it
+    bool first = id >= 0;
+    float d = 0.f;
+    for (int j = 0; j < p.top; ++j) {
+      const int e = __shfl_sync(kAll, id, j);
+      const float gj = __shfl_sync(kAll, g, j);
+      if (e == id && id >= 0) {
+        d += gj;
+        if (j < lane) first = false;
+      }
+    }
+    const float pr = id < 0 || c == -INFINITY ? 0.f : expf(c - m) * inv;
+    const float pf = first ? pr : 0.f;
+    float all = pr * g;                    // G, a slot's share
+    all = warp_sum(all);
+    // the p of the experts that were not chosen
+    for (int j = 0; j < p.top; ++j) {
+      const int e = __shfl_sync(kAll, id, j);
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (i * 32 + lane == e) out[i] = 0.f;
+    }
+    float rest = 0.f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      out[i] *= inv;
+      rest += out[i];
+      out[i] *= -all;
+    }
+    rest = warp_sum(rest);
+    float h = d * rest;
+    for (int j = 0; j < p.top; ++j) h = fmaf(__shfl_sync(kAll, pf, j), d - __shfl_sync(kAll, d, j), h);
+    if (first) value = pr * h;
+  }
+  for (int j = 0; j < p.top; ++j) {
+    const int e = __shfl_sync(kAll, id, j);
+    const float v = __shfl_sync(kAll, value, j);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (i * 32 + lane == e) out[i] += v;
+  }
+  T *o = static_cast<T *>(p.dlogits) + row * p.out_stride;
+  __syncwarp();   // dlogits may be the logits: every lane has read its own
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (i * 32 + lane < p.experts) from_f(o + i * 32 + lane, out[i]);
+}
+
+// calls f with the values a lane holds: the least of kPerLane that cover the row
+template <typename F>
+void per_lane(int experts, F &&f) {
+  const int n = (experts + 31) / 32;
+  if (n <= 1) f(std::integral_constant<int, 1>());
+  else if (n <= 2) f(std::integral_constant<int, 2>());
+  else if (n <= 4) f(std::integral_constant<int, 4>());
+  else if (n <= 8) f(std::integral_constant<int, 8>());
+  else if (n <= 12) f(std::integral_constant<int, 12>());
+  else if (n <= 16) f(std::integral_constant<int, 16>());
+  else f(std::integral_constant<int, 32>());
+}
+
+bool bad_type(int t) { return t != MUON_BF16 && t != MUON_F32; }
+bool bad_score(int s) { return s != MUON_SCORE_SOFTMAX && s != MUON_SCORE_SIGMOID; }
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+int muon_route(const void *logits, int64_t stride, const float *bias, int64_t rows, int64_t experts, int type,
+               int top, int score, int normalize, float scale, int64_t *ids, float *weights, muon_stream_t stream) {
+  if (rows < 0 || experts < 1 || bad_type(type) || bad_score(score) || top < 1 || top > experts || stride < experts ||
+      !isfinite(scale))
+    return MUON_ERR_INVALID_ARG;
+  if (top > kMaxTop || experts > kMaxExperts || rows > kMaxRows) return MUON_ERR_UNSUPPORTED;
+  if (rows == 0) return MUON_OK;
+  if (!logits || !ids || !weights) return MUON_ERR_INVALID_ARG;
+  if (!on_elements({logits}, type == MUON_BF16 ? 2 : 4) || !on_elements({bias, weights}, 4) || !on_elements({ids}, 8))
+    return MUON_ERR_UNSUPPORTED;
+  const Args a{logits, stride, bias, rows, (int)experts, top, score == MUON_SCORE_SOFTMAX, normalize != 0, scale, ids,
+               weights};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned blocks = (unsigned)((rows + kWarps - 1) / kWarps);
+  trace_before(kTraceRoute, s);
+  per_lane((int)experts, [&](auto r) {
+    constexpr int R = decltype(r)::value;
+    if (type == MUON_BF16) {
+      if (bias) route_kernel<__nv_bfloat16, R, true><<<blocks, kThreads, 0, s>>>(a);
+      else route_kernel<__nv_bfloat16, R, false><<<blocks, kThreads, 0, s>>>(a);
+    } else {
+      if (bias) route_kernel<float, R, true><<<blocks, kThreads, 0, s>>>(a);
+      else route_kernel<float, R, false><<<blocks, kThreads, 0, s>>>(a);
+    }
+  });
+  return trace_after(kTraceRoute, s);
+}
+
+int muon_route_backward(const float *dweights, const void *logits, int64_t stride, const int64_t *ids, int64_t rows,
+                        int64_t experts, int type, int top, int score, int normalize, float scale, void *dlogits,
+                        int64_t dlogits_stride, muon_stream_t stream) {
+  if (rows < 0 || experts < 1 || bad_type(type) || bad_score(score) || top < 1 || top > experts || stride < experts ||
+      dlogits_stride < experts || !isfinite(scale))
+    return MUON_ERR_INVALID_ARG;
+  if (top > kMaxTop || experts > kMaxExperts || rows > kMaxRows) return MUON_ERR_UNSUPPORTED;
+  if (rows == 0) return MUON_OK;
+  if (!dweights || !logits || !ids || !dlogits) return MUON_ERR_INVALID_ARG;
+  if (!on_elements({logits, dlogits}, type == MUON_BF16 ? 2 : 4) || !on_elements({dweights}, 4) ||
+      !on_elements({ids}, 8))
+    return MUON_ERR_UNSUPPORTED;
+  const BwdArgs a{dweights, logits, stride, ids, rows, (int)experts, top, score == MUON_SCORE_SOFTMAX, normalize != 0,
+                  scale, dlogits, dlogits_stride, device_error_word()};
+  if (!a.err) return MUON_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned blocks = (unsigned)((rows + kWarps - 1) / kWarps);
+  trace_before(kTraceRouteBwd, s);
+  per_lane((int)experts, [&](auto r) {
+    constexpr int R = decltype(r)::value;
+    if (type == MUON_BF16) route_backward_kernel<__nv_bfloat16, R><<<blocks, kThreads, 0, s>>>(a);
+    else route_backward_kernel<float, R><<<blocks, kThreads, 0, s>>>(a);
+  });
+  return trace_after(kTraceRouteBwd, s);
+}
+
+}  // extern "C"
