@@ -49,26 +49,36 @@ template <> struct Raw<4> { typedef uint32_t type; };
 template <> struct Raw<2> { typedef uint16_t type; };
 
 template <typename T, int N>
-__device__ __forceinline__ void load(float (&f)[N], const T *p) {
-  typedef typename Raw<sizeof(T) * N>::type R;
+using Access = typename Raw<sizeof(T) * N>::type;
+
+template <typename T, int N>
+__device__ __forceinline__ Access<T, N> load(const T *p) {
+  return *reinterpret_cast<const Access<T, N> *>(p);
+}
+// rows that nothing reads again
+template <typename T, int N>
+__device__ __forceinline__ Access<T, N> load_once(const T *p) {
+  return __ldcs(reinterpret_cast<const Access<T, N> *>(p));
+}
+template <typename T, int N>
+__device__ __forceinline__ void unpack(float (&f)[N], const Access<T, N> &r) {
   union {
-    R r;
+    Access<T, N> r;
     Vec<T, N> v;
   } u;
-  u.r = *reinterpret_cast<const R *>(p);
+  u.r = r;
 #pragma unroll
   for (int i = 0; i < N; ++i) f[i] = to_f(u.v.v[i]);
 }
 template <typename T, int N>
 __device__ __forceinline__ void store(T *p, const float (&f)[N]) {
-  typedef typename Raw<sizeof(T) * N>::type R;
   union {
-    R r;
+    Access<T, N> r;
     Vec<T, N> v;
   } u;
 #pragma unroll
   for (int i = 0; i < N; ++i) from_f(&u.v.v[i], f[i]);
-  *reinterpret_cast<R *>(p) = u.r;
+  *reinterpret_cast<Access<T, N> *>(p) = u.r;
 }
 
 // the expert of a slot as the sort takes it: slots that are not routed come last
@@ -185,7 +195,7 @@ struct RowArgs {
   float *dweights;
   int64_t tokens;
   int top, hidden, vecs;   // vecs: accesses of a row
-  int tx;                  // threads of a token, a power of two
+  int tx, turns;           // threads of a token, a power of two; tokens one after the other in a block
   const int64_t *ids;      // few slots: what place is made of
   int experts;
   int64_t *offsets, *place_out;
@@ -203,7 +213,7 @@ __device__ __forceinline__ int64_t row_of(int64_t place, int64_t slots, bool *ze
   return r;
 }
 
-// Copies of a token's row: one access of it a thread, written k times.
+// Copies of one access of a token's row, written k times.
 template <int BYTES>
 __device__ __forceinline__ void copy_out(const RowArgs &p, int64_t token, int c, const int64_t *place) {
   typedef typename Raw<BYTES>::type R;
@@ -217,12 +227,61 @@ __device__ __forceinline__ void copy_out(const RowArgs &p, int64_t token, int c,
   }
 }
 
+// A block's tokens are blockIdx.x * turns * (kThreads / tx) and on, kThreads / tx of them at a time. Their places and
+// weights come first, all at once: with each token reading its own, a block spent as long on waiting for the
+// places as on the rows (combine, 16384 tokens x 8 of 6144 bf16: 346 us).
+// A routed slot's row is >= 0, that of one which is not -1 - row, kNoRow one out of range.
+constexpr int kBatchSlots = 1024, kPartSlots = 128, kNoRow = INT_MIN;
+struct Batch {
+  int row[kBatchSlots];
+  float w[kBatchSlots];
+
+  // tokens of this block
+  __device__ __forceinline__ int load(const RowArgs &p, int64_t first) {
+    const int n = (int)min((int64_t)p.turns * (kThreads / p.tx), p.tokens - first);
+    const int64_t slots = p.tokens * p.top, s0 = first * p.top;
+    for (int i = threadIdx.x; i < n * p.top; i += kThreads) {
+      const int64_t at = p.place[s0 + i];
+      const bool in = at < slots && at >= -slots;
+      if (!in) atomicOr(p.err, kErrDevice);
+      row[i] = in ? (int)at : kNoRow;
+      w[i] = p.weights ? p.weights[s0 + i] : 1.f;
+    }
+    __syncthreads();
+    return n;
+  }
+};
+
+// Accesses of a thread: 16 bytes' worth, so that narrow ones (rows or strides that are no multiple of 16 bytes)
+// have as much in flight.
+template <int BYTES>
+constexpr int kAccesses = 16 / BYTES;
+
 template <int BYTES>
 __global__ void __launch_bounds__(kThreads) dispatch_rows_kernel(const RowArgs p) {
-  const int64_t token = blockIdx.x * (int64_t)(kThreads / p.tx) + threadIdx.x / p.tx;
-  const int c = blockIdx.y * p.tx + threadIdx.x % p.tx;
+  typedef typename Raw<BYTES>::type R;
+  constexpr int U = kAccesses<BYTES>;
+  __shared__ Batch batch;
+  const int per = kThreads / p.tx, sub = threadIdx.x / p.tx, c0 = blockIdx.y * p.tx * U + threadIdx.x % p.tx;
+  const int64_t first = blockIdx.x * (int64_t)(p.turns * per);
   wait_for_previous_grid();
-  if (token < p.tokens && c < p.vecs) copy_out<BYTES>(p, token, c, p.place + token * p.top);
+  const int n = batch.load(p, first);
+  const R *x = reinterpret_cast<const R *>(p.x);
+  R *rows = reinterpret_cast<R *>(p.rows);
+  for (int t = sub; t < n; t += per) {
+    R v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + u * p.tx < p.vecs) v[u] = __ldcs(x + (first + t) * p.ldx + c0 + u * p.tx);
+    for (int j = 0; j < p.top; ++j) {
+      const int r = batch.row[t * p.top + j];
+      if (r == kNoRow) continue;
+      R *dst = rows + (int64_t)(r < 0 ? -1 - r : r) * p.vecs + c0;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c0 + u * p.tx < p.vecs) dst[u * p.tx] = r < 0 ? R{} : v[u];
+    }
+  }
 }
 
 // Few slots: a block per token finds its k places by counting, block `tokens` makes the offsets.
@@ -287,106 +346,138 @@ __global__ void __launch_bounds__(kThreads) dispatch_few_kernel(const RowArgs p)
   if (c < p.vecs) copy_out<BYTES>(p, token, c, place);
 }
 
-// out[t]: one access of a row a thread, its k rows' loads in flight together
+// out[t]: a thread has the same place of the k rows, their loads in flight together
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const RowArgs p) {
-  const int64_t token = blockIdx.x * (int64_t)(kThreads / p.tx) + threadIdx.x / p.tx;
-  const int c = (blockIdx.y * p.tx + threadIdx.x % p.tx) * N;
-  if (token >= p.tokens || c >= p.hidden) return;
-  const T *y = static_cast<const T *>(p.y);
-  const int64_t slots = p.tokens * p.top;
-  const int64_t *place = p.place + token * p.top;
-  const float *weights = p.weights ? p.weights + token * p.top : nullptr;
-  float sum[N];
+  constexpr int U = kAccesses<sizeof(T) * N>;
+  __shared__ Batch batch;
+  const int per = kThreads / p.tx, sub = threadIdx.x / p.tx, step = p.tx * N;
+  const int c0 = (blockIdx.y * p.tx * U + threadIdx.x % p.tx) * N;
+  const int64_t first = blockIdx.x * (int64_t)(p.turns * per);
+  const int n = batch.load(p, first);
+  const T *y = static_cast<const T *>(p.y) + c0;
+  T *out = static_cast<T *>(p.out) + c0;
+  for (int t = sub; t < n; t += per) {
+    float sum[U][N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) sum[i] = 0.f;
-  for (int j0 = 0; j0 < p.top; j0 += kSlots) {
-    float v[kSlots][N];
-    bool has[kSlots];
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
-      has[j] = false;
-      if (j0 + j < p.top) {
-        bool zero;
-        const int64_t r = row_of(__ldg(place + j0 + j), slots, &zero, p.err);
-        has[j] = r >= 0 && !zero;
-        if (has[j]) load<T, N>(v[j], y + r * p.hidden + c);
-      }
+      for (int i = 0; i < N; ++i) sum[u][i] = 0.f;
+    for (int j0 = 0; j0 < p.top; j0 += kSlots) {
+      Access<T, N> v[kSlots][U];
+      const int *row = batch.row + t * p.top + j0;
+      const float *w = batch.w + t * p.top + j0;
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j)
+        if (j0 + j < p.top && row[j] >= 0) {
+          const T *src = y + (int64_t)row[j] * p.hidden;
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (c0 + u * step < p.hidden) v[j][u] = load_once<T, N>(src + u * step);
+        }
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j)
+        if (j0 + j < p.top && row[j] >= 0) {
+          const float wj = w[j];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            float f[N];
+            unpack<T, N>(f, v[j][u]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) sum[u][i] = fmaf(wj, f[i], sum[u][i]);
+          }
+        }
     }
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j)
-      if (has[j]) {
-        const float w = weights ? __ldg(weights + j0 + j) : 1.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) sum[i] = fmaf(w, v[j][i], sum[i]);
-      }
+    for (int u = 0; u < U; ++u)
+      if (c0 + u * step < p.hidden) store<T, N>(out + (first + t) * p.ldo + u * step, sum[u]);
   }
-  store<T, N>(static_cast<T *>(p.out) + token * p.ldo + c, sum);
 }
 
 // The gradient: a token's threads go over its row once for every kSlots slots, each access of dout
-// meeting those of y; the products' sums are joined over the threads in a fixed tree.
+// meeting those of y.  The products' sums: a thread's in turn, a tree over the warp, and the warps' in order
+// when the block's tokens are done.
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const RowArgs p) {
-  __shared__ float part[kThreads / 32][kSlots];
-  const int tx = p.tx, me = threadIdx.x % tx, lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-  const int64_t token = blockIdx.x * (int64_t)(kThreads / tx) + threadIdx.x / tx;
-  const bool in = token < p.tokens;
-  const T *y = static_cast<const T *>(p.y), *dout = static_cast<const T *>(p.x) + token * p.ldx;
+  constexpr int U = kAccesses<sizeof(T) * N>;
+  __shared__ Batch batch;
+  __shared__ float part[kThreads / 32][kPartSlots];   // per warp of a token: its slots' sums
+  const int tx = p.tx, me = threadIdx.x % tx, lane = threadIdx.x & 31, per = kThreads / tx, sub = threadIdx.x / tx;
+  const int warps = tx / 32, wp = me >> 5;                                // of a token; 0: tokens share a warp
+  const int64_t first = blockIdx.x * (int64_t)(p.turns * per);
+  const int n = batch.load(p, first);
+  const T *y = static_cast<const T *>(p.y);
   T *dy = static_cast<T *>(p.rows);
-  const int64_t slots = p.tokens * p.top;
-  for (int j0 = 0; j0 < p.top; j0 += kSlots) {
-    int64_t at[kSlots];
-    bool zero[kSlots];
-    float w[kSlots], dot[kSlots];
+  for (int t0 = 0; t0 < n; t0 += per) {
+    const int t = t0 + sub;
+    const bool in = t < n;
+    const T *dout = static_cast<const T *>(p.x) + (first + t) * p.ldx;
+    for (int j0 = 0; j0 < p.top; j0 += kSlots) {
+      const int *row = batch.row + t * p.top + j0;
+      const float *w = batch.w + t * p.top + j0;
+      float dot[kSlots];
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
-      at[j] = -1, zero[j] = true, w[j] = 1.f, dot[j] = 0.f;
-      if (in && j0 + j < p.top) {
-        at[j] = row_of(__ldg(p.place + token * p.top + j0 + j), slots, &zero[j], p.err);
-        if (p.weights) w[j] = __ldg(p.weights + token * p.top + j0 + j);
-      }
-    }
-    if (in)
-      for (int c = me * N; c < p.hidden; c += tx * N) {
-        float d[N], v[kSlots][N];
-        load<T, N>(d, dout + c);
-        if (p.dweights)
+      for (int j = 0; j < kSlots; ++j) dot[j] = 0.f;
+      if (in)
+        for (int c = me * N; c < p.hidden; c += tx * N * U) {
+          float d[U][N];
+          Access<T, N> v[kSlots][U];
+          if (p.dweights)
+#pragma unroll
+            for (int j = 0; j < kSlots; ++j)
+              if (j0 + j < p.top && row[j] >= 0) {
+                const T *src = y + (int64_t)row[j] * p.hidden + c;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                  if (c + u * tx * N < p.hidden) v[j][u] = load_once<T, N>(src + u * tx * N);
+              }
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (c + u * tx * N < p.hidden) unpack<T, N>(d[u], load<T, N>(dout + c + u * tx * N));
 #pragma unroll
           for (int j = 0; j < kSlots; ++j)
-            if (at[j] >= 0 && !zero[j]) load<T, N>(v[j], y + at[j] * p.hidden + c);
+            if (j0 + j < p.top && row[j] != kNoRow) {
+              const int r = row[j];
+              T *dst = dy + (int64_t)(r < 0 ? -1 - r : r) * p.hidden + c;
+              const float wj = w[j];
+#pragma unroll
+              for (int u = 0; u < U; ++u) {
+                if (c + u * tx * N >= p.hidden) break;
+                float o[N];
+                if (dy) {
+#pragma unroll
+                  for (int i = 0; i < N; ++i) o[i] = r < 0 ? 0.f : wj * d[u][i];
+                  store<T, N>(dst + u * tx * N, o);
+                }
+                if (p.dweights && r >= 0) {
+                  unpack<T, N>(o, v[j][u]);
+#pragma unroll
+                  for (int i = 0; i < N; ++i) dot[j] = fmaf(d[u][i], o[i], dot[j]);
+                }
+              }
+            }
+        }
+      if (!p.dweights) continue;
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j)
+        for (int o = min(tx, 32) / 2; o; o >>= 1) dot[j] += __shfl_xor_sync(kAll, dot[j], o);
+      if (warps > 1) {
 #pragma unroll
         for (int j = 0; j < kSlots; ++j)
-          if (at[j] >= 0) {
-            float o[N];
+          if (in && lane == j && j0 + j < p.top) part[wp][t * p.top + j0 + j] = dot[j];
+      } else if (in && me == 0) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) o[i] = zero[j] ? 0.f : w[j] * d[i];
-            if (dy) store<T, N>(dy + at[j] * p.hidden + c, o);
-            if (p.dweights && !zero[j])
-#pragma unroll
-              for (int i = 0; i < N; ++i) dot[j] = fmaf(d[i], v[j][i], dot[j]);
-          }
+        for (int j = 0; j < kSlots; ++j)
+          if (j0 + j < p.top) p.dweights[(first + t) * p.top + j0 + j] = dot[j];
       }
-    if (!p.dweights) continue;
-#pragma unroll
-    for (int j = 0; j < kSlots; ++j)
-      for (int o = min(tx, 32) / 2; o; o >>= 1) dot[j] += __shfl_xor_sync(kAll, dot[j], o);
-    if (tx > 32) {
-      __syncthreads();   // the sums before these have been read
-#pragma unroll
-      for (int j = 0; j < kSlots; ++j)
-        if (lane == j) part[wp][j] = dot[j];
-      __syncthreads();
-      if (in && me < kSlots && j0 + me < p.top) {
-        float s = 0.f;
-        for (int k = 0; k < tx / 32; ++k) s += part[wp + k][me];
-        p.dweights[token * p.top + j0 + me] = s;
-      }
-    } else if (in && me == 0) {
-#pragma unroll
-      for (int j = 0; j < kSlots; ++j)
-        if (j0 + j < p.top) p.dweights[token * p.top + j0 + j] = dot[j];
     }
+  }
+  if (!p.dweights || warps <= 1) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n * p.top; i += kThreads) {
+    float s = part[0][i];
+    for (int k = 1; k < warps; ++k) s += part[k][i];
+    p.dweights[first * p.top + i] = s;
   }
 }
 
@@ -409,11 +500,18 @@ int access_bytes(int size, int64_t hidden, std::initializer_list<const void *> p
   return b;
 }
 
-// threads of a token: a power of two that covers its accesses, 8 to 256
-int threads_of(int vecs) {
-  int t = 8;
-  while (t < kThreads && t < vecs) t *= 2;
-  return t;
+// How a kernel by tokens is laid out: threads of a token (a power of two that covers its accesses, 8 to 256), the
+// columns' blocks, and how many tokens a block takes in turn: up to 8, as many as leave four blocks for each that
+// the SMs hold, and whose slots fit `most` (a batch's).
+dim3 layout(RowArgs &p, int accesses, bool columns, int most) {
+  const int need = (p.vecs + accesses - 1) / accesses;
+  p.tx = 8;
+  while (p.tx < kThreads && p.tx < need) p.tx *= 2;
+  const int per = kThreads / p.tx;
+  const int64_t cols = columns ? (need + p.tx - 1) / p.tx : 1;
+  const int64_t turns = std::min<int64_t>(p.tokens * cols / (16ll * per * num_sms()), 8);
+  p.turns = (int)std::clamp<int64_t>(turns, 1, std::max(1, most / (per * p.top)));
+  return dim3((unsigned)((p.tokens + per * p.turns - 1) / (per * p.turns)), (unsigned)cols);
 }
 
 template <typename F>
@@ -501,10 +599,8 @@ int muon_dispatch(const void *x, int64_t x_stride, const int64_t *ids, int64_t t
   }
   const int so = order({ids, (int)(tokens * top), (int)experts, offsets, place, err}, s);
   if (so != MUON_OK) return so;
-  p.tx = threads_of(p.vecs);
-  const int per = kThreads / p.tx;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((tokens + per - 1) / per), (unsigned)((p.vecs + p.tx - 1) / p.tx));
+  cfg.gridDim = layout(p, 16 / bytes, true, kBatchSlots);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -539,12 +635,10 @@ int muon_combine(const void *y, const int64_t *place, const float *weights, int6
   p.top = (int)top;
   p.hidden = (int)hidden;
   p.vecs = (int)(hidden * size / bytes);
-  p.tx = threads_of(p.vecs);
   p.err = device_error_word();
   if (!p.err) return MUON_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int per = kThreads / p.tx;
-  const dim3 grid((unsigned)((tokens + per - 1) / per), (unsigned)((p.vecs + p.tx - 1) / p.tx));
+  const dim3 grid = layout(p, 16 / bytes, true, kBatchSlots);
   trace_before(kTraceCombine, s);
   with_vec(type, bytes, [&](auto t, auto n) {
     combine_kernel<decltype(t), decltype(n)::value><<<grid, kThreads, 0, s>>>(p);
@@ -580,12 +674,10 @@ int muon_combine_backward(const void *dout, int64_t dout_stride, const void *y, 
   p.top = (int)top;
   p.hidden = (int)hidden;
   p.vecs = (int)(hidden * size / bytes);
-  p.tx = threads_of(p.vecs);
   p.err = device_error_word();
   if (!p.err) return MUON_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int per = kThreads / p.tx;
-  const unsigned blocks = (unsigned)((tokens + per - 1) / per);
+  const unsigned blocks = layout(p, 16 / bytes, false, kPartSlots).x;
   trace_before(kTraceCombineBwd, s);
   with_vec(type, bytes, [&](auto t, auto n) {
     combine_backward_kernel<decltype(t), decltype(n)::value><<<blocks, kThreads, 0, s>>>(p);
