@@ -95,14 +95,27 @@ struct OrderArgs {
   unsigned *err;
 };
 
-// One cluster of 8 blocks of 32 warps.  Each warp takes a run of consecutive slots: first it counts
+// One cluster of 16 blocks of 32 warps.  Each warp takes a run of consecutive slots: first it counts
 // them by expert, then, with the counts of all warps before it added up, gives them their rows in
 // order, 32 at a time (lanes of one expert by their number).  Counters are whole numbers and each
-// warp's own, so the order is that of the slots.  16384 tokens x 8: see the table of the operators.
-constexpr int kOrderBlocks = 8, kOrderThreads = 1024, kOrderWarps = kOrderThreads / 32;
+// warp's own, so the order is that of the slots.  The ids of kAhead steps are loaded together: a
+// warp does little between two loads, and there are few warps.
+constexpr int kAhead = 8;
 
-__global__ void __cluster_dims__(kOrderBlocks, 1, 1) __launch_bounds__(kOrderThreads)
-    expert_order_kernel(const OrderArgs p) {
+// lanes whose key is this lane's, by a vote on each of its bits
+__device__ __forceinline__ unsigned same_key(int key, int bits) {
+  unsigned same = kAll;
+  for (int b = 0; b < bits; ++b) {
+    const bool set = (key >> b) & 1;
+    const unsigned v = __ballot_sync(kAll, set);
+    same &= set ? v : ~v;
+  }
+  return same;
+}
+
+constexpr int kOrderBlocks = 16, kOrderThreads = 1024, kOrderWarps = kOrderThreads / 32;
+
+__global__ void __launch_bounds__(kOrderThreads) expert_order_kernel(const OrderArgs p) {
   extern __shared__ unsigned order_smem[];
   const int E = p.experts, width = E + 1;
   unsigned *hist = order_smem;                          // [kOrderWarps][width]
@@ -118,32 +131,43 @@ __global__ void __cluster_dims__(kOrderBlocks, 1, 1) __launch_bounds__(kOrderThr
   const long long run = ((long long)p.n + 32 * runs - 1) / (32 * runs) * 32;
   const long long lo = min((long long)p.n, (rank * kOrderWarps + wp) * run), hi = min((long long)p.n, lo + run);
   unsigned *mine = hist + wp * width;
-  for (long long b = lo; b < hi; b += 32) {
-    const bool in = b + lane < hi;
-    const int key = in ? key_of(p.ids[b + lane], E, p.err) : -1;
-    const unsigned same = __match_any_sync(kAll, key);
-    if (in && (same & ((1u << lane) - 1u)) == 0u) mine[key] += __popc(same);
-    __syncwarp();
+  for (long long b = lo; b < hi; b += 32 * kAhead) {
+    int64_t id[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) id[a] = b + 32 * a + lane < hi ? p.ids[b + 32 * a + lane] : 0;
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (b + 32 * a + lane < hi) atomicAdd(&mine[key_of(id[a], E, p.err)], 1u);
   }
   __syncthreads();
   for (int e = tid; e < width; e += kOrderThreads) {
-    unsigned sum = 0u;
+    unsigned v[kOrderWarps], sum = 0u;
+#pragma unroll
+    for (int w = 0; w < kOrderWarps; ++w) v[w] = hist[w * width + e];
+#pragma unroll
     for (int w = 0; w < kOrderWarps; ++w) {
-      const unsigned v = hist[w * width + e];
       hist[w * width + e] = sum;
-      sum += v;
+      sum += v[w];
     }
     total[e] = sum;
   }
   cluster.sync();
   // this thread's expert (at most kOrderThreads of them): slots of it in all blocks and in those before this one
   unsigned all = 0u, before = 0u;
-  if (tid < E)
+  if (tid < E) {
+#pragma unroll
     for (int r = 0; r < kOrderBlocks; ++r) {
       const unsigned v = cluster.map_shared_rank(total, r)[tid];
       all += v;
-      if (r < rank) before += v;
+      before += r < rank ? v : 0u;
     }
+  }
+  // the slots before this block's that are not routed
+  if (wp == kOrderWarps - 1) {
+    const unsigned v = lane < rank ? cluster.map_shared_rank(total, lane)[E] : 0u;
+    const unsigned sum = __reduce_add_sync(kAll, v);
+    if (lane == 0) start[E] = sum;
+  }
   unsigned upto = all;
   for (int o = 1; o < 32; o <<= 1) {
     const unsigned v = __shfl_up_sync(kAll, upto, o);
@@ -162,22 +186,27 @@ __global__ void __cluster_dims__(kOrderBlocks, 1, 1) __launch_bounds__(kOrderThr
     if (rank == 0) p.offsets[tid] = first;
   }
   if (tid == 0) {
-    unsigned b = 0u;
-    for (int r = 0; r < rank; ++r) b += cluster.map_shared_rank(total, r)[E];
-    start[E] = routed + b;
+    start[E] += routed;
     if (rank == 0) p.offsets[E] = p.n;   // rows of no slot count to the last expert
   }
   __syncthreads();
-  for (long long b = lo; b < hi; b += 32) {
-    const bool in = b + lane < hi;
-    const int key = in ? key_of(p.ids[b + lane], E, p.err) : -1;
-    const unsigned same = __match_any_sync(kAll, key), below = same & ((1u << lane) - 1u);
-    unsigned at = 0u;
-    if (in) at = start[key] + mine[key] + __popc(below);
-    __syncwarp();
-    if (in && below == 0u) mine[key] += __popc(same);
-    __syncwarp();
-    if (in) p.place[b + lane] = key < E ? (int64_t)at : -1 - (int64_t)at;
+  const int bits = 32 - __clz(E + 1);   // of a key, and of E + 1, which the lanes behind the run's end have
+  for (long long b = lo; b < hi; b += 32 * kAhead) {
+    int64_t id[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) id[a] = b + 32 * a + lane < hi ? p.ids[b + 32 * a + lane] : 0;
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const bool in = b + 32 * a + lane < hi;
+      const int key = in ? key_of(id[a], E, p.err) : E + 1;
+      const unsigned same = same_key(key, bits), below = same & ((1u << lane) - 1u);
+      unsigned at = 0u;
+      if (in) at = start[key] + mine[key] + __popc(below);
+      __syncwarp();
+      if (in && below == 0u) mine[key] += __popc(same);
+      __syncwarp();
+      if (in) p.place[b + 32 * a + lane] = key < E ? (int64_t)at : -1 - (int64_t)at;
+    }
   }
   cluster.sync();   // no block leaves while another reads its totals
 }
@@ -548,11 +577,26 @@ int order(const OrderArgs &a, cudaStream_t s) {
   std::call_once(once[dev], [&] {
     attr_err[dev] = cudaFuncSetAttribute(expert_order_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)bytes(kMaxExperts));
+    if (attr_err[dev] == cudaSuccess)
+      attr_err[dev] = cudaFuncSetAttribute(expert_order_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   });
   if (attr_err[dev] != cudaSuccess) return MUON_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kOrderBlocks);
+  cfg.blockDim = dim3(kOrderThreads);
+  cfg.dynamicSmemBytes = bytes(a.experts);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kOrderBlocks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   trace_before(kTraceExpertOrder, s);
-  expert_order_kernel<<<kOrderBlocks, kOrderThreads, bytes(a.experts), s>>>(a);
-  return trace_after(kTraceExpertOrder, s);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, expert_order_kernel, a);
+  const int st = trace_after(kTraceExpertOrder, s);
+  return e == cudaSuccess ? st : MUON_ERR_CUDA;
 }
 
 }  // namespace

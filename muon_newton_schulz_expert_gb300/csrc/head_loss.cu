@@ -35,7 +35,7 @@ int check_shape(const HeadShape &h) {
 // Joins a row's partial statistics, in a fixed order: 32 rows a block (lane = row, so that reads of a part are
 // whole lines), the parts spread over the block's warps.
 //   loss = (m - z_target) + log s: the two logits' difference first, since it is what is small where a target is likely
-constexpr int kJoinWarps = 16;
+constexpr int kJoinWarps = 32, kJoinAhead = 8;   // kJoinAhead parts of a warp are loaded together
 __global__ void __launch_bounds__(32 * kJoinWarps)
     head_join_kernel(const float2 *parts, int64_t num, const float *target_logit, const int64_t *targets, int64_t rows,
                      int64_t vocab, float *loss, float *lse, unsigned *err) {
@@ -46,13 +46,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   let_next_grid_start();
   float m = -INFINITY, s = 0.f;
   if (row < rows) {
-#pragma unroll 4
-    for (int64_t c = wp; c < num; c += kJoinWarps) {
-      const float2 v = __ldcs(parts + c * rows + row);
-      const float most = fmaxf(m, v.x);
+    for (int64_t c = wp; c < num; c += kJoinWarps * kJoinAhead) {
+      float2 v[kJoinAhead];
+#pragma unroll
+      for (int i = 0; i < kJoinAhead; ++i)
+        v[i] = c + i * kJoinWarps < num ? __ldcs(parts + (c + i * kJoinWarps) * rows + row) : make_float2(-INFINITY, 0.f);
+      float most = m;
+#pragma unroll
+      for (int i = 0; i < kJoinAhead; ++i) most = fmaxf(most, v[i].x);
       // -inf on both sides (a part beyond the vocabulary's end has no sum) leaves the sum as it is
-      const float a = m == most ? 1.f : expf(m - most), b = v.x == most ? 1.f : expf(v.x - most);
-      s = s * a + v.y * b;
+      s *= m == most ? 1.f : expf(m - most);
+#pragma unroll
+      for (int i = 0; i < kJoinAhead; ++i) s = fmaf(v[i].y, v[i].x == most ? 1.f : expf(v[i].x - most), s);
       m = most;
     }
   }

@@ -86,6 +86,7 @@ struct Schedule {
 
 struct Args {
   CUtensorMap a, b;        // STATS, DLOGITS: x and W, K-major;  GRADS: dx's d (K-major) and W (MN-major)
+  CUtensorMap a_last;      // a by boxes of the rows that the last CTA with any has
   CUtensorMap a2, b2;      // GRADS: dW's d and x, MN-major
   CUtensorMap out, out2;   // DLOGITS: d;  GRADS: dx or its sums, and dW
   long long rows, vocab, v0;
@@ -138,6 +139,13 @@ struct Tile {
     }
   }
 };
+
+// Rows of an operand K-major on M (x, or dx's d) that a CTA loads from its first one on: there is nothing to load
+// behind the last row, and rows that are not loaded leave the others' results as they are.  (With whole boxes, of
+// zeros behind the end, one row of 6144 over 128000 entries took 418 us, 128 rows 274.)
+__device__ __forceinline__ int rows_from(long long rows, int first) {
+  return (int)max(0ll, min(rows - first, (long long)BM));
+}
 
 // the i-th tile of this pair, or -1
 template <int MODE>
@@ -246,7 +254,12 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
         const int bnh = MODE == GRADS ? BNH : p.bn / 2;
         const int m_a = cur.tm * CM + (int)rank * BM;                  // first of this CTA's places on M and N
         const int n_b = cur.tn * (2 * bnh) + (int)rank * bnh;
-        const uint32_t kb_bytes = (uint32_t)(A_STAGE + bnh * (BK * 2));
+        const bool by_rows = MODE != GRADS || !cur.dw;
+        const int mine = by_rows ? rows_from(p.rows, m_a) : BM;
+        const CUtensorMap *map_a = mine == BM ? &p.a : &p.a_last;
+        // of both CTAs
+        const int both = by_rows ? rows_from(p.rows, cur.tm * CM) + rows_from(p.rows, cur.tm * CM + BM) : CM;
+        const uint32_t kb_bytes = (uint32_t)((both + 2 * bnh) * (BK * 2));
         for (int kb = 0; kb < cur.num_kb; kb += KSUB) {
           if (!wait_polled(empty(stage), phase ^ 1u, w)) {
             ok = false;
@@ -257,7 +270,7 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
           // end of K still completes its phase, with no bytes
           if (rank == 0)
 #pragma unroll
-            for (int j = 0; j < KSUB; ++j) mbar_expect_tx(full(stage, j), j < valid ? 2 * kb_bytes : 0);
+            for (int j = 0; j < KSUB; ++j) mbar_expect_tx(full(stage, j), j < valid ? kb_bytes : 0);
           issued |= 1u << stage;
           issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
 #pragma unroll
@@ -267,10 +280,10 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
             const uint32_t sa = sbase + stage * STAGE_BYTES + j * KB_BYTES, sb = sa + A_STAGE;
             const uint32_t bar = map_to_rank(full(stage, j), 0);
             if (MODE != GRADS) {
-              tma_load_3d_pair(sa, &p.a, bar, k, m_a, 0, p.err);
+              if (mine) tma_load_3d_pair(sa, map_a, bar, k, m_a, 0, p.err);
               tma_load_3d_pair(sb, &p.b, bar, k, (int)p.v0 + n_b, 0, p.err);
             } else if (!cur.dw) {
-              tma_load_3d_pair(sa, &p.a, bar, k, m_a, 0, p.err);
+              if (mine) tma_load_3d_pair(sa, map_a, bar, k, m_a, 0, p.err);
               load_columns(sb, &p.b, bar, n_b, (int)p.v0 + k, 0, p.wide, p.err);
             } else {
               load_columns(sa, &p.a2, bar, m_a, k, 0, true, p.err);
@@ -558,6 +571,12 @@ int launch(Args &p, int64_t tiles, int trace_kind, cudaStream_t s) {
     if (_st != MUON_OK) return _st; \
   } while (0)
 
+// a's maps: whole boxes, and boxes of the rows that the last CTA has
+int map_rows(Args &p, const void *base, int64_t rows, int64_t cols, int64_t ld) {
+  HEAD_TRY(make_map(&p.a, base, 1, rows, cols, BM, ld));
+  return make_map(&p.a_last, base, 1, rows, cols, (int)((rows - 1) % BM + 1), ld);
+}
+
 int pairs_of_sms() { return std::max(1, num_sms() / 2); }
 
 // columns of a tile of z: the most that leave a tile for each pair of CTAs
@@ -578,7 +597,7 @@ int head_stats(const HeadShape &h, const void *x, int64_t ldx, const void *w, co
                float *target_logit, cudaStream_t s) {
   Args p{};
   p.bn = head_stats_columns(h);
-  HEAD_TRY(make_map(&p.a, x, 1, h.rows, h.hidden, BM, ldx));
+  HEAD_TRY(map_rows(p, x, h.rows, h.hidden, ldx));
   HEAD_TRY(make_map(&p.b, w, 1, h.vocab, h.hidden, p.bn / 2));
   p.rows = h.rows;
   p.vocab = h.vocab;
@@ -620,7 +639,7 @@ int head_dlogits(const HeadShape &h, const HeadPlan &plan, int64_t v0, const voi
                  const HeadRow *row, void *d, cudaStream_t s) {
   Args p{};
   p.bn = columns(h, plan.width(), 128);
-  HEAD_TRY(make_map(&p.a, x, 1, h.rows, h.hidden, BM, ldx));
+  HEAD_TRY(map_rows(p, x, h.rows, h.hidden, ldx));
   HEAD_TRY(make_map(&p.b, w, 1, h.vocab, h.hidden, p.bn / 2));
   HEAD_TRY(make_map(&p.out, d, 1, h.rows, plan.width(), 32));
   p.rows = h.rows;
@@ -652,7 +671,7 @@ int head_grads(const HeadShape &h, const HeadPlan &plan, int64_t v0, bool first,
   p.kblocks2 = (int)cdiv(h.rows, BK);
   p.splits = plan.splits;
   if (dx) {
-    HEAD_TRY(make_map(&p.a, d, 1, h.rows, plan.width(), BM));
+    HEAD_TRY(map_rows(p, d, h.rows, plan.width(), plan.width()));
     HEAD_TRY(p.wide ? make_map_blocks(&p.b, w, 1, h.vocab, h.hidden, BK, 2) : make_map(&p.b, w, 1, h.vocab, h.hidden, BK));
     p.out_kind = plan.pieces == 1 && plan.splits == 1 ? 0 : first ? 1 : 2;
     HEAD_TRY(p.out_kind == 0 ? make_map(&p.out, dx, 1, h.rows, h.hidden, 32, lddx)
