@@ -5,12 +5,13 @@
 //   without a bias: both scores grow with x), ties to the lowest index; their
 //   weights w_i = scale s_i, or scale s_i / sum of the chosen s
 //
-// A warp takes a row and keeps it in registers as 32-bit keys in the values' order (lane l:
-// experts l, l + 32, ..), so the logits are read once.  The k-th largest of the lanes' own
-// maxima bounds the k-th largest key from below; the few keys that reach it are gathered in shared
-// memory (k = 8 of 384: about 10) and ranked by counting who is larger.  The kernel is bound by
-// instructions, not by its bytes: k rounds of one warp-wide maximum each, in which only the
-// winning lane's values changed, took 34 us for 16384 rows of 384 with bias, this MEASURED.
+// A warp takes a row and keeps its keys in registers (lane l: experts l, l + 32, ..), so the
+// logits are read once.  The k-th largest of the lanes' own maxima bounds the k-th largest key
+// from below (redux.sync on fp32); the few keys that reach it are gathered in shared memory (k = 8
+// of 384: about 10) and ranked by counting who is larger.  The kernel is bound by instructions,
+// not by its bytes: 16384 rows of 384 with bias, top 8, took 34 us as k rounds of a warp-wide
+// maximum in which the winning lane looked at its values again, 23 us with integer keys made
+// of every value, 16.6 us so.
 //
 // With a bias the keys are sums of two numbers, and fp32 may not tell two of them apart
 // that 64 bits do.  Where two neighbours in the order are closer than the keys' error
@@ -37,10 +38,8 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float
 __device__ __forceinline__ void from_f(float *d, float v) { *d = v; }
 __device__ __forceinline__ void from_f(__nv_bfloat16 *d, float v) { *d = __float2bfloat16_rn(v); }
 
-// Keys in the values' order: 0 for -inf (never chosen), the largest for NaN; -0 is 0.
+// Whole numbers in the values' order; -0 is 0.  In 64 bits 0 for -inf (never chosen), the largest for NaN.
 __device__ __forceinline__ uint32_t order_of(float v) {
-  if (v == -INFINITY) return 0u;
-  if (v != v) return 0xffffffffu;
   const uint32_t b = __float_as_uint(v + 0.f);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
@@ -54,10 +53,31 @@ __device__ __forceinline__ unsigned long long order_of(double v) {
   return b >> 63 ? ~b : b | (1ull << 63);
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-  return v;
+__device__ __forceinline__ float warp_max(float v) {   // a NaN counts for nothing
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float warp_max_nan(float v) {   // NaN if any is
+  float r;
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// 2^x, 1/x: within 2^-22 of themselves
+__device__ __forceinline__ float fast_exp(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+__device__ __forceinline__ float fast_inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 template <typename F>
 __device__ __forceinline__ F warp_sum(F v) {
@@ -85,22 +105,35 @@ struct Args {
 template <typename T, int R>
 __device__ __noinline__ int choose_in_64(const T *x, const float *bias, int experts, int top, bool softmax) {
   const int lane = threadIdx.x & 31;
-  double most = -INFINITY, sum = 1.0;
+  double v[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) v[i] = i * 32 + lane < experts ? (double)to_f(x[i * 32 + lane]) : -INFINITY;
   if (softmax && bias) {
-    for (int e = lane; e < experts; e += 32) most = fmax(most, (double)to_f(x[e]));
+    double most = v[0], sum = 0.0;
+#pragma unroll
+    for (int i = 1; i < R; ++i) most = fmax(most, v[i]);
     for (int o = 16; o; o >>= 1) most = fmax(most, __shfl_xor_sync(kAll, most, o));
-    sum = 0.0;
-    for (int e = lane; e < experts; e += 32) sum += exp((double)to_f(x[e]) - most);
-    sum = warp_sum(sum);
+#pragma unroll 1
+    for (int i = 0; i < R; ++i) {
+      const double e = v[0] == -INFINITY ? 0.0 : exp(v[0] - most);   // once around: each in turn is v[0]
+      sum += e;
+#pragma unroll
+      for (int k = 0; k + 1 < R; ++k) v[k] = v[k + 1];
+      v[R - 1] = e;
+    }
+    sum = 1.0 / warp_sum(sum);
+#pragma unroll
+    for (int i = 0; i < R; ++i) v[i] *= sum;
+  } else if (bias) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) v[i] = sigmoid(v[i]);
   }
-  auto key_of = [&](int e) {
-    const double v = to_f(x[e]);
-    if (!bias || v == -INFINITY) return order_of(v);
-    return order_of((softmax ? exp(v - most) / sum : sigmoid(v)) + (double)bias[e]);
-  };
   unsigned long long key[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) key[i] = i * 32 + lane < experts ? key_of(i * 32 + lane) : 0ull;
+  for (int i = 0; i < R; ++i) {
+    const int e = i * 32 + lane;
+    key[i] = e >= experts || (bias && to_f(x[e]) == -INFINITY) ? 0ull : order_of(bias ? v[i] + (double)bias[e] : v[i]);
+  }
   int mine = -1;
   for (int j = 0; j < top; ++j) {
     unsigned long long best = 0ull;
@@ -123,11 +156,14 @@ __device__ __noinline__ int choose_in_64(const T *x, const float *bias, int expe
   return mine;
 }
 
-// A warp's candidates, and the first of them in order.
-struct Candidate {
-  uint32_t key;
-  int e;
-};
+// A warp's candidates (key and complemented index in one number: the larger comes first), and the first of
+// them in order.
+typedef unsigned long long Candidate;
+__device__ __forceinline__ Candidate candidate(float key, int e) {
+  return (Candidate)order_of(key) << 32 | (0xffffffffu - (unsigned)e);
+}
+__device__ __forceinline__ int expert_of(Candidate c) { return (int)(0xffffffffu - (unsigned)c); }
+__device__ __forceinline__ float key_of(Candidate c) { return value_of((uint32_t)(c >> 32)); }
 template <bool BIAS>
 struct Gathered {
   Candidate c[kCandidates], sorted[kMaxTop + 1];
@@ -135,52 +171,50 @@ struct Gathered {
 };
 
 template <typename T, int R, bool BIAS>
-__global__ void __launch_bounds__(kThreads) route_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, R <= 12 ? 5 : R <= 16 ? 4 : 3) route_kernel(const Args p) {
   __shared__ Gathered<BIAS> gathered[kWarps];
   const int lane = threadIdx.x & 31;
+  Gathered<BIAS> &g = gathered[threadIdx.x >> 5];
   const int64_t row = blockIdx.x * (int64_t)kWarps + (threadIdx.x >> 5);
   if (row >= p.rows) return;   // a warp together
-  Gathered<BIAS> &g = gathered[threadIdx.x >> 5];
   const T *x = static_cast<const T *>(p.logits) + row * p.stride;
-  uint32_t key[R], best = 0u;
+  float key[R], best = -INFINITY;
   float m = -INFINITY, sum = 1.f;
-  {
-    float v[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) v[i] = i * 32 + lane < p.experts ? to_f(x[i * 32 + lane]) : -INFINITY;
-    // the softmax's sum, where keys or weights need it
-    if (p.softmax && (BIAS || !p.normalize)) {
+  for (int i = 0; i < R; ++i) key[i] = i * 32 + lane < p.experts ? to_f(x[i * 32 + lane]) : -INFINITY;
+  // the softmax's sum, where keys or weights need it
+  if (p.softmax && (BIAS || !p.normalize)) {
 #pragma unroll
-      for (int i = 0; i < R; ++i) m = fmaxf(m, v[i]);
-      m = warp_max(m);
-      sum = 0.f;
+    for (int i = 0; i < R; ++i) m = fmaxf(m, key[i]);
+    m = warp_max(m);
+    float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < R; ++i) sum += v[i] == -INFINITY ? 0.f : __expf(v[i] - m);
-      sum = warp_sum(sum);
+    for (int i = 0; i < R; ++i) part[i & 3] += key[i] == -INFINITY ? 0.f : fast_exp(key[i] - m);
+    sum = warp_sum((part[0] + part[1]) + (part[2] + part[3]));
+  }
+  const float inv = 1.f / sum;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (BIAS) {
+      const float s = p.softmax ? fast_exp(key[i] - m) * inv : fast_inverse(1.f + fast_exp(-key[i]));
+      key[i] = key[i] == -INFINITY ? key[i] : s + __ldg(p.bias + i * 32 + lane);
     }
-    const float inv = 1.f / sum;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (BIAS && v[i] != -INFINITY)
-        v[i] = (p.softmax ? __expf(v[i] - m) * inv : __fdividef(1.f, 1.f + __expf(-v[i]))) +
-               __ldg(p.bias + i * 32 + lane);
-      key[i] = order_of(v[i]);
-      best = max(best, key[i]);
-    }
+    best = max_nan(best, key[i]);
   }
   // Keys are within eps and 2^-23 of themselves: a fast exponential is within 2^-22 + 2^-24 |its argument| of
-  // itself, which a sigmoid turns into 2^-20 at most and a softmax, whose sum of up to 1024 terms takes 36
-  // roundings, into 2^-18 of its largest score (s |x - m| is at most 0.37 of that).
-  const float eps = p.softmax ? 0x1p-17f / sum : 0x1p-20f;
+  // itself, which a sigmoid turns into 2^-20 at most and a softmax, whose sum of up to 1024 terms takes 14
+  // roundings on a path, into 2^-19 of its largest score (s |x - m| is at most 0.37 of that).
+  const float eps = p.softmax ? 0x1p-19f * inv : 0x1p-20f;
   // at least `top` keys (with a bias one more, to see how far the border is) reach the bound
-  uint32_t bound = 0u;
+  float bound = -INFINITY;
   for (int j = 0, need = p.top + (BIAS ? 1 : 0); j < need; ++j) {
-    bound = __reduce_max_sync(kAll, best);
-    if (bound == 0u) break;
-    if (best == bound) best = 0u;
+    bound = warp_max_nan(best);
+    if (!(bound > -INFINITY)) break;
+    if (best == bound) best = -INFINITY;
   }
-  if (BIAS && bound) bound = order_of(value_of(bound) - 2.f * eps - fabsf(value_of(bound)) * 0x1p-21f);
-  bound = max(bound, 1u);   // -inf is no candidate
+  if (BIAS && bound > -INFINITY) bound -= 2.f * eps + fabsf(bound) * 0x1p-21f;
+  bool whole = bound != bound;                  // a NaN among the keys, or an infinite one with a bias
+  bound = fmaxf(bound, -3.402823466e38f);       // -inf is no candidate
   int count = 0;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -188,52 +222,52 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const Args p) {
     const unsigned who = __ballot_sync(kAll, is);
     if (who == 0u) continue;
     const int at = count + __popc(who & ((1u << lane) - 1u));
-    if (is && at < kCandidates) g.c[at] = {key[i], i * 32 + lane};
+    if (is && at < kCandidates) g.c[at] = candidate(key[i], i * 32 + lane);
     count += __popc(who);
   }
+  whole = whole || count > kCandidates;         // ties
   __syncwarp();
-  int mine = -1;            // lane j: the j-th expert
-  if (count > kCandidates) {   // ties
-    mine = choose_in_64<T, R>(x, p.bias, p.experts, p.top, p.softmax);
-  } else {
+  int mine = -1;                                // lane j: the j-th expert
+  if (!whole) {
     for (int c = lane; c < count; c += 32) {
       const Candidate a = g.c[c];
       int before = 0;
-      for (int j = 0; j < count; ++j) {
-        const Candidate b = g.c[j];
-        before += b.key > a.key || (b.key == a.key && b.e < a.e);
-      }
+#pragma unroll 4
+      for (int j = 0; j < count; ++j) before += g.c[j] > a;
       if (before <= kMaxTop) g.sorted[before] = a;
     }
     __syncwarp();
-    if (lane < min(count, p.top)) mine = g.sorted[lane].e;
+    const bool has = lane < min(count, p.top);
+    if (has) mine = expert_of(g.sorted[lane]);
     if (BIAS) {
       bool unsure = false;
-      if (lane < p.top && lane + 1 < count) {
+      if (has && lane + 1 < count) {
         const Candidate next = g.sorted[lane + 1];
-        const float a = value_of(g.sorted[lane].key), b = value_of(next.key);
+        const float a = key_of(g.sorted[lane]), b = key_of(next);
         unsure = a - b <= 2.f * eps + (fabsf(a) + fabsf(b)) * 0x1p-23f &&
-                 (to_f(x[mine]) != to_f(x[next.e]) || __ldg(p.bias + mine) != __ldg(p.bias + next.e));
+                 (to_f(x[mine]) != to_f(x[expert_of(next)]) || __ldg(p.bias + mine) != __ldg(p.bias + expert_of(next)));
       }
       if (__any_sync(kAll, unsure)) {
-        if (p.softmax) {
-          mine = choose_in_64<T, R>(x, p.bias, p.experts, p.top, p.softmax);
-        } else {
-          for (int c = lane; c < count; c += 32)
-            g.key64[c] = order_of(sigmoid((double)to_f(x[g.c[c].e])) + (double)__ldg(p.bias + g.c[c].e));
+        whole = p.softmax;
+        if (!whole) {
+          for (int c = lane; c < count; c += 32) {
+            const int e = expert_of(g.c[c]);
+            g.key64[c] = order_of(sigmoid((double)to_f(x[e])) + (double)__ldg(p.bias + e));
+          }
           __syncwarp();
           for (int c = lane; c < count; c += 32) {
             int before = 0;
             for (int j = 0; j < count; ++j)
-              before += g.key64[j] > g.key64[c] || (g.key64[j] == g.key64[c] && g.c[j].e < g.c[c].e);
+              before += g.key64[j] > g.key64[c] || (g.key64[j] == g.key64[c] && expert_of(g.c[j]) < expert_of(g.c[c]));
             if (before <= kMaxTop) g.sorted[before] = g.c[c];
           }
           __syncwarp();
-          if (lane < min(count, p.top)) mine = g.sorted[lane].e;
+          if (has) mine = expert_of(g.sorted[lane]);
         }
       }
     }
   }
+  if (whole) mine = choose_in_64<T, R>(x, p.bias, p.experts, p.top, p.softmax);
   if (lane >= p.top) mine = -1;
   float s = 0.f;
   const float c = mine >= 0 ? to_f(x[mine]) : -INFINITY;
