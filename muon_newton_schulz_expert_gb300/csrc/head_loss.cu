@@ -34,7 +34,9 @@ int check_shape(const HeadShape &h) {
 
 // Joins a row's partial statistics, in a fixed order: 32 rows a block (lane = row, so that reads of a part are
 // whole lines), the parts spread over the block's warps.
-//   loss = (m - z_target) + log s: the two logits' difference first, since it is what is small where a target is likely
+// Statistics are in powers of two: s = sum 2^(z log2(e) - c).
+//   loss = ((c - z_target log2(e)) + log2 s) ln 2: the difference first, since it is what is small where a target is
+//   likely, with one rounding
 constexpr int kJoinWarps = 32, kJoinAhead = 8;   // kJoinAhead parts of a warp are loaded together
 __global__ void __launch_bounds__(32 * kJoinWarps)
     head_join_kernel(const float2 *parts, int64_t num, const float *target_logit, const int64_t *targets, int64_t rows,
@@ -44,7 +46,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   const int64_t row = blockIdx.x * 32ll + lane;
   wait_for_previous_grid();
   let_next_grid_start();
-  float m = -INFINITY, s = 0.f;
+  float m = -INFINITY, s = 0.f;   // the largest c so far
   if (row < rows) {
     for (int64_t c = wp; c < num; c += kJoinWarps * kJoinAhead) {
       float2 v[kJoinAhead];
@@ -55,9 +57,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 #pragma unroll
       for (int i = 0; i < kJoinAhead; ++i) most = fmaxf(most, v[i].x);
       // -inf on both sides (a part beyond the vocabulary's end has no sum) leaves the sum as it is
-      s *= m == most ? 1.f : expf(m - most);
+      s *= m == most ? 1.f : exp2f(m - most);
 #pragma unroll
-      for (int i = 0; i < kJoinAhead; ++i) s = fmaf(v[i].y, v[i].x == most ? 1.f : expf(v[i].x - most), s);
+      for (int i = 0; i < kJoinAhead; ++i) s = fmaf(v[i].y, v[i].x == most ? 1.f : exp2f(v[i].x - most), s);
       m = most;
     }
   }
@@ -67,20 +69,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   for (int i = 1; i < kJoinWarps; ++i) {
     const float2 v = part[i][lane];
     const float most = fmaxf(m, v.x);
-    const float a = m == most ? 1.f : expf(m - most), b = v.x == most ? 1.f : expf(v.x - most);
+    const float a = m == most ? 1.f : exp2f(m - most), b = v.x == most ? 1.f : exp2f(v.x - most);
     s = s * a + v.y * b;
     m = most;
   }
-  const float ls = logf(s);
-  if (lse) lse[row] = m + ls;
+  const float ls = log2f(s);
+  constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+  if (lse) lse[row] = (m + ls) * kLn2;
   if (!loss) return;
   const int64_t t = targets[row];
   if (t >= vocab) atomicOr(err, kErrDevice);
-  loss[row] = t < 0 ? 0.f : t < vocab ? (m - target_logit[row]) + ls : NAN;
+  loss[row] = t < 0 ? 0.f : t < vocab ? (fmaf(-target_logit[row], kLog2e, m) + ls) * kLn2 : NAN;
 }
 
-// The rows' factors, and x without the rows that take no part (0 times a NaN would reach dW): dense, `cols` wide
-// (hidden rounded up to 64, zeros behind it).  16 bytes a thread and step.
+// The rows' factors, and x without the rows that take no part (0 times a NaN would reach dW, and d): dense, `cols`
+// wide (hidden rounded up to 64, zeros behind it).  16 bytes a thread and step.
 __global__ void __launch_bounds__(256)
     head_rows_kernel(const float *dloss, const float *dlse, const float *lse, const int64_t *targets, int64_t rows,
                      int64_t vocab, const uint4 *x, int64_t ldx, int hidden8, int cols8, HeadRow *out, uint4 *xc,
@@ -96,7 +99,6 @@ __global__ void __launch_bounds__(256)
     if (part) r = {lse[row], dloss[row] + (dlse ? dlse[row] : 0.f), dloss[row], (int)t};
     out[row] = r;
   }
-  if (!xc) return;
   for (int c = threadIdx.x; c < cols8; c += 256)
     xc[row * cols8 + c] = part && c < hidden8 ? x[row * ldx + c] : make_uint4(0u, 0u, 0u, 0u);
 }
@@ -210,7 +212,7 @@ struct Regions {
     xc_cols = cdiv(h.hidden, 64) * 64;
     row = 0;
     xc = row + align256((size_t)h.rows * sizeof(HeadRow));
-    d = xc + (need_dw ? align256((size_t)h.rows * xc_cols * 2) : 0);
+    d = xc + align256((size_t)h.rows * xc_cols * 2);
     acc = d + align256((size_t)h.rows * plan.width() * 2);
     const bool sums = need_dx && (plan.pieces > 1 || plan.splits > 1);
     bytes = acc + (sums ? align256((size_t)plan.splits * h.rows * h.hidden * 4) : 0);
@@ -223,14 +225,14 @@ int backward(const HeadShape &h, const Regions &g, const float *dloss, const flo
   unsigned *err = device_error_word();
   if (!err) return MUON_ERR_CUDA;
   HeadRow *row = reinterpret_cast<HeadRow *>(scratch + g.row);
-  uint4 *xc = dweight ? reinterpret_cast<uint4 *>(scratch + g.xc) : nullptr;
+  uint4 *xc = reinterpret_cast<uint4 *>(scratch + g.xc);
   void *d = scratch + g.d;
   float *acc = reinterpret_cast<float *>(scratch + g.acc);
   const int hidden8 = (int)(h.hidden / 8);
   MUON_TRY(launch_after(head_rows_kernel, (unsigned)h.rows, 256, kTraceHeadRows, s, dloss, dlse, lse, targets, h.rows,
                         h.vocab, static_cast<const uint4 *>(x), ldx / 8, hidden8, (int)(g.xc_cols / 8), row, xc, err));
   for (int64_t v0 = 0; v0 < h.vocab; v0 += g.plan.width()) {
-    MUON_TRY(head_dlogits(h, g.plan, v0, x, ldx, w, row, d, s));
+    MUON_TRY(head_dlogits(h, g.plan, v0, xc, g.xc_cols, w, row, d, s));
     MUON_TRY(head_grads(h, g.plan, v0, v0 == 0, d, w, xc, g.xc_cols, dx, lddx, acc, dweight, s));
   }
   if (dx && (g.plan.pieces > 1 || g.plan.splits > 1)) {

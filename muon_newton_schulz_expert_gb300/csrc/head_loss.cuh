@@ -14,8 +14,8 @@ struct HeadShape {
 
 // columns of z in a tile of head_stats, chosen so that there are tiles for all SMs
 int head_stats_columns(const HeadShape &h);
-// Partial softmax statistics of z: parts[c][row] = (m, sum exp(z - m)) over the c-th part of the vocabulary
-// (head_parts of them), and target_logit[row] = z[row][targets[row]] where that target is in the vocabulary.
+// Partial softmax statistics of z: parts[i][row] = (c, sum 2^(z log2(e) - c)) over the i-th part of the vocabulary
+// (head_parts of them), c a whole number, and target_logit[row] = z[row][targets[row]] where that target is in the vocabulary.
 int64_t head_parts(const HeadShape &h);
 int head_stats(const HeadShape &h, const void *x, int64_t ldx, const void *w, const int64_t *targets, float2 *parts,
                float *target_logit, cudaStream_t s);
@@ -32,11 +32,11 @@ struct HeadPlan {
   int64_t width() const { return piece_tiles * 256; }
 };
 HeadPlan head_plan(const HeadShape &h, bool need_dx, bool need_dw);
-// d[rows][plan.width()] (bf16) of the piece from vocabulary entry v0 on, zeros past the vocabulary's end
-int head_dlogits(const HeadShape &h, const HeadPlan &plan, int64_t v0, const void *x, int64_t ldx, const void *w,
+// d[rows][plan.width()] (bf16) of the piece from vocabulary entry v0 on, zeros past the vocabulary's end.  xc: dense
+// rows of x of width xc_cols, a multiple of 64, zeros in rows that take no part.
+int head_dlogits(const HeadShape &h, const HeadPlan &plan, int64_t v0, const void *xc, int64_t xc_cols, const void *w,
                  const HeadRow *row, void *d, cudaStream_t s);
-// From that piece: its rows of dweight (xc: dense rows of x of width xc_cols, a multiple of 64, zeros in rows that
-// take no part) and its part of dx: dx itself where there are neither pieces nor splits, else sums in
+// From that piece: its rows of dweight and its part of dx: dx itself where there are neither pieces nor splits, else sums in
 // acc[splits][rows][hidden] (`first`: written, else added to).
 int head_grads(const HeadShape &h, const HeadPlan &plan, int64_t v0, bool first, const void *d, const void *w,
                const void *xc, int64_t xc_cols, void *dx, int64_t lddx, float *acc, void *dweight, cudaStream_t s);

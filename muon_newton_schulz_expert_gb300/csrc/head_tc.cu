@@ -162,6 +162,71 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float x, float y) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 split(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Waits for the loads that are under way into v.
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  // the registers are only valid from here on
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
+}
+
+// Running softmax statistics of a row in powers of two: s = sum 2^(z log2(e) - c).  c is a whole number, so that
+// z log2(e) - c is one fused operation whose reference has no rounding, and moves up to the largest logit's.
+struct Stats {
+  float c = -INFINITY, s = 0.f;
+
+  __device__ __forceinline__ void add(const uint32_t (&v)[32]) {
+    float most = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+#pragma unroll
+    for (int i = 3; i + 1 < 32; i += 2) most = max3(most, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+    most = fmaxf(most, __uint_as_float(v[31])) * kLog2e;
+    if (most > c) {
+      const float up = ceilf(most);
+      s *= ex2(c - up);   // c = -inf: s is 0, and so is the factor
+      c = up;
+    }
+    // a NaN, +inf or a whole chunk of -inf makes the differences NaN, and the row's sum with them
+    const f32x2 scale = pair(kLog2e, kLog2e), ref = pair(-c, -c);
+    f32x2 a = pair(0.f, 0.f), b = a;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      const float2 p = split(fma2(pair(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), scale, ref));
+      const float2 q = split(fma2(pair(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), scale, ref));
+      a = add2(a, pair(ex2(p.x), ex2(p.y)));
+      b = add2(b, pair(ex2(q.x), ex2(q.y)));
+    }
+    const float2 r = split(add2(a, b));
+    s += r.x + r.y;
+  }
+};
+
 __device__ __forceinline__ void tma_add_3d(const CUtensorMap *map, uint32_t src, int c0, int c1, int c2,
                                            unsigned *err) {
   if (!dcheck((c0 & 15) == 0 && c0 >= 0 && c1 >= 0 && c2 >= 0, err)) return;
@@ -381,104 +446,88 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
       if (!__all_sync(0xffffffffu, wait_bounded(accf(acc), acc_phase, w))) break;   // warp-uniform
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
-      if (MODE == STATS) {
-        if (row0 < p.rows) {
-          const int each = p.bn / 2;
-          float m = -INFINITY, s = 0.f;
-#pragma unroll 1
-          for (int cc = half * each; cc < half * each + each; cc += 32) {
-            const long long n0 = (long long)cur.tn * p.bn + cc;
-            if (n0 >= p.vocab) break;
-            uint32_t v[32];
-            tmem_ld32(taddr + (uint32_t)cc, v);
-            float z[32];
-            const int left = (int)min(p.vocab - n0, 32ll);
+      // This warp's half of the columns, 32 at a time, the next 32 on their way while these are worked on.  The
+      // accumulator is free again when the last are in registers.
+      const int chunks = MODE == GRADS ? BNH / 32 : p.bn / 64, first = half * (MODE == GRADS ? BNH : p.bn / 2);
+      bool busy = row0 < p.rows;
+      int row_at = row0;
+      bool sums = false;
+      if (MODE == GRADS) {
+        if (cur.dw) row_at += (int)p.v0;
+        // a part without k-blocks (of a last piece that is short) has nothing to add
+        busy = (cur.dw ? p.v0 + row0 < p.vocab : busy) && cur.num_kb > 0;
+        sums = !cur.dw && p.out_kind != 0;
+      }
+      const CUtensorMap *map = MODE == GRADS && cur.dw ? &p.out2 : &p.out;
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(acce(acc), 0));
+      };
+      if (!busy) release();
+      Stats stats;
+      uint32_t v[2][32], wo[32];
+      if (busy) {
+        const float ref = -hr.lse * kLog2e;
+        tmem_ld32_issue(taddr + (uint32_t)first, v[0]);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) z[c] = c < left ? __uint_as_float(v[c]) : -INFINITY;
-            const long long hit = target - n0;
+        for (int ch = 0; ch < BNH / 32; ++ch) {
+          if (ch >= chunks) break;
+          uint32_t (&z)[32] = v[ch & 1];
+          tmem_wait(z);
+          if (ch + 1 < chunks) tmem_ld32_issue(taddr + (uint32_t)(first + 32 * (ch + 1)), v[(ch + 1) & 1]);
+          else release();
+          const int col0 = cur.tn * (MODE == GRADS ? BN : p.bn) + first + 32 * ch;   // of z's piece, or of hidden
+          if (MODE == STATS) {
+            const int left = (int)max(0ll, min(p.vocab - col0, 32ll));
+            if (left == 0) continue;
+            if (left < 32)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i >= left) z[i] = __float_as_uint(-INFINITY);
+            const long long hit = target - col0;
             if (__any_sync(0xffffffffu, hit >= 0 && hit < left)) {
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (hit == c && c < left) p.target_logit[row] = z[c];
+              for (int i = 0; i < 32; ++i)
+                if (hit == i && i < left) p.target_logit[row] = __uint_as_float(z[i]);
             }
-            float most = z[0];
+            stats.add(z);
+          } else if (MODE == DLOGITS) {
+            // rows that take no part have g = 0 and finite z (x's copy holds zeros there)
+            float d[32];
+            const f32x2 scale = pair(kLog2e, kLog2e), r2 = pair(ref, ref);
 #pragma unroll
-            for (int c = 1; c < 32; ++c) most = fmaxf(most, z[c]);
-            if (most > m) {
-              s *= ex2((m - most) * kLog2e);   // m = -inf: s is 0, and so is the factor
-              m = most;
-            }
-            // a NaN, +inf or a whole chunk of -inf makes the differences NaN, and the row's sum with them
-            float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              s0 += ex2((z[c] - m) * kLog2e);
-              s1 += ex2((z[c + 1] - m) * kLog2e);
-            }
-            s += s0 + s1;
-          }
-          if (row < p.rows) p.parts[((long long)cur.tn * 2 + half) * p.rows + row] = make_float2(m, s);
-        }
-      } else if (MODE == DLOGITS) {
-        if (row0 < p.rows) {
-#pragma unroll 1
-          for (int cc = half * (p.bn / 2); cc < (half + 1) * (p.bn / 2); cc += 64) {
-            const int col0 = cur.tn * p.bn + cc;     // in the piece
-            uint32_t lo[32], hi[32], wo[32];
-            tmem_ld64(taddr + (uint32_t)cc, lo, hi);
-            const int left = (int)max(0ll, min(p.vocab - p.v0 - col0, 64ll));
-            float d[64];
-#pragma unroll
-            for (int c = 0; c < 64; ++c) {
-              const float z = __uint_as_float(c < 32 ? lo[c & 31] : hi[c & 31]);
-              d[c] = hr.g * ex2((z - hr.lse) * kLog2e);
+            for (int i = 0; i < 32; i += 2) {
+              const float2 e = split(fma2(pair(__uint_as_float(z[i]), __uint_as_float(z[i + 1])), scale, r2));
+              d[i] = hr.g * ex2(e.x);
+              d[i + 1] = hr.g * ex2(e.y);
             }
             const int hit = hr.target < 0 ? -1 : (int)(hr.target - p.v0) - col0;
-            if (__any_sync(0xffffffffu, hit >= 0 && hit < 64)) {
+            if (__any_sync(0xffffffffu, hit >= 0 && hit < 32)) {
 #pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (hit == c) d[c] -= hr.hit;
+              for (int i = 0; i < 32; ++i)
+                if (hit == i) d[i] -= hr.hit;
             }
-            // a row that takes no part, whatever its z are, and columns past the vocabulary
-            const int keep = hr.target < 0 ? 0 : left;
+            const long long left = p.vocab - p.v0 - col0;
+            if (left < 32)
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              wo[c] = pack_bf16(2 * c < keep ? d[2 * c] : 0.f, 2 * c + 1 < keep ? d[2 * c + 1] : 0.f);
-            out.put(wo, &p.out, lane, col0, row0, 0, p.err);
-          }
-        }
-      } else {
-        const long long rows_m = cur.dw ? p.vocab - p.v0 : p.rows;
-        // a part without k-blocks (of a last piece that is short) has nothing to add
-        if (row0 < rows_m && cur.num_kb > 0) {
-          const bool sums = !cur.dw && p.out_kind != 0;
-          const CUtensorMap *map = cur.dw ? &p.out2 : &p.out;
-          const int row_at = row0 + (cur.dw ? (int)p.v0 : 0);
-#pragma unroll 1
-          for (int cc = half * 128; cc < half * 128 + 128; cc += 64) {
-            const int col0 = cur.tn * BN + cc;
-            if (col0 >= p.hidden) break;
-            uint32_t lo[32], hi[32];
-            tmem_ld64(taddr + (uint32_t)cc, lo, hi);
-            if (sums) {
-              put_sums(out, lo, map, p.out_kind == 2, lane, col0, row_at, cur.part, p.err);
-              if (col0 + 32 < p.hidden)
-                put_sums(out, hi, map, p.out_kind == 2, lane, col0 + 32, row_at, cur.part, p.err);
-            } else {
-              uint32_t wo[32];
+              for (int i = 0; i < 32; ++i)
+                if (i >= left) d[i] = 0.f;
 #pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                wo[c] = pack_bf16(__uint_as_float(lo[2 * c]), __uint_as_float(lo[2 * c + 1]));
-                wo[16 + c] = pack_bf16(__uint_as_float(hi[2 * c]), __uint_as_float(hi[2 * c + 1]));
-              }
-              out.put(wo, map, lane, col0, row_at, 0, p.err);
-            }
+            for (int i = 0; i < 16; ++i) wo[(ch & 1) * 16 + i] = pack_bf16(d[2 * i], d[2 * i + 1]);
+            if (ch & 1) out.put(wo, map, lane, col0 - 32, row0, 0, p.err);
+          } else if (sums) {
+            if (col0 < p.hidden) put_sums(out, z, map, p.out_kind == 2, lane, col0, row_at, cur.part, p.err);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              wo[(ch & 1) * 16 + i] = pack_bf16(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1]));
+            if ((ch & 1) && col0 - 32 < p.hidden) out.put(wo, map, lane, col0 - 32, row_at, 0, p.err);
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(map_to_rank(acce(acc), 0));
+      if (MODE == STATS && row < p.rows)
+        p.parts[((long long)cur.tn * 2 + half) * p.rows + row] = make_float2(stats.c, stats.s);
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
@@ -635,11 +684,11 @@ HeadPlan head_plan(const HeadShape &h, bool need_dx, bool need_dw) {
   return plan;
 }
 
-int head_dlogits(const HeadShape &h, const HeadPlan &plan, int64_t v0, const void *x, int64_t ldx, const void *w,
+int head_dlogits(const HeadShape &h, const HeadPlan &plan, int64_t v0, const void *xc, int64_t xc_cols, const void *w,
                  const HeadRow *row, void *d, cudaStream_t s) {
   Args p{};
   p.bn = columns(h, plan.width(), 128);
-  HEAD_TRY(map_rows(p, x, h.rows, h.hidden, ldx));
+  HEAD_TRY(map_rows(p, xc, h.rows, h.hidden, xc_cols));
   HEAD_TRY(make_map(&p.b, w, 1, h.vocab, h.hidden, p.bn / 2));
   HEAD_TRY(make_map(&p.out, d, 1, h.rows, plan.width(), 32));
   p.rows = h.rows;
