@@ -661,11 +661,13 @@ int head_stats(const HeadShape &h, const void *x, int64_t ldx, const void *w, co
   return launch<STATS>(p, (int64_t)p.tiles_m * p.tiles_n, kTraceHeadStats, s);
 }
 
-// A piece is at most as wide as makes d 128 MB (or 8192 columns, which keep the additions to dx's sums cheap),
-// and of those widths from three quarters of that on the one that leaves the least of the last wave empty.
+// A piece is at most as wide as makes d 256 MB (16384 columns of many rows: few additions to dx's sums, few last
+// waves), and of those widths from three quarters of that on the one that leaves the least of the last wave empty.
+// With 64, 128, 256 and 512 MB: 4096 rows of 6144 over 64000 entries 5.39, 5.24, 5.18, 5.10 ms; 16384 of 2048 over
+// 40003 4.57, 4.55, 4.58, 4.31 ms; 4096 of 512 over 50003 562, 502, 465, 438 us.
 HeadPlan head_plan(const HeadShape &h, bool need_dx, bool need_dw) {
   const int64_t all = cdiv(h.vocab, CM), tm = cdiv(h.rows, CM), pairs = pairs_of_sms();
-  const int64_t most = std::min(all, std::max<int64_t>(32, (int64_t(128) << 20) / (h.rows * CM * 2)));
+  const int64_t most = std::min(all, std::max<int64_t>(64, (int64_t(256) << 20) / (h.rows * CM * 2)));
   HeadPlan plan{most, 1, 1};
   if (most < all) {
     double best = 0;
@@ -676,10 +678,12 @@ HeadPlan head_plan(const HeadShape &h, bool need_dx, bool need_dw) {
     plan.pieces = cdiv(all, plan.piece_tiles);
   }
   if (need_dx) {
-    // a dx tile no longer than a pair's share of the whole
+    // a dx tile no longer than half a pair's share of the whole (4 rows of 6144 over 64000 entries 439 us, 508 with
+    // tiles of a whole share; 4096 of 512 over 50003 432 and 465)
     const int64_t th = cdiv(h.hidden, BN), kb = plan.piece_tiles * (CM / BK);
     const int64_t work = tm * th * kb + (need_dw ? plan.piece_tiles * th * (cdiv(h.rows, BK) + 4) : 0);
-    plan.splits = (int)std::clamp<int64_t>(kb * pairs / std::max<int64_t>(work, 1), 1, std::min<int64_t>(16, std::max<int64_t>(1, kb / 8)));
+    plan.splits = (int)std::clamp<int64_t>(2 * kb * pairs / std::max<int64_t>(work, 1), 1,
+                                         std::min<int64_t>(16, std::max<int64_t>(1, kb / 8)));
   }
   return plan;
 }

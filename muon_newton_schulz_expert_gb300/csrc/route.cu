@@ -18,6 +18,7 @@
 // bound, and not equal logits with equal biases, the choice is made again from keys in
 // 64 bits: of the candidates only (sigmoid: a key needs its own logit), or of the whole
 // row (softmax, whose sum needs every logit).
+#include <limits.h>
 #include <math.h>
 
 #include <algorithm>
@@ -292,6 +293,134 @@ __global__ void __launch_bounds__(kThreads, R <= 12 ? 5 : R <= 16 ? 4 : 3) route
   }
 }
 
+// Few experts: a row for every L lanes of a warp, R values each, and k rounds of the L lanes' maximum, whose winner
+// looks at its R values again.  65536 rows of 64 bf16, softmax, top 6: 14 us, 20 us with a warp a row; of 16 fp32, top
+// 2, 7.5 and 16 us; of 128, top 8, in 16 lanes 34 and 27 us, so those take a warp.
+template <int L>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+#pragma unroll
+  for (int o = L / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ int group_min(int v) {
+#pragma unroll
+  for (int o = L / 2; o; o >>= 1) v = min(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float group_max(float v) {   // a NaN counts for nothing
+#pragma unroll
+  for (int o = L / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+// 0 for -inf (never chosen), the largest for NaN
+__device__ __forceinline__ uint32_t whole_order_of(float v) {
+  return v == -INFINITY ? 0u : v != v ? 0xffffffffu : order_of(v);
+}
+
+template <typename T, int L, int R, bool BIAS>
+__global__ void __launch_bounds__(kThreads) route_few_kernel(const Args p) {
+  const int lane = threadIdx.x & 31, me = lane & (L - 1);
+  const int64_t first = (blockIdx.x * (int64_t)kWarps + (threadIdx.x >> 5)) * (32 / L);   // the warp's first row
+  if (first >= p.rows) return;   // a warp together
+  const int64_t row = min(first + lane / L, p.rows - 1);   // groups behind the last row do it again
+  const T *x = static_cast<const T *>(p.logits) + row * p.stride;
+  uint32_t key[R];
+  float m = -INFINITY, sum = 1.f;
+  {
+    float v[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) v[i] = i * L + me < p.experts ? to_f(x[i * L + me]) : -INFINITY;
+    if (p.softmax && (BIAS || !p.normalize)) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) m = fmaxf(m, v[i]);
+      m = group_max<L>(m);
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < R; ++i) sum += v[i] == -INFINITY ? 0.f : fast_exp(v[i] - m);
+      sum = group_sum<L>(sum);
+    }
+    const float inv = 1.f / sum;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (BIAS && v[i] != -INFINITY)
+        v[i] = (p.softmax ? fast_exp(v[i] - m) * inv : fast_inverse(1.f + fast_exp(-v[i]))) +
+               __ldg(p.bias + i * L + me);
+      key[i] = whole_order_of(v[i]);
+    }
+  }
+  const float eps = p.softmax ? 0x1p-19f / sum : 0x1p-20f;   // as above
+  uint32_t best = 0u;
+  int at = 0;
+  auto look = [&] {
+    best = 0u;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (key[i] > best) best = key[i], at = i;
+  };
+  look();
+  int mine = -1, last_e = -1;   // the group's j-th lane: its j-th expert
+  float last = 0.f;
+  bool unsure = false;
+  for (int j = 0; j < p.top + (BIAS ? 1 : 0); ++j) {
+    const uint32_t k = group_max<L>(best);
+    const int e = group_min<L>(best == k ? at * L + me : INT_MAX);
+    if (BIAS) {
+      const float v = value_of(k);
+      if (j > 0 && k && last - v <= 2.f * eps + (fabsf(last) + fabsf(v)) * 0x1p-23f)
+        unsure = unsure || to_f(x[last_e]) != to_f(x[e]) || __ldg(p.bias + last_e) != __ldg(p.bias + e);
+      last = v, last_e = k ? e : last_e;
+    }
+    if (me == j && k && j < p.top) mine = e;
+    if (best == k && at * L + me == e) {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (i == at) key[i] = 0u;
+      look();
+    }
+  }
+  if (BIAS) {
+    // the rows that are not sure of their order, one after the other by the whole warp
+    unsigned rows = __ballot_sync(kAll, unsure);
+    while (rows) {
+      const int group = (__ffs(rows) - 1) / L;
+      const T *xr = static_cast<const T *>(p.logits) + min(first + group, p.rows - 1) * p.stride;
+      const int e = choose_in_64<T, (L * R + 31) / 32>(xr, p.bias, p.experts, p.top, p.softmax);
+      const int of = __shfl_sync(kAll, e, me);
+      if (lane / L == group) mine = me < p.top ? of : -1;
+      rows &= ~(((1u << (L - 1) << 1) - 1u) << (group * L));
+    }
+  }
+  float s = 0.f;
+  const float c = mine >= 0 ? to_f(x[mine]) : -INFINITY;
+  if (p.softmax) {
+    if (p.normalize) {
+      m = group_max<L>(c);
+      // a NaN or +inf that was not chosen is in the choice's sum all the same
+      s = mine < 0 ? 0.f : BIAS && sum != sum ? sum : expf(c - m);
+    } else {
+      s = mine >= 0 ? expf(c - m) / sum : 0.f;
+    }
+  } else if (mine >= 0) {
+    s = sigmoid(c);
+  }
+  if (p.normalize) {
+    const float total = group_sum<L>(s);
+    s = total == 0.f ? 0.f : s / total;   // sigmoids that are all 0 in fp32
+  }
+  if (me < p.top && first + lane / L < p.rows) {
+    p.ids[row * p.top + me] = mine;
+    p.weights[row * p.top + me] = p.scale * s;
+  }
+}
+
 // ---------------------------------------------------------------------------- gradient
 //   with g_i = scale dw_i, and for a normalised call share_i = s_i / sum of the chosen s:
 //   softmax, normalised:  dx_i = share_i h_i;         h_i = sum_j share_j (g_i - g_j)
@@ -315,39 +444,43 @@ struct BwdArgs {
   unsigned *err;
 };
 
-template <typename T, int R>
+// A row for every L lanes, R values each (L below 32 for few experts: 30001 rows of 61, softmax, top 6, 7.4 us,
+// 12.3 us with a warp a row).
+template <typename T, int L, int R>
 __global__ void __launch_bounds__(kThreads) route_backward_kernel(const BwdArgs p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = blockIdx.x * (int64_t)kWarps + (threadIdx.x >> 5);
-  if (row >= p.rows) return;   // a warp together
+  const int lane = threadIdx.x & 31, me = lane & (L - 1);
+  const int64_t first_row = (blockIdx.x * (int64_t)kWarps + (threadIdx.x >> 5)) * (32 / L);
+  if (first_row >= p.rows) return;   // a warp together
+  const bool in = first_row + lane / L < p.rows;
+  const int64_t row = in ? first_row + lane / L : p.rows - 1;
   const T *x = static_cast<const T *>(p.logits) + row * p.stride;
   int id = -1;
   float g = 0.f, c = -INFINITY;
-  if (lane < p.top) {
-    const int64_t v = p.ids[row * p.top + lane];
+  if (in && me < p.top) {
+    const int64_t v = p.ids[row * p.top + me];
     if (v >= p.experts) atomicOr(p.err, kErrDevice);
     else if (v >= 0) id = (int)v;
-    if (id >= 0) g = p.scale * p.dweights[row * p.top + lane], c = to_f(x[id]);
+    if (id >= 0) g = p.scale * p.dweights[row * p.top + me], c = to_f(x[id]);
   }
   // the warp's row of the gradient where slots meet it: first which experts are chosen, then what is added there
-  __shared__ float slots[kWarps][R * 32];
-  float *at = slots[threadIdx.x >> 5];
+  __shared__ float slots[kThreads / L][R * L];
+  float *at = slots[threadIdx.x / L];
 #pragma unroll
-  for (int i = 0; i < R; ++i) at[i * 32 + lane] = 0.f;
+  for (int i = 0; i < R; ++i) at[i * L + me] = 0.f;
   __syncwarp();
   float out[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) out[i] = 0.f;
   // the slots of this lane's expert; the first of them stands for it
-  const unsigned same = __match_any_sync(kAll, id >= 0 ? id : -1 - lane);
+  const unsigned same = __match_any_sync(kAll, id >= 0 ? lane / L << 16 | id : -1 - lane);
   const bool first = id >= 0 && (same & ((1u << lane) - 1u)) == 0u;
   const bool twice = __any_sync(kAll, (same & (same - 1u)) != 0u);
   auto added = [&](float v) {              // the sum of v over an expert's slots, for the first of them
     if (!twice) return v;
     float s = 0.f;
     for (int j = 0; j < p.top; ++j) {
-      const float o = __shfl_sync(kAll, v, j);
-      if (same >> j & 1u) s += o;
+      const float o = __shfl_sync(kAll, v, j, L);
+      if (same >> (lane - me + j) & 1u) s += o;
     }
     return s;
   };
@@ -356,27 +489,27 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const BwdArgs 
   if (!p.softmax && !p.normalize) {
     if (id >= 0) value = g * sigmoid(c) * (1.f / (1.f + expf(c)));
   } else if (!whole) {
-    const float m = p.softmax ? warp_max(c) : 0.f;
+    const float m = p.softmax ? group_max<L>(c) : 0.f;
     const float s = id < 0 || c == -INFINITY ? 0.f : p.softmax ? expf(c - m) : sigmoid(c);
-    const float total = warp_sum(s), share = total == 0.f ? 0.f : s / total;
+    const float total = group_sum<L>(s), share = total == 0.f ? 0.f : s / total;
     float h = 0.f;
-    for (int j = 0; j < p.top; ++j) h = fmaf(__shfl_sync(kAll, share, j), g - __shfl_sync(kAll, g, j), h);
+    for (int j = 0; j < p.top; ++j) h = fmaf(__shfl_sync(kAll, share, j, L), g - __shfl_sync(kAll, g, j, L), h);
     if (id >= 0) value = share * h * (p.softmax ? 1.f : 1.f / (1.f + expf(c)));
   } else {
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      out[i] = i * 32 + lane < p.experts ? to_f(x[i * 32 + lane]) : -INFINITY;
+      out[i] = i * L + me < p.experts ? to_f(x[i * L + me]) : -INFINITY;
       m = fmaxf(m, out[i]);
     }
-    m = warp_max(m);
+    m = group_max<L>(m);
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       out[i] = out[i] == -INFINITY ? 0.f : expf(out[i] - m);
       sum += out[i];
     }
-    sum = warp_sum(sum);
+    sum = group_sum<L>(sum);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;   // a row with nothing but -inf
     const float d = added(g);              // slots of one expert count as one, with their g added
     if (first) at[id] = 1.f;
@@ -384,43 +517,47 @@ __global__ void __launch_bounds__(kThreads) route_backward_kernel(const BwdArgs 
     const float pr = id < 0 || c == -INFINITY ? 0.f : expf(c - m) * inv;
     const float pf = first ? pr : 0.f;
     float all = pr * g;                    // G, a slot's share
-    all = warp_sum(all);
+    all = group_sum<L>(all);
     float rest = 0.f;                      // the p of the experts that were not chosen
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      out[i] = at[i * 32 + lane] == 0.f ? out[i] * inv : 0.f;
+      out[i] = at[i * L + me] == 0.f ? out[i] * inv : 0.f;
       rest += out[i];
       out[i] *= -all;
     }
     __syncwarp();
-    rest = warp_sum(rest);
+    rest = group_sum<L>(rest);
     float h = d * rest;
-    for (int j = 0; j < p.top; ++j) h = fmaf(__shfl_sync(kAll, pf, j), d - __shfl_sync(kAll, d, j), h);
+    for (int j = 0; j < p.top; ++j) h = fmaf(__shfl_sync(kAll, pf, j, L), d - __shfl_sync(kAll, d, j, L), h);
     if (first) value = pr * h;
   }
   if (!whole) value = added(value);
   if (first) at[id] = value;               // 0 elsewhere, but for `whole` where each chosen expert has its own
   __syncwarp();
 #pragma unroll
-  for (int i = 0; i < R; ++i) out[i] += at[i * 32 + lane];
+  for (int i = 0; i < R; ++i) out[i] += at[i * L + me];
   T *o = static_cast<T *>(p.dlogits) + row * p.out_stride;
   __syncwarp();   // dlogits may be the logits: every lane has read its own
 #pragma unroll
   for (int i = 0; i < R; ++i)
-    if (i * 32 + lane < p.experts) from_f(o + i * 32 + lane, out[i]);
+    if (in && i * L + me < p.experts) from_f(o + i * L + me, out[i]);
 }
 
-// calls f with the values a lane holds: the least of kPerLane that cover the row
+// Calls f with the lanes of a row and the values of a lane.  8 lanes for few experts (figures above); each holds one of
+// the row's choices, so 8 of those at most.
 template <typename F>
-void per_lane(int experts, F &&f) {
-  const int n = (experts + 31) / 32;
-  if (n <= 1) f(std::integral_constant<int, 1>());
-  else if (n <= 2) f(std::integral_constant<int, 2>());
-  else if (n <= 4) f(std::integral_constant<int, 4>());
-  else if (n <= 8) f(std::integral_constant<int, 8>());
-  else if (n <= 12) f(std::integral_constant<int, 12>());
-  else if (n <= 16) f(std::integral_constant<int, 16>());
-  else f(std::integral_constant<int, 32>());
+void lanes_of_a_row(int experts, int top, F &&f) {
+  constexpr std::integral_constant<int, 8> few{};
+  constexpr std::integral_constant<int, 32> warp{};
+  if (top <= 8 && experts <= 16) f(few, std::integral_constant<int, 2>());
+  else if (top <= 8 && experts <= 32) f(few, std::integral_constant<int, 4>());
+  else if (top <= 8 && experts <= 64) f(few, std::integral_constant<int, 8>());
+  else if (experts <= 64) f(warp, std::integral_constant<int, 2>());
+  else if (experts <= 128) f(warp, std::integral_constant<int, 4>());
+  else if (experts <= 256) f(warp, std::integral_constant<int, 8>());
+  else if (experts <= 384) f(warp, std::integral_constant<int, 12>());
+  else if (experts <= 512) f(warp, std::integral_constant<int, 16>());
+  else f(warp, std::integral_constant<int, 32>());
 }
 
 bool bad_type(int t) { return t != MUON_BF16 && t != MUON_F32; }
@@ -446,17 +583,22 @@ int muon_route(const void *logits, int64_t stride, const float *bias, int64_t ro
   const Args a{logits, stride, bias, rows, (int)experts, top, score == MUON_SCORE_SOFTMAX, normalize != 0, scale, ids,
                weights};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned blocks = (unsigned)((rows + kWarps - 1) / kWarps);
   trace_before(kTraceRoute, s);
-  per_lane((int)experts, [&](auto r) {
-    constexpr int R = decltype(r)::value;
-    if (type == MUON_BF16) {
-      if (bias) route_kernel<__nv_bfloat16, R, true><<<blocks, kThreads, 0, s>>>(a);
-      else route_kernel<__nv_bfloat16, R, false><<<blocks, kThreads, 0, s>>>(a);
-    } else {
-      if (bias) route_kernel<float, R, true><<<blocks, kThreads, 0, s>>>(a);
-      else route_kernel<float, R, false><<<blocks, kThreads, 0, s>>>(a);
-    }
+  lanes_of_a_row((int)experts, top, [&](auto l, auto r) {
+    constexpr int L = decltype(l)::value, R = decltype(r)::value;
+    const unsigned blocks = (unsigned)((rows + kThreads / L - 1) / (kThreads / L));
+    auto run = [&](auto element, auto with_bias) {
+      typedef decltype(element) T;
+      constexpr bool BIAS = decltype(with_bias)::value;
+      if constexpr (L == 32) route_kernel<T, R, BIAS><<<blocks, kThreads, 0, s>>>(a);
+      else route_few_kernel<T, L, R, BIAS><<<blocks, kThreads, 0, s>>>(a);
+    };
+    auto with = [&](auto element) {
+      if (bias) run(element, std::true_type());
+      else run(element, std::false_type());
+    };
+    if (type == MUON_BF16) with(__nv_bfloat16());
+    else with(float());
   });
   return trace_after(kTraceRoute, s);
 }
@@ -477,12 +619,12 @@ int muon_route_backward(const float *dweights, const void *logits, int64_t strid
                   scale, dlogits, dlogits_stride, device_error_word()};
   if (!a.err) return MUON_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned blocks = (unsigned)((rows + kWarps - 1) / kWarps);
   trace_before(kTraceRouteBwd, s);
-  per_lane((int)experts, [&](auto r) {
-    constexpr int R = decltype(r)::value;
-    if (type == MUON_BF16) route_backward_kernel<__nv_bfloat16, R><<<blocks, kThreads, 0, s>>>(a);
-    else route_backward_kernel<float, R><<<blocks, kThreads, 0, s>>>(a);
+  lanes_of_a_row((int)experts, top, [&](auto l, auto r) {
+    constexpr int L = decltype(l)::value, R = decltype(r)::value;
+    const unsigned blocks = (unsigned)((rows + kThreads / L - 1) / (kThreads / L));
+    if (type == MUON_BF16) route_backward_kernel<__nv_bfloat16, L, R><<<blocks, kThreads, 0, s>>>(a);
+    else route_backward_kernel<float, L, R><<<blocks, kThreads, 0, s>>>(a);
   });
   return trace_after(kTraceRouteBwd, s);
 }
