@@ -7,12 +7,11 @@
 //
 // One kernel, instantiated for the three; persistent CTA pairs on output tiles of
 // 256 x up to 256 (tcgen05.mma.cta_group::2, M = 256, K = 16, bf16 operands, fp32
-// accumulation in TMEM), fed by TMA through a ring of three stages of two k-blocks
-// of 64.
+// accumulation in TMEM), fed by TMA through a ring of k-blocks of 64.
 //
 // Rows of x are on M, the vocabulary on N: a thread of the epilogue then holds 32
 // columns of one row at a time, so the softmax's maximum and sum need no exchange
-// between threads; each half of a tile's columns leaves one (m, s) per row.  Tiles
+// between threads but at a tile's end, where one (c, s) per row is left.  Tiles
 // walk the vocabulary with the row tiles of a group fastest, a group being as many row
 // tiles as keep their x in L2 (kGroupBytes), so that W is read once per group.
 // With few tiles N is 128 or 64, so that more pairs of CTAs have one.
@@ -25,8 +24,8 @@
 // Rounding: d is stored in bf16, the operand type of the products that read it, once
 // (the feed-forward products round h, dg and du the same way); the rest is fp32.
 //
-// Roles per CTA (320 threads): warp 0 TMA producer, warp 1 MMA issuer (even CTA) and
-// TMEM owner, warps 2..9 epilogue.  Two accumulators, so that the epilogue of one tile
+// Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (even CTA) and TMEM owner, the
+// others (8, in STATS 16) epilogue.  Two accumulators, so that the epilogue of one tile
 // overlaps the next tile's products.  Every wait is bounded (tc.cuh).
 #include <math.h>
 
@@ -44,21 +43,29 @@ constexpr int UMMA_K = 16;
 constexpr int A_STAGE = BM * BK * 2;
 constexpr int B_STAGE = BNH * BK * 2;
 constexpr int KB_BYTES = A_STAGE + B_STAGE;
-constexpr int STAGES = 3, KSUB = 2;
-constexpr int STAGE_BYTES = KSUB * KB_BYTES;
-constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int ACC_COLS = BN;
 constexpr int TMEM_COLS = 2 * ACC_COLS;
-constexpr int NFULL = STAGES * KSUB;
-constexpr int NUM_BARS = NFULL + STAGES + 5;
-constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * BOX_BYTES + NUM_BARS * 8 + 16;
-static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+constexpr int MAX_STAGES = 16;      // of the ring, whose stages are as many as fit (Args)
+
+enum Mode { STATS = 0, DLOGITS, GRADS };
+
+// Shared memory of a mode: the ring of k-blocks (stages of KSUB), and what the epilogue's warps need.
+template <int MODE>
+struct Form {
+  static constexpr int KSUB = 2;
+  // STATS has 16 warps, 4 on each scheduler: a warp's work on a tile is a chain of latencies
+  static constexpr int EPI_WARPS = MODE == STATS ? 16 : 8;
+  static constexpr int BOXES = 1;   // staging boxes of a warp
+  static constexpr int RING_BYTES = 6 * KB_BYTES;
+  static constexpr int EPI_BYTES = MODE == STATS ? 2 * 4 * BM * (int)sizeof(float2) : EPI_WARPS * BOXES * BOX_BYTES;
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int NUM_BARS = MAX_STAGES * KSUB + MAX_STAGES + 5;
+  static constexpr int SMEM_BYTES = 1024 + RING_BYTES + EPI_BYTES + NUM_BARS * 8 + 16;
+  static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+};
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int64_t kGroupBytes = 48 << 20;   // of x that is used again and again, beside W's stream through 129 MB of L2
-
-enum Mode { STATS = 0, DLOGITS, GRADS };
 
 // GRADS: dx's tiles (`longs` of them) and then dW's (`shorts`), dealt to the pairs one after the
 // other.  Where dx's do not come out even, the pairs without the last one take `extra` of dW's
@@ -89,11 +96,13 @@ struct Args {
   CUtensorMap a_last;      // a by boxes of the rows that the last CTA with any has
   CUtensorMap a2, b2;      // GRADS: dW's d and x, MN-major
   CUtensorMap out, out2;   // DLOGITS: d;  GRADS: dx or its sums, and dW
-  long long rows, vocab, v0;
+  int rows, vocab, v0;     // vocab: entries from v0 on
   int hidden;
   int kblocks, kblocks2;   // of K;  GRADS: of dx's K (the piece) and of dW's (the rows)
   int tiles_m, tiles_n;    // row tiles and vocabulary tiles (of bn);  GRADS: row tiles and tiles of H
   int bn, group;           // columns of a tile, row tiles of a group
+  int step_n, step_r;      // STATS, DLOGITS: a step of the number of pairs, in vocabulary tiles and row tiles of a group
+  int stages, a_bytes;     // of the ring; of A in a k-block (less than A_STAGE where there are few rows)
   int tiles_v, splits;     // GRADS: vocabulary tiles of the piece, parts of dx's K
   Schedule schedule;
   bool wide;               // GRADS: W's 128 columns load in one piece
@@ -106,55 +115,69 @@ struct Args {
   unsigned long long timeout_ns;
 };
 
-// A tile: its places on M and N in tiles, first k-block and their number.
+// A pair's tiles, one after the other: places on M and N in tiles, first k-block and their number.
 template <int MODE>
-struct Tile {
+struct Walk {
   int tm, tn, kb0 = 0, num_kb;
   int part = 0;       // GRADS, dx: of a cut sum
   bool dw = false;    // GRADS: a tile of dW (M = the piece's vocabulary entries, N = H)
+  int i = 0, group = 0, r = -1, gm = 0;
 
-  __device__ Tile(const Args &p, int t) {
-    if (MODE != GRADS) {
-      const int per = p.group * p.tiles_n, g = t / per, r = t - g * per;
-      const int gm = min(p.group, p.tiles_m - g * p.group);
-      tn = r / gm;
-      tm = g * p.group + (r - tn * gm);
-      num_kb = p.kblocks;
-      return;
+  // the next tile of this pair, or false.  STATS, DLOGITS: tile tn * gm + r of the group's gm row tiles; moving on by
+  // the number of pairs takes no division (with one in each step, and 64-bit places, a STATS epilogue took 4250
+  // cycles whatever K was).
+  __device__ __forceinline__ bool next(const Args &p) {
+    const int c = (int)(blockIdx.x >> 1), ncl = (int)(gridDim.x >> 1);
+    if (MODE == GRADS) {
+      int t = p.schedule.tile(i++, c, ncl);
+      if (t < 0) return false;
+      dw = t >= p.schedule.longs;
+      kb0 = 0;
+      if (dw) {
+        t -= p.schedule.longs;
+        tm = t / p.tiles_n;
+        tn = t - tm * p.tiles_n;
+        num_kb = p.kblocks2;
+      } else {
+        const int per = p.tiles_m * p.tiles_n;
+        part = t / per;
+        t -= part * per;
+        tm = t / p.tiles_n;
+        tn = t - tm * p.tiles_n;
+        kb0 = (int)((long long)p.kblocks * part / p.splits);
+        num_kb = (int)((long long)p.kblocks * (part + 1) / p.splits) - kb0;
+      }
+      return true;
     }
-    dw = t >= p.schedule.longs;
-    if (dw) {
-      t -= p.schedule.longs;
-      tm = t / p.tiles_n;
-      tn = t - tm * p.tiles_n;
-      num_kb = p.kblocks2;
+    int step = ncl;
+    if (r < 0) {
+      gm = min(p.group, p.tiles_m), tn = 0, r = 0, step = c, num_kb = p.kblocks;
+    }
+    if (gm == p.group) {   // as the host divided it
+      tn += step == ncl ? p.step_n : step / gm;
+      r += step == ncl ? p.step_r : step % gm;
     } else {
-      const int per = p.tiles_m * p.tiles_n;
-      part = t / per;
-      t -= part * per;
-      tm = t / p.tiles_n;
-      tn = t - tm * p.tiles_n;
-      kb0 = (int)((long long)p.kblocks * part / p.splits);
-      num_kb = (int)((long long)p.kblocks * (part + 1) / p.splits) - kb0;
+      tn += step / gm, r += step % gm;
     }
+    if (r >= gm) r -= gm, ++tn;
+    while (tn >= p.tiles_n) {
+      // the rest of the step is in the next group
+      const int over = (tn - p.tiles_n) * gm + r;
+      group += p.group;
+      if (group >= p.tiles_m) return false;
+      gm = min(p.group, p.tiles_m - group);
+      tn = over / gm;
+      r = over - tn * gm;
+    }
+    tm = group + r;
+    return true;
   }
 };
 
 // Rows of an operand K-major on M (x, or dx's d) that a CTA loads from its first one on: there is nothing to load
 // behind the last row, and rows that are not loaded leave the others' results as they are.  (With whole boxes, of
 // zeros behind the end, one row of 6144 over 128000 entries took 418 us, 128 rows 274.)
-__device__ __forceinline__ int rows_from(long long rows, int first) {
-  return (int)max(0ll, min(rows - first, (long long)BM));
-}
-
-// the i-th tile of this pair, or -1
-template <int MODE>
-__device__ __forceinline__ int tile_of(const Args &p, int i) {
-  const int c = (int)(blockIdx.x >> 1), ncl = (int)(gridDim.x >> 1);
-  if (MODE == GRADS) return p.schedule.tile(i, c, ncl);
-  const long long t = (long long)i * ncl + c;
-  return t < (long long)p.tiles_m * p.tiles_n ? (int)t : -1;
-}
+__device__ __forceinline__ int rows_from(int rows, int first) { return max(0, min(rows - first, BM)); }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -198,32 +221,58 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&v)[32]) {
 }
 
 // Running softmax statistics of a row in powers of two: s = sum 2^(z log2(e) - c).  c is a whole number, so that
-// z log2(e) - c is one fused operation whose reference has no rounding, and moves up to the largest logit's.
+// z log2(e) - c is one fused operation whose reference has no rounding.
 struct Stats {
   float c = -INFINITY, s = 0.f;
 
+  // 32 columns with c as it is: right while no term passes 2^100, so that c need not be the largest logit's, any of
+  // the row's will do, and no maximum is looked for.
+  __device__ __forceinline__ float terms(const uint32_t (&v)[32]) const {
+    const f32x2 scale = pair(kLog2e, kLog2e), ref = pair(-c, -c);
+    f32x2 a[4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 p = split(fma2(pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), scale, ref));
+      const f32x2 e = pair(ex2(p.x), ex2(p.y));
+      a[i & 3] = i < 4 ? e : add2(a[i & 3], e);
+    }
+    const float2 r = split(add2(add2(a[0], a[1]), add2(a[2], a[3])));
+    return r.x + r.y;
+  }
   __device__ __forceinline__ void add(const uint32_t (&v)[32]) {
+    if (c == -INFINITY) c = ceilf(__uint_as_float(v[0]) * kLog2e);
+    const float more = terms(v);
+    if (more < 0x1p100f) {
+      s += more;
+    } else {
+      uint32_t copy[32];   // its address is taken, and registers have none
+#pragma unroll
+      for (int i = 0; i < 32; ++i) copy[i] = v[i];
+      *this = add_any(*this, copy);
+    }
+  }
+  // s between 1 and 2
+  __device__ __forceinline__ void normalise() {
+    if (!(s > 0.f && s < INFINITY)) return;
+    const uint32_t b = __float_as_uint(s);
+    c += (float)((int)(b >> 23) - 127);
+    s = __uint_as_float((b & 0x7fffffu) | 0x3f800000u);
+  }
+
+  // any values
+  static __device__ __noinline__ Stats add_any(Stats a, const uint32_t (&v)[32]) {
     float most = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
 #pragma unroll
     for (int i = 3; i + 1 < 32; i += 2) most = max3(most, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
     most = fmaxf(most, __uint_as_float(v[31])) * kLog2e;
-    if (most > c) {
+    if (most > a.c) {
       const float up = ceilf(most);
-      s *= ex2(c - up);   // c = -inf: s is 0, and so is the factor
-      c = up;
+      a.s *= ex2(a.c - up);   // c = -inf: s is 0, and so is the factor
+      a.c = up;
     }
     // a NaN, +inf or a whole chunk of -inf makes the differences NaN, and the row's sum with them
-    const f32x2 scale = pair(kLog2e, kLog2e), ref = pair(-c, -c);
-    f32x2 a = pair(0.f, 0.f), b = a;
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      const float2 p = split(fma2(pair(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), scale, ref));
-      const float2 q = split(fma2(pair(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), scale, ref));
-      a = add2(a, pair(ex2(p.x), ex2(p.y)));
-      b = add2(b, pair(ex2(q.x), ex2(q.y)));
-    }
-    const float2 r = split(add2(a, b));
-    s += r.x + r.y;
+    a.s += a.terms(v);
+    return a;
   }
 };
 
@@ -255,12 +304,13 @@ __device__ __forceinline__ void put_sums(const Writer &out, const uint32_t (&v)[
 }
 
 template <int MODE>
-__global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_constant__ Args p) {
+__global__ void __launch_bounds__(Form<MODE>::THREADS, 1) head_gemm_kernel(const __grid_constant__ Args p) {
+  constexpr int KSUB = Form<MODE>::KSUB, EPI_WARPS = Form<MODE>::EPI_WARPS, NFULL = MAX_STAGES * KSUB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *epi_smem = smem + STAGES * STAGE_BYTES;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(epi_smem + EPI_WARPS * BOX_BYTES);
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NUM_BARS);
+  uint8_t *epi_smem = smem + Form<MODE>::RING_BYTES;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(epi_smem + Form<MODE>::EPI_BYTES);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Form<MODE>::NUM_BARS);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
   const uint32_t sbase = smem_u32(smem);
@@ -269,13 +319,13 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
   const uint32_t rank = cluster_rank();  // 0: issues the MMAs; 1: its peer
   auto full = [&](int s, int j) { return bar0 + 8u * (uint32_t)(s * KSUB + j); };
   auto empty = [&](int s) { return bar0 + 8u * (uint32_t)(NFULL + s); };
-  auto accf = [&](int a) { return bar0 + 8u * (uint32_t)(NFULL + STAGES + a); };
-  auto acce = [&](int a) { return bar0 + 8u * (uint32_t)(NFULL + STAGES + 2 + a); };
-  const uint32_t drain_bar = bar0 + 8u * (uint32_t)(NFULL + STAGES + 4);
+  auto accf = [&](int a) { return bar0 + 8u * (uint32_t)(NFULL + MAX_STAGES + a); };
+  auto acce = [&](int a) { return bar0 + 8u * (uint32_t)(NFULL + MAX_STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (uint32_t)(NFULL + MAX_STAGES + 4);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NFULL; ++s) mbar_init(bar0 + 8u * s, 1);   // used in CTA 0: expect_tx for both halves
-    for (int s = 0; s < STAGES; ++s) mbar_init(empty(s), 1);       // multicast commit
+    for (int s = 0; s < MAX_STAGES; ++s) mbar_init(empty(s), 1);       // multicast commit
     for (int a = 0; a < 2; ++a) {
       mbar_init(accf(a), 1);               // multicast commit
       mbar_init(acce(a), 2 * EPI_WARPS);   // used in CTA 0: every epilogue warp of the pair
@@ -302,6 +352,8 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
   const uint32_t tmem = *tmem_slot;
   const Watch w{abort_flag, p.err, p.timeout_ns};
   const unsigned long long drain_ns = p.timeout_ns < 20000000ull ? p.timeout_ns : 20000000ull;
+  const uint32_t a_bytes = MODE == GRADS ? A_STAGE : (uint32_t)p.a_bytes;
+  const uint32_t kb_smem = MODE == GRADS ? KB_BYTES : a_bytes + (uint32_t)p.bn * (BK * 2) / 2;
   wait_for_previous_grid();
   let_next_grid_start();
 
@@ -312,10 +364,7 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
       uint32_t phase = 0;
       uint32_t issued = 0, issued_parity = 0;  // stages ever filled, and the parity of their last fill
       bool ok = true;
-      for (int i = 0; ok; ++i) {
-        const int t = tile_of<MODE>(p, i);
-        if (t < 0) break;
-        const Tile<MODE> cur(p, t);
+      for (Walk<MODE> cur; ok && cur.next(p);) {
         const int bnh = MODE == GRADS ? BNH : p.bn / 2;
         const int m_a = cur.tm * CM + (int)rank * BM;                  // first of this CTA's places on M and N
         const int n_b = cur.tn * (2 * bnh) + (int)rank * bnh;
@@ -342,20 +391,20 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
           for (int j = 0; j < KSUB; ++j) {
             if (j >= valid) break;
             const int k = (cur.kb0 + kb + j) * BK;
-            const uint32_t sa = sbase + stage * STAGE_BYTES + j * KB_BYTES, sb = sa + A_STAGE;
+            const uint32_t sa = sbase + (uint32_t)(stage * KSUB + j) * kb_smem, sb = sa + a_bytes;
             const uint32_t bar = map_to_rank(full(stage, j), 0);
             if (MODE != GRADS) {
               if (mine) tma_load_3d_pair(sa, map_a, bar, k, m_a, 0, p.err);
-              tma_load_3d_pair(sb, &p.b, bar, k, (int)p.v0 + n_b, 0, p.err);
+              tma_load_3d_pair(sb, &p.b, bar, k, p.v0 + n_b, 0, p.err);
             } else if (!cur.dw) {
               if (mine) tma_load_3d_pair(sa, map_a, bar, k, m_a, 0, p.err);
-              load_columns(sb, &p.b, bar, n_b, (int)p.v0 + k, 0, p.wide, p.err);
+              load_columns(sb, &p.b, bar, n_b, p.v0 + k, 0, p.wide, p.err);
             } else {
               load_columns(sa, &p.a2, bar, m_a, k, 0, true, p.err);
               load_columns(sb, &p.b2, bar, n_b, k, 0, true, p.err);
             }
           }
-          if (++stage == STAGES) {
+          if (++stage == p.stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -363,7 +412,7 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
       }
       // After an abort, stages may still be filling: let those copies land.
       if (*abort_flag && rank == 0)
-        for (int s2 = 0; s2 < STAGES; ++s2)
+        for (int s2 = 0; s2 < p.stages; ++s2)
           if (issued & (1u << s2))
             for (int j = 0; j < KSUB; ++j) drain_wait(full(s2, j), (issued_parity >> s2) & 1u, drain_ns);
     }
@@ -376,10 +425,7 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
-      for (int i = 0; ok; ++i) {
-        const int t = tile_of<MODE>(p, i);
-        if (t < 0) break;
-        const Tile<MODE> cur(p, t);
+      for (Walk<MODE> cur; ok && cur.next(p);) {
         ok = wait_bounded(acce(acc), acc_phase ^ 1u, w);
         if (!ok) break;
         tc_fence_after();
@@ -397,7 +443,7 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
               break;
             }
             tc_fence_after();
-            const uint32_t sa = sbase + stage * STAGE_BYTES + j * KB_BYTES, sb = sa + A_STAGE;
+            const uint32_t sa = sbase + (uint32_t)(stage * KSUB + j) * kb_smem, sb = sa + a_bytes;
             // K-major: advance 16 K-elements (32 bytes) inside the swizzle row.
             // MN-major: advance 16 K-rows (two 8-row groups of 1024 bytes);
             // 8192 bytes between 64-wide atoms, 1024 between 8-row groups.
@@ -412,7 +458,7 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
           }
           if (!ok) break;
           tc_commit_mc(empty(stage), 0x3);  // both CTAs may refill this stage
-          if (++stage == STAGES) {
+          if (++stage == p.stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -429,33 +475,40 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
   } else {
     // ---------------------------------------------------------------- epilogue (both CTAs)
     const int ew = warp - 2;
-    const int q = warp & 3, half = ew >> 2;  // TMEM lanes 32q.., and which half of the columns
-    uint8_t *box = epi_smem + ew * BOX_BYTES;
+    // TMEM lanes 32q.., and which of the tile's column ranges: halves, quarters in STATS (32 columns at least)
+    const int q = warp & 3, range = ew >> 2;
+    const int each = MODE == GRADS ? BNH : MODE == DLOGITS ? p.bn / 2 : max(p.bn / 4, 32);
+    uint8_t *box = epi_smem + ew * (Form<MODE>::BOXES * BOX_BYTES);
     Writer out{box, smem_u32(box)};
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int i = 0;; ++i) {
-      const int t = tile_of<MODE>(p, i);
-      if (t < 0) break;
-      const Tile<MODE> cur(p, t);
+    bool ok = true;
+    for (Walk<MODE> cur; cur.next(p);) {
       const int row0 = cur.tm * CM + (int)rank * BM + q * 32, row = row0 + lane;
       HeadRow hr{0.f, 0.f, 0.f, -1};
-      long long target = -1;
-      if (MODE == DLOGITS && row < p.rows) hr = p.row[row];
-      if (MODE == STATS && row < p.rows) target = __ldg(p.targets + row);
-      if (!__all_sync(0xffffffffu, wait_bounded(accf(acc), acc_phase, w))) break;   // warp-uniform
+      int target = -1;   // counted from v0
+      if (MODE == DLOGITS && row < p.rows) {
+        hr = p.row[row];
+        target = hr.target < 0 ? -1 : hr.target - p.v0;
+      }
+      if (MODE == STATS && row < p.rows) {
+        const int64_t v = __ldg(p.targets + row);
+        target = v >= 0 && v < p.vocab ? (int)v : -1;
+      }
+      if (ok) ok = __all_sync(0xffffffffu, wait_bounded(accf(acc), acc_phase, w));   // warp-uniform
+      if (!ok && MODE != STATS) break;   // in STATS a warp that gave up still meets the others of its rows
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
-      // This warp's half of the columns, 32 at a time, the next 32 on their way while these are worked on.  The
+      // This warp's columns, 32 at a time, the next 32 on their way while these are worked on.  The
       // accumulator is free again when the last are in registers.
-      const int chunks = MODE == GRADS ? BNH / 32 : p.bn / 64, first = half * (MODE == GRADS ? BNH : p.bn / 2);
-      bool busy = row0 < p.rows;
+      const int chunks = each / 32, first = range * each;
+      bool busy = row0 < p.rows && (MODE != STATS || first < p.bn);
       int row_at = row0;
       bool sums = false;
       if (MODE == GRADS) {
-        if (cur.dw) row_at += (int)p.v0;
+        if (cur.dw) row_at += p.v0;
         // a part without k-blocks (of a last piece that is short) has nothing to add
-        busy = (cur.dw ? p.v0 + row0 < p.vocab : busy) && cur.num_kb > 0;
+        busy = (cur.dw ? row0 < p.vocab : busy) && cur.num_kb > 0;
         sums = !cur.dw && p.out_kind != 0;
       }
       const CUtensorMap *map = MODE == GRADS && cur.dw ? &p.out2 : &p.out;
@@ -464,33 +517,36 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(map_to_rank(acce(acc), 0));
       };
-      if (!busy) release();
+      if (!ok) busy = false;
+      else if (!busy) release();
       Stats stats;
       uint32_t v[2][32], wo[32];
       if (busy) {
         const float ref = -hr.lse * kLog2e;
+        // a target among this warp's columns?  Rarely, and then once.
+        const int col_first = cur.tn * (MODE == GRADS ? BN : p.bn) + first;   // of z's piece, or of hidden
+        const int hit0 = MODE != GRADS && (unsigned)(target - col_first) < (unsigned)each ? target - col_first : -1;
+        const bool any_hit = MODE != GRADS && __any_sync(0xffffffffu, hit0 >= 0);
         tmem_ld32_issue(taddr + (uint32_t)first, v[0]);
 #pragma unroll
-        for (int ch = 0; ch < BNH / 32; ++ch) {
+        for (int ch = 0; ch < (MODE == STATS ? 2 : BNH / 32); ++ch) {
           if (ch >= chunks) break;
           uint32_t (&z)[32] = v[ch & 1];
           tmem_wait(z);
           if (ch + 1 < chunks) tmem_ld32_issue(taddr + (uint32_t)(first + 32 * (ch + 1)), v[(ch + 1) & 1]);
           else release();
-          const int col0 = cur.tn * (MODE == GRADS ? BN : p.bn) + first + 32 * ch;   // of z's piece, or of hidden
+          const int col0 = col_first + 32 * ch;
           if (MODE == STATS) {
-            const int left = (int)max(0ll, min(p.vocab - col0, 32ll));
-            if (left == 0) continue;
+            const int left = p.vocab - col0;
+            if (left <= 0) continue;
             if (left < 32)
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (i >= left) z[i] = __float_as_uint(-INFINITY);
-            const long long hit = target - col0;
-            if (__any_sync(0xffffffffu, hit >= 0 && hit < left)) {
+            if (any_hit)
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (hit == i && i < left) p.target_logit[row] = __uint_as_float(z[i]);
-            }
+                if (hit0 == 32 * ch + i && i < left) p.target_logit[row] = __uint_as_float(z[i]);
             stats.add(z);
           } else if (MODE == DLOGITS) {
             // rows that take no part have g = 0 and finite z (x's copy holds zeros there)
@@ -502,13 +558,11 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
               d[i] = hr.g * ex2(e.x);
               d[i + 1] = hr.g * ex2(e.y);
             }
-            const int hit = hr.target < 0 ? -1 : (int)(hr.target - p.v0) - col0;
-            if (__any_sync(0xffffffffu, hit >= 0 && hit < 32)) {
+            if (any_hit)
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (hit == i) d[i] -= hr.hit;
-            }
-            const long long left = p.vocab - p.v0 - col0;
+                if (hit0 == 32 * ch + i) d[i] -= hr.hit;
+            const int left = p.vocab - col0;
             if (left < 32)
 #pragma unroll
               for (int i = 0; i < 32; ++i)
@@ -526,8 +580,24 @@ __global__ void __launch_bounds__(THREADS, 1) head_gemm_kernel(const __grid_cons
           }
         }
       }
-      if (MODE == STATS && row < p.rows)
-        p.parts[((long long)cur.tn * 2 + half) * p.rows + row] = make_float2(stats.c, stats.s);
+      if (MODE == STATS && row0 < p.rows) {
+        // the four ranges of these rows' columns meet; the next tile writes the other half of the array
+        stats.normalise();
+        float2 *meet = reinterpret_cast<float2 *>(epi_smem) + acc * (4 * BM) + q * 32 + lane;
+        meet[range * BM] = make_float2(stats.c, stats.s);
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
+        if (range == 0 && row < p.rows) {
+          float c = stats.c, s = stats.s;
+#pragma unroll
+          for (int r = 1; r < 4; ++r) {
+            const float2 o = meet[r * BM];
+            const float up = fmaxf(c, o.x);
+            s = s * (c == up ? 1.f : ex2(c - up)) + o.y * (o.x == up ? 1.f : ex2(o.x - up));
+            c = up;
+          }
+          p.parts[(long long)cur.tn * p.rows + row] = make_float2(c, s);
+        }
+      }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
@@ -574,7 +644,7 @@ int launch(Args &p, int64_t tiles, int trace_kind, cudaStream_t s) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MUON_ERR_CUDA;
   auto *kernel = head_gemm_kernel<MODE>;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.blockDim = dim3(Form<MODE>::THREADS, 1, 1);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -584,9 +654,10 @@ int launch(Args &p, int64_t tiles, int trace_kind, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;   // the occupancy query knows clusters only
-  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.dynamicSmemBytes = Form<MODE>::SMEM_BYTES;
   std::call_once(attr_once[dev], [&] {
-    attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Form<MODE>::SMEM_BYTES);
     int n = 0;
     cfg.gridDim = dim3(2 * (unsigned)std::max(1, num_sms() / 2), 1, 1);
     if (attr_err[dev] == cudaSuccess && cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0)
@@ -599,7 +670,12 @@ int launch(Args &p, int64_t tiles, int trace_kind, cudaStream_t s) {
   p.err = device_error_word();
   p.timeout_ns = wait_timeout_ns();
   if (!p.err) return MUON_ERR_CUDA;
+  // few rows or columns leave room for more k-blocks on their way: short ones arrive one latency after the other
+  p.a_bytes = MODE == GRADS ? A_STAGE : (int)((std::min<int64_t>(p.rows, BM) + 7) / 8 * 8 * BK * 2);
+  const int kb_smem = p.a_bytes + (MODE == GRADS ? B_STAGE : p.bn * BK);
+  p.stages = std::min(MAX_STAGES, (Form<MODE>::RING_BYTES - (A_STAGE - p.a_bytes)) / (kb_smem * Form<MODE>::KSUB));
   const int64_t pairs = std::min<int64_t>(tiles, max_pairs[dev]);
+  if (MODE != GRADS) p.step_n = (int)pairs / p.group, p.step_r = (int)pairs % p.group;
   cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
   cfg.numAttrs = 2;
   cfg.stream = s;
@@ -640,7 +716,7 @@ int group_of(const HeadShape &h) { return (int)std::clamp<int64_t>(kGroupBytes /
 }  // namespace
 
 int head_stats_columns(const HeadShape &h) { return columns(h, h.vocab, 64); }
-int64_t head_parts(const HeadShape &h) { return 2 * cdiv(h.vocab, head_stats_columns(h)); }
+int64_t head_parts(const HeadShape &h) { return cdiv(h.vocab, head_stats_columns(h)); }
 
 int head_stats(const HeadShape &h, const void *x, int64_t ldx, const void *w, const int64_t *targets, float2 *parts,
                float *target_logit, cudaStream_t s) {
@@ -648,8 +724,8 @@ int head_stats(const HeadShape &h, const void *x, int64_t ldx, const void *w, co
   p.bn = head_stats_columns(h);
   HEAD_TRY(map_rows(p, x, h.rows, h.hidden, ldx));
   HEAD_TRY(make_map(&p.b, w, 1, h.vocab, h.hidden, p.bn / 2));
-  p.rows = h.rows;
-  p.vocab = h.vocab;
+  p.rows = (int)h.rows;
+  p.vocab = (int)h.vocab;
   p.hidden = (int)h.hidden;
   p.kblocks = (int)cdiv(h.hidden, BK);
   p.tiles_m = (int)cdiv(h.rows, CM);
@@ -695,10 +771,10 @@ int head_dlogits(const HeadShape &h, const HeadPlan &plan, int64_t v0, const voi
   HEAD_TRY(map_rows(p, xc, h.rows, h.hidden, xc_cols));
   HEAD_TRY(make_map(&p.b, w, 1, h.vocab, h.hidden, p.bn / 2));
   HEAD_TRY(make_map(&p.out, d, 1, h.rows, plan.width(), 32));
-  p.rows = h.rows;
-  p.vocab = h.vocab;
+  p.rows = (int)h.rows;
+  p.vocab = (int)(h.vocab - v0);
   p.hidden = (int)h.hidden;
-  p.v0 = v0;
+  p.v0 = (int)v0;
   p.kblocks = (int)cdiv(h.hidden, BK);
   p.tiles_m = (int)cdiv(h.rows, CM);
   // the last piece ends with the vocabulary's last 256 columns
@@ -713,10 +789,10 @@ int head_grads(const HeadShape &h, const HeadPlan &plan, int64_t v0, bool first,
   Args p{};
   const int64_t tiles_v = std::min(plan.piece_tiles, cdiv(h.vocab - v0, CM));
   p.wide = h.hidden % 64 == 0;
-  p.rows = h.rows;
-  p.vocab = h.vocab;
+  p.rows = (int)h.rows;
+  p.vocab = (int)(h.vocab - v0);
   p.hidden = (int)h.hidden;
-  p.v0 = v0;
+  p.v0 = (int)v0;
   p.tiles_m = (int)cdiv(h.rows, CM);
   p.tiles_n = (int)cdiv(h.hidden, BN);
   p.tiles_v = (int)tiles_v;
