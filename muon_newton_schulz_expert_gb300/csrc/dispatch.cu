@@ -11,6 +11,8 @@
 // Every kernel goes by token: the token's own row is read once (or written once) and its k
 // others meet it in registers.  Sums run over the slots in their order, in fp32.
 #include <cooperative_groups.h>
+#include <limits.h>
+
 
 #include <algorithm>
 #include <type_traits>
@@ -27,8 +29,9 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kThreads = 256;
 constexpr int kMaxTop = 32, kSlots = 8;     // slots of a token, and of those in registers at once
 constexpr int64_t kMaxExperts = 1024, kMaxSlots = int64_t(1) << 30, kMaxHidden = int64_t(1) << 20;
-// Slots that every token's block sorts for itself, in one launch: its k places need one pass over
-// the ids each.
+// Slots that every token's block sorts for itself, in one launch: its places need one look at all ids each.  With
+// 512 of 6144 bf16 for 256, 1024 and 2048 slots of 4 a token 3.3, 5.2 and 8.0 us, against 8.5, 12.6 and 14.3 us with the
+// sort in a launch of its own; the looks grow with the square.
 constexpr int64_t kFewSlots = 2048;
 
 __device__ __forceinline__ float to_f(float v) { return v; }
@@ -352,14 +355,17 @@ __global__ void __launch_bounds__(kThreads) dispatch_few_kernel(const RowArgs p)
   }
   const int token = (int)blockIdx.x;
   if (tid < p.top) count[tid] = 0u;
+  int key[kFewSlots / kThreads];   // of this thread's slots, all read at once
+#pragma unroll
+  for (int a = 0; a < kFewSlots / kThreads; ++a)
+    key[a] = a * kThreads + tid < n ? key_of(p.ids[a * kThreads + tid], p.experts, p.err) : INT_MAX;
   __syncthreads();
   for (int j = 0; j < p.top; ++j) {
-    const int slot = token * p.top + j, key = key_of(p.ids[slot], p.experts, p.err);
+    const int slot = token * p.top + j, mine = key_of(p.ids[slot], p.experts, p.err);
     unsigned before = 0u;
-    for (int i = tid; i < n; i += kThreads) {
-      const int k = key_of(p.ids[i], p.experts, p.err);
-      before += k < key || (k == key && i < slot);
-    }
+#pragma unroll
+    for (int a = 0; a < kFewSlots / kThreads; ++a)
+      before += key[a] < mine || (key[a] == mine && a * kThreads + tid < slot);
     before = __reduce_add_sync(kAll, before);
     if (lane == 0 && before) atomicAdd(&count[j], before);
   }
@@ -371,8 +377,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_few_kernel(const RowArgs p)
     if (blockIdx.y == 0) p.place_out[token * p.top + tid] = v;
   }
   __syncthreads();
-  const int c = blockIdx.y * kThreads + tid;
-  if (c < p.vecs) copy_out<BYTES>(p, token, c, place);
+  for (int c = blockIdx.y * kThreads + tid; c < p.vecs; c += gridDim.y * kThreads) copy_out<BYTES>(p, token, c, place);
 }
 
 // out[t]: a thread has the same place of the k rows, their loads in flight together
@@ -573,12 +578,12 @@ int order(const OrderArgs &a, cudaStream_t s) {
   static cudaError_t attr_err[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MUON_ERR_CUDA;
+  auto *kernel = expert_order_kernel;
   auto bytes = [](int64_t experts) { return (size_t)(kOrderWarps + 2) * (experts + 1) * sizeof(unsigned); };
   std::call_once(once[dev], [&] {
-    attr_err[dev] = cudaFuncSetAttribute(expert_order_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)bytes(kMaxExperts));
+    attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes(kMaxExperts));
     if (attr_err[dev] == cudaSuccess)
-      attr_err[dev] = cudaFuncSetAttribute(expert_order_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   });
   if (attr_err[dev] != cudaSuccess) return MUON_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -594,7 +599,7 @@ int order(const OrderArgs &a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   trace_before(kTraceExpertOrder, s);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, expert_order_kernel, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
   const int st = trace_after(kTraceExpertOrder, s);
   return e == cudaSuccess ? st : MUON_ERR_CUDA;
 }
@@ -636,12 +641,15 @@ int muon_dispatch(const void *x, int64_t x_stride, const int64_t *ids, int64_t t
     p.experts = (int)experts;
     p.offsets = offsets;
     p.place_out = place;
-    const dim3 grid((unsigned)tokens + 1, (unsigned)((p.vecs + kThreads - 1) / kThreads));
+    // every block sorts again, so a token's row is shared among blocks only while SMs are left
+    const int64_t share = std::min<int64_t>((p.vecs + kThreads - 1) / kThreads, std::max<int64_t>(1, 2 * num_sms() / tokens));
+    const dim3 grid((unsigned)tokens + 1, (unsigned)share);
     trace_before(kTraceDispatchRows, s);
     with_bytes(bytes, [&](auto b) { dispatch_few_kernel<decltype(b)::value><<<grid, kThreads, 0, s>>>(p); });
     return trace_after(kTraceDispatchRows, s);
   }
-  const int so = order({ids, (int)(tokens * top), (int)experts, offsets, place, err}, s);
+  const OrderArgs oa{ids, (int)(tokens * top), (int)experts, offsets, place, err};
+  const int so = order(oa, s);
   if (so != MUON_OK) return so;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = layout(p, 16 / bytes, true, kBatchSlots);

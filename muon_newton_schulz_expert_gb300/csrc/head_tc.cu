@@ -14,7 +14,7 @@
 // between threads but at a tile's end, where one (c, s) per row is left.  Tiles
 // walk the vocabulary with the row tiles of a group fastest, a group being as many row
 // tiles as keep their x in L2 (kGroupBytes), so that W is read once per group.
-// With few tiles N is 128 or 64, so that more pairs of CTAs have one.
+// With few tiles N is 128 or 64, so that more pairs of CTAs load and reduce one.
 //
 // GRADS runs dx's and dW's tiles in one launch: dx has few tiles with long sums (K =
 // the piece), dW many with short ones (K = rows), and the short ones fill what the long
@@ -704,10 +704,13 @@ int map_rows(Args &p, const void *base, int64_t rows, int64_t cols, int64_t ld) 
 
 int pairs_of_sms() { return std::max(1, num_sms() / 2); }
 
-// columns of a tile of z: the most that leave a tile for each pair of CTAs
+// Columns of a tile of z: fewer than 256 only where the tiles still come out as one for each pair of CTAs.  A k-block
+// takes 485 to 512 cycles of MMAs with 64 columns as with 256 (the rows on M are read for each), so narrow tiles spread
+// the loads and the epilogue and save no products: 513 rows of 4320 over 3802 entries, gradient: 62 us with 45 tiles
+// of 256, 79 us with 90 of 128.
 int columns(const HeadShape &h, int64_t vocab, int least) {
   int bn = BN;
-  while (bn > least && cdiv(h.rows, CM) * cdiv(vocab, bn) < pairs_of_sms()) bn /= 2;
+  while (bn > least && cdiv(h.rows, CM) * cdiv(vocab, bn / 2) <= pairs_of_sms()) bn /= 2;
   return bn;
 }
 
