@@ -53,11 +53,10 @@ enum Mode { STATS = 0, DLOGITS, GRADS };
 template <int MODE>
 struct Form {
   static constexpr int KSUB = 2;
-  // STATS has 16 warps, 4 on each scheduler: a warp's work on a tile is a chain of latencies
-  static constexpr int EPI_WARPS = MODE == STATS ? 16 : 8;
-  static constexpr int BOXES = 1;   // staging boxes of a warp
+  // the exponentials take 16 warps, 4 on each scheduler: a warp's work on a tile is a chain of latencies
+  static constexpr int EPI_WARPS = MODE == GRADS ? 8 : 16;
   static constexpr int RING_BYTES = 6 * KB_BYTES;
-  static constexpr int EPI_BYTES = MODE == STATS ? 2 * 4 * BM * (int)sizeof(float2) : EPI_WARPS * BOXES * BOX_BYTES;
+  static constexpr int EPI_BYTES = MODE == STATS ? 2 * 4 * BM * (int)sizeof(float2) : MODE == GRADS ? EPI_WARPS * BOX_BYTES : 0;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
   static constexpr int NUM_BARS = MAX_STAGES * KSUB + MAX_STAGES + 5;
   static constexpr int SMEM_BYTES = 1024 + RING_BYTES + EPI_BYTES + NUM_BARS * 8 + 16;
@@ -95,7 +94,7 @@ struct Args {
   CUtensorMap a, b;        // STATS, DLOGITS: x and W, K-major;  GRADS: dx's d (K-major) and W (MN-major)
   CUtensorMap a_last;      // a by boxes of the rows that the last CTA with any has
   CUtensorMap a2, b2;      // GRADS: dW's d and x, MN-major
-  CUtensorMap out, out2;   // DLOGITS: d;  GRADS: dx or its sums, and dW
+  CUtensorMap out, out2;   // GRADS: dx or its sums, and dW
   int rows, vocab, v0;     // vocab: entries from v0 on
   int hidden;
   int kblocks, kblocks2;   // of K;  GRADS: of dx's K (the piece) and of dW's (the rows)
@@ -111,6 +110,8 @@ struct Args {
   float2 *parts;
   float *target_logit;
   const HeadRow *row;      // DLOGITS
+  __nv_bfloat16 *d;
+  int width;
   unsigned *err;
   unsigned long long timeout_ns;
 };
@@ -210,6 +211,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+
+// 32 bytes, a whole sector, at once
+__device__ __forceinline__ void store_sector(void *p, const uint32_t *w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 // Waits for the loads that are under way into v.
@@ -337,7 +345,7 @@ __global__ void __launch_bounds__(Form<MODE>::THREADS, 1) head_gemm_kernel(const
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&p.a);
     tma_prefetch_desc(&p.b);
-    if (MODE != STATS) tma_prefetch_desc(&p.out);
+    if (MODE == GRADS) tma_prefetch_desc(&p.out2);
   }
   if (warp == 1) {  // one warp in each CTA of the pair allocates the same columns in both
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -475,10 +483,10 @@ __global__ void __launch_bounds__(Form<MODE>::THREADS, 1) head_gemm_kernel(const
   } else {
     // ---------------------------------------------------------------- epilogue (both CTAs)
     const int ew = warp - 2;
-    // TMEM lanes 32q.., and which of the tile's column ranges: halves, quarters in STATS (32 columns at least)
+    // TMEM lanes 32q.., and which of the tile's column ranges: halves in GRADS, else quarters (32 columns at least)
     const int q = warp & 3, range = ew >> 2;
-    const int each = MODE == GRADS ? BNH : MODE == DLOGITS ? p.bn / 2 : max(p.bn / 4, 32);
-    uint8_t *box = epi_smem + ew * (Form<MODE>::BOXES * BOX_BYTES);
+    const int each = MODE == GRADS ? BNH : max(p.bn / 4, 32);
+    uint8_t *box = epi_smem + (MODE == GRADS ? ew * BOX_BYTES : 0);
     Writer out{box, smem_u32(box)};
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -502,7 +510,7 @@ __global__ void __launch_bounds__(Form<MODE>::THREADS, 1) head_gemm_kernel(const
       // This warp's columns, 32 at a time, the next 32 on their way while these are worked on.  The
       // accumulator is free again when the last are in registers.
       const int chunks = each / 32, first = range * each;
-      bool busy = row0 < p.rows && (MODE != STATS || first < p.bn);
+      bool busy = row0 < p.rows && (MODE == GRADS || first < p.bn);
       int row_at = row0;
       bool sums = false;
       if (MODE == GRADS) {
@@ -529,7 +537,7 @@ __global__ void __launch_bounds__(Form<MODE>::THREADS, 1) head_gemm_kernel(const
         const bool any_hit = MODE != GRADS && __any_sync(0xffffffffu, hit0 >= 0);
         tmem_ld32_issue(taddr + (uint32_t)first, v[0]);
 #pragma unroll
-        for (int ch = 0; ch < (MODE == STATS ? 2 : BNH / 32); ++ch) {
+        for (int ch = 0; ch < (MODE == GRADS ? BNH / 32 : 2); ++ch) {
           if (ch >= chunks) break;
           uint32_t (&z)[32] = v[ch & 1];
           tmem_wait(z);
@@ -568,8 +576,12 @@ __global__ void __launch_bounds__(Form<MODE>::THREADS, 1) head_gemm_kernel(const
               for (int i = 0; i < 32; ++i)
                 if (i >= left) d[i] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) wo[(ch & 1) * 16 + i] = pack_bf16(d[2 * i], d[2 * i + 1]);
-            if (ch & 1) out.put(wo, map, lane, col0 - 32, row0, 0, p.err);
+            for (int i = 0; i < 16; ++i) wo[i] = pack_bf16(d[2 * i], d[2 * i + 1]);
+            if (row < p.rows) {
+              __nv_bfloat16 *dst = p.d + (long long)row * p.width + col0;
+              store_sector(dst, wo);
+              store_sector(dst + 16, wo + 8);
+            }
           } else if (sums) {
             if (col0 < p.hidden) put_sums(out, z, map, p.out_kind == 2, lane, col0, row_at, cur.part, p.err);
           } else {
@@ -601,7 +613,7 @@ __global__ void __launch_bounds__(Form<MODE>::THREADS, 1) head_gemm_kernel(const
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
-    if (lane == 0) bulk_wait_all();
+    if (MODE == GRADS && lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -773,7 +785,8 @@ int head_dlogits(const HeadShape &h, const HeadPlan &plan, int64_t v0, const voi
   p.bn = columns(h, plan.width(), 128);
   HEAD_TRY(map_rows(p, xc, h.rows, h.hidden, xc_cols));
   HEAD_TRY(make_map(&p.b, w, 1, h.vocab, h.hidden, p.bn / 2));
-  HEAD_TRY(make_map(&p.out, d, 1, h.rows, plan.width(), 32));
+  p.d = static_cast<__nv_bfloat16 *>(d);
+  p.width = (int)plan.width();
   p.rows = (int)h.rows;
   p.vocab = (int)(h.vocab - v0);
   p.hidden = (int)h.hidden;
