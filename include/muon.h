@@ -531,7 +531,8 @@ int muon_route_backward(const float *dweights, const void *logits, int64_t strid
  *             results are zeros, and add nothing to gradients).
  *   place     device, int64, [tokens][top]: each slot's row; -1 - row for a slot
  *             that is not routed
- * The order is the same for equal calls.  No workspace, no synchronisation.
+ * The order is the same for equal calls.  x and rows must not overlap.  No workspace,
+ * no synchronisation.
  * tokens == 0 writes zero offsets.  top <= 32, experts <= 1024, tokens * top <=
  * 2^30, hidden <= 2^20 and pointers aligned to their element, else
  * MUON_ERR_UNSUPPORTED (16-byte aligned rows take the widest accesses).
@@ -546,14 +547,14 @@ int muon_dispatch_backward(const void *drows, const int64_t *place, int64_t toke
 /* out[t] = sum of weights[t][j] y[place[t][j]] over the slots that are routed, in the
  * order of the slots and in fp32; y is [tokens * top][hidden] dense, out has y's type.
  * weights: device, fp32, [tokens][top]; NULL stands for ones.  The rows of slots
- * that are not routed are not read.  A place outside 0 .. tokens * top - 1 takes no part and
- * is reported as MUON_ERR_DEVICE. */
+ * that are not routed are not read.  A place that names no row takes no part and is
+ * reported as MUON_ERR_DEVICE.  out must not overlap y.  Limits as muon_dispatch's. */
 int muon_combine(const void *y, const int64_t *place, const float *weights, int64_t tokens, int64_t top,
                  int64_t hidden, int type, void *out, int64_t out_stride, muon_stream_t stream);
 
 /* Its gradients: dy[place[t][j]] = weights[t][j] dout[t] (zeros in rows of slots that are
  * not routed) and dweights[t][j] = <dout[t], y[place[t][j]]> (fp32 sums; 0 for such a slot).
- * Either may be NULL; y is read for dweights alone. */
+ * Either may be NULL; y is read for dweights alone.  dy must not overlap dout or y. */
 int muon_combine_backward(const void *dout, int64_t dout_stride, const void *y, const int64_t *place,
                           const float *weights, int64_t tokens, int64_t top, int64_t hidden, int type, void *dy,
                           float *dweights, muon_stream_t stream);

@@ -509,8 +509,9 @@ PyObject *route(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int score = (int)integer(a[3]), normalize = truth(a[4]);
     const float scale = (float)number(a[5]);
     Out ids, weights;
-    ids.t = c.empty({T, std::max(top, 0)}, x.options().dtype(at::kLong));
-    weights.t = c.empty({T, std::max(top, 0)}, x.options().dtype(at::kFloat));
+    const int64_t k = std::min(std::max(top, 0), 32);   // the library refuses more
+    ids.t = c.empty({T, k}, x.options().dtype(at::kLong));
+    weights.t = c.empty({T, k}, x.options().dtype(at::kFloat));
     const int st = p_route(x.data_ptr(), stride, bias, T, E, code, top, score, normalize, scale,
                            ids.t.data_ptr<int64_t>(), weights.t.data_ptr<float>(), c.stream());
     if (st != MUON_OK) return PyLong_FromLong(st);
@@ -569,6 +570,7 @@ PyObject *dispatch(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int64_t H = xt.size(1);
     const at::Tensor &x = c.rows(a[0], "x", xt.scalar_type(), T, H, &ldx);
     const int experts = small_integer(a[2], "experts");
+    if (k > 32) return PyLong_FromLong(MUON_ERR_UNSUPPORTED);   // before the rows of so many slots are allocated
     Out rows, offsets, place;
     if (given(a[3])) {
       rows.t = c.dense(a[3], "out", x.scalar_type(), {T * k, H});

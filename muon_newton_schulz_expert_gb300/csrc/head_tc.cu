@@ -343,9 +343,14 @@ __global__ void __launch_bounds__(Form<MODE>::THREADS, 1) head_gemm_kernel(const
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&p.a);
-    tma_prefetch_desc(&p.b);
-    if (MODE == GRADS) tma_prefetch_desc(&p.out2);
+    if (MODE != GRADS || p.schedule.longs) {
+      tma_prefetch_desc(&p.a);
+      tma_prefetch_desc(&p.b);
+    }
+    if (MODE == GRADS && p.schedule.shorts) {
+      tma_prefetch_desc(&p.a2);
+      tma_prefetch_desc(&p.b2);
+    }
   }
   if (warp == 1) {  // one warp in each CTA of the pair allocates the same columns in both
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),

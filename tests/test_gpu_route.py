@@ -296,3 +296,12 @@ def test_refusals(mk):
         mk.muon_route_backward(torch.zeros(4, 3, device="cuda"), x, ids)
     with pytest.raises(TypeError, match="ids"):
         mk.muon_route_backward(torch.zeros(4, 2, device="cuda"), x, ids.int())
+
+
+def test_a_refused_count_allocates_nothing(mk):
+    x = torch.zeros(4000, 64, device="cuda")
+    torch.cuda.synchronize()
+    before = torch.cuda.max_memory_allocated()
+    with pytest.raises(mk.MuonError, match="INVALID"):
+        mk.muon_route(x, 1_000_000)
+    assert torch.cuda.max_memory_allocated() - before < 1 << 24
