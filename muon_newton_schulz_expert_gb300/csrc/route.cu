@@ -11,7 +11,7 @@
 // of 384: about 10) and ranked by counting who is larger.  The kernel is bound by instructions,
 // not by its bytes: 16384 rows of 384 with bias, top 8, took 34 us as k rounds of a warp-wide
 // maximum in which the winning lane looked at its values again, 23 us with integer keys made
-// of every value, 16.6 us so.
+// of every value, 16.1 us so.
 //
 // With a bias the keys are sums of two numbers, and fp32 may not tell two of them apart
 // that 64 bits do.  Where two neighbours in the order are closer than the keys' error
@@ -163,6 +163,10 @@ typedef unsigned long long Candidate;
 __device__ __forceinline__ Candidate candidate(float key, int e) {
   return (Candidate)order_of(key) << 32 | (0xffffffffu - (unsigned)e);
 }
+// as it is gathered, before its key is put in order
+__device__ __forceinline__ Candidate gathered_as(float key, int e) {
+  return (Candidate)__float_as_uint(key) << 32 | (unsigned)e;
+}
 __device__ __forceinline__ int expert_of(Candidate c) { return (int)(0xffffffffu - (unsigned)c); }
 __device__ __forceinline__ float key_of(Candidate c) { return value_of((uint32_t)(c >> 32)); }
 template <bool BIAS>
@@ -194,14 +198,21 @@ __global__ void __launch_bounds__(kThreads, R <= 12 ? 5 : R <= 16 ? 4 : 3) route
     sum = warp_sum((part[0] + part[1]) + (part[2] + part[3]));
   }
   const float inv = 1.f / sum;
+  if (BIAS) {
+    float bias[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (BIAS) {
-      const float s = p.softmax ? fast_exp(key[i] - m) * inv : fast_inverse(1.f + fast_exp(-key[i]));
-      key[i] = key[i] == -INFINITY ? key[i] : s + __ldg(p.bias + i * 32 + lane);
+    for (int i = 0; i < R; ++i) bias[i] = i * 32 + lane < p.experts ? __ldg(p.bias + i * 32 + lane) : 0.f;
+    if (p.softmax) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) key[i] = key[i] == -INFINITY ? key[i] : fmaf(fast_exp(key[i] - m), inv, bias[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        key[i] = key[i] == -INFINITY ? key[i] : fast_inverse(1.f + fast_exp(-key[i])) + bias[i];
     }
-    best = max_nan(best, key[i]);
   }
+#pragma unroll
+  for (int i = 0; i < R; ++i) best = max_nan(best, key[i]);
   // Keys are within eps and 2^-23 of themselves: a fast exponential is within 2^-22 + 2^-24 |its argument| of
   // itself, which a sigmoid turns into 2^-20 at most and a softmax, whose sum of up to 1024 terms takes 14
   // roundings on a path, into 2^-19 of its largest score (s |x - m| is at most 0.37 of that).
@@ -223,13 +234,16 @@ __global__ void __launch_bounds__(kThreads, R <= 12 ? 5 : R <= 16 ? 4 : 3) route
     const unsigned who = __ballot_sync(kAll, is);
     if (who == 0u) continue;
     const int at = count + __popc(who & ((1u << lane) - 1u));
-    if (is && at < kCandidates) g.c[at] = candidate(key[i], i * 32 + lane);
+    if (is && at < kCandidates) g.c[at] = gathered_as(key[i], i * 32 + lane);
     count += __popc(who);
   }
   whole = whole || count > kCandidates;         // ties
   __syncwarp();
   int mine = -1;                                // lane j: the j-th expert
   if (!whole) {
+    for (int c = lane; c < count; c += 32)
+      g.c[c] = candidate(__uint_as_float((uint32_t)(g.c[c] >> 32)), (int)(uint32_t)g.c[c]);
+    __syncwarp();
     for (int c = lane; c < count; c += 32) {
       const Candidate a = g.c[c];
       int before = 0;
