@@ -27,7 +27,7 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kThreads = 256;
-constexpr int kMaxTop = 32, kSlots = 8;     // slots of a token, and of those in registers at once
+constexpr int kMaxTop = 32;     // slots of a token
 constexpr int64_t kMaxExperts = 1024, kMaxSlots = int64_t(1) << 30, kMaxHidden = int64_t(1) << 20;
 // Slots that every token's block sorts for itself, in one launch: its places need one look at all ids each.  With
 // 512 of 6144 bf16 for 256, 1024 and 2048 slots of 4 a token 3.3, 5.2 and 8.0 us, against 8.5, 12.6 and 14.3 us with the
@@ -380,8 +380,9 @@ __global__ void __launch_bounds__(kThreads) dispatch_few_kernel(const RowArgs p)
   for (int c = blockIdx.y * kThreads + tid; c < p.vecs; c += gridDim.y * kThreads) copy_out<BYTES>(p, token, c, place);
 }
 
-// out[t]: a thread has the same place of the k rows, their loads in flight together
-template <typename T, int N>
+// out[t]: a thread has the same place of the k rows, the loads of kSlots of them in flight together.  kSlots is 2, 4 or 8
+// by k: fewer registers leave more blocks on an SM (gradient of 30000 tokens x 1 of 2048: 78 us with 2, 133 us with 8).
+template <typename T, int N, int kSlots>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const RowArgs p) {
   constexpr int U = kAccesses<sizeof(T) * N>;
   __shared__ Batch batch;
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const RowArgs p) {
 // The gradient: a token's threads go over its row once for every kSlots slots, each access of dout
 // meeting those of y.  The products' sums: a thread's in turn, a tree over the warp, and the warps' in order
 // when the block's tokens are done.
-template <typename T, int N>
+template <typename T, int N, int kSlots>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const RowArgs p) {
   constexpr int U = kAccesses<sizeof(T) * N>;
   __shared__ Batch batch;
@@ -494,7 +495,8 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const RowArg
       if (!p.dweights) continue;
 #pragma unroll
       for (int j = 0; j < kSlots; ++j)
-        for (int o = min(tx, 32) / 2; o; o >>= 1) dot[j] += __shfl_xor_sync(kAll, dot[j], o);
+        if (j0 + j < p.top)   // the same for all
+          for (int o = min(tx, 32) / 2; o; o >>= 1) dot[j] += __shfl_xor_sync(kAll, dot[j], o);
       if (warps > 1) {
 #pragma unroll
         for (int j = 0; j < kSlots; ++j)
@@ -535,15 +537,17 @@ int access_bytes(int size, int64_t hidden, std::initializer_list<const void *> p
 }
 
 // How a kernel by tokens is laid out: threads of a token (a power of two that covers its accesses, 8 to 256), the
-// columns' blocks, and how many tokens a block takes in turn: up to 8, as many as leave four blocks for each that
-// the SMs hold, and whose slots fit `most` (a batch's).
-dim3 layout(RowArgs &p, int accesses, bool columns, int most) {
+// columns' blocks, and how many tokens a block takes in turn: up to 8, as many as leave `each` blocks an SM, and whose
+// slots fit `most` (a batch's).  Measured with 16 and 8 blocks an SM: combine's gradient, 4099 tokens x 8 of 2048, 61.6
+// and 54.6 us, dispatch's gradient, 4099 x 4 of 1001 fp32, 21.3 and 17.1, but dispatch 34.0 and 35.4; up to 16 tokens in
+// turn are slower where there are many (16384 x 8 of 6144: combine 277 and 287).
+dim3 layout(RowArgs &p, int accesses, bool columns, int most, int64_t each) {
   const int need = (p.vecs + accesses - 1) / accesses;
   p.tx = 8;
   while (p.tx < kThreads && p.tx < need) p.tx *= 2;
   const int per = kThreads / p.tx;
   const int64_t cols = columns ? (need + p.tx - 1) / p.tx : 1;
-  const int64_t turns = std::min<int64_t>(p.tokens * cols / (16ll * per * num_sms()), 8);
+  const int64_t turns = std::min<int64_t>(p.tokens * cols / (each * per * num_sms()), 8);
   p.turns = (int)std::clamp<int64_t>(turns, 1, std::max(1, most / (per * p.top)));
   return dim3((unsigned)((p.tokens + per * p.turns - 1) / (per * p.turns)), (unsigned)cols);
 }
@@ -557,13 +561,18 @@ void with_bytes(int bytes, F &&f) {
     default: f(std::integral_constant<int, 2>()); break;
   }
 }
-// f(element, elements of an access)
+// f(element, elements of an access, slots in registers at once)
 template <typename F>
-void with_vec(int type, int bytes, F &&f) {
+void with_vec(int type, int bytes, int top, F &&f) {
   with_bytes(bytes, [&](auto b) {
     constexpr int B = decltype(b)::value;
-    if (type == MUON_BF16) f(__nv_bfloat16(), std::integral_constant<int, B / 2>());
-    else if constexpr (B >= 4) f(float(), std::integral_constant<int, B / 4>());
+    auto slots = [&](auto element, auto n) {
+      if (top <= 2) f(element, n, std::integral_constant<int, 2>());
+      else if (top <= 4) f(element, n, std::integral_constant<int, 4>());
+      else f(element, n, std::integral_constant<int, 8>());
+    };
+    if (type == MUON_BF16) slots(__nv_bfloat16(), std::integral_constant<int, B / 2>());
+    else if constexpr (B >= 4) slots(float(), std::integral_constant<int, B / 4>());
   });
 }
 
@@ -652,7 +661,7 @@ int muon_dispatch(const void *x, int64_t x_stride, const int64_t *ids, int64_t t
   const int so = order(oa, s);
   if (so != MUON_OK) return so;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = layout(p, 16 / bytes, true, kBatchSlots);
+  cfg.gridDim = layout(p, 16 / bytes, true, kBatchSlots, 16);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -690,10 +699,10 @@ int muon_combine(const void *y, const int64_t *place, const float *weights, int6
   p.err = device_error_word();
   if (!p.err) return MUON_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid = layout(p, 16 / bytes, true, kBatchSlots);
+  const dim3 grid = layout(p, 16 / bytes, true, kBatchSlots, 8);
   trace_before(kTraceCombine, s);
-  with_vec(type, bytes, [&](auto t, auto n) {
-    combine_kernel<decltype(t), decltype(n)::value><<<grid, kThreads, 0, s>>>(p);
+  with_vec(type, bytes, p.top, [&](auto t, auto n, auto k) {
+    combine_kernel<decltype(t), decltype(n)::value, decltype(k)::value><<<grid, kThreads, 0, s>>>(p);
   });
   return trace_after(kTraceCombine, s);
 }
@@ -729,10 +738,10 @@ int muon_combine_backward(const void *dout, int64_t dout_stride, const void *y, 
   p.err = device_error_word();
   if (!p.err) return MUON_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned blocks = layout(p, 16 / bytes, false, kPartSlots).x;
+  const unsigned blocks = layout(p, 16 / bytes, false, kPartSlots, 8).x;
   trace_before(kTraceCombineBwd, s);
-  with_vec(type, bytes, [&](auto t, auto n) {
-    combine_backward_kernel<decltype(t), decltype(n)::value><<<blocks, kThreads, 0, s>>>(p);
+  with_vec(type, bytes, p.top, [&](auto t, auto n, auto k) {
+    combine_backward_kernel<decltype(t), decltype(n)::value, decltype(k)::value><<<blocks, kThreads, 0, s>>>(p);
   });
   return trace_after(kTraceCombineBwd, s);
 }
