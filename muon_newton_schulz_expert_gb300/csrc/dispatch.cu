@@ -567,8 +567,10 @@ void with_vec(int type, int bytes, int top, F &&f) {
   with_bytes(bytes, [&](auto b) {
     constexpr int B = decltype(b)::value;
     auto slots = [&](auto element, auto n) {
+      // rows of 16-bit elements on 2- or 4-byte boundaries: 16384 tokens x 6 of 2001, 122 us with 4 slots, 140 with 8
+      const bool narrow = B <= 4 && sizeof(element) == 2;
       if (top <= 2) f(element, n, std::integral_constant<int, 2>());
-      else if (top <= 4) f(element, n, std::integral_constant<int, 4>());
+      else if (top <= 4 || narrow) f(element, n, std::integral_constant<int, 4>());
       else f(element, n, std::integral_constant<int, 8>());
     };
     if (type == MUON_BF16) slots(__nv_bfloat16(), std::integral_constant<int, B / 2>());
