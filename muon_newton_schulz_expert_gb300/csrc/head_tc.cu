@@ -247,10 +247,11 @@ struct Stats {
     const float2 r = split(add2(add2(a[0], a[1]), add2(a[2], a[3])));
     return r.x + r.y;
   }
-  __device__ __forceinline__ void add(const uint32_t (&v)[32]) {
+  // `in`: of a row that there is; the others hold anything
+  __device__ __forceinline__ void add(const uint32_t (&v)[32], bool in) {
     if (c == -INFINITY) c = ceilf(__uint_as_float(v[0]) * kLog2e);
     const float more = terms(v);
-    if (more < 0x1p100f) {
+    if (more < 0x1p100f || !in) {
       s += more;
     } else {
       uint32_t copy[32];   // its address is taken, and registers have none
@@ -560,7 +561,7 @@ __global__ void __launch_bounds__(Form<MODE>::THREADS, 1) head_gemm_kernel(const
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (hit0 == 32 * ch + i && i < left) p.target_logit[row] = __uint_as_float(z[i]);
-            stats.add(z);
+            stats.add(z, row < p.rows);
           } else if (MODE == DLOGITS) {
             // rows that take no part have g = 0 and finite z (x's copy holds zeros there)
             float d[32];
