@@ -1,17 +1,18 @@
 // Tensor-core products of the loss over a head matrix W [V][H] and rows x [T][H]:
 //   z = x W^T  (T x V), lse = log sum_v exp z_v, loss = lse - z_target
 //   d_v = g p_v - hit [v = target],  dx = d W,  dW = d^T x
-// z and d exist as tiles only: STATS reduces a tile of z to a maximum and a sum per
+// z and d exist as tiles only: STATS reduces a tile of z to a reference and a sum per
 // row in its epilogue; the backward pass recomputes z by pieces of the vocabulary,
 // DLOGITS stores a piece of d in bf16 and GRADS forms both products that read it.
 //
 // One kernel, instantiated for the three; persistent CTA pairs on output tiles of
 // 256 x up to 256 (tcgen05.mma.cta_group::2, M = 256, K = 16, bf16 operands, fp32
-// accumulation in TMEM), fed by TMA through a ring of k-blocks of 64.
+// accumulation in TMEM), fed by TMA through a ring of k-blocks of 64.  Loop bound: a k-block
+// of MMAs is 512 cycles, and takes 560 to 600 with its operands' way into shared memory.
 //
 // Rows of x are on M, the vocabulary on N: a thread of the epilogue then holds 32
-// columns of one row at a time, so the softmax's maximum and sum need no exchange
-// between threads but at a tile's end, where one (c, s) per row is left.  Tiles
+// columns of one row at a time, so the softmax's sum needs no exchange between
+// threads but at a tile's end, where one (c, s) per row is left.  Tiles
 // walk the vocabulary with the row tiles of a group fastest, a group being as many row
 // tiles as keep their x in L2 (kGroupBytes), so that W is read once per group.
 // With few tiles N is 128 or 64, so that more pairs of CTAs load and reduce one.
@@ -25,7 +26,7 @@
 // (the feed-forward products round h, dg and du the same way); the rest is fp32.
 //
 // Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (even CTA) and TMEM owner, the
-// others (8, in STATS 16) epilogue.  Two accumulators, so that the epilogue of one tile
+// others (16, in GRADS 8) epilogue.  Two accumulators, so that the epilogue of one tile
 // overlaps the next tile's products.  Every wait is bounded (tc.cuh).
 #include <math.h>
 
@@ -49,13 +50,13 @@ constexpr int MAX_STAGES = 16;      // of the ring, whose stages are as many as 
 
 enum Mode { STATS = 0, DLOGITS, GRADS };
 
-// Shared memory of a mode: the ring of k-blocks (stages of KSUB), and what the epilogue's warps need.
+// Shared memory of a mode: the ring of k-blocks (stages of KSUB, each given back by one commit: with one a k-block
+// 4096 rows of 6144 over 128000 entries took 3290 us, not 3082), and what the epilogue's warps need.
+constexpr int KSUB = 2, RING_BYTES = 6 * KB_BYTES;
 template <int MODE>
 struct Form {
-  static constexpr int KSUB = 2;
   // the exponentials take 16 warps, 4 on each scheduler: a warp's work on a tile is a chain of latencies
   static constexpr int EPI_WARPS = MODE == GRADS ? 8 : 16;
-  static constexpr int RING_BYTES = 6 * KB_BYTES;
   static constexpr int EPI_BYTES = MODE == STATS ? 2 * 4 * BM * (int)sizeof(float2) : MODE == GRADS ? EPI_WARPS * BOX_BYTES : 0;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
   static constexpr int NUM_BARS = MAX_STAGES * KSUB + MAX_STAGES + 5;
@@ -102,7 +103,7 @@ struct Args {
   int bn, group;           // columns of a tile, row tiles of a group
   int step_n, step_r;      // STATS, DLOGITS: a step of the number of pairs, in vocabulary tiles and row tiles of a group
   int stages, a_bytes;     // of the ring; of A in a k-block (less than A_STAGE where there are few rows)
-  int tiles_v, splits;     // GRADS: vocabulary tiles of the piece, parts of dx's K
+  int splits;              // GRADS: parts of dx's K
   Schedule schedule;
   bool wide;               // GRADS: W's 128 columns load in one piece
   int out_kind;            // GRADS: 0 dx in bf16, 1 sums written, 2 sums added to
@@ -314,10 +315,10 @@ __device__ __forceinline__ void put_sums(const Writer &out, const uint32_t (&v)[
 
 template <int MODE>
 __global__ void __launch_bounds__(Form<MODE>::THREADS, 1) head_gemm_kernel(const __grid_constant__ Args p) {
-  constexpr int KSUB = Form<MODE>::KSUB, EPI_WARPS = Form<MODE>::EPI_WARPS, NFULL = MAX_STAGES * KSUB;
+  constexpr int EPI_WARPS = Form<MODE>::EPI_WARPS, NFULL = MAX_STAGES * KSUB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *epi_smem = smem + Form<MODE>::RING_BYTES;
+  uint8_t *epi_smem = smem + RING_BYTES;
   uint64_t *bars = reinterpret_cast<uint64_t *>(epi_smem + Form<MODE>::EPI_BYTES);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + Form<MODE>::NUM_BARS);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -688,10 +689,11 @@ int launch(Args &p, int64_t tiles, int trace_kind, cudaStream_t s) {
   p.err = device_error_word();
   p.timeout_ns = wait_timeout_ns();
   if (!p.err) return MUON_ERR_CUDA;
-  // few rows or columns leave room for more k-blocks on their way: short ones arrive one latency after the other
+  // Few rows leave room for more k-blocks on their way (5 rows of 2048 over 120000 entries 86 us, 93 with three stages
+  // of whole ones).  The MMAs read 128 rows of A all the same, of what lies behind, inside the ring.
   p.a_bytes = MODE == GRADS ? A_STAGE : (int)((std::min<int64_t>(p.rows, BM) + 7) / 8 * 8 * BK * 2);
   const int kb_smem = p.a_bytes + (MODE == GRADS ? B_STAGE : p.bn * BK);
-  p.stages = std::min(MAX_STAGES, (Form<MODE>::RING_BYTES - (A_STAGE - p.a_bytes)) / (kb_smem * Form<MODE>::KSUB));
+  p.stages = std::min(MAX_STAGES, (RING_BYTES - (A_STAGE - p.a_bytes)) / (kb_smem * KSUB));
   const int64_t pairs = std::min<int64_t>(tiles, max_pairs[dev]);
   if (MODE != GRADS) p.step_n = (int)pairs / p.group, p.step_r = (int)pairs % p.group;
   cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
@@ -817,7 +819,6 @@ int head_grads(const HeadShape &h, const HeadPlan &plan, int64_t v0, bool first,
   p.v0 = (int)v0;
   p.tiles_m = (int)cdiv(h.rows, CM);
   p.tiles_n = (int)cdiv(h.hidden, BN);
-  p.tiles_v = (int)tiles_v;
   p.kblocks = (int)(tiles_v * (CM / BK));
   p.kblocks2 = (int)cdiv(h.rows, BK);
   p.splits = plan.splits;
@@ -833,7 +834,7 @@ int head_grads(const HeadShape &h, const HeadPlan &plan, int64_t v0, bool first,
     HEAD_TRY(make_map_blocks(&p.a2, d, 1, h.rows, plan.width(), BK, 2));
     HEAD_TRY(make_map_blocks(&p.b2, xc, 1, h.rows, xc_cols, BK, 2));
     HEAD_TRY(make_map(&p.out2, dweight, 1, h.vocab, h.hidden, 32));
-    p.schedule.shorts = p.tiles_v * p.tiles_n;
+    p.schedule.shorts = (int)tiles_v * p.tiles_n;
   }
   return launch<GRADS>(p, (int64_t)p.schedule.longs + p.schedule.shorts, kTraceHeadGrads, s);
 }

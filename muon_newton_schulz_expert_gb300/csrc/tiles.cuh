@@ -45,28 +45,18 @@ struct Writer {
   uint8_t *box;
   uint32_t box_s;
 
-  int turn = 0;
-
-  // BOXES 2: two boxes in turn, one behind the other
-  template <int BOXES = 1>
   __device__ void put(const uint32_t (&w)[32], const CUtensorMap *map, int lane, int col0, int row0, int mat,
                       unsigned *err) {
-    // the box's last store has read it
-    if (BOXES == 2) {
-      turn ^= BOX_BYTES;
-      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-    } else if (lane == 0) {
-      bulk_wait_read_all();
-    }
+    if (lane == 0) bulk_wait_read_all();  // the box's last store has read it
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < 8; ++c)
-      *reinterpret_cast<uint4 *>(box + turn + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+      *reinterpret_cast<uint4 *>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
           make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_3d(map, box_s + turn, col0, row0, mat, err);
+      tma_store_3d(map, box_s, col0, row0, mat, err);
       bulk_commit();
     }
   }
