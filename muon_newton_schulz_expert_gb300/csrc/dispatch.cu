@@ -108,7 +108,9 @@ constexpr int kAhead = 8;
 // lanes whose key is this lane's, by a vote on each of its bits
 __device__ __forceinline__ unsigned same_key(int key, int bits) {
   unsigned same = kAll;
-  for (int b = 0; b < bits; ++b) {
+#pragma unroll
+  for (int b = 0; b < 11; ++b) {   // kMaxExperts + 1 has 11
+    if (b >= bits) break;
     const bool set = (key >> b) & 1;
     const unsigned v = __ballot_sync(kAll, set);
     same &= set ? v : ~v;
@@ -198,17 +200,23 @@ __global__ void __launch_bounds__(kOrderThreads) expert_order_kernel(const Order
     int64_t id[kAhead];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) id[a] = b + 32 * a + lane < hi ? p.ids[b + 32 * a + lane] : 0;
+    unsigned same[kAhead];
+    int key[kAhead];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      const bool in = b + 32 * a + lane < hi;
-      const int key = in ? key_of(id[a], E, p.err) : E + 1;
-      const unsigned same = same_key(key, bits), below = same & ((1u << lane) - 1u);
+      key[a] = b + 32 * a + lane < hi ? key_of(id[a], E, p.err) : E + 1;
+      same[a] = same_key(key[a], bits);
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const bool in = key[a] <= E;
+      const unsigned below = same[a] & ((1u << lane) - 1u);
       unsigned at = 0u;
-      if (in) at = start[key] + mine[key] + __popc(below);
+      if (in) at = start[key[a]] + mine[key[a]] + __popc(below);
       __syncwarp();
-      if (in && below == 0u) mine[key] += __popc(same);
+      if (in && below == 0u) mine[key[a]] += __popc(same[a]);
       __syncwarp();
-      if (in) p.place[b + 32 * a + lane] = key < E ? (int64_t)at : -1 - (int64_t)at;
+      if (in) p.place[b + 32 * a + lane] = key[a] < E ? (int64_t)at : -1 - (int64_t)at;
     }
   }
   cluster.sync();   // no block leaves while another reads its totals
