@@ -470,18 +470,23 @@ def _ops():
     return _ops_module
 
 
+_torch_c = None
+
+
 def _raw_stream(stream):
     """The stream's handle, its device and whether they are the current ones for certain.
 
     None is the current stream of the current device, which a bare handle is on too.
     """
-    from torch import _C
+    global _torch_c
+    if _torch_c is None:      # an import statement took half a microsecond of every call
+        from torch import _C as _torch_c
     if stream is None:
-        device = _C._cuda_getDevice()
-        return _C._cuda_getCurrentRawStream(device), device, True
+        device = _torch_c._cuda_getDevice()
+        return _torch_c._cuda_getCurrentRawStream(device), device, True
     if hasattr(stream, "cuda_stream"):
         return stream.cuda_stream, stream.device_index, False
-    return int(stream), _C._cuda_getDevice(), False
+    return int(stream), _torch_c._cuda_getDevice(), False
 
 
 def _outputs(call, result):
