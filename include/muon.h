@@ -583,7 +583,8 @@ int muon_head_loss(const void *x, int64_t x_stride, const void *weight, const in
  * formed again, piece by piece, and with p_v = exp(z_v - lse)
  *   d_v = (dloss + dlse) p_v - dloss 1[v = target];   dx = d weight;   dweight = d^T x
  * lse is the forward call's; dlse (fp32, rows) may be NULL (zero).  A row with a
- * negative target takes no part, whatever else it holds, and its dx is zeros; one
+ * negative target takes no part, whatever else it holds, and its dx is zeros (a NaN
+ * or infinity in weight is in every row's dx); one
  * >= vocab is treated so and reported as MUON_ERR_DEVICE.  dx (rows dx_stride apart) and
  * dweight ([vocab][hidden]) are bf16, written whole, and either may be NULL.  d is rounded to
  * bf16 before the products that read it, sums are fp32 and in a fixed order.

@@ -11,7 +11,10 @@
 // of 384: about 10) and ranked by counting who is larger.  The kernel is bound by instructions,
 // not by its bytes: 16384 rows of 384 with bias, top 8, took 34 us as k rounds of a warp-wide
 // maximum in which the winning lane looked at its values again, 23 us with integer keys made
-// of every value, 16.1 us so.
+// of every value, 16.1 us so.  Where ties (a router before its first step, bf16 logits) or a long
+// choice leave more candidates, the bound is found by bisection and equal keys are cut off by
+// index: all 384 logits and biases equal 71 us, 357 with the choice made in 64 bits; top 32 of
+// 1024 bf16 63 and 448 us.  An ordinary row's 10.3 us (no bias) become 10.9 by it.
 //
 // With a bias the keys are sums of two numbers, and fp32 may not tell two of them apart
 // that 64 bits do.  Where two neighbours in the order are closer than the keys' error
@@ -31,7 +34,7 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kMaxTop = 32, kCandidates = 128;
+constexpr int kMaxTop = 32, kCandidates = 64;
 constexpr int64_t kMaxExperts = 1024, kMaxRows = int64_t(1) << 27;
 
 __device__ __forceinline__ float to_f(float v) { return v; }
@@ -217,27 +220,81 @@ __global__ void __launch_bounds__(kThreads, R <= 12 ? 5 : R <= 16 ? 4 : 3) route
   // itself, which a sigmoid turns into 2^-20 at most and a softmax, whose sum of up to 1024 terms takes 14
   // roundings on a path, into 2^-19 of its largest score (s |x - m| is at most 0.37 of that).
   const float eps = p.softmax ? 0x1p-19f * inv : 0x1p-20f;
-  // at least `top` keys (with a bias one more, to see how far the border is) reach the bound
+  // at least `need` keys reach the bound: with a bias one more than the choice, to see how far the border is
+  constexpr float kLowest = -3.402823466e38f;   // -inf is no candidate
+  const int need = p.top + (BIAS ? 1 : 0);
   float bound = -INFINITY;
-  for (int j = 0, need = p.top + (BIAS ? 1 : 0); j < need; ++j) {
+  for (int j = 0; j < need; ++j) {
     bound = warp_max_nan(best);
     if (!(bound > -INFINITY)) break;
     if (best == bound) best = -INFINITY;
   }
-  if (BIAS && bound > -INFINITY) bound -= 2.f * eps + fabsf(bound) * 0x1p-21f;
-  bool whole = bound != bound;                  // a NaN among the keys, or an infinite one with a bias
-  bound = fmaxf(bound, -3.402823466e38f);       // -inf is no candidate
-  int count = 0;
+  bool whole = bound != bound || (BIAS && bound == INFINITY);   // a NaN among the keys; differences of infinities
+  const float least = fmaxf(bound, kLowest);
+  // what reaches v or may, with the keys' error
+  auto below = [&](float v) { return BIAS ? fmaxf(v - (2.f * eps + fabsf(v) * 0x1p-21f), kLowest) : v; };
+  // the number of keys that reach `bound`, which are gathered; of those that are `border` the first `room` alone
+  auto gather = [&](int room, float border) {
+    int count = 0, met = 0;
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const bool is = key[i] >= bound;
-    const unsigned who = __ballot_sync(kAll, is);
-    if (who == 0u) continue;
-    const int at = count + __popc(who & ((1u << lane) - 1u));
-    if (is && at < kCandidates) g.c[at] = gathered_as(key[i], i * 32 + lane);
-    count += __popc(who);
+    for (int i = 0; i < R; ++i) {
+      bool is = key[i] >= bound;
+      if (room) {
+        const unsigned on = __ballot_sync(kAll, key[i] == border);
+        is = is && (key[i] != border || met + __popc(on & ((1u << lane) - 1u)) < room);
+        met += __popc(on);
+      }
+      const unsigned who = __ballot_sync(kAll, is);
+      if (who == 0u) continue;
+      const int at = count + __popc(who & ((1u << lane) - 1u));
+      if (is && at < kCandidates) g.c[at] = gathered_as(key[i], i * 32 + lane);
+      count += __popc(who);
+    }
+    return count;
+  };
+  bound = below(least);
+  int count = gather(0, 0.f);
+  if (!whole && count > kCandidates) {
+    // Ties, or a choice so long that the lanes' maxima say little.  The bound by bisection over the numbers in their
+    // order, until few enough keys reach it or it is the border itself, with many keys on it or, with a bias, near it.
+    auto reach = [&](float v) {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < R; ++i) n += key[i] >= v;
+      return __reduce_add_sync(kAll, n);
+    };
+    float most = key[0];
+#pragma unroll
+    for (int i = 1; i < R; ++i) most = fmaxf(most, key[i]);
+    most = warp_max(most);
+    uint32_t lo = order_of(least), hi = order_of(most) + 1u;   // `need` keys reach lo, fewer hi
+    while (hi - lo > 1u && count > kCandidates) {
+      const uint32_t mid = lo + (hi - lo) / 2u;
+      if (reach(value_of(mid)) >= need) lo = mid, bound = below(value_of(mid)), count = reach(bound);
+      else hi = mid;
+    }
+    const float border = value_of(lo);
+    int room = 0;
+    if (count > kCandidates) {   // hi is the next number
+      if (BIAS) {
+        // sure if none is just below, and those on the border are one logit with one bias
+        int first = INT_MAX;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (key[i] == border) first = min(first, i * 32 + lane);
+        first = __reduce_min_sync(kAll, first);
+        const float xf = to_f(x[first]), bf = __ldg(p.bias + first);
+        bool differ = border == INFINITY || reach(border) != count;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (key[i] == border) differ = differ || to_f(x[i * 32 + lane]) != xf || __ldg(p.bias + i * 32 + lane) != bf;
+        whole = __any_sync(kAll, differ);
+      }
+      bound = border;
+      room = need - reach(value_of(hi));
+    }
+    if (!whole) count = gather(room, border);
   }
-  whole = whole || count > kCandidates;         // ties
   __syncwarp();
   int mine = -1;                                // lane j: the j-th expert
   if (!whole) {
@@ -255,12 +312,22 @@ __global__ void __launch_bounds__(kThreads, R <= 12 ? 5 : R <= 16 ? 4 : 3) route
     const bool has = lane < min(count, p.top);
     if (has) mine = expert_of(g.sorted[lane]);
     if (BIAS) {
-      bool unsure = false;
-      if (has && lane + 1 < count) {
-        const Candidate next = g.sorted[lane + 1];
-        const float a = key_of(g.sorted[lane]), b = key_of(next);
-        unsure = a - b <= 2.f * eps + (fabsf(a) + fabsf(b)) * 0x1p-23f &&
-                 (to_f(x[mine]) != to_f(x[expert_of(next)]) || __ldg(p.bias + mine) != __ldg(p.bias + expert_of(next)));
+      // two keys so close may be in the wrong order, unless they are one logit with one bias
+      auto close = [&](float a, float b) { return a - b <= 2.f * eps + (fabsf(a) + fabsf(b)) * 0x1p-23f; };
+      auto differ = [&](int a, int b) {
+        return to_f(x[a]) != to_f(x[b]) || __ldg(p.bias + a) != __ldg(p.bias + b);
+      };
+      const Candidate next = g.sorted[min(lane + 1, kMaxTop)];
+      bool unsure = has && lane + 1 < count && close(key_of(g.sorted[min(lane, kMaxTop)]), key_of(next));
+      if (__any_sync(kAll, unsure)) {
+        unsure = unsure && differ(mine, expert_of(next));
+        // the first that was not chosen may be the same as the last that was, and hide another
+        if (count > p.top) {
+          const Candidate last = g.sorted[p.top - 1];
+          for (int c = lane; c < count; c += 32)
+            if (g.c[c] < last && close(key_of(last), key_of(g.c[c])))
+              unsure = unsure || differ(expert_of(last), expert_of(g.c[c]));
+        }
       }
       if (__any_sync(kAll, unsure)) {
         whole = p.softmax;
@@ -383,22 +450,29 @@ __global__ void __launch_bounds__(kThreads) route_few_kernel(const Args p) {
   int mine = -1, last_e = -1;   // the group's j-th lane: its j-th expert
   float last = 0.f;
   bool unsure = false;
-  for (int j = 0; j < p.top + (BIAS ? 1 : 0); ++j) {
+  // two keys so close may be in the wrong order, unless they are one logit with one bias
+  auto close = [&](float a, float b) { return a - b <= 2.f * eps + (fabsf(a) + fabsf(b)) * 0x1p-23f; };
+  auto differ = [&](int a, int b) { return to_f(x[a]) != to_f(x[b]) || __ldg(p.bias + a) != __ldg(p.bias + b); };
+  for (int j = 0; j < p.top; ++j) {
     const uint32_t k = group_max<L>(best);
     const int e = group_min<L>(best == k ? at * L + me : INT_MAX);
-    if (BIAS) {
+    if (BIAS && k) {
       const float v = value_of(k);
-      if (j > 0 && k && last - v <= 2.f * eps + (fabsf(last) + fabsf(v)) * 0x1p-23f)
-        unsure = unsure || to_f(x[last_e]) != to_f(x[e]) || __ldg(p.bias + last_e) != __ldg(p.bias + e);
-      last = v, last_e = k ? e : last_e;
+      if (j > 0 && close(last, v)) unsure = unsure || differ(last_e, e);
+      last = v, last_e = e;
     }
-    if (me == j && k && j < p.top) mine = e;
+    if (me == j && k) mine = e;
     if (best == k && at * L + me == e) {
 #pragma unroll
       for (int i = 0; i < R; ++i)
         if (i == at) key[i] = 0u;
       look();
     }
+  }
+  if (BIAS && best && close(last, value_of(best))) {   // the last of the choice and all that were not chosen
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (key[i] && close(last, value_of(key[i]))) unsure = unsure || differ(last_e, i * L + me);
   }
   if (BIAS) {
     // the rows that are not sure of their order, one after the other by the whole warp

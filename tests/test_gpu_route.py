@@ -110,6 +110,36 @@ def test_sums_that_fp32_cannot_tell_apart(mk, score):
         assert torch.equal(mk.muon_route(x, top, bias=bias, score=score).ids, chosen64(x, bias, score, top))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("bias", ["none", "zeros", "levels", "near", "infinite"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,top", [(16, 2), (30, 1), (64, 8), (70, 1), (128, 8), (200, 32), (384, 8), (384, 31), (1000, 16), (1024, 32)])
+def test_many_equal_keys(mk, E, top, score, bias, dt):
+    """Logits and biases of a few levels each, so that hundreds of keys meet at the border of the choice."""
+    g = torch.Generator(device="cuda").manual_seed(E + top)
+    T = 200
+    x = torch.randint(-2, 3, (T, E), generator=g, device="cuda").float()
+    x[0] = 0.0                                         # a router before its first step
+    x[1], x[1, top // 2:] = 1.0, -0.0
+    x[2], x[2, -top:] = -INF, 0.5                      # as many as are asked for
+    x[3], x[3, E // 2] = torch.finfo(torch.bfloat16).min, -INF
+    x[4], x[4, :40] = 3.0, INF if score == "sigmoid" else 3.5
+    x[100:150] = torch.randn(50, E, generator=g, device="cuda")
+    x = x.to(DT[dt])
+    b = {"none": None, "zeros": torch.zeros(E, device="cuda"),
+         "levels": torch.randint(0, 3, (E,), generator=g, device="cuda") * 0.125,
+         # sums a step or two apart, which only 64 bits put in order
+         "near": 0.25 + torch.randint(0, 3, (E,), generator=g, device="cuda") * 2.0 ** -25,
+         "infinite": torch.where(torch.rand(E, generator=g, device="cuda") < 0.3, INF, 0.0)}[bias]
+    if bias == "infinite":
+        b[::7] = -INF
+    got = mk.muon_route(x, top, bias=b, score=score)
+    ids = chosen64(x, b, score, top)
+    assert torch.equal(got.ids, ids)
+    want = weights64(x, ids, score, True, 1.0)
+    assert bool(((got.weights.double() - want).abs() <= 2.0 ** -16 * want.abs()).all())
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_more_candidates_than_lanes_at_the_border(mk, score):
     # sums with a bias of 1000 are multiples of 2^-14 in fp32: nearly all are equal there, none in 64 bits
