@@ -140,6 +140,17 @@ def test_many_equal_keys(mk, E, top, score, bias, dt):
     assert bool(((got.weights.double() - want).abs() <= 2.0 ** -16 * want.abs()).all())
 
 
+@pytest.mark.parametrize("spread", [0.3, 3.0])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,top", [(60000, 64, 8), (30000, 100, 16), (20000, 384, 8), (20000, 1000, 32)])
+def test_many_rows_choose_as_64_bits(mk, T, E, top, score, spread):
+    """So many rows that some hold sums which meet by chance, of unlike scores and biases."""
+    g = torch.Generator(device="cuda").manual_seed(E)
+    x = torch.randn(T, E, generator=g, device="cuda") * spread
+    b = torch.randn(E, generator=g, device="cuda") * (2.0 / E if score == "softmax" else 0.1)
+    assert torch.equal(mk.muon_route(x, top, bias=b, score=score).ids, chosen64(x, b, score, top))
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_more_candidates_than_lanes_at_the_border(mk, score):
     # sums with a bias of 1000 are multiples of 2^-14 in fp32: nearly all are equal there, none in 64 bits
