@@ -582,7 +582,8 @@ int muon_head_loss(const void *x, int64_t x_stride, const void *weight, const in
 /* The gradients of sum_rows dloss loss + dlse lse, by pieces of the vocabulary: z is
  * formed again, piece by piece, and with p_v = exp(z_v - lse)
  *   d_v = (dloss + dlse) p_v - dloss 1[v = target];   dx = d weight;   dweight = d^T x
- * lse is the forward call's; dlse (fp32, rows) may be NULL (zero).  A row with a
+ * lse is the forward call's; dlse (fp32, rows) may be NULL (zero).  p has lse's rounding,
+ * 2^-24 |lse| of itself, and 1 - p of a nearly certain target that much absolutely.  A row with a
  * negative target takes no part, whatever else it holds, and its dx is zeros (a NaN
  * or infinity in weight is in every row's dx); one
  * >= vocab is treated so and reported as MUON_ERR_DEVICE.  dx (rows dx_stride apart) and
