@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(Form<MODE>::THREADS, 1) head_gemm_kernel(const
         target = v >= 0 && v < p.vocab ? (int)v : -1;
       }
       if (ok) ok = __all_sync(0xffffffffu, wait_bounded(accf(acc), acc_phase, w));   // warp-uniform
-      if (!ok && MODE != STATS) break;   // in STATS a warp that gave up still meets the others of its rows
+      if (!ok && MODE != STATS) break;   // in STATS a warp that gave up still meets the others of its quarter
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
       // This warp's columns, 32 at a time, the next 32 on their way while these are worked on.  The
@@ -601,13 +601,18 @@ __global__ void __launch_bounds__(Form<MODE>::THREADS, 1) head_gemm_kernel(const
           }
         }
       }
-      if (MODE == STATS && row0 < p.rows) {
-        // the four ranges of these rows' columns meet; the next tile writes the other half of the array
-        stats.normalise();
+      if (MODE == STATS) {
+        // The four ranges of these rows' columns meet; the next tile writes the other half of the array.  Quarters
+        // without rows meet too: the barrier of the tile between is what keeps a tile's reads before the writes to
+        // the same half two tiles later, and a pair's tiles may have rows here, none, and rows again.
+        const bool rows_here = row0 < p.rows;
         float2 *meet = reinterpret_cast<float2 *>(epi_smem) + acc * (4 * BM) + q * 32 + lane;
-        meet[range * BM] = make_float2(stats.c, stats.s);
+        if (rows_here) {
+          stats.normalise();
+          meet[range * BM] = make_float2(stats.c, stats.s);
+        }
         asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
-        if (range == 0 && row < p.rows) {
+        if (rows_here && range == 0 && row < p.rows) {
           float c = stats.c, s = stats.s;
 #pragma unroll
           for (int r = 1; r < 4; ++r) {

@@ -156,6 +156,18 @@ def test_rows_of_several_passes(mk):
     assert mk.muon_get_device_status() == 0
 
 
+@pytest.mark.parametrize("T,V,H", [(513, 120000, 8), (700, 40000, 64), (1025, 60001, 16)])
+def test_row_tiles_that_end_early_between_others(mk, T, V, H):
+    """A pair of CTAs goes from a row tile with rows to one without for most of its warps and back, many times."""
+    x, w, t, _, _ = inputs(T, V, H)
+    got = mk.muon_head_loss(x, w, t)
+    assert mk.muon_get_device_status() == 0
+    check_forward(got, x, w, t)
+    for _ in range(20):
+        again = mk.muon_head_loss(x, w, t)
+        assert torch.equal(again.loss, got.loss) and torch.equal(again.lse, got.lse)
+
+
 def test_weight_past_32_bits(mk):
     T, V, H = 4, 360001, 6144                                   # 2.2e9 elements
     g = torch.Generator(device="cuda").manual_seed(3)
