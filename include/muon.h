@@ -568,8 +568,9 @@ int muon_combine_backward(const void *dout, int64_t dout_stride, const void *y, 
  *   targets   device, int64, rows.  A negative target is not scored (loss 0);
  *             one >= vocab gives NaN and MUON_ERR_DEVICE.
  *   loss, lse device, fp32, rows (either may be NULL)
- * bf16 operands, fp32 accumulation; z is not rounded.  A NaN or infinity stays in
- * its row.  A row's result depends on that row and the weight alone, but for the
+ * bf16 operands, fp32 accumulation; z is not rounded.  Logits may be of any size up to
+ * 2^126; -inf is a logit whose exponential is 0.  A NaN or +inf makes its row NaN and stays in
+ * it.  A row's result depends on that row and the weight alone, but for the
  * order of its sums, which the sizes choose.  hidden and x_stride
  * multiples of 8, x and weight 16-byte aligned, vocab <= 2^30, rows <= 2^24, else
  * MUON_ERR_UNSUPPORTED.  workspace as muon_gated_ffn; rows == 0 is a no-op.

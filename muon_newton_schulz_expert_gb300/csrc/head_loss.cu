@@ -34,9 +34,8 @@ int check_shape(const HeadShape &h) {
 
 // Joins a row's partial statistics, in a fixed order: 32 rows a block (lane = row, so that reads of a part are
 // whole lines), the parts spread over the block's warps.
-// Statistics are in powers of two: s = sum 2^(z log2(e) - c).
 //   loss = ((c - z_target log2(e)) + log2 s) ln 2: the difference first, since it is what is small where a target is
-//   likely, with one rounding
+//   likely, with one rounding;  of far logits (z_largest - z_target) + ln s
 constexpr int kJoinWarps = 32, kJoinAhead = 8;   // kJoinAhead parts of a warp are loaded together
 __global__ void __launch_bounds__(32 * kJoinWarps)
     head_join_kernel(const float2 *parts, int64_t num, const float *target_logit, const int64_t *targets, int64_t rows,
@@ -74,12 +73,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     m = most;
   }
   const float ls = log2f(s);
-  constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
-  if (lse) lse[row] = (m + ls) * kLn2;
+  constexpr float kLn2 = 0.6931471805599453f;
+  const bool far = is_far(m);
+  if (lse) lse[row] = far ? fmaf(ls, kLn2, far_logit(m)) : (m + ls) * kLn2;
   if (!loss) return;
   const int64_t t = targets[row];
   if (t >= vocab) atomicOr(err, kErrDevice);
-  loss[row] = t < 0 ? 0.f : t < vocab ? (fmaf(-target_logit[row], kLog2e, m) + ls) * kLn2 : NAN;
+  float v = t < 0 ? 0.f : NAN;
+  if (t >= 0 && t < vocab) {
+    const float zt = target_logit[row];
+    v = far ? fmaf(ls, kLn2, far_logit(m) - zt) : (fmaf(-zt, kLog2e, m) + ls) * kLn2;
+  }
+  loss[row] = v;
 }
 
 // The rows' factors, and x without the rows that take no part (0 times a NaN would reach dW, and d): dense, `cols`

@@ -12,10 +12,21 @@ struct HeadShape {
   int64_t rows, vocab, hidden;
 };
 
+// Softmax statistics (c, s) of a row: s = sum 2^(z log2(e) - c), c a whole number.  Up to 2^23 such a c can be moved by any
+// exponent exactly, and up to 2^30 the product z log2(e) is rounded by 2^5 at most, so that c stays next to the largest
+// term's exponent.  From there on (logits beyond 7e8, where two are 64 apart or equal, so that the sum counts the
+// largest alone) c is twice the largest logit itself: such a c is beyond 2^30, in the logits' order with whole ones too,
+// and so far from any other that 2^(c' - c) is 0 as it has to be.  Joins of statistics need not tell the two apart.
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kWholeReference = 0x1p23f, kFarReference = 0x1p30f;
+__device__ __forceinline__ float far_reference(float most) { return 2.f * most; }   // beyond 2^127: infinite
+__device__ __forceinline__ bool is_far(float c) { return fabsf(c) >= kFarReference; }
+__device__ __forceinline__ float far_logit(float c) { return 0.5f * c; }
+
 // columns of z in a tile of head_stats, chosen so that there are tiles for all SMs
 int head_stats_columns(const HeadShape &h);
-// Partial softmax statistics of z: parts[i][row] = (c, sum 2^(z log2(e) - c)) over the i-th part of the vocabulary
-// (head_parts of them), c a whole number, and target_logit[row] = z[row][targets[row]] where that target is in the vocabulary.
+// Partial softmax statistics of z: parts[i][row] = (c, s) over the i-th part of the vocabulary (head_parts of them), and
+// target_logit[row] = z[row][targets[row]] where that target is in the vocabulary.
 int64_t head_parts(const HeadShape &h);
 int head_stats(const HeadShape &h, const void *x, int64_t ldx, const void *w, const int64_t *targets, float2 *parts,
                float *target_logit, cudaStream_t s);

@@ -64,7 +64,6 @@ struct Form {
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 };
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int64_t kGroupBytes = 48 << 20;   // of x that is used again and again, beside W's stream through 129 MB of L2
 
 // GRADS: dx's tiles (`longs` of them) and then dW's (`shorts`), dealt to the pairs one after the
@@ -229,8 +228,8 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&v)[32]) {
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
 }
 
-// Running softmax statistics of a row in powers of two: s = sum 2^(z log2(e) - c).  c is a whole number, so that
-// z log2(e) - c is one fused operation whose reference has no rounding.
+// Running softmax statistics of a row, Reference and sum as in head_loss.cuh: s = sum 2^(z log2(e) - c).  c is a whole
+// number, so that z log2(e) - c is one fused operation whose reference has no rounding.
 struct Stats {
   float c = -INFINITY, s = 0.f;
 
@@ -252,7 +251,7 @@ struct Stats {
   __device__ __forceinline__ void add(const uint32_t (&v)[32], bool in) {
     if (c == -INFINITY) c = ceilf(__uint_as_float(v[0]) * kLog2e);
     const float more = terms(v);
-    if (more < 0x1p100f || !in) {
+    if ((more < 0x1p100f && fabsf(c) < kWholeReference) || !in) {
       s += more;
     } else {
       uint32_t copy[32];   // its address is taken, and registers have none
@@ -261,9 +260,9 @@ struct Stats {
       *this = add_any(*this, copy);
     }
   }
-  // s between 1 and 2
+  // s between 1 and 2, where c can be moved by its exponent exactly; else its terms had the largest logit as reference
   __device__ __forceinline__ void normalise() {
-    if (!(s > 0.f && s < INFINITY)) return;
+    if (!(s > 0.f && s < INFINITY) || fabsf(c) >= kWholeReference) return;
     const uint32_t b = __float_as_uint(s);
     c += (float)((int)(b >> 23) - 127);
     s = __uint_as_float((b & 0x7fffffu) | 0x3f800000u);
@@ -274,14 +273,30 @@ struct Stats {
     float most = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
 #pragma unroll
     for (int i = 3; i + 1 < 32; i += 2) most = max3(most, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-    most = fmaxf(most, __uint_as_float(v[31])) * kLog2e;
-    if (most > a.c) {
-      const float up = ceilf(most);
-      a.s *= ex2(a.c - up);   // c = -inf: s is 0, and so is the factor
-      a.c = up;
+    most = fmaxf(most, __uint_as_float(v[31]));
+    if (a.s == 0.f) a.c = -INFINITY;   // a guess that no term has met
+    if (fabsf(most * kLog2e) < kFarReference) {
+      const float up = ceilf(most * kLog2e);
+      if (up > a.c) {
+        a.s *= ex2(a.c - up);   // c = -inf: s is 0, and so is the factor
+        a.c = up;
+      }
+      a.s += a.terms(v);   // a NaN is one of the sum
+    } else {
+      // Logits so large are 64 apart or equal: those of the largest count one, the others nothing.
+      const float ref = far_reference(most);
+      if (ref > a.c) {
+        a.s *= ex2(a.c - ref);
+        a.c = ref;
+      }
+      // +inf makes the sum NaN; a whole chunk of -inf adds nothing
+      const float one = ref != a.c || ref == -INFINITY ? 0.f : ref < INFINITY ? 1.f : NAN;
+#pragma unroll 4
+      for (int i = 0; i < 32; ++i) {
+        const float z = __uint_as_float(v[i]);
+        a.s += z != z ? z : z == most ? one : 0.f;
+      }
     }
-    // a NaN, +inf or a whole chunk of -inf makes the differences NaN, and the row's sum with them
-    a.s += a.terms(v);
     return a;
   }
 };

@@ -257,6 +257,52 @@ def test_large_logits(mk):
     check_backward(mk.muon_head_loss_backward(dl, x, w, t, got.lse), x, w, t, got.lse, dl, None)
 
 
+def exact_logits(V, power, seed=0):
+    """x, weight, targets and logits in 64 bits whose products have one term each: z is exact, with many equal ones.
+
+    Of each eight rows the last has negative logits alone; every other target is the largest logit.
+    """
+    g = torch.Generator(device="cuda").manual_seed(seed + V)
+    w = torch.randn(V, 8, generator=g, device="cuda").clamp(-3.9, 3.9).to(BF)
+    w[:, 7] = -w[:, 7].abs() - 0.0625
+    x = torch.zeros(24, 8, device="cuda", dtype=BF)
+    x[torch.arange(24), torch.arange(24) % 8] = 2.0 ** power
+    z = x.double() @ w.double().T
+    t = torch.randint(0, V, (24,), generator=g, device="cuda")
+    t[::2] = z[::2].argmax(1)
+    return x, w, t, z
+
+
+# below 2^23 and above, around 2^30 and up to the largest that are allowed
+@pytest.mark.parametrize("power", [0, 8, 20, 23, 25, 28, 29, 30, 31, 33, 50, 100, 124])
+@pytest.mark.parametrize("V", [1, 40, 300, 5003])
+def test_logits_of_any_size(mk, V, power):
+    """Bounds as above without z's error: 2^-17, and what rounds the results themselves."""
+    x, w, t, z = exact_logits(V, power)
+    got = mk.muon_head_loss(x, w, t)
+    lse = torch.logsumexp(z, 1)
+    most = z.amax(1)
+    loss = (most - z.gather(1, t[:, None])[:, 0]) + (z - most[:, None]).exp().sum(1).log()
+    assert bool(((got.lse.double() - lse).abs() <= 2.0 ** -17 + 2.0 ** -22 * lse.abs()).all())
+    assert bool(((got.loss.double() - loss).abs() <= 2.0 ** -17 + 2.0 ** -21 * loss.abs()).all())
+
+
+def test_logits_of_minus_infinity(mk):
+    """Columns that no row takes, a whole tile's share of them among others; a row with nothing else has lse -inf."""
+    x, w, t, _ = exact_logits(5003, 3)
+    x[:, 1:], x[:, 0] = 0.0, 1.0
+    w[64:96, 0] = w[100:1000:3, 0] = w[1024:2048, 0] = -math.inf
+    w[5000, 0] = 1.0
+    t[:] = 5000
+    z = w[:, 0].double()
+    got = mk.muon_head_loss(x, w, t)
+    lse = float(torch.logsumexp(z, 0))
+    assert float((got.lse.double() - lse).abs().max()) <= 2.0 ** -17 + 2.0 ** -22 * abs(lse)
+    assert float((got.loss.double() - (lse - 1.0)).abs().max()) <= 2.0 ** -17 + 2.0 ** -21 * abs(lse)
+    w[:, 0] = -math.inf
+    assert bool((mk.muon_head_loss(x, w, t).lse == -math.inf).all())
+
+
 def test_targets_out_of_range_are_reported(mk):
     x, w, t, dl, _ = inputs(10, 100, 64)
     want = mk.muon_head_loss(x, w, t)
