@@ -207,6 +207,11 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -554,7 +559,6 @@ __global__ void __launch_bounds__(Form<MODE>::THREADS, 1) head_gemm_kernel(const
       Stats stats;
       uint32_t v[2][32], wo[32];
       if (busy) {
-        const float ref = -hr.lse * kLog2e;
         // a target among this warp's columns?  Rarely, and then once.
         const int col_first = cur.tn * (MODE == GRADS ? BN : p.bn) + first;   // of z's piece, or of hidden
         const int hit0 = MODE != GRADS && (unsigned)(target - col_first) < (unsigned)each ? target - col_first : -1;
@@ -581,12 +585,14 @@ __global__ void __launch_bounds__(Form<MODE>::THREADS, 1) head_gemm_kernel(const
                 if (hit0 == 32 * ch + i && i < left) p.target_logit[row] = __uint_as_float(z[i]);
             stats.add(z, row < p.rows);
           } else if (MODE == DLOGITS) {
-            // rows that take no part have g = 0 and finite z (x's copy holds zeros there)
+            // rows that take no part have g = 0 and finite z (x's copy holds zeros there).  The difference first: next
+            // to a certain target it is exact, and p has no rounding but lse's own.
             float d[32];
-            const f32x2 scale = pair(kLog2e, kLog2e), r2 = pair(ref, ref);
+            const f32x2 scale = pair(kLog2e, kLog2e), minus = pair(-hr.lse, -hr.lse);
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              const float2 e = split(fma2(pair(__uint_as_float(z[i]), __uint_as_float(z[i + 1])), scale, r2));
+              const f32x2 below = add2(pair(__uint_as_float(z[i]), __uint_as_float(z[i + 1])), minus);
+              const float2 e = split(mul2(below, scale));
               d[i] = hr.g * ex2(e.x);
               d[i + 1] = hr.g * ex2(e.y);
             }

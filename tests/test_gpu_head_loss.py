@@ -303,6 +303,29 @@ def test_logits_of_minus_infinity(mk):
     assert bool((mk.muon_head_loss(x, w, t).lse == -math.inf).all())
 
 
+@pytest.mark.parametrize("power", [8, 13, 20, 23, 28, 31, 50, 100])
+def test_gradients_of_certain_targets(mk, power):
+    """Where the target's logit is lse itself and the others far below, p is 1 and d nothing but what dlse adds."""
+    V = 40
+    x = torch.zeros(24, 8, device="cuda", dtype=BF)
+    x[torch.arange(24), torch.arange(24) % 8] = 2.0 ** power
+    t = torch.arange(24, device="cuda") % 8 + 11
+    w = torch.zeros(V, 8, device="cuda", dtype=BF)
+    w[11 + torch.arange(8), torch.arange(8)] = (1 + torch.arange(8, device="cuda") * 2.0 ** -7 * 9).to(BF)
+    lse = (x.float() @ w.float().T).amax(1)             # one term each: exact
+    assert float(lse.min()) > 104                       # exp(-lse) is nothing in fp32
+    one, dz = torch.ones(24, device="cuda"), torch.rand(24, device="cuda")
+    dx, dw = mk.muon_head_loss_backward(one, x, w, t, lse)
+    assert not bool(dx.any()) and not bool(dw.any())
+    # d = dlse at the target, which dx and dw have as their one term: roundings of d and of the results
+    dx, dw = mk.muon_head_loss_backward(one, x, w, t, lse, dlse=dz)
+    want = dz.double()[:, None] * w.double()[t]
+    assert bool(((dx.double() - want).abs() <= 2.0 ** -6.9 * want.abs() + 2.0 ** -22 * w.double()[t]).all())
+    want = torch.zeros(V, 8, device="cuda", dtype=torch.float64).index_add_(0, t, dz.double()[:, None] * x.double())
+    most = torch.zeros(V, 8, device="cuda", dtype=torch.float64).index_add_(0, t, x.double())
+    assert bool(((dw.double() - want).abs() <= 2.0 ** -6.9 * want.abs() + 2.0 ** -22 * most).all())
+
+
 def test_targets_out_of_range_are_reported(mk):
     x, w, t, dl, _ = inputs(10, 100, 64)
     want = mk.muon_head_loss(x, w, t)
