@@ -73,9 +73,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     m = most;
   }
   const float ls = log2f(s);
-  constexpr float kLn2 = 0.6931471805599453f;
+  // 1 / kLog2e in two parts, of the very kLog2e that the logits were multiplied by, so that lse is rounded once
+  constexpr float kLn2 = (float)(1.0 / kLog2e), kLn2Rest = (float)(1.0 / kLog2e - kLn2);
   const bool far = is_far(m);
-  if (lse) lse[row] = far ? fmaf(ls, kLn2, far_logit(m)) : (m + ls) * kLn2;
+  if (lse) lse[row] = far ? fmaf(ls, kLn2, far_logit(m)) : fmaf(m, kLn2, fmaf(m, kLn2Rest, ls * kLn2));
   if (!loss) return;
   const int64_t t = targets[row];
   if (t >= vocab) atomicOr(err, kErrDevice);

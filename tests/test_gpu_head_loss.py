@@ -326,6 +326,31 @@ def test_gradients_of_certain_targets(mk, power):
     assert bool(((dw.double() - want).abs() <= 2.0 ** -6.9 * want.abs() + 2.0 ** -22 * most).all())
 
 
+@pytest.mark.parametrize("power", [5, 8, 13, 20, 23, 26, 29, 31, 50, 100])
+def test_lse_is_rounded_once(mk, power):
+    """One logit far above the others: lse is that logit, and a certain target has no gradient through both calls."""
+    V = 300
+    x = torch.zeros(24, 8, device="cuda", dtype=BF)
+    x[torch.arange(24), torch.arange(24) % 8] = 2.0 ** power
+    t = torch.arange(24, device="cuda") % 8 + 250
+    w = torch.full((V, 8), -1.0, device="cuda", dtype=BF)
+    w[250 + torch.arange(8), torch.arange(8)] = (2 + torch.arange(8, device="cuda") * 2.0 ** -6 * 9).to(BF)
+    z = x.float() @ w.float().T                         # one term each: exact, 2^5 times 3 apart
+    got = mk.muon_head_loss(x, w, t)
+    assert torch.equal(got.lse, z.amax(1))              # exp(-96) is nothing beside the rounding of 64
+    if power >= 8:
+        dx, dw = mk.muon_head_loss_backward(torch.ones(24, device="cuda"), x, w, t, got.lse)
+        assert not bool(dx.any()) and not bool(dw.any())
+
+
+@pytest.mark.parametrize("power", [10, 13, 16, 20])
+def test_lse_within_its_own_rounding(mk, power):
+    x, w, t, z = exact_logits(5003, power, seed=5)
+    lse = torch.logsumexp(z, 1)
+    tol = 2.0 ** -17 + 2.0 ** -24 * (1 + 2.0 ** -6) * lse.abs()   # its terms' and sums' part, then one rounding
+    assert bool(((mk.muon_head_loss(x, w, t).lse.double() - lse).abs() <= tol).all())
+
+
 def test_targets_out_of_range_are_reported(mk):
     x, w, t, dl, _ = inputs(10, 100, 64)
     want = mk.muon_head_loss(x, w, t)
