@@ -567,7 +567,7 @@ int muon_combine_backward(const void *dout, int64_t dout_stride, const void *y, 
  *   weight    device, bf16, [vocab][hidden]
  *   targets   device, int64, rows.  A negative target is not scored (loss 0);
  *             one >= vocab gives NaN and MUON_ERR_DEVICE.
- *   loss, lse device, fp32, rows (either may be NULL)
+ *   loss, lse device, fp32, rows (either may be NULL); a loss is never negative
  * bf16 operands, fp32 accumulation; z is not rounded.  Logits may be of any size up to
  * 2^126; -inf is a logit whose exponential is 0.  A NaN or +inf makes its row NaN and stays in
  * it.  A row's result depends on that row and the weight alone, but for the

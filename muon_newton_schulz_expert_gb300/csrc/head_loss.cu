@@ -34,8 +34,10 @@ int check_shape(const HeadShape &h) {
 
 // Joins a row's partial statistics, in a fixed order: 32 rows a block (lane = row, so that reads of a part are
 // whole lines), the parts spread over the block's warps.
-//   loss = ((c - z_target log2(e)) + log2 s) ln 2: the difference first, since it is what is small where a target is
-//   likely, with one rounding;  of far logits (z_largest - z_target) + ln s
+//   loss = ((c - z_target log2(e)) + log2 s) ln 2;  of far logits (z_largest - z_target) + ln s
+// c is a whole number and not the largest logit's exponent, so a likely target's loss is the difference of two numbers of
+// up to 1, one of which has the exponentials' errors (2^-22, and a rounding of exponents up to 100): it is within 2^-18
+// absolutely, whatever its size, and what would be below 0 by that is 0.
 constexpr int kJoinWarps = 32, kJoinAhead = 8;   // kJoinAhead parts of a warp are loaded together
 __global__ void __launch_bounds__(32 * kJoinWarps)
     head_join_kernel(const float2 *parts, int64_t num, const float *target_logit, const int64_t *targets, int64_t rows,
@@ -84,6 +86,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   if (t >= 0 && t < vocab) {
     const float zt = target_logit[row];
     v = far ? fmaf(ls, kLn2, far_logit(m) - zt) : (fmaf(-zt, kLog2e, m) + ls) * kLn2;
+    if (v < 0.f) v = 0.f;   // a NaN stays
   }
   loss[row] = v;
 }

@@ -351,6 +351,28 @@ def test_lse_within_its_own_rounding(mk, power):
     assert bool(((mk.muon_head_loss(x, w, t).lse.double() - lse).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("V", [1, 2, 33, 300, 5003])
+def test_losses_are_not_negative(mk, V):
+    """Targets that are all of their row's sum, or all but a little: 0 within the exponentials' error, and never below."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    T = 3000
+    x = torch.zeros(T, 8, device="cuda", dtype=BF)
+    x[:, 0] = (5 + 35 * torch.rand(T, generator=g, device="cuda")).to(BF)
+    x[:, 1] = (x[:, 0].float() - 8 - 40 * torch.rand(T, generator=g, device="cuda")).to(BF)
+    w = torch.zeros(V, 8, device="cuda", dtype=BF)
+    w[:, 1] = 1.0
+    t = torch.randint(0, V, (T,), generator=g, device="cuda")
+    w[t[0]], t[:] = torch.tensor([1.0] + 7 * [0.0], device="cuda", dtype=BF), int(t[0])
+    got = mk.muon_head_loss(x, w, t)
+    z = x.double() @ w.double().T
+    zt = z[torch.arange(T), t]
+    rest = (z - zt[:, None]).exp()
+    rest[torch.arange(T), t] = 0.0
+    want = torch.log1p(rest.sum(1))                     # all others are 8 or more below the target
+    assert bool((got.loss >= 0).all())
+    assert bool(((got.loss.double() - want).abs() <= 2.0 ** -17 + 2.0 ** -21 * want).all())
+
+
 def test_targets_out_of_range_are_reported(mk):
     x, w, t, dl, _ = inputs(10, 100, 64)
     want = mk.muon_head_loss(x, w, t)
