@@ -573,7 +573,9 @@ int muon_combine_backward(const void *dout, int64_t dout_stride, const void *y, 
  * it.  A row's result depends on that row and the weight alone, but for the
  * order of its sums, which the sizes choose.  hidden and x_stride
  * multiples of 8, x and weight 16-byte aligned, vocab <= 2^30, rows <= 2^24, else
- * MUON_ERR_UNSUPPORTED.  workspace as muon_gated_ffn; rows == 0 is a no-op.
+ * MUON_ERR_UNSUPPORTED.  workspace as muon_gated_ffn; rows == 0 is a no-op.  The size asked
+ * for holds a copy of up to 16384 rows where they are read often; a call whose x begins on 128
+ * bytes, with x_stride a multiple of 64, makes none and does without that part.
  */
 size_t muon_head_loss_workspace_bytes(int64_t rows, int64_t vocab, int64_t hidden);
 int muon_head_loss(const void *x, int64_t x_stride, const void *weight, const int64_t *targets, int64_t rows,

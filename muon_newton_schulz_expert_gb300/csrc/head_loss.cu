@@ -199,32 +199,34 @@ HeadShape pass_of(const HeadShape &h) { return {std::min(h.rows, kPassRows), h.v
 
 size_t parts_bytes(const HeadShape &h) { return align256((size_t)head_parts(h) * h.rows * sizeof(float2)); }
 
-// the forward call's workspace: offsets and the whole
+// Is x copied first?  Where its rows do not begin on 128 bytes, and are read often enough: from two row tiles of a CTA
+// and two tiles a pair of CTAs on.
+bool off_lines(const void *x, int64_t ldx) { return ldx % 64 || (reinterpret_cast<uintptr_t>(x) & 127u); }
+bool read_often(const HeadShape &pass) {
+  return pass.rows > 128 && cdiv(pass.rows, 256) * cdiv(pass.vocab, 256) >= num_sms();
+}
+
+// the forward call's workspace: offsets and the whole.  `off`: x may have to be copied (a pass of fewer rows is read no
+// more often than the first, and its rows begin where the first's do).
 struct ForwardRegions {
   size_t parts, xa, bytes;
 
-  explicit ForwardRegions(const HeadShape &h) {
+  ForwardRegions(const HeadShape &h, bool off) {
     const HeadShape pass = pass_of(h), last{h.rows % kPassRows, h.vocab, h.hidden};
     // a shorter last pass may cut the vocabulary finer
     const size_t rest = h.rows > kPassRows && last.rows ? parts_bytes(last) : 0;
     parts = align256((size_t)pass.rows * 4);   // behind the targets' logits
     xa = parts + std::max(parts_bytes(pass), rest);
-    bytes = xa + align256((size_t)pass.rows * cdiv(h.hidden, 64) * 128);
+    bytes = xa + (off && read_often(pass) ? align256((size_t)pass.rows * cdiv(h.hidden, 64) * 128) : 0);
   }
 };
-
-// Is x copied first?  Where its rows do not begin on 128 bytes, and are read often enough: from two row tiles of a CTA
-// and two tiles a pair of CTAs on.
-bool aligns(const HeadShape &h, const void *x, int64_t ldx) {
-  return (ldx % 64 || (reinterpret_cast<uintptr_t>(x) & 127u)) && h.rows > 128 &&
-         cdiv(h.rows, 256) * cdiv(h.vocab, 256) >= num_sms();
-}
 
 int forward(const HeadShape &h, const void *x, int64_t ldx, const void *w, const int64_t *targets, float *loss,
             float *lse, uint8_t *scratch, cudaStream_t s) {
   unsigned *err = device_error_word();
   if (!err) return MUON_ERR_CUDA;
-  const ForwardRegions g(h);
+  const bool off = off_lines(x, ldx);
+  const ForwardRegions g(h, off);
   float *target_logit = reinterpret_cast<float *>(scratch);
   float2 *parts = reinterpret_cast<float2 *>(scratch + g.parts);
   const int64_t cols = cdiv(h.hidden, 64) * 64;
@@ -232,7 +234,7 @@ int forward(const HeadShape &h, const void *x, int64_t ldx, const void *w, const
     const HeadShape pass{std::min(kPassRows, h.rows - r), h.vocab, h.hidden};
     const void *xr = static_cast<const uint8_t *>(x) + r * ldx * 2;
     int64_t ld = ldx;
-    if (aligns(pass, xr, ldx)) {
+    if (off && read_often(pass)) {
       MUON_TRY(launch_after(head_align_kernel, (unsigned)pass.rows, 256, kTraceHeadRows, s,
                             static_cast<const uint4 *>(xr), ldx / 8, (int)(h.hidden / 8), (int)(cols / 8),
                             reinterpret_cast<uint4 *>(scratch + g.xa)));
@@ -298,7 +300,7 @@ extern "C" {
 size_t muon_head_loss_workspace_bytes(int64_t rows, int64_t vocab, int64_t hidden) {
   const HeadShape h{rows, vocab, hidden};
   if (rows < 1 || check_shape(h) != MUON_OK) return 0;
-  return ForwardRegions(h).bytes;
+  return ForwardRegions(h, true).bytes;
 }
 
 int muon_head_loss(const void *x, int64_t x_stride, const void *weight, const int64_t *targets, int64_t rows,
@@ -312,7 +314,7 @@ int muon_head_loss(const void *x, int64_t x_stride, const void *weight, const in
     return MUON_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   Scratch ws(s);
-  MUON_TRY(ws.take(workspace, workspace_bytes, ForwardRegions(h).bytes));
+  MUON_TRY(ws.take(workspace, workspace_bytes, ForwardRegions(h, off_lines(x, x_stride)).bytes));
   return ws.done(forward(h, x, x_stride, weight, targets, loss, lse, ws.p, s));
 }
 

@@ -414,6 +414,30 @@ def test_strides_outputs_and_workspaces(mk):
             f()
 
 
+def test_a_copy_that_is_not_made_takes_no_workspace(mk):
+    """Rows that begin on 128 bytes are read where they are; so are few rows, and rows over few entries."""
+    T, V, H = 300, 50003, 192
+    x, w, t, _, _ = inputs(T, V, H)
+    wide = torch.zeros(T, 200, device="cuda", dtype=BF)
+    off = wide[:, 8:]
+    off.copy_(x)
+    need = mk.muon_head_loss_workspace_bytes(T, V, H)
+    copy = T * H * 2
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    want = mk.muon_head_loss(off, w, t, workspace=ws)
+    got = mk.muon_head_loss(x, w, t, workspace=ws[:need - copy])
+    assert torch.equal(got.loss, want.loss) and torch.equal(got.lse, want.lse)
+    with pytest.raises(mk.MuonError, match="NO_MEMORY"):
+        mk.muon_head_loss(off, w, t, workspace=ws[:need - copy])
+    # targets' logits and statistics alone, 8 bytes a row and part of 256 or fewer entries
+    for rows, vocab in ((100, 50003), (2000, 300)):
+        small = mk.muon_head_loss_workspace_bytes(rows, vocab, 6144)
+        assert small <= rows * 4 + rows * -(-vocab // 64) * 8 + 512
+        xs, ws_, ts, _, _ = inputs(rows, vocab, 136)    # off 128 bytes
+        check_forward(mk.muon_head_loss(xs, ws_, ts, workspace=torch.empty(
+            mk.muon_head_loss_workspace_bytes(rows, vocab, 136), dtype=torch.uint8, device="cuda")), xs, ws_, ts)
+
+
 def test_allocation_failure_launches_nothing(mk):
     x, w, t, dl, _ = inputs(20, 300, 64)
     lse = mk.muon_head_loss(x, w, t).lse
