@@ -149,6 +149,28 @@ def test_pieces_of_the_vocabulary(mk):
     check_backward(alone, x, w, t, got.lse, dl, dz, which=(True, False))
 
 
+@pytest.mark.parametrize("T,V,H", [(5000, 2500, 6144), (8192, 1003, 6144)])
+def test_more_row_tiles_than_a_group(mk, T, V, H):
+    """Row tiles whose x outgrows a group's share of L2 (16 of them here): a shorter last group, and whole ones.  Sums of 96
+    k-blocks, many turns of the ring."""
+    x, w, t, dl, dz = inputs(T, V, H)
+    got = mk.muon_head_loss(x, w, t)
+    check_forward(got, x, w, t)
+    grads = mk.muon_head_loss_backward(dl, x, w, t, got.lse, dlse=dz)
+    assert mk.muon_get_device_status() == 0
+    check_backward(grads, x, w, t, got.lse, dl, dz)
+
+
+def test_gradients_of_more_rows_than_a_forward_pass(mk):
+    T, V, H = 17000, 20003, 24                                  # pieces of the vocabulary besides
+    x, w, t, dl, dz = inputs(T, V, H)
+    got = mk.muon_head_loss(x, w, t)
+    check_forward(got, x, w, t)
+    grads = mk.muon_head_loss_backward(dl, x, w, t, got.lse, dlse=dz)
+    assert mk.muon_get_device_status() == 0
+    check_backward(grads, x, w, t, got.lse, dl, dz)
+
+
 def test_rows_of_several_passes(mk):
     T, V, H = 16384 * 2 + 5, 700, 24
     x, w, t, _, _ = inputs(T, V, H)
