@@ -57,6 +57,34 @@ def test_gradients_of_the_whole_block():
         assert err < 0.04, (k, err)
 
 
+def test_a_step_moves_each_parameter_against_its_own_gradient():
+    """The first step of AdamW is lr sign(g) wherever g is far above eps; the router's bias goes towards the experts with
+    less than the mean load.  Muon's step is the gradient with its singular values made one (0.7 to 1.2 by five steps),
+    so the product of the two is the sum of those, at least the gradient's norm by matrix: of 6 matrices of
+    rank 128 their cosine is at least 0.7 / 1.2 / sqrt(6 128) = 0.021.
+    """
+    require_gpu()
+    from examples.train_routed import RoutedBlock
+    block = RoutedBlock(vocab=200, hidden=128, ffn=136, experts=6, top=3)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    tokens = torch.randint(0, 200, (700,), generator=g, device="cuda")
+    targets = torch.randint(0, 200, (700,), generator=g, device="cuda")
+    targets[::9] = -1
+    before = {k: v.clone() for k, v in {**block.p, **block.w, "bias": block.bias}.items()}
+    _, grads, ids = block.gradients(tokens, targets)
+    block.step(tokens, targets, adam_lr=0.25)           # above the rounding of parameters of about 1
+    for k in block.p:
+        move, d = block.p[k].double() - before[k].double(), grads[k].double()
+        clear = d.abs() > 1e-6                          # eps is 1e-8
+        assert bool(clear.any()) and bool((move[clear] * d[clear] < 0).all()), k
+    for k in block.w:
+        move, d = block.w[k].double() - before[k].double(), grads[k].double()
+        assert float((move * d).sum()) < -0.02 * float(move.norm() * d.norm()), k
+    load = torch.stack([(ids == e).sum() for e in range(block.experts)]).double()
+    moved = block.bias.double() - before["bias"].double()
+    assert bool((moved.sign() == (load.mean() - load).sign()).all())
+
+
 def test_the_example_runs():
     require_gpu()
     from examples.train_routed import main
