@@ -498,7 +498,8 @@ int muon_token_logprobs_backward(const void *logits, int64_t stride, const int64
  * are left, the last ids are -1 with weight 0.  A NaN counts as the largest and
  * makes its row's weights NaN (its own alone where weights are single sigmoids), as
  * +inf does under a softmax; ids stay in range and other rows as they are.  Sums
- * are fp32.  No workspace.  MUON_ERR_INVALID_ARG: top < 1 or > experts;
+ * are fp32, and so are sigmoids: one below fp32's range (a logit below about -88) is 0
+ * in weights and gradients, and a row that chose such ones alone has weights of 0.  No workspace.  MUON_ERR_INVALID_ARG: top < 1 or > experts;
  * MUON_ERR_UNSUPPORTED: top > 32, experts > 1024, rows > 2^27, or a pointer not
  * aligned to its element.
  */
@@ -533,6 +534,8 @@ int muon_route_backward(const float *dweights, const void *logits, int64_t strid
  *             that is not routed
  * The order is the same for equal calls.  x and rows must not overlap.  No workspace,
  * no synchronisation.
+ * More than 2048 slots are sorted by a cluster of 16 blocks, which a whole GB300 runs; where a
+ * partition of one cannot, the call is MUON_ERR_CUDA and writes nothing.
  * tokens == 0 writes zero offsets.  top <= 32, experts <= 1024, tokens * top <=
  * 2^30, hidden <= 2^20 and pointers aligned to their element, else
  * MUON_ERR_UNSUPPORTED (16-byte aligned rows take the widest accesses).
@@ -586,7 +589,8 @@ int muon_head_loss(const void *x, int64_t x_stride, const void *weight, const in
  * formed again, piece by piece, and with p_v = exp(z_v - lse)
  *   d_v = (dloss + dlse) p_v - dloss 1[v = target];   dx = d weight;   dweight = d^T x
  * lse is the forward call's; dlse (fp32, rows) may be NULL (zero).  p has lse's rounding,
- * 2^-24 |lse| of itself, and 1 - p of a nearly certain target that much absolutely.  A row with a
+ * 2^-24 |lse| of itself (beside z's error and about 2^-20), and 1 - p of a nearly certain target that
+ * much absolutely.  A row with a
  * negative target takes no part, whatever else it holds, and its dx is zeros (a NaN
  * or infinity in weight is in every row's dx); one
  * >= vocab is treated so and reported as MUON_ERR_DEVICE.  dx (rows dx_stride apart) and

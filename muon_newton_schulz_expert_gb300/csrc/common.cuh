@@ -54,7 +54,7 @@ enum TraceKind : int {
   kTraceDispatchRows,
   kTraceCombine,       // and the gradient of a dispatch
   kTraceCombineBwd,
-  kTraceHeadStats,     // maxima and sums of tiles of x W^T (tensor cores)
+  kTraceHeadStats,     // references and sums of tiles of x W^T (tensor cores)
   kTraceHeadJoin,
   kTraceHeadRows,
   kTraceHeadDlogits,   // a piece of the logits' gradient (tensor cores)

@@ -29,9 +29,9 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kThreads = 256;
 constexpr int kMaxTop = 32;     // slots of a token
 constexpr int64_t kMaxExperts = 1024, kMaxSlots = int64_t(1) << 30, kMaxHidden = int64_t(1) << 20;
-// Slots that every token's block sorts for itself, in one launch: its places need one look at all ids each.  With
-// 512 of 6144 bf16 for 256, 1024 and 2048 slots of 4 a token 3.3, 5.2 and 8.0 us, against 8.5, 12.6 and 14.3 us with the
-// sort in a launch of its own; the looks grow with the square.
+// Slots that every token's block sorts for itself, in one launch: its places need one look at all ids each.  64, 256
+// and 512 tokens of 6144 bf16, 4 slots each: 3.5, 5.3 and 8.2 us, against 8.5, 12.6 and 14.3 us with the sort in a launch
+// of its own; the looks grow with the square.
 constexpr int64_t kFewSlots = 2048;
 
 __device__ __forceinline__ float to_f(float v) { return v; }

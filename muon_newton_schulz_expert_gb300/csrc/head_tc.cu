@@ -8,7 +8,8 @@
 // One kernel, instantiated for the three; persistent CTA pairs on output tiles of
 // 256 x up to 256 (tcgen05.mma.cta_group::2, M = 256, K = 16, bf16 operands, fp32
 // accumulation in TMEM), fed by TMA through a ring of k-blocks of 64.  Loop bound: a k-block
-// of MMAs is 512 cycles, and takes 560 to 600 with its operands' way into shared memory.
+// of MMAs is 512 cycles (128 and 256 with 64 and 128 columns), and takes 560 to 600 with its operands' way into
+// shared memory.
 //
 // Rows of x are on M, the vocabulary on N: a thread of the epilogue then holds 32
 // columns of one row at a time, so the softmax's sum needs no exchange between
@@ -23,7 +24,9 @@
 // than a pair's share of the work, its K is cut and the parts are added in order.
 //
 // Rounding: d is stored in bf16, the operand type of the products that read it, once
-// (the feed-forward products round h, dg and du the same way); the rest is fp32.
+// (the feed-forward products round h, dg and du the same way); the rest is fp32.  Its two
+// halves as two operands would leave dx and dW their own rounding alone, 0.0017 instead of 0.0024 from 64 bits over the
+// batch, for four products in place of two: two thirds more of the whole call's.
 //
 // Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (even CTA) and TMEM owner, the
 // others (16, in GRADS 8) epilogue.  Two accumulators, so that the epilogue of one tile
@@ -752,10 +755,10 @@ int map_rows(Args &p, const void *base, int64_t rows, int64_t cols, int64_t ld) 
 
 int pairs_of_sms() { return std::max(1, num_sms() / 2); }
 
-// Columns of a tile of z: fewer than 256 only where the tiles still come out as one for each pair of CTAs.  A k-block
-// takes 485 to 512 cycles of MMAs with 64 columns as with 256 (the rows on M are read for each), so narrow tiles spread
-// the loads and the epilogue and save no products: 513 rows of 4320 over 3802 entries, gradient: 62 us with 45 tiles
-// of 256, 79 us with 90 of 128.
+// Columns of a tile of z: fewer than 256 only where the tiles still come out as one for each pair of CTAs.  The tensor
+// pipe is busy for 128, 256 and 512 cycles a k-block with 64, 128 and 256 columns, but the loop takes about 485 with the
+// fewest too: A's 16 KB for each CTA come in whatever N is.  So narrow tiles spread the loads of W and the epilogue and save no
+// time on the products: 513 rows of 4320 over 3802 entries, gradient: 62 us with 45 tiles of 256, 79 us with 90 of 128.
 int columns(const HeadShape &h, int64_t vocab, int least) {
   int bn = BN;
   while (bn > least && cdiv(h.rows, CM) * cdiv(vocab, bn / 2) <= pairs_of_sms()) bn /= 2;
